@@ -60,6 +60,15 @@ _SIGS = {
     "moe_grouped_ffn_nvfp4_workspace_size": (SZ, [I64, I, I]),
     "moe_grouped_ffn_nvfp4": (I, [P, P, P, P, I64, I, I, I, P, P, P, P, P, P, P, P, SZ, P, P]),
     "moe_grouped_ffn_mx": (I, [P, P, P, I, I, P, I64, I, I, I, P, P, P, P, P, P, SZ, P, P]),
+    "moe_token_logprobs": (I, [P, I, I64, I64, I64, P, I, F, P, P, P, P]),
+    "moe_policy_loss_workspace_size": (SZ, [I64, I64]),
+    "moe_policy_loss": (I, [P, I, I64, I64, I64, P, I, P, P, P, P, F, F, F, F, F, F, F, P, P, P, I64, P, SZ, P, P]),
+    "moe_router_logits_workspace_size": (SZ, [I, I, I]),
+    "moe_router_logits": (I, [P, P, I, I, I, P, P, SZ, P, P]),
+    "moe_balance_loss_workspace_size": (SZ, [I, I, I]),
+    "moe_balance_loss": (I, [P, P, P, P, I, I, I, I, I, I, F, F, F, F, P, P, P, P, P, SZ, P, P]),
+    "moe_router_backward_dense_workspace_size": (SZ, [I, I, I]),
+    "moe_router_backward_dense": (I, [P, P, P, I, I, I, P, P, P, SZ, P, P]),
     "moe_debug_bounded_wait": (I, [I64, P, P]),
     "moe_device_sm_count": (I, []),
 }
@@ -698,6 +707,219 @@ def moe_combine(out_sorted, slot_to_sorted, gates, y=None, stream=None):
     _check("moe_combine", _lib.moe_combine(
         _ptr(out_sorted), _ptr(slot_to_sorted), _ptr(gates), T, k, d, _ptr(y), _stream(stream)))
     return y
+
+
+MOE_LOGITS_BF16, MOE_LOGITS_F32 = 0, 1
+
+
+def _logit_rows(t, name, like=None):
+    """(dtype code, row stride) of a [N, V] tensor of vocabulary logits: unit
+    column stride, any row stride >= V (like: the type and shape to have)."""
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    if t.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"{name}: expected torch.bfloat16 or torch.float32, got {t.dtype}")
+    if like is not None and (t.dtype != like.dtype or t.shape != like.shape):
+        raise ValueError(f"{name}: expected {like.dtype} {tuple(like.shape)}, got {t.dtype} {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a CUDA tensor")
+    N, V = t.shape
+    if V > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: must have unit column stride")
+    ld = t.stride(0) if N > 1 else V
+    if ld < V:
+        raise ValueError(f"{name}: rows overlap")
+    return (MOE_LOGITS_BF16 if t.dtype == torch.bfloat16 else MOE_LOGITS_F32), ld
+
+
+def _target_bits(targets, N) -> int:
+    if targets.dtype not in (torch.int32, torch.int64):
+        raise TypeError(f"targets: expected torch.int32 or torch.int64, got {targets.dtype}")
+    _want(targets, targets.dtype, (N,), "targets")
+    return 64 if targets.dtype == torch.int64 else 32
+
+
+def moe_token_logprobs(logits, targets, temperature=1.0, logprobs=None, entropy=None, dev_status=None, stream=None):
+    """Log-probabilities [N] fp32 of targets [N] under softmax(logits [N, V] /
+    temperature) -> (logprobs, entropy or None).  entropy: True allocates, a
+    tensor is written.  Rows with a negative target give 0."""
+    dt, ld = _logit_rows(logits, "logits")
+    N, V = logits.shape
+    bits = _target_bits(targets, N)
+    if logprobs is None:
+        logprobs = _empty((N,), torch.float32, logits)
+    else:
+        _want(logprobs, torch.float32, (N,), "logprobs")
+    if entropy is True:
+        entropy = _empty((N,), torch.float32, logits)
+    elif entropy is not None and entropy is not False:
+        _want(entropy, torch.float32, (N,), "entropy")
+    else:
+        entropy = None
+    if dev_status is not None:
+        _want(dev_status, torch.int32, (1,), "dev_status")
+    _check("moe_token_logprobs", _lib.moe_token_logprobs(
+        _ptr(logits), dt, N, V, ld, _ptr(targets), bits, temperature, _ptr(logprobs), _ptr(entropy),
+        _ptr(dev_status), _stream(stream)))
+    return logprobs, entropy
+
+
+def moe_policy_loss_workspace_size(N: int, V: int) -> int:
+    return int(_lib.moe_policy_loss_workspace_size(N, V))
+
+
+def moe_policy_loss(logits, targets, old_logprobs, advantages, ref_logprobs=None, weights=None, temperature=1.0,
+                    clip_low=0.2, clip_high=0.2, kl_coef=0.0, entropy_coef=0.0, norm=0.0, grad_scale=1.0,
+                    stats=None, logprobs=None, dlogits=True, workspace=None, dev_status=None, stream=None):
+    """The clipped policy loss with a KL term and its gradient -> (stats [6]
+    fp32 = loss, mean pg, kl, entropy, clipped share, norm; logprobs [N];
+    dlogits [N, V] in the logits' type or None).  dlogits: True allocates, a
+    tensor is written (it may be logits itself), False / None skips."""
+    dt, ld = _logit_rows(logits, "logits")
+    N, V = logits.shape
+    bits = _target_bits(targets, N)
+    _want(old_logprobs, torch.float32, (N,), "old_logprobs")
+    _want(advantages, torch.float32, (N,), "advantages")
+    if ref_logprobs is not None:
+        _want(ref_logprobs, torch.float32, (N,), "ref_logprobs")
+    if weights is not None:
+        _want(weights, torch.float32, (N,), "weights")
+    if stats is None:
+        stats = _empty((6,), torch.float32, logits)
+    else:
+        _want(stats, torch.float32, (6,), "stats")
+    if logprobs is None:
+        logprobs = _empty((N,), torch.float32, logits)
+    else:
+        _want(logprobs, torch.float32, (N,), "logprobs")
+    ld_d = V
+    if dlogits is True:
+        dlogits = _empty((N, V), logits.dtype, logits)
+    elif dlogits is not None and dlogits is not False:
+        _, ld_d = _logit_rows(dlogits, "dlogits", like=logits)
+    else:
+        dlogits = None
+    if workspace is None:
+        workspace = _empty((moe_policy_loss_workspace_size(N, V),), torch.uint8, logits)
+    if dev_status is not None:
+        _want(dev_status, torch.int32, (1,), "dev_status")
+    _check("moe_policy_loss", _lib.moe_policy_loss(
+        _ptr(logits), dt, N, V, ld, _ptr(targets), bits, _ptr(old_logprobs), _ptr(advantages), _ptr(ref_logprobs),
+        _ptr(weights), temperature, clip_low, clip_high, kl_coef, entropy_coef, norm, grad_scale, _ptr(stats),
+        _ptr(logprobs), _ptr(dlogits), ld_d, _ptr(workspace), workspace.numel() * workspace.element_size(),
+        _ptr(dev_status), _stream(stream)))
+    return stats, logprobs, dlogits
+
+
+def moe_router_logits_workspace_size(T: int, d: int, E: int) -> int:
+    return int(_lib.moe_router_logits_workspace_size(T, d, E))
+
+
+def moe_router_logits(x, w_router, logits=None, workspace=None, dev_status=None, stream=None):
+    """Every expert's router logit [T, E] fp32 (tensor cores, fp32 sums)."""
+    T, d = x.shape
+    E = w_router.shape[0]
+    _want(x, torch.bfloat16, (T, d), "x")
+    _want(w_router, torch.bfloat16, (E, d), "w_router")
+    if logits is None:
+        logits = _empty((T, E), torch.float32, x)
+    else:
+        _want(logits, torch.float32, (T, E), "logits")
+    if workspace is None:
+        workspace = _empty((moe_router_logits_workspace_size(T, d, E),), torch.uint8, x)
+    if dev_status is not None:
+        _want(dev_status, torch.int32, (1,), "dev_status")
+    _check("moe_router_logits", _lib.moe_router_logits(
+        _ptr(x), _ptr(w_router), T, d, E, _ptr(logits), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _ptr(dev_status), _stream(stream)))
+    return logits
+
+
+def moe_balance_loss_workspace_size(T: int, E: int, B: int) -> int:
+    return int(_lib.moe_balance_loss_workspace_size(T, E, B))
+
+
+def moe_balance_loss(logits, topk_ids, score_fn, balance_coef, z_coef=0.0, token_mask=None, seq_offsets=None,
+                     d_gates=None, renorm=1, route_scale=1.0, grad_scale=1.0, counts=None, losses=None,
+                     d_logits=True, workspace=None, dev_status=None, stream=None):
+    """Balance and z losses of the router -> (losses [2] fp32, counts [B, E]
+    int32, d_logits [T, E] fp32 or None).  token_mask [T] bool or uint8,
+    seq_offsets [B+1] int32 (None: one sequence), d_gates [T, k] adds the
+    gradient through the gates.  d_logits: True allocates, a tensor is
+    written, False / None skips."""
+    T, E = logits.shape
+    k = topk_ids.shape[1]
+    _want(logits, torch.float32, (T, E), "logits")
+    _want(topk_ids, torch.int32, (T, k), "topk_ids")
+    if token_mask is not None:
+        if token_mask.dtype not in (torch.bool, torch.uint8):
+            raise TypeError(f"token_mask: expected torch.bool or torch.uint8, got {token_mask.dtype}")
+        _want(token_mask, token_mask.dtype, (T,), "token_mask")
+    B = 1
+    if seq_offsets is not None:
+        B = seq_offsets.numel() - 1
+        _want(seq_offsets, torch.int32, (B + 1,), "seq_offsets")
+    if d_gates is not None:
+        _want(d_gates, torch.float32, (T, k), "d_gates")
+    if counts is None:
+        counts = _empty((max(B, 0), E), torch.int32, logits)
+    else:
+        _want(counts, torch.int32, (B, E), "counts")
+    if losses is None:
+        losses = _empty((2,), torch.float32, logits)
+    else:
+        _want(losses, torch.float32, (2,), "losses")
+    if d_logits is True:
+        d_logits = _empty((T, E), torch.float32, logits)
+    elif d_logits is not None and d_logits is not False:
+        _want(d_logits, torch.float32, (T, E), "d_logits")
+    else:
+        d_logits = None
+    if workspace is None:
+        workspace = _empty((moe_balance_loss_workspace_size(T, E, B),), torch.uint8, logits)
+    if dev_status is not None:
+        _want(dev_status, torch.int32, (1,), "dev_status")
+    _check("moe_balance_loss", _lib.moe_balance_loss(
+        _ptr(logits), _ptr(topk_ids), _ptr(token_mask), _ptr(seq_offsets), T, E, k, B, score_fn, renorm, route_scale,
+        balance_coef, z_coef, grad_scale, _ptr(d_gates), _ptr(counts), _ptr(losses), _ptr(d_logits),
+        _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(dev_status), _stream(stream)))
+    return losses, counts, d_logits
+
+
+def moe_router_backward_dense_workspace_size(T: int, d: int, E: int) -> int:
+    return int(_lib.moe_router_backward_dense_workspace_size(T, d, E))
+
+
+def moe_router_backward_dense(x, w_router, d_logits, dx=True, dw_router=True, workspace=None, dev_status=None,
+                              stream=None):
+    """Router gradients from dense d_logits [T, E] fp32 -> (dx [T, d] fp32 or
+    None, dw_router [E, d] fp32 or None).  dx / dw_router: True allocates, a
+    tensor is written, False / None skips."""
+    T, d = x.shape
+    E = w_router.shape[0]
+    _want(x, torch.bfloat16, (T, d), "x")
+    _want(w_router, torch.bfloat16, (E, d), "w_router")
+    _want(d_logits, torch.float32, (T, E), "d_logits")
+    if dx is True:
+        dx = _empty((T, d), torch.float32, x)
+    elif dx is not None and dx is not False:
+        _want(dx, torch.float32, (T, d), "dx")
+    else:
+        dx = None
+    if dw_router is True:
+        dw_router = _empty((E, d), torch.float32, x)
+    elif dw_router is not None and dw_router is not False:
+        _want(dw_router, torch.float32, (E, d), "dw_router")
+    else:
+        dw_router = None
+    if workspace is None:
+        workspace = _empty((moe_router_backward_dense_workspace_size(T, d, E),), torch.uint8, x)
+    if dev_status is not None:
+        _want(dev_status, torch.int32, (1,), "dev_status")
+    _check("moe_router_backward_dense", _lib.moe_router_backward_dense(
+        _ptr(x), _ptr(w_router), _ptr(d_logits), T, d, E, _ptr(dx), _ptr(dw_router), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _ptr(dev_status), _stream(stream)))
+    return dx, dw_router
 
 
 def moe_debug_bounded_wait(timeout_ns, dev_status, stream=None):

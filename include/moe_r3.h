@@ -561,6 +561,131 @@ moe_status moe_combine_slots(const uint16_t *out_slots, const int32_t *slot_to_s
                              int T, int k, int d, uint16_t *y, void *stream);
 
 /* ------------------------------------------------------------------------
+ * Losses of an RL training step around the layer ("RL at 1T Scale": the
+ * trainer of asynchronous RL for large MoE models, "Router replay").
+ *
+ * Two of them work on the model's logits over the vocabulary, three on the
+ * router's logits over all experts, which the routing calls do not keep (a
+ * replay forms only the chosen ones).
+ *
+ * Rows of vocabulary logits are bf16 (MOE_LOGITS_BF16) or fp32
+ * (MOE_LOGITS_F32), row stride ld >= V elements, no alignment beyond the
+ * element's.  targets [N] are int32 (target_bits 32) or int64 (64).  A row
+ * with a negative target is not scored; one with a target >= V, or with no
+ * logit above -inf, is not scored either and sets MOE_DEV_BAD_IDS.  A row
+ * that is not scored gives logprob 0, entropy 0 and a zero gradient, whatever
+ * its other inputs hold.  A logit of -inf has probability 0; a NaN or +inf
+ * logit of a scored row makes the row's results NaN.
+ *
+ * moe_token_logprobs
+ *   z[t,v] = logits[t,v] / temperature, LSE[t] = log sum_v exp z[t,v],
+ *   p[t,v] = exp(z[t,v] - LSE[t]);
+ *   logprobs[t] = z[t,y_t] - LSE[t], y = targets;
+ *   entropy[t]  = LSE[t] - sum_v p[t,v] z[t,v]  (nullable).
+ *   Sums in fp32, in an order fixed by N and V.
+ * Errors: SHAPE (N < 0, V < 1, N or V >= 2^31, ld < V, dtype, target_bits,
+ * temperature not finite and > 0), NULL, ALIGN (logits not aligned to its
+ * element), CUDA.
+ *
+ * moe_policy_loss -- the clipped policy loss with a KL term, and its gradient
+ *   With lp = logprobs, H = entropy as above and, per token, old_logprobs,
+ *   advantages A, ref_logprobs (nullable: then kl = 0) and weights w
+ *   (nullable: 1), a token with w = 0 not scored:
+ *     r  = exp(min(lp - old, 80)),
+ *     pg = max(-A r, -A clip(r, 1 - clip_low, 1 + clip_high)),
+ *     q  = min(ref - lp, 80),  kl = exp(q) - q - 1,
+ *     loss = 1/norm * sum_t w (pg + kl_coef kl - entropy_coef H),
+ *   norm = the argument if > 0, else sum_t w_t over all N rows (a sum of 0
+ *   gives zeros throughout).  stats [6] = loss, then the weighted means
+ *   (sum_t w (.) / norm) of pg, kl, H and of the clipped tokens (those whose
+ *   clipped side is the larger), then norm.
+ *   dlogits[t,v] (nullable) = grad_scale w / (norm temperature) *
+ *     (g (1[v = y] - p_v) + entropy_coef p_v (log p_v + H)),
+ *     g = (0 if clipped else -A r) + kl_coef (1 - exp(q)),
+ *   in the logits' type (bf16: rounded once, to nearest even), row stride
+ *   ld_d.  dlogits may be logits itself (the gradient replaces them).
+ *   The row is read from memory once where the chip can hold it.
+ * workspace: moe_policy_loss_workspace_size(N, V) bytes, 16-byte aligned; its
+ * contents need no initialisation.  N may be 0: stats are 0.
+ * Errors: as above, and SHAPE (clip_low, clip_high, kl_coef, entropy_coef,
+ * norm or grad_scale not finite, clip bounds negative, norm < 0, ld_d < V),
+ * WORKSPACE.
+ * ---------------------------------------------------------------------- */
+#define MOE_LOGITS_BF16 0
+#define MOE_LOGITS_F32 1
+moe_status moe_token_logprobs(const void *logits, int logits_dtype, int64_t N, int64_t V, int64_t ld,
+                              const void *targets, int target_bits, float temperature, float *logprobs,
+                              float *entropy, int32_t *dev_status, void *stream);
+size_t moe_policy_loss_workspace_size(int64_t N, int64_t V);
+moe_status moe_policy_loss(const void *logits, int logits_dtype, int64_t N, int64_t V, int64_t ld,
+                           const void *targets, int target_bits, const float *old_logprobs,
+                           const float *advantages, const float *ref_logprobs, const float *weights,
+                           float temperature, float clip_low, float clip_high, float kl_coef,
+                           float entropy_coef, float norm, float grad_scale, float *stats, float *logprobs,
+                           void *dlogits, int64_t ld_d, void *workspace, size_t workspace_bytes,
+                           int32_t *dev_status, void *stream);
+
+/* ------------------------------------------------------------------------
+ * The router's losses over all experts ("Router replay": the trainer trains
+ * the router beside the replayed decisions).
+ *
+ * moe_router_logits    logits[t,e] = sum_i x[t,i] w_router[e,i] in fp32 for
+ *                      every expert: tensor-core products summed in fp32, not
+ *                      the fma chain of moe_route_topk (equal to within
+ *                      rounding, not bit for bit).
+ * moe_balance_loss     from logits [T,E] and the ids the tokens went to:
+ *   tokens: t belongs to sequence b if seq_offsets[b] <= t < seq_offsets[b+1]
+ *     (nullable with B = 1: all tokens, one sequence), and is counted if
+ *     token_mask[t] != 0 (nullable: all); n_b = counted tokens of b, n their
+ *     sum over b, B' = number of b with n_b > 0;
+ *   counts[b,e] = counted slots (t,j), t in b, with topk_ids[t,j] = e;
+ *   q[t,:] = softmax(logits[t,:]) (score_fn SOFTMAX) or
+ *     sigmoid(logits[t,:]) / sum_e sigmoid (SIGMOID);
+ *   f[b,e] = E counts[b,e] / (k n_b);
+ *   losses[0] = balance_coef / B' * sum_b sum_e f[b,e] (1/n_b) sum_{t in b} q[t,e],
+ *   losses[1] = z_coef / n * sum_t LSE(logits[t,:])^2  (counted tokens);
+ *   d_logits[t,e] (nullable) = grad_scale * d(losses[0] + losses[1]) /
+ *     d logits[t,e], the counts held fixed, plus, when d_gates [T,k] is given,
+ *     the gradient through the gates of moe_route_topk (score_fn, renorm,
+ *     route_scale; the full softmax over E, renorm 0, included), for every
+ *     token whether counted or not.
+ *   An id outside [0,E) is not counted; a token with such an id, or with a
+ *   repeated one, sets MOE_DEV_BAD_IDS and gets no gradient through its gates.
+ *   A counted token with no logit above -inf adds nothing to the losses.  A
+ *   token that is not counted and whose d_gates are all 0 gets zeros whatever
+ *   its logits hold.  seq_offsets that decrease or leave [0,T] set
+ *   MOE_DEV_ROWS (a token is then in some sequence or in none).
+ *   Sums run in an order fixed by T, E, B and the device; counts are exact.
+ * moe_router_backward_dense  from d_logits [T,E]:
+ *   dx[t,i] = sum_e d_logits[t,e] w_router[e,i]  (nullable),
+ *   dw_router[e,i] = sum_t d_logits[t,e] x[t,i]  (nullable), both fp32.
+ *   d_logits enters the tensor cores as three bf16 parts whose sum holds its
+ *   24 significant bits (parts below the smallest normal bf16 excepted), so
+ *   the products are those of fp32.
+ * x [T,d], w_router [E,d] bf16; logits, d_logits [T,E], dx [T,d], dw_router
+ * [E,d], losses [2] fp32; topk_ids [T,k], counts [B,E], seq_offsets [B+1]
+ * int32; token_mask [T] uint8.  x, w_router, dx, dw_router 16-byte aligned.
+ * workspace: the call's _workspace_size bytes, 256-byte aligned; its contents
+ * need no initialisation.  T may be 0: counts, losses and dw_router, where
+ * given, are zeroed and the [T, .] arrays may be NULL.
+ * Errors: NULL, SHAPE (also B < 1, B > 65535, B > 1 without seq_offsets,
+ * coefficients not finite), ALIGN, WORKSPACE, CUDA.
+ * ---------------------------------------------------------------------- */
+size_t moe_router_logits_workspace_size(int T, int d, int E);
+moe_status moe_router_logits(const uint16_t *x, const uint16_t *w_router, int T, int d, int E, float *logits,
+                             void *workspace, size_t workspace_bytes, int32_t *dev_status, void *stream);
+size_t moe_balance_loss_workspace_size(int T, int E, int B);
+moe_status moe_balance_loss(const float *logits, const int32_t *topk_ids, const uint8_t *token_mask,
+                            const int32_t *seq_offsets, int T, int E, int k, int B, int score_fn, int renorm,
+                            float route_scale, float balance_coef, float z_coef, float grad_scale,
+                            const float *d_gates, int32_t *counts, float *losses, float *d_logits,
+                            void *workspace, size_t workspace_bytes, int32_t *dev_status, void *stream);
+size_t moe_router_backward_dense_workspace_size(int T, int d, int E);
+moe_status moe_router_backward_dense(const uint16_t *x, const uint16_t *w_router, const float *d_logits, int T,
+                                     int d, int E, float *dx, float *dw_router, void *workspace,
+                                     size_t workspace_bytes, int32_t *dev_status, void *stream);
+
+/* ------------------------------------------------------------------------
  * moe_debug_bounded_wait -- exercises the bounded device wait that every
  * pipelined kernel uses: one CTA waits on an mbarrier that nothing arrives
  * at, for at most timeout_ns, then sets MOE_DEV_TIMEOUT in *dev_status and

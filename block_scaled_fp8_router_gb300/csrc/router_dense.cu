@@ -1,55 +1,11 @@
-// router_dense.cu -- the router over all experts: dense logits, the balance
-// and z losses with per-expert counts and the gradient of the logits, and the
-// router's gradients from dense logit gradients.
-#include "common.cuh"
+// router_dense.cu -- the router over all experts: the balance and z losses with
+// per-expert counts and the gradient of the logits, and the entry points of
+// the dense products (router_gemm.cu).
+#include "router_dense.cuh"
 
 #include <math.h>
 
 namespace moe {
-
-// ---------------------------------------------------------------- products
-
-// C[m, n] = sum_k A[m, k] B[k, n] in fp32 with arbitrary strides, 64 x 64
-// tiles, 4 x 4 per thread.
-template <typename TA, typename TB>
-__global__ void __launch_bounds__(256) matmul_kernel(const TA *__restrict__ A, int64_t am, int64_t ak,
-                                                     const TB *__restrict__ B, int64_t bk, int64_t bn,
-                                                     float *__restrict__ C, int M, int N, int K)
-{
-    __shared__ float sa[16][65], sb[16][65];
-    const int m0 = blockIdx.y * 64, n0 = blockIdx.x * 64, tid = threadIdx.x;
-    float acc[4][4] = {};
-    auto get = [](auto v) -> float {
-        if constexpr (sizeof(v) == 2) return bf16_bits_to_f32(v);
-        else return v;
-    };
-    for (int k0 = 0; k0 < K; k0 += 16) {
-        for (int i = tid; i < 1024; i += 256) {
-            const int k = ak == 1 ? i % 16 : i / 64, m = ak == 1 ? i / 16 : i % 64;
-            sa[k][m] = (m0 + m < M && k0 + k < K) ? get(A[(m0 + m) * am + (k0 + k) * ak]) : 0.0f;
-            const int kb = bk == 1 ? i % 16 : i / 64, n = bk == 1 ? i / 16 : i % 64;
-            sb[kb][n] = (n0 + n < N && k0 + kb < K) ? get(B[(k0 + kb) * bk + (n0 + n) * bn]) : 0.0f;
-        }
-        __syncthreads();
-        for (int k = 0; k < 16; k++)
-            for (int i = 0; i < 4; i++)
-                for (int j = 0; j < 4; j++)
-                    acc[i][j] = fmaf(sa[k][tid / 16 + 16 * i], sb[k][tid % 16 + 16 * j], acc[i][j]);
-        __syncthreads();
-    }
-    for (int i = 0; i < 4; i++)
-        for (int j = 0; j < 4; j++) {
-            const int m = m0 + tid / 16 + 16 * i, n = n0 + tid % 16 + 16 * j;
-            if (m < M && n < N) C[(int64_t)m * N + n] = acc[i][j];
-        }
-}
-
-template <typename TA, typename TB>
-static void matmul(const TA *A, int64_t am, int64_t ak, const TB *B, int64_t bk, int64_t bn, float *C, int M, int N,
-                   int K, cudaStream_t st)
-{
-    matmul_kernel<<<dim3((N + 63) / 64, (M + 63) / 64), 256, 0, st>>>(A, am, ak, B, bk, bn, C, M, N, K);
-}
 
 // ------------------------------------------------------------ balance loss
 
@@ -264,8 +220,7 @@ using namespace moe;
 
 MOE_API size_t moe_router_logits_workspace_size(int T, int d, int E)
 {
-    (void)T; (void)d; (void)E;
-    return 256;
+    return check_dense(T, d, E) == MOE_OK ? router_logits_workspace(T, d, E) : 0;
 }
 
 MOE_API moe_status moe_router_logits(const uint16_t *x, const uint16_t *w_router, int T, int d, int E, float *logits,
@@ -278,8 +233,7 @@ MOE_API moe_status moe_router_logits(const uint16_t *x, const uint16_t *w_router
     if (!aligned16(x) || !aligned16(w_router)) return MOE_ERR_ALIGN;
     if (!workspace || workspace_bytes < moe_router_logits_workspace_size(T, d, E)) return MOE_ERR_WORKSPACE;
     if (!aligned256(workspace)) return MOE_ERR_ALIGN;
-    matmul(x, d, 1, w_router, 1, d, logits, T, E, d, as_stream(stream));
-    return launch_status();
+    return router_logits(x, w_router, T, d, E, logits, workspace, dev_status, as_stream(stream));
 }
 
 MOE_API size_t moe_balance_loss_workspace_size(int T, int E, int B)
@@ -331,8 +285,7 @@ MOE_API moe_status moe_balance_loss(const float *logits, const int32_t *topk_ids
 
 MOE_API size_t moe_router_backward_dense_workspace_size(int T, int d, int E)
 {
-    (void)T; (void)d; (void)E;
-    return 256;
+    return check_dense(T, d, E) == MOE_OK ? router_backward_workspace(T, d, E) : 0;
 }
 
 MOE_API moe_status moe_router_backward_dense(const uint16_t *x, const uint16_t *w_router, const float *d_logits, int T,
@@ -353,7 +306,5 @@ MOE_API moe_status moe_router_backward_dense(const uint16_t *x, const uint16_t *
     if ((x && !aligned16(x)) || (w_router && !aligned16(w_router)) || (dx && !aligned16(dx))) return MOE_ERR_ALIGN;
     if (!workspace || workspace_bytes < moe_router_backward_dense_workspace_size(T, d, E)) return MOE_ERR_WORKSPACE;
     if (!aligned256(workspace)) return MOE_ERR_ALIGN;
-    if (dx) matmul(d_logits, E, 1, w_router, d, 1, dx, T, d, E, st);
-    if (dw_router) matmul(d_logits, 1, E, x, d, 1, dw_router, E, d, T, st);
-    return launch_status();
+    return router_backward(x, w_router, d_logits, T, d, E, dx, dw_router, workspace, dev_status, st);
 }

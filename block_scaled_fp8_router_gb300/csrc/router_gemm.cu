@@ -1,0 +1,538 @@
+// router_gemm.cu -- the dense products of the router on the tensor cores, all
+// with fp32 accuracy: every expert's logit x W_r^T, and from dense logit
+// gradients dl the input gradient dl W_r and the weight gradient dl^T x.
+//
+// x and W_r are bf16, so their products are exact in fp32.  dl is fp32: it is
+// cut once into three bf16 parts by truncation (hi + mid + lo = dl exactly,
+// 8 significant bits each), and every K block is multiplied part by part
+// against the same B tile, three MMAs for one.
+//
+// The tensor core's running sum truncates: a chain of MMAs on one accumulator
+// drifts toward zero by about half a unit in the last place per step.  So a
+// chain stays within CHUNK K blocks; the epilogue warps add each chunk to
+// fp32 registers, rounding to nearest (two or more TMEM buffers, so that the
+// next chunk's MMAs run meanwhile).
+//
+// One persistent CTA per SM: a producer warp (TMA, 128-byte swizzle), an MMA
+// warp and up to 16 epilogue warps.  The work is the list of K blocks of all
+// output tiles, cut into equal runs of blocks, one run per CTA (whole tiles
+// where there are many): a CTA has at most one tile begun by another and one
+// that another ends, which go to its two fp32 slots in the workspace;
+// reduce_kernel adds a tile's slots in order.
+#include "tcgen05.cuh"
+#include "router_dense.cuh"
+
+namespace moe {
+namespace rg {
+
+using namespace ffn;
+
+constexpr int TM = 128;                   // tile rows
+constexpr int KB = 64;                    // K block: 128 bytes of bf16
+constexpr int CHUNK = 4;                  // K blocks per accumulator chain
+constexpr int A_TILE = TM * KB * 2;       // 16 KB
+constexpr int MAX_CTAS = 160;
+constexpr int SLOT_COLS = 256;
+constexpr size_t SLOT_FLOATS = (size_t)TM * SLOT_COLS;
+
+enum Mode { LOGITS, DX, DW };
+
+template <Mode MODE, int BN>
+struct Cfg {
+    static constexpr int P = MODE == LOGITS ? 1 : 3;              // parts of A
+    static constexpr bool A_MN = MODE == DW, B_MN = MODE != LOGITS;
+    static constexpr int B_TILE = BN * KB * 2;
+    static constexpr int STAGE = P * A_TILE + B_TILE;
+    static constexpr int STAGES = P == 3 ? 2 : (BN == 256 ? 3 : 4);
+    static constexpr int BUFS = BN == 256 ? 2 : 4;
+    static constexpr int CGS = BN / 32 < 4 ? BN / 32 : 4;         // column groups of the epilogue
+    static constexpr int WCOLS = BN / CGS;                        // columns of one epilogue warp
+    static constexpr int EPI = 4 * CGS;
+};
+
+template <Mode MODE, int BN>
+struct Smem {
+    using C = Cfg<MODE, BN>;
+    uint8_t ring[C::STAGES][C::STAGE];    // the parts' A tiles, then the B tile
+    float stage[C::EPI][32 * 32];         // a warp's 32 x 32 sub-tile for its TMA store
+    uint64_t full[C::STAGES], empty[C::STAGES];
+    uint64_t tfull[C::BUFS], tempty[C::BUFS];
+    uint64_t mma_done;
+    uint32_t tmem_base;
+    int abort_flag;
+};
+
+struct Params {
+    int M, N;
+    int nkb;                  // K blocks of a tile
+    int n_tiles;              // tiles along N
+    int64_t blocks;           // K blocks in all
+    int gran;                 // cuts fall on multiples of this many blocks
+    float *c;                 // [M, N]
+    int direct_tma;           // whole tiles may be stored through tm_c
+    int32_t *dev_status;
+};
+
+// first K block of CTA c's run
+__host__ __device__ __forceinline__ int64_t run_begin(int64_t blocks, int gran, int ctas, int64_t c)
+{
+    return c * (blocks / gran) / ctas * gran;
+}
+
+__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *tm, int x, int y, int z, uint64_t *bar)
+{
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+                 "%3, %4}], [%5];" ::"r"(smem_u32(dst)),
+                 "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+                 : "memory");
+}
+__device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *tm, int x, int y, int z, int w,
+                                            uint64_t *bar)
+{
+    asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+                 "%3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
+                 "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+                 : "memory");
+}
+
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap *tm, const void *src, int x, int y)
+{
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                     reinterpret_cast<uint64_t>(tm)),
+                 "r"(x), "r"(y), "r"(smem_u32(src))
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+
+// bf16 x bf16 -> fp32
+__device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                         uint32_t accumulate)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+                 "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+                 : "memory");
+}
+
+// MN-major operand tile: 64-element (128-byte) groups along M/N, each [64 k
+// rows][128 bytes] with the 128-byte swizzle.  Leading offset 8192 B from
+// group to group, stride offset 1024 B from 8 k rows to the next 8.
+__device__ __forceinline__ uint64_t sw128_desc_mn(uint32_t saddr)
+{
+    uint64_t desc = 0;
+    desc |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+    desc |= (uint64_t)(8192u >> 4) << 16;
+    desc |= (uint64_t)(1024u >> 4) << 32;
+    desc |= (uint64_t)1 << 46;
+    desc |= (uint64_t)2 << 61;
+    return desc;
+}
+
+// fp32 accumulate, A = B = bf16, majorness bits 15 / 16 (1 = MN-major)
+constexpr uint32_t idesc_bf16(int M, int N, bool a_mn, bool b_mn)
+{
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) |
+           ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+template <Mode MODE, int BN>
+__global__ void __launch_bounds__(THREADS, 1)
+    gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+                const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ CUtensorMap tm_slots, const Params p)
+{
+    using C = Cfg<MODE, BN>;
+    extern __shared__ uint8_t smem_raw[];
+    Smem<MODE, BN> &s =
+        *reinterpret_cast<Smem<MODE, BN> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::STAGES; i++) {
+            mbar_init(&s.full[i], 1);
+            mbar_init(&s.empty[i], 1);
+        }
+        for (int i = 0; i < C::BUFS; i++) {
+            mbar_init(&s.tfull[i], 1);
+            mbar_init(&s.tempty[i], C::EPI);
+        }
+        mbar_init(&s.mma_done, 1);
+        s.abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    if (warp == MMA_WARP) tmem_alloc(&s.tmem_base, TMEM_COLS);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s.tmem_base;
+    volatile int *abort_flag = &s.abort_flag;
+    const int64_t b0 = run_begin(p.blocks, p.gran, gridDim.x, blockIdx.x);
+    const int64_t b1 = run_begin(p.blocks, p.gran, gridDim.x, blockIdx.x + 1);
+
+    if (warp == PRODUCER_WARP) {
+        if (lane == 0) {
+            uint32_t j = 0;
+            for (int64_t b = b0; b < b1; b++, j++) {
+                const int tile = (int)(b / p.nkb), kb = (int)(b - (int64_t)tile * p.nkb);
+                const int mt = tile / p.n_tiles, nt = tile - mt * p.n_tiles;
+                const int st = j % C::STAGES;
+                if (!wait_or_abort(&s.empty[st], ((j / C::STAGES) & 1) ^ 1, abort_flag, p.dev_status)) break;
+                mbar_arrive_expect_tx(&s.full[st], C::STAGE);
+#pragma unroll
+                for (int q = 0; q < C::P; q++) {
+                    if (C::A_MN)
+                        tma_load_4d(s.ring[st] + q * A_TILE, &tm_a, 0, kb * KB, mt * (TM / 64), q, &s.full[st]);
+                    else
+                        tma_load_3d(s.ring[st] + q * A_TILE, &tm_a, kb * KB * 2, mt * TM, q, &s.full[st]);
+                }
+                if (C::B_MN)
+                    tma_load_3d(s.ring[st] + C::P * A_TILE, &tm_b, 0, kb * KB, nt * (BN / 64), &s.full[st]);
+                else
+                    tma_load_2d(s.ring[st] + C::P * A_TILE, &tm_b, kb * KB * 2, nt * BN, &s.full[st]);
+            }
+            // no copy may still be in flight when the CTA exits
+            for (int i = 0; i < C::STAGES && (uint32_t)i < j; i++) {
+                const uint32_t last = j - 1 - ((j - 1 - i) % C::STAGES);
+                const uint64_t t0 = globaltimer_ns();
+                while (!mbar_try_wait(&s.full[i], (last / C::STAGES) & 1) && globaltimer_ns() - t0 < TIMEOUT_NS) {}
+            }
+        }
+    } else if (warp == MMA_WARP) {
+        if (lane == 0) {
+            constexpr uint32_t IDESC = idesc_bf16(TM, BN, C::A_MN, C::B_MN);
+            constexpr int A_STEP = C::A_MN ? 2048 >> 4 : 32 >> 4, B_STEP = C::B_MN ? 2048 >> 4 : 32 >> 4;
+            uint32_t j = 0, jc = 0;
+            int in_chunk = 0;
+            for (int64_t b = b0; b < b1; b++, j++) {
+                const int st = j % C::STAGES, buf = jc % C::BUFS;
+                if ((in_chunk == 0 &&
+                     !wait_or_abort(&s.tempty[buf], ((jc / C::BUFS) & 1) ^ 1, abort_flag, p.dev_status)) ||
+                    !wait_or_abort(&s.full[st], (j / C::STAGES) & 1, abort_flag, p.dev_status))
+                    break;
+                tc_fence_after();
+                const uint32_t ring = smem_u32(s.ring[st]);
+                const uint64_t bdesc = C::B_MN ? sw128_desc_mn(ring + C::P * A_TILE) : sw128_desc(ring + C::P * A_TILE);
+#pragma unroll
+                for (int q = C::P - 1; q >= 0; q--) {      // the small parts first
+                    const uint64_t adesc = C::A_MN ? sw128_desc_mn(ring + q * A_TILE) : sw128_desc(ring + q * A_TILE);
+#pragma unroll
+                    for (int ks = 0; ks < KB / 16; ks++)
+                        mma_bf16(tmem + buf * BN, adesc + A_STEP * ks, bdesc + B_STEP * ks, IDESC,
+                                 in_chunk > 0 || q < C::P - 1 || ks > 0);
+                }
+                mma_commit(&s.empty[st]);
+                in_chunk++;
+                if (in_chunk == CHUNK || (b + 1) % p.nkb == 0 || b + 1 == b1) {
+                    mma_commit(&s.tfull[buf]);
+                    jc++;
+                    in_chunk = 0;
+                }
+            }
+            mma_commit(&s.mma_done);
+            const uint64_t t0 = globaltimer_ns();
+            while (!mbar_try_wait(&s.mma_done, 0) && globaltimer_ns() - t0 < TIMEOUT_NS) {}
+        }
+        __syncwarp();
+    } else if (warp < C::EPI) {
+        // warp (q, cg): TMEM lanes 32q .. 32q+31 (tile rows), columns WCOLS cg ..
+        const int q = warp & 3, cg = warp >> 2;
+        const uint32_t lane_addr = (uint32_t)(q * 32) << 16;
+        float *stg = s.stage[warp];
+        uint32_t jc = 0;
+        bool aborted = false;
+        for (int64_t b = b0; b < b1 && !aborted;) {
+            const int tile = (int)(b / p.nkb), kb0 = (int)(b - (int64_t)tile * p.nkb);
+            const int mt = tile / p.n_tiles, nt = tile - mt * p.n_tiles;
+            const int64_t left = b1 - b;
+            const int n = (int)(left < p.nkb - kb0 ? left : p.nkb - kb0);   // K blocks of this tile here
+            float acc[C::WCOLS];
+#pragma unroll
+            for (int i = 0; i < C::WCOLS; i++) acc[i] = 0.0f;
+            for (int k = 0; k < n; k += CHUNK, jc++) {
+                const int buf = jc % C::BUFS;
+                if (!wait_or_abort(&s.tfull[buf], (jc / C::BUFS) & 1, abort_flag, p.dev_status)) {
+                    aborted = true;
+                    break;
+                }
+                tc_fence_after();
+#pragma unroll
+                for (int h = 0; h < C::WCOLS / 16; h++) {
+                    float v[16];
+                    tmem_ld16(tmem + lane_addr + buf * BN + C::WCOLS * cg + 16 * h, v);
+#pragma unroll
+                    for (int i = 0; i < 16; i++) acc[16 * h + i] += v[i];
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s.tempty[buf]);
+            }
+            if (aborted) break;
+            const bool whole = n == p.nkb;
+            const int row0 = mt * TM + 32 * q;
+            const bool slot0 = b == b0;
+#pragma unroll
+            for (int h = 0; h < C::WCOLS / 32; h++) {
+                const int col_t = C::WCOLS * cg + 32 * h, col0 = nt * BN + col_t;
+                if (row0 >= p.M || col0 >= p.N) break;
+                if (whole && !p.direct_tma) {
+                    if (row0 + lane < p.M)
+                        for (int i = 0; i < 32; i++)
+                            if (col0 + i < p.N) p.c[(int64_t)(row0 + lane) * p.N + col0 + i] = acc[32 * h + i];
+                    continue;
+                }
+                // the previous store has read the staging tile
+                if (lane == 0) bulk_wait_read_all();
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 8; i++)
+                    *reinterpret_cast<float4 *>(stg + lane * 32 + 4 * (i ^ (lane & 7))) =
+                        make_float4(acc[32 * h + 4 * i], acc[32 * h + 4 * i + 1], acc[32 * h + 4 * i + 2],
+                                    acc[32 * h + 4 * i + 3]);
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) {
+                    if (whole)
+                        tma_store_2d_evict_first(&tm_c, stg, col0, row0);
+                    else
+                        tma_store_2d(&tm_slots, stg, col_t, ((int)blockIdx.x * 2 + (slot0 ? 0 : 1)) * TM + 32 * q);
+                }
+            }
+            b += n;
+        }
+        if (lane == 0) bulk_wait_all();
+        __syncwarp();
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == MMA_WARP) tmem_dealloc(tmem, TMEM_COLS);
+}
+
+// C tiles that several CTAs have parts of: the parts added in order of K.
+// grid (tile, 8 row groups), 256 threads over 16 rows x BN columns
+template <int BN>
+__global__ void __launch_bounds__(256) reduce_kernel(const float *__restrict__ slots, Params p, int ctas)
+{
+    const int tile = blockIdx.x, mt = tile / p.n_tiles, nt = tile - mt * p.n_tiles;
+    const int64_t k0 = (int64_t)tile * p.nkb, k1 = k0 + p.nkb;
+    const int64_t ub = p.blocks / p.gran;
+    const int c0 = (int)(((k0 / p.gran + 1) * ctas - 1) / ub), c1 = (int)((((k1 - 1) / p.gran + 1) * ctas - 1) / ub);
+    if (c0 == c1) return;
+    const int rows = min(16, p.M - mt * TM - 16 * (int)blockIdx.y), cols = min(BN, p.N - nt * BN);
+    if (rows <= 0) return;
+    const int tc = threadIdx.x % (BN / 4), tr = threadIdx.x / (BN / 4);
+    for (int r = tr; r < rows; r += 256 / (BN / 4)) {
+        if (4 * tc >= cols) continue;
+        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int c = c0; c <= c1; c++) {
+            const int slot = 2 * c + (run_begin(p.blocks, p.gran, ctas, c) >= k0 ? 0 : 1);
+            const float4 v = __ldcs(reinterpret_cast<const float4 *>(
+                slots + (size_t)slot * SLOT_FLOATS + (size_t)(16 * blockIdx.y + r) * SLOT_COLS + 4 * tc));
+            acc.x += v.x;
+            acc.y += v.y;
+            acc.z += v.z;
+            acc.w += v.w;
+        }
+        float *o = p.c + (int64_t)(mt * TM + 16 * blockIdx.y + r) * p.N + nt * BN + 4 * tc;
+        const float v[4] = {acc.x, acc.y, acc.z, acc.w};
+        if (p.direct_tma) {
+            *reinterpret_cast<float4 *>(o) = acc;
+        } else {
+            for (int i = 0; i < 4; i++)
+                if (4 * tc + i < cols) o[i] = v[i];
+        }
+    }
+}
+
+// dl [T, E] fp32 -> parts [3][T][Ep] bf16 by truncation, zeros in columns E ..
+// Ep - 1; one thread per eight columns
+__global__ void __launch_bounds__(256) split_kernel(const float *__restrict__ dl, int T, int E, int Ep,
+                                                    uint16_t *__restrict__ parts)
+{
+    const int per = Ep / 8;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= (int64_t)T * per) return;
+    const int64_t t = i / per;
+    const int e = 8 * (int)(i - t * per);
+    float v[8];
+    if (e + 8 <= E && (E & 3) == 0 && (reinterpret_cast<uintptr_t>(dl) & 15u) == 0) {
+        const float4 a = __ldg(reinterpret_cast<const float4 *>(dl + t * E + e));
+        const float4 b = __ldg(reinterpret_cast<const float4 *>(dl + t * E + e) + 1);
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    } else {
+#pragma unroll
+        for (int u = 0; u < 8; u++) v[u] = e + u < E ? __ldg(dl + t * E + e + u) : 0.0f;
+    }
+    const int64_t plane = (int64_t)T * Ep;
+#pragma unroll
+    for (int q = 0; q < 3; q++) {
+        uint32_t w[4];
+#pragma unroll
+        for (int u = 0; u < 4; u++) {
+            const uint32_t lo = __float_as_uint(v[2 * u]) & 0xFFFF0000u, hi = __float_as_uint(v[2 * u + 1]) & 0xFFFF0000u;
+            w[u] = (lo >> 16) | hi;
+            v[2 * u] -= __uint_as_float(lo);
+            v[2 * u + 1] -= __uint_as_float(hi);
+        }
+        *reinterpret_cast<uint4 *>(parts + q * plane + t * Ep + e) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+// ------------------------------------------------------------------- host
+
+static inline int pad64(int v) { return (v + 63) / 64 * 64; }
+
+struct Plan {
+    int ctas, gran, m_tiles, n_tiles, nkb;
+    int64_t blocks;
+    bool slots;          // some tile is cut
+};
+
+static Plan plan(int M, int N, int K, int bn)
+{
+    Plan r;
+    r.m_tiles = (M + TM - 1) / TM;
+    r.n_tiles = (N + bn - 1) / bn;
+    r.nkb = (K + KB - 1) / KB;
+    const int64_t tiles = (int64_t)r.m_tiles * r.n_tiles;
+    r.blocks = tiles * r.nkb;
+    int sms = sm_count();
+    if (sms > MAX_CTAS) sms = MAX_CTAS;
+    // whole tiles where every CTA has four or more (the last ones then cost a
+    // quarter at most), else cut tiles, CHUNK blocks a CTA at the least
+    r.gran = tiles >= 4 * sms || r.nkb == 1 ? r.nkb : 1;
+    const int64_t units = r.gran == 1 && r.nkb > 1 ? (r.blocks + CHUNK - 1) / CHUNK : tiles;
+    r.ctas = (int)(units < sms ? units : sms);
+    r.slots = r.gran != r.nkb;
+    return r;
+}
+
+static size_t slots_bytes(const Plan &r) { return r.slots ? (size_t)r.ctas * 2 * SLOT_FLOATS * sizeof(float) : 0; }
+
+static int logits_bn(int E) { return E <= 64 ? 64 : E <= 128 ? 128 : 256; }
+static int hidden_bn(int d) { return d % 256 == 0 ? 256 : 128; }
+
+// [parts][rows][k] bf16, k contiguous: box 64 k x box_rows rows of one part
+static bool map_k_major(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap *m, const void *base, uint64_t k,
+                        uint64_t rows, uint64_t parts, uint32_t box_rows)
+{
+    const cuuint64_t dims[3] = {k * 2, rows, parts};
+    const cuuint64_t strides[2] = {k * 2, k * 2 * rows};
+    const cuuint32_t box[3] = {128, box_rows, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// [parts][k rows][mn] bf16, mn contiguous (a multiple of 64), as (128 bytes,
+// k, 64-element group, part): box 64 k rows x `groups` groups of one part
+static bool map_mn_major(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap *m, const void *base, uint64_t mn,
+                         uint64_t k, uint64_t parts, uint32_t groups, int rank)
+{
+    const cuuint64_t dims[4] = {128, k, mn / 64, parts};
+    const cuuint64_t strides[3] = {mn * 2, 128, mn * 2 * k};
+    const cuuint32_t box[4] = {128, KB, groups, 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, const_cast<void *>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <Mode MODE, int BN>
+static moe_status launch(const void *a, const void *b, float *c, int M, int N, int K, float *slots,
+                         int32_t *dev_status, cudaStream_t st)
+{
+    using C = Cfg<MODE, BN>;
+    const Plan pl = plan(M, N, K, BN);
+    auto enc = encode_fn();
+    if (!enc) return MOE_ERR_CUDA;
+    CUtensorMap ma, mb, mc, ms;
+    const bool ok_a = C::A_MN ? map_mn_major(enc, &ma, a, pad64(M), K, C::P, TM / 64, 4)
+                              : map_k_major(enc, &ma, a, MODE == DX ? pad64(K) : K, M, C::P, TM);
+    const bool ok_b = C::B_MN ? map_mn_major(enc, &mb, b, N, K, 1, BN / 64, 3)
+                              : make_map(enc, &mb, b, (uint64_t)K * 2, N, BN);
+    if (!ok_a || !ok_b) return MOE_ERR_CUDA;
+    Params p;
+    p.M = M;
+    p.N = N;
+    p.nkb = pl.nkb;
+    p.n_tiles = pl.n_tiles;
+    p.blocks = pl.blocks;
+    p.gran = pl.gran;
+    p.c = c;
+    p.direct_tma = N % 4 == 0 && aligned16(c);
+    p.dev_status = dev_status;
+    if (p.direct_tma) {
+        if (!make_map_f32_store(enc, &mc, c, (uint64_t)N, (uint64_t)M)) return MOE_ERR_CUDA;
+    }
+    if (pl.slots) {
+        if (!make_map_f32_store(enc, &ms, slots, SLOT_COLS, (uint64_t)pl.ctas * 2 * TM)) return MOE_ERR_CUDA;
+    } else {
+        ms = p.direct_tma ? mc : ma;     // not used
+    }
+    if (!p.direct_tma) mc = ms;          // not used
+    constexpr size_t smem = sizeof(Smem<MODE, BN>) + 1024;
+    static_assert(smem <= 227 * 1024, "shared memory");
+    if (cudaFuncSetAttribute(gemm_kernel<MODE, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
+        cudaSuccess)
+        return MOE_ERR_CUDA;
+    gemm_kernel<MODE, BN><<<pl.ctas, THREADS, smem, st>>>(ma, mb, mc, ms, p);
+    if (pl.slots)
+        reduce_kernel<BN><<<dim3((unsigned)(pl.m_tiles * pl.n_tiles), 8), 256, 0, st>>>(slots, p, pl.ctas);
+    return launch_status();
+}
+
+static size_t align_up(size_t v) { return (v + 255) & ~(size_t)255; }
+
+} // namespace rg
+
+size_t router_logits_workspace(int T, int d, int E)
+{
+    using namespace rg;
+    return 256 + slots_bytes(plan(T, E, d, logits_bn(E)));
+}
+
+moe_status router_logits(const uint16_t *x, const uint16_t *w, int T, int d, int E, float *logits, void *ws,
+                         int32_t *dev_status, cudaStream_t st)
+{
+    using namespace rg;
+    float *slots = (float *)ws;
+    switch (logits_bn(E)) {
+    case 64: return launch<LOGITS, 64>(x, w, logits, T, E, d, slots, dev_status, st);
+    case 128: return launch<LOGITS, 128>(x, w, logits, T, E, d, slots, dev_status, st);
+    default: return launch<LOGITS, 256>(x, w, logits, T, E, d, slots, dev_status, st);
+    }
+}
+
+size_t router_backward_workspace(int T, int d, int E)
+{
+    using namespace rg;
+    const size_t sx = slots_bytes(plan(T, d, E, hidden_bn(d))), sw = slots_bytes(plan(E, d, T, hidden_bn(d)));
+    return 256 + align_up((size_t)3 * T * pad64(E) * 2) + (sx > sw ? sx : sw);
+}
+
+moe_status router_backward(const uint16_t *x, const uint16_t *w, const float *dl, int T, int d, int E, float *dx,
+                           float *dw, void *ws, int32_t *dev_status, cudaStream_t st)
+{
+    using namespace rg;
+    const int Ep = pad64(E);
+    uint16_t *parts = (uint16_t *)ws;
+    float *slots = (float *)((uint8_t *)ws + align_up((size_t)3 * T * Ep * 2));
+    const int64_t n = (int64_t)T * (Ep / 8);
+    split_kernel<<<(unsigned)((n + 255) / 256), 256, 0, st>>>(dl, T, E, Ep, parts);
+    moe_status s = launch_status();
+    if (s != MOE_OK) return s;
+    if (dx) {
+        s = hidden_bn(d) == 256 ? launch<DX, 256>(parts, w, dx, T, d, E, slots, dev_status, st)
+                                : launch<DX, 128>(parts, w, dx, T, d, E, slots, dev_status, st);
+        if (s != MOE_OK) return s;
+    }
+    if (dw)
+        s = hidden_bn(d) == 256 ? launch<DW, 256>(parts, x, dw, E, d, T, slots, dev_status, st)
+                                : launch<DW, 128>(parts, x, dw, E, d, T, slots, dev_status, st);
+    return s;
+}
+
+} // namespace moe

@@ -8,9 +8,16 @@
 //   log p_y = ln2 (t_y - log2 S),  H = ln2 (log2 S - U / S),
 // and the gradient of w (pg + beta kl - eta H) / norm is
 //   dl_v = coef (g 1[v = y] + 2^t_v / S (-g + eta (ln2 (t_v - log2 S) + H))).
-// One shift per thread, the maximum so far, its sums rescaled when it grows;
-// the threads' (c, S, U) are joined in a fixed order.  (l_v - c) k2 and not
-// l_v k2 - c k2: the largest logit's t is then exactly 0.
+// (l_v - c) k2 and not l_v k2 - c k2: the largest logit's t is then exactly 0.
+//
+// token_rows_kernel: one cluster of C CTAs per row.  A row's 16-byte vectors
+// are dealt to the threads of the cluster, up to NV of them kept in registers
+// from the one read to the gradient's write (a longer row's remainder is read
+// again, from L2).  A warp takes its maximum, sums 2^t and 2^t t against it;
+// the warps' sums are joined in shared memory, the CTAs' through one 16-byte
+// message to every CTA of the cluster (st.async on an mbarrier), always in the
+// same order.  So a row costs one CTA barrier, one exchange and one more CTA
+// barrier, and several CTAs per SM keep HBM busy across them.
 #include "common.cuh"
 
 #include <math.h>
@@ -30,7 +37,7 @@ __device__ __forceinline__ float ex2(float x)
 }
 
 // the sums of one part of a row, relative to the shift c (c = -inf: no logit
-// above -inf so far, S = U = 0)
+// above -inf, S = U = 0)
 struct RowSum {
     float c, S, U;
 };
@@ -50,6 +57,98 @@ __device__ __forceinline__ RowSum join(const RowSum &a, const RowSum &b, float k
     return r;
 }
 
+// joins over the lanes 0 .. n-1 of a warp (n a power of two), the same bits in
+// each: the lower lane's sums always come first
+__device__ __forceinline__ RowSum warp_join(RowSum s, int n, int lane, float k2)
+{
+    for (int o = 1; o < n; o <<= 1) {
+        RowSum b;
+        b.c = __shfl_xor_sync(0xFFFFFFFFu, s.c, o);
+        b.S = __shfl_xor_sync(0xFFFFFFFFu, s.S, o);
+        b.U = __shfl_xor_sync(0xFFFFFFFFu, s.U, o);
+        s = (lane & o) ? join(b, s, k2) : join(s, b, k2);
+    }
+    return s;
+}
+
+// ---- two fp32 at a time ----
+__device__ __forceinline__ uint64_t pack2(float a, float b)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float &a, float &b)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+// a 16-byte vector of logits: 8 bf16 or 4 fp32
+template <typename T>
+struct Vec;
+template <>
+struct Vec<uint16_t> {
+    static constexpr int W = 8;
+    static constexpr uint32_t NINF = 0xFF80FF80u;
+    static __device__ __forceinline__ float max(const uint4 &v)
+    {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        __nv_bfloat162 m[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) m[i] = *reinterpret_cast<const __nv_bfloat162 *>(&w[i]);
+        const __nv_bfloat162 a = __hmax2(__hmax2(m[0], m[1]), __hmax2(m[2], m[3]));
+        return fmaxf(__low2float(a), __high2float(a));
+    }
+    // pair i (0 .. 3) as two fp32
+    static __device__ __forceinline__ uint64_t pair(const uint4 &v, int i)
+    {
+        const uint32_t w = i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+        return pack2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+    }
+    static __device__ __forceinline__ uint4 make(const float *f)
+    {
+        return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                          pack_bf16x2(f[6], f[7]));
+    }
+};
+template <>
+struct Vec<float> {
+    static constexpr int W = 4;
+    static constexpr uint32_t NINF = 0xFF800000u;
+    static __device__ __forceinline__ float max(const uint4 &v)
+    {
+        return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)),
+                     fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
+    }
+    static __device__ __forceinline__ uint64_t pair(const uint4 &v, int i)
+    {
+        return i == 0 ? pack2(__uint_as_float(v.x), __uint_as_float(v.y))
+                      : pack2(__uint_as_float(v.z), __uint_as_float(v.w));
+    }
+    static __device__ __forceinline__ uint4 make(const float *f)
+    {
+        return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+    }
+};
+
 template <typename T>
 __device__ __forceinline__ float load_logit(const T *p);
 template <>
@@ -64,29 +163,61 @@ __device__ __forceinline__ void store_grad(uint16_t *p, float v)
 }
 __device__ __forceinline__ void store_grad(float *p, float v) { *p = v; }
 
-// one element of a thread's part of the row
-__device__ __forceinline__ void add_logit(RowSum &s, float l, float k2)
-{
-    if (l > s.c) {
-        if (s.S != 0.0f) {
-            const float d = fmaxf((s.c - l) * k2, TMIN), f = ex2(d);
-            s.U = (s.U + d * s.S) * f;
-            s.S *= f;
-        }
-        s.c = l;
+// a row as 16-byte vectors: vector j holds the elements W j - head .. + W - 1
+// of the row, those outside [0, V) absent
+template <typename T>
+struct Row {
+    const T *l;
+    int head, nvec;
+    int64_t V;
+    __device__ __forceinline__ Row(const T *p, int64_t n) : l(p), V(n)
+    {
+        constexpr int W = Vec<T>::W;
+        head = (int)((reinterpret_cast<uintptr_t>(p) & 15u) / sizeof(T));
+        nvec = (int)((n + head + W - 1) / W);
     }
-    if (l == -INFINITY) return;
-    const float t = (l - (s.c == -INFINITY ? 0.0f : s.c)) * k2;
-    const float e = ex2(t);
-    s.S += e;
-    s.U = fmaf(e, fmaxf(t, TMIN), s.U);
-}
+    __device__ __forceinline__ bool inside(int j) const
+    {
+        constexpr int W = Vec<T>::W;
+        const int64_t e = (int64_t)W * j - head;
+        return e >= 0 && e + W <= V;
+    }
+    // absent elements read as -inf
+    __device__ __forceinline__ uint4 load(int j) const
+    {
+        constexpr int W = Vec<T>::W;
+        constexpr uint32_t NI = Vec<T>::NINF;
+        if (j >= nvec) return make_uint4(NI, NI, NI, NI);
+        const int64_t e = (int64_t)W * j - head;
+        if (e >= 0 && e + W <= V) {
+            uint4 v;
+            asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                         : "l"(l + e)
+                         : "memory");
+            return v;
+        }
+        float f[W];
+#pragma unroll
+        for (int u = 0; u < W; u++) f[u] = e + u >= 0 && e + u < V ? load_logit(l + e + u) : -INFINITY;
+        return Vec<T>::make(f);
+    }
+};
 
 struct PolicyArgs {
     const float *old_lp, *adv, *ref_lp, *w;
     float clip_lo, clip_hi, beta, eta, norm, grad_scale, inv_tau;
     int64_t ld_d;
-    double *partial;     // [CTA][5]
+    float *stats;
+    struct Ws *ws;
+};
+
+// workspace: the weights' sum, the rows done so far, and per row w pg, w kl,
+// w H and w [clipped]
+struct Ws {
+    double norm;
+    uint32_t done, pad;
+    float4 row[1];
 };
 
 // exp(q) - q - 1 without the cancellation near 0: its series for |q| < 1/2
@@ -101,133 +232,384 @@ __device__ __forceinline__ float kl_term(float q)
     return expf(q) - q - 1.0f;
 }
 
-template <typename T, bool POLICY>
-__global__ void __launch_bounds__(512) token_rows_kernel(const T *logits, int64_t N, int64_t V,
-                                                         int64_t ld, const void *__restrict__ targets, int t64,
-                                                         float k2, float *__restrict__ logprobs,
-                                                         float *__restrict__ entropy, T *dlogits, PolicyArgs a,
-                                                         int32_t *dev_status)
+// sum of the weights in a fixed order; resets the count of rows done
+__global__ void __launch_bounds__(1024) policy_norm_kernel(const float *__restrict__ w, int64_t N, float norm, Ws *ws)
 {
-    __shared__ RowSum s_part[16];
-    __shared__ RowSum s_row;
-    __shared__ double s_norm[16];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    double norm = 0.0;
-    if (POLICY) {
-        if (a.norm > 0.0f) {
-            norm = a.norm;
-        } else {
-            double v = 0.0;
-            for (int64_t i = tid; i < N; i += 512) v += a.w ? (double)a.w[i] : 1.0;
-            for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-            if (lane == 0) s_norm[warp] = v;
-            __syncthreads();
-            for (int i = 0; i < 16; i++) norm += s_norm[i];
-        }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    __shared__ double s_v[32];
+    const int tid = threadIdx.x;
+    double v = 0.0;
+    if (norm > 0.0f) {
+        v = tid == 0 ? (double)norm : 0.0;
+    } else if (!w) {
+        v = tid == 0 ? (double)N : 0.0;
+    } else {
+        for (int64_t i = tid; i < N; i += 1024) v += (double)__ldg(w + i);
     }
-    double acc[4] = {0.0, 0.0, 0.0, 0.0};
-    for (int64_t row = blockIdx.x; row < N; row += gridDim.x) {
-        const int64_t y = t64 ? ((const int64_t *)targets)[row] : (int64_t)((const int32_t *)targets)[row];
-        const float w = POLICY ? (a.w ? a.w[row] : 1.0f) : 1.0f;
-        bool live = y >= 0 && y < V && w != 0.0f;
-        if (y >= V && w != 0.0f && tid == 0) dev_flag(dev_status, MOE_DEV_BAD_IDS);
-        const T *l = logits + row * ld;
-        T *d = POLICY && dlogits ? dlogits + row * a.ld_d : nullptr;
-        RowSum s = {-INFINITY, 0.0f, 0.0f};
-        if (live) {
-            for (int64_t i = tid; i < V; i += 512) add_logit(s, load_logit(l + i), k2);
-            for (int o = 16; o; o >>= 1) {
-                RowSum b;
-                b.c = __shfl_xor_sync(0xFFFFFFFFu, s.c, o);
-                b.S = __shfl_xor_sync(0xFFFFFFFFu, s.S, o);
-                b.U = __shfl_xor_sync(0xFFFFFFFFu, s.U, o);
-                s = (lane & o) ? join(b, s, k2) : join(s, b, k2);
-            }
-            if (lane == 0) s_part[warp] = s;
-            __syncthreads();
-            if (tid == 0) {
-                s = s_part[0];
-                for (int i = 1; i < 16; i++) s = join(s, s_part[i], k2);
-                s_row = s;
-            }
-            __syncthreads();
-            s = s_row;
-            if (s.c == -INFINITY && s.S == 0.0f) {
-                live = false;
-                if (tid == 0) dev_flag(dev_status, MOE_DEV_BAD_IDS);
-            }
-        }
-        float lp = 0.0f, H = 0.0f, A0 = 0.0f, B0 = 0.0f, gy = 0.0f;
-        if (live) {
-            const float ls = log2f(s.S);
-            lp = LN2 * ((load_logit(l + y) - s.c) * k2 - ls);
-            H = LN2 * (ls - s.U / s.S);
-            if (POLICY) {
-                const float A = a.adv[row];
-                float dlt = lp - a.old_lp[row];
-                dlt = dlt > 80.0f ? 80.0f : dlt;
-                const float r = expf(dlt);
-                const float rc = r < a.clip_lo ? a.clip_lo : (r > a.clip_hi ? a.clip_hi : r);
-                const float p0 = -A * r, p1 = -A * rc;
-                const bool clipped = p1 > p0;
-                float g = clipped ? 0.0f : p0, kl = 0.0f;
-                if (a.ref_lp) {
-                    float q = a.ref_lp[row] - lp;
-                    q = q > 80.0f ? 80.0f : q;
-                    kl = kl_term(q);
-                    g = fmaf(-a.beta, expm1f(q), g);
-                }
-                if (tid == 0) {
-                    acc[0] += (double)w * (clipped ? p1 : p0);
-                    acc[1] += (double)w * kl;
-                    acc[2] += (double)w * H;
-                    acc[3] += clipped ? (double)w : 0.0;
-                }
-                const float coef = norm != 0.0 ? (float)((double)w * a.grad_scale * a.inv_tau / norm) : 0.0f;
-                gy = coef * g;
-                A0 = coef * (-g + a.eta * (H - LN2 * ls)) / s.S;
-                B0 = coef * a.eta * LN2 / s.S;
-            }
-        }
-        if (tid == 0) {
-            if (logprobs) logprobs[row] = lp;
-            if (!POLICY && entropy) entropy[row] = H;
-        }
-        if (POLICY && d) {
-            __syncthreads();
-            for (int64_t i = tid; i < V; i += 512) {
-                float v = 0.0f;
-                if (live) {
-                    const float t = (load_logit(l + i) - s.c) * k2;
-                    v = ex2(t) * fmaf(B0, fmaxf(t, TMIN), A0);
-                    if (i == y) v += gy;
-                }
-                store_grad(d + i, v);
-            }
-        }
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    if ((tid & 31) == 0) s_v[tid >> 5] = v;
+    __syncthreads();
+    if (tid == 0) {
+        v = 0.0;
+        for (int i = 0; i < 32; i++) v += s_v[i];
+        ws->norm = v;
+        ws->done = 0;
     }
-    if (POLICY && tid == 0)
-        for (int i = 0; i < 4; i++) a.partial[(int64_t)blockIdx.x * 5 + i] = acc[i];
-    if (POLICY && tid == 0) a.partial[(int64_t)blockIdx.x * 5 + 4] = norm;
 }
 
-__global__ void policy_stats_kernel(const double *__restrict__ partial, int ncta, float beta, float eta,
-                                    float *__restrict__ stats)
+__device__ __forceinline__ uint32_t cluster_rank()
 {
-    double m[4] = {0.0, 0.0, 0.0, 0.0};
-    const double norm = partial[4];
-    for (int c = 0; c < ncta; c++)
-        for (int i = 0; i < 4; i++) m[i] += partial[(int64_t)c * 5 + i];
-    for (int i = 0; i < 4; i++) m[i] = norm != 0.0 ? m[i] / norm : 0.0;
-    stats[0] = (float)(m[0] + beta * m[1] - eta * m[2]);
-    for (int i = 0; i < 4; i++) stats[1 + i] = (float)m[i];
-    stats[5] = (float)norm;
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank)
+{
+    uint32_t out;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(out) : "r"(addr), "r"(rank));
+    return out;
+}
+
+constexpr int ROW_THREADS = 512;        // at most
+constexpr uint64_t ROW_TIMEOUT_NS = 1000ull * 1000ull * 1000ull;
+
+// what a row's gradient needs: dl_v = 2^t_v (A0 + B0 t_v) + gy 1[v = y]
+struct RowGrad {
+    float c, A0, B0, gy;
+};
+
+// sums of one vector against the shift m, two elements at a time
+template <typename T>
+__device__ __forceinline__ void add_vec(const uint4 &v, uint64_t nm2, uint64_t k22, uint64_t &S, uint64_t &U)
+{
+#pragma unroll
+    for (int i = 0; i < Vec<T>::W / 2; i++) {
+        const uint64_t t = mul2(add2(Vec<T>::pair(v, i), nm2), k22);
+        float t0, t1;
+        unpack2(t, t0, t1);
+        const uint64_t e = pack2(ex2(t0), ex2(t1));
+        S = add2(S, e);
+        U = fma2(e, pack2(fmaxf(t0, TMIN), fmaxf(t1, TMIN)), U);
+    }
+}
+
+template <typename T, bool ETA>
+__device__ __forceinline__ void grad_vec(const uint4 &v, const RowGrad &g, uint64_t nm2, uint64_t k22, float *f)
+{
+#pragma unroll
+    for (int i = 0; i < Vec<T>::W / 2; i++) {
+        const uint64_t t = mul2(add2(Vec<T>::pair(v, i), nm2), k22);
+        float t0, t1;
+        unpack2(t, t0, t1);
+        const uint64_t e = pack2(ex2(t0), ex2(t1));
+        uint64_t a = pack2(g.A0, g.A0);
+        if (ETA) a = fma2(pack2(g.B0, g.B0), pack2(fmaxf(t0, TMIN), fmaxf(t1, TMIN)), a);
+        unpack2(mul2(e, a), f[2 * i], f[2 * i + 1]);
+    }
+}
+
+// Row blockIdx.x / C by a cluster of C CTAs.  POLICY: the policy loss and its
+// gradient (else log-probabilities and entropy); ETA: with an entropy bonus.
+template <typename T, int NV, bool POLICY, bool ETA>
+__global__ void __launch_bounds__(ROW_THREADS, 2)
+    token_rows_kernel(const T *logits, int64_t N, int64_t V, int64_t ld, const void *__restrict__ targets, int t64,
+                      float k2, int C, float *__restrict__ logprobs, float *__restrict__ entropy, T *dlogits,
+                      const PolicyArgs a, int32_t *dev_status)
+{
+    constexpr int W = Vec<T>::W;
+    __shared__ RowSum s_part[ROW_THREADS / 32];
+    __shared__ float4 s_msg[8];
+    __shared__ RowGrad s_grad;
+    __shared__ int s_live;
+    __shared__ uint64_t s_bar;
+    __shared__ double s_tot[ROW_THREADS / 32][4];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, TH = blockDim.x, nw = TH >> 5;
+    const int64_t row = blockIdx.x / (unsigned)C;
+    const int rank = C > 1 ? (int)cluster_rank() : 0;
+    if (C > 1) {
+        if (tid == 0) {
+            mbar_init(&s_bar, 1);
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        }
+        __syncwarp();
+        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    }
+    const int64_t y = t64 ? ((const int64_t *)targets)[row] : (int64_t)((const int32_t *)targets)[row];
+    const float w = POLICY && a.w ? a.w[row] : 1.0f;
+    bool live = y >= 0 && y < V && w != 0.0f;
+    if (y >= V && w != 0.0f && tid == 0 && rank == 0) dev_flag(dev_status, MOE_DEV_BAD_IDS);
+    const Row<T> R(logits + row * ld, V);
+    const int j0 = rank * TH + tid, dj = C * TH;   // my vectors: j0, j0 + dj, ...
+    const uint64_t k22 = pack2(k2, k2);
+    uint4 raw[NV];
+    float lp = 0.0f, H = 0.0f;
+    float4 st = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (live) {
+#pragma unroll
+        for (int i = 0; i < NV; i++) raw[i] = R.load(j0 + i * dj);
+        const float ly = warp == 0 ? load_logit(R.l + y) : 0.0f;
+        float m = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < NV; i++) m = fmaxf(m, Vec<T>::max(raw[i]));
+        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+        RowSum s = {m, 0.0f, 0.0f};
+        {
+            const float sh = m == -INFINITY ? 0.0f : -m;
+            const uint64_t nm2 = pack2(sh, sh);
+            uint64_t S = 0, U = 0;
+#pragma unroll
+            for (int i = 0; i < NV; i++) add_vec<T>(raw[i], nm2, k22, S, U);
+            float x, z;
+            unpack2(S, x, z);
+            s.S = x + z;
+            unpack2(U, x, z);
+            s.U = x + z;
+        }
+        // the rest of a row longer than the registers hold, NV vectors at a time
+        for (int jb = NV * dj; jb < R.nvec; jb += NV * dj) {
+            uint4 v[NV];
+            float mm = s.c;
+#pragma unroll
+            for (int i = 0; i < NV; i++) v[i] = R.load(jb + j0 + i * dj);
+#pragma unroll
+            for (int i = 0; i < NV; i++) mm = fmaxf(mm, Vec<T>::max(v[i]));
+            for (int o = 16; o; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xFFFFFFFFu, mm, o));
+            if (mm > s.c) {
+                if (s.c != -INFINITY) {
+                    const float d = fmaxf((s.c - mm) * k2, TMIN), f = ex2(d);
+                    s.U = (s.U + d * s.S) * f;
+                    s.S *= f;
+                }
+                s.c = mm;
+            }
+            const float sh = s.c == -INFINITY ? 0.0f : -s.c;
+            const uint64_t nm2 = pack2(sh, sh);
+            uint64_t S = 0, U = 0;
+#pragma unroll
+            for (int i = 0; i < NV; i++) add_vec<T>(v[i], nm2, k22, S, U);
+            float x, z;
+            unpack2(S, x, z);
+            s.S += x + z;
+            unpack2(U, x, z);
+            s.U += x + z;
+        }
+        for (int o = 16; o; o >>= 1) {
+            s.S += __shfl_xor_sync(0xFFFFFFFFu, s.S, o);
+            s.U += __shfl_xor_sync(0xFFFFFFFFu, s.U, o);
+        }
+        if (lane == 0) s_part[warp] = s;
+        __syncthreads();
+        if (warp == 0) {
+            s = lane < nw ? s_part[lane] : RowSum{-INFINITY, 0.0f, 0.0f};
+            s = warp_join(s, nw, lane, k2);
+            if (C > 1) {
+                // the peers have set up their barriers; lane r sends (c, S, U,
+                // l_y) to CTA r.  l_y travels too so that it has been read
+                // before any CTA can write the gradient over it
+                asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+                if (lane == 0) mbar_arrive_expect_tx(&s_bar, 16 * C);
+                if (lane < C)
+                    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, "
+                                 "%4}, [%5];" ::"r"(map_rank(smem_u32(&s_msg[rank]), lane)),
+                                 "r"(__float_as_uint(s.c)), "r"(__float_as_uint(s.S)), "r"(__float_as_uint(s.U)),
+                                 "r"(__float_as_uint(ly)), "r"(map_rank(smem_u32(&s_bar), lane))
+                                 : "memory");
+                if (!mbar_wait_bounded(&s_bar, 0, ROW_TIMEOUT_NS) && lane == 0) dev_flag(dev_status, MOE_DEV_TIMEOUT);
+                __syncwarp();
+                const float4 q = lane < C ? s_msg[lane] : make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
+                s = warp_join(RowSum{q.x, q.y, q.z}, C, lane, k2);
+            }
+            s.c = __shfl_sync(0xFFFFFFFFu, s.c, 0);
+            s.S = __shfl_sync(0xFFFFFFFFu, s.S, 0);
+            s.U = __shfl_sync(0xFFFFFFFFu, s.U, 0);
+            if (s.c == -INFINITY && s.S == 0.0f) {       // no logit above -inf: not scored
+                live = false;
+                if (lane == 0 && rank == 0) dev_flag(dev_status, MOE_DEV_BAD_IDS);
+            } else {
+                const float ls = log2f(s.S);
+                lp = LN2 * ((ly - s.c) * k2 - ls);
+                H = LN2 * (ls - s.U / s.S);
+                RowGrad g = {s.c, 0.0f, 0.0f, 0.0f};
+                if (POLICY) {
+                    const float A = a.adv[row];
+                    float dlt = lp - a.old_lp[row];
+                    dlt = dlt > 80.0f ? 80.0f : dlt;
+                    const float r = expf(dlt);
+                    const float rc = r < a.clip_lo ? a.clip_lo : (r > a.clip_hi ? a.clip_hi : r);
+                    const float p0 = -A * r, p1 = -A * rc;
+                    const bool clipped = p1 > p0;
+                    float gl = clipped ? 0.0f : p0, kl = 0.0f;
+                    if (a.ref_lp) {
+                        float q = a.ref_lp[row] - lp;
+                        q = q > 80.0f ? 80.0f : q;
+                        kl = kl_term(q);
+                        gl = fmaf(-a.beta, expm1f(q), gl);
+                    }
+                    st = make_float4(w * (clipped ? p1 : p0), w * kl, w * H, clipped ? w : 0.0f);
+                    asm volatile("griddepcontrol.wait;" ::: "memory");
+                    const double norm = __ldcg(&a.ws->norm);
+                    const float coef = norm != 0.0 ? (float)((double)w * a.grad_scale * a.inv_tau / norm) : 0.0f;
+                    g.gy = coef * gl;
+                    g.A0 = coef * (-gl + a.eta * (H - LN2 * ls)) / s.S;
+                    g.B0 = coef * a.eta * LN2 / s.S;
+                }
+                if (lane == 0) s_grad = g;
+            }
+            if (lane == 0) s_live = live;
+        } else if (C > 1) {
+            asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+        }
+    } else if (C > 1) {
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    }
+    if (POLICY && dlogits) {
+        const bool was = live || (y >= 0 && y < V && w != 0.0f);   // the same for the whole cluster
+        if (was) {
+            __syncthreads();
+            live = s_live != 0;
+        }
+        const RowGrad g = live ? s_grad : RowGrad{0.0f, 0.0f, 0.0f, 0.0f};
+        const uint64_t nm2 = pack2(-g.c, -g.c);
+        T *d = dlogits + row * a.ld_d;
+        // vector stores where the gradient's rows are aligned as the logits' are
+        const bool same = ((reinterpret_cast<uintptr_t>(d) ^ reinterpret_cast<uintptr_t>(R.l)) & 15u) == 0;
+        const int jy = live ? (int)((y + R.head) / W) : -1, uy = live ? (int)((y + R.head) % W) : 0;
+        auto put = [&](int j, const uint4 &v) {
+            if (j >= R.nvec) return;
+            float f[W];
+            if (live) {
+                grad_vec<T, ETA>(v, g, nm2, k22, f);
+                if (j == jy) {
+#pragma unroll
+                    for (int u = 0; u < W; u++) f[u] += u == uy ? g.gy : 0.0f;
+                }
+            } else {
+#pragma unroll
+                for (int u = 0; u < W; u++) f[u] = 0.0f;
+            }
+            const int64_t e = (int64_t)W * j - R.head;
+            if (same && R.inside(j)) {
+                __stcs(reinterpret_cast<uint4 *>(d + e), Vec<T>::make(f));
+            } else {
+#pragma unroll
+                for (int u = 0; u < W; u++)
+                    if (e + u >= 0 && e + u < V) store_grad(d + e + u, f[u]);
+            }
+        };
+#pragma unroll
+        for (int i = 0; i < NV; i++) put(j0 + i * dj, raw[i]);
+        for (int j = j0 + NV * dj; j < R.nvec; j += dj) put(j, live ? R.load(j) : raw[0]);
+    }
+    if (rank == 0 && tid == 0) {
+        if (logprobs) logprobs[row] = lp;
+        if (!POLICY && entropy) entropy[row] = H;
+    }
+    if (POLICY && rank == 0) {
+        // the CTA that finishes the last row sums the rows' parts in order
+        __shared__ int s_last;
+        if (tid == 0) {
+            asm volatile("griddepcontrol.wait;" ::: "memory");
+            a.ws->row[row] = st;
+            __threadfence();
+            s_last = atomicAdd(&a.ws->done, 1u) == (uint32_t)(N - 1);
+        }
+        __syncthreads();
+        if (!s_last) return;
+        __threadfence();
+        double v[4] = {0.0, 0.0, 0.0, 0.0};
+        for (int64_t i = tid; i < N; i += TH) {
+            const float4 q = __ldcg(&a.ws->row[i]);
+            v[0] += q.x;
+            v[1] += q.y;
+            v[2] += q.z;
+            v[3] += q.w;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            for (int o = 16; o; o >>= 1) v[i] += __shfl_xor_sync(0xFFFFFFFFu, v[i], o);
+            if (lane == 0) s_tot[warp][i] = v[i];
+        }
+        __syncthreads();
+        if (tid == 0) {
+            const double norm = __ldcg(&a.ws->norm);
+            double m[4];
+            for (int i = 0; i < 4; i++) {
+                m[i] = 0.0;
+                for (int k = 0; k < nw; k++) m[i] += s_tot[k][i];
+                m[i] = norm != 0.0 ? m[i] / norm : 0.0;
+                a.stats[1 + i] = (float)m[i];
+            }
+            a.stats[0] = (float)(m[0] + (a.ref_lp ? (double)a.beta : 0.0) * m[1] - (double)a.eta * m[2]);
+            a.stats[5] = (float)norm;
+        }
+    }
+}
+
+// how a row is spread: threads of a CTA, CTAs of a cluster, vectors kept per
+// thread.  A CTA takes 256 threads, so that four share an SM and their phases
+// interleave; a row takes as many CTAs as it needs to stay in registers
+// (eight at most), then as many as fill the GPU when rows are few, while each
+// thread keeps a vector.
+struct RowPlan {
+    int threads, C, NV;
+};
+static RowPlan row_plan(int64_t N, int64_t V, int w, bool aligned)
+{
+    const int64_t nvec = (V + w - 1) / w + (aligned ? 0 : 1);
+    RowPlan p = {256, 1, 8};
+    while (p.C < 8 && (int64_t)p.C * p.threads * 8 < nvec) p.C *= 2;
+    if ((int64_t)p.C * p.threads * 8 < nvec) p.threads = 512;
+    const int64_t fill = 4LL * sm_count();
+    while (p.C < 8 && N * p.C * 2 <= fill && (int64_t)p.C * p.threads < nvec) p.C *= 2;
+    while (p.NV > 1 && (int64_t)p.C * p.threads * (p.NV / 2) >= nvec) p.NV /= 2;
+    return p;
+}
+
+template <typename T, int NV, bool POLICY, bool ETA>
+static cudaError_t launch_rows_nv(const RowPlan &p, const T *logits, int64_t N, int64_t V, int64_t ld,
+                                  const void *targets, int t64, float k2, float *logprobs, float *entropy, T *dlogits,
+                                  const PolicyArgs &a, int32_t *dev_status, cudaStream_t st)
+{
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = p.C;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3((unsigned)(N * p.C));
+    cfg.blockDim = dim3(p.threads);
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = POLICY ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, token_rows_kernel<T, NV, POLICY, ETA>, logits, N, V, ld, targets, t64, k2, p.C,
+                              logprobs, entropy, dlogits, a, dev_status);
+}
+
+template <typename T, bool POLICY, bool ETA>
+static cudaError_t launch_rows(const T *logits, int64_t N, int64_t V, int64_t ld, const void *targets, int t64,
+                               float k2, float *logprobs, float *entropy, T *dlogits, const PolicyArgs &a,
+                               int32_t *dev_status, cudaStream_t st)
+{
+    const bool aligned = aligned16(logits) && (N == 1 || ld % Vec<T>::W == 0);
+    const RowPlan p = row_plan(N, V, Vec<T>::W, aligned);
+#define MOE_ROWS(NV)                                                                                                  \
+    launch_rows_nv<T, NV, POLICY, ETA>(p, logits, N, V, ld, targets, t64, k2, logprobs, entropy, dlogits, a,          \
+                                       dev_status, st)
+    switch (p.NV) {
+    case 1: return MOE_ROWS(1);
+    case 2: return MOE_ROWS(2);
+    case 4: return MOE_ROWS(4);
+    default: return MOE_ROWS(8);
+    }
+#undef MOE_ROWS
 }
 
 static moe_status check_rows(const void *logits, int dtype, int64_t N, int64_t V, int64_t ld, const void *targets,
                              int target_bits, float temperature)
 {
-    if (N < 0 || V < 1 || N >= (1LL << 31) || V >= (1LL << 31) || ld < V) return MOE_ERR_SHAPE;
+    if (N < 0 || V < 1 || N >= (1LL << 28) || V >= (1LL << 31) || ld < V) return MOE_ERR_SHAPE;
     if (dtype != MOE_LOGITS_BF16 && dtype != MOE_LOGITS_F32) return MOE_ERR_SHAPE;
     if (target_bits != 32 && target_bits != 64) return MOE_ERR_SHAPE;
     if (!isfinite(temperature) || !(temperature > 0.0f)) return MOE_ERR_SHAPE;
@@ -236,14 +618,6 @@ static moe_status check_rows(const void *logits, int dtype, int64_t N, int64_t V
     const uintptr_t es = dtype == MOE_LOGITS_BF16 ? 2 : 4, ts = target_bits / 8;
     if ((uintptr_t)logits % es || (uintptr_t)targets % ts) return MOE_ERR_ALIGN;
     return MOE_OK;
-}
-
-constexpr int MAX_ROW_CTAS = 1024;
-static unsigned row_grid(int64_t N)
-{
-    const int64_t g = 4LL * sm_count();
-    const int64_t c = g < MAX_ROW_CTAS ? g : MAX_ROW_CTAS;
-    return (unsigned)(N < c ? N : c);
 }
 
 } // namespace moe
@@ -260,22 +634,21 @@ MOE_API moe_status moe_token_logprobs(const void *logits, int logits_dtype, int6
     if (!logprobs) return MOE_ERR_NULL;
     const float k2 = (float)(1.4426950408889634 / (double)temperature);
     PolicyArgs a = {};
-    if (logits_dtype == MOE_LOGITS_BF16)
-        token_rows_kernel<uint16_t, false><<<row_grid(N), 512, 0, as_stream(stream)>>>(
-            (const uint16_t *)logits, N, V, ld, targets, target_bits == 64, k2, logprobs, entropy, nullptr, a,
-            dev_status);
-    else
-        token_rows_kernel<float, false><<<row_grid(N), 512, 0, as_stream(stream)>>>(
-            (const float *)logits, N, V, ld, targets, target_bits == 64, k2, logprobs, entropy, nullptr, a,
-            dev_status);
-    return launch_status();
+    cudaStream_t st = as_stream(stream);
+    const int t64 = target_bits == 64;
+    const cudaError_t e =
+        logits_dtype == MOE_LOGITS_BF16
+            ? launch_rows<uint16_t, false, false>((const uint16_t *)logits, N, V, ld, targets, t64, k2, logprobs,
+                                                  entropy, nullptr, a, dev_status, st)
+            : launch_rows<float, false, false>((const float *)logits, N, V, ld, targets, t64, k2, logprobs, entropy,
+                                               nullptr, a, dev_status, st);
+    return e == cudaSuccess ? launch_status() : MOE_ERR_CUDA;
 }
 
 MOE_API size_t moe_policy_loss_workspace_size(int64_t N, int64_t V)
 {
-    (void)N;
     (void)V;
-    return sizeof(double) * 5 * MAX_ROW_CTAS;
+    return sizeof(Ws) + sizeof(float4) * (size_t)(N > 0 ? N : 0);
 }
 
 MOE_API moe_status moe_policy_loss(const void *logits, int logits_dtype, int64_t N, int64_t V, int64_t ld,
@@ -302,19 +675,25 @@ MOE_API moe_status moe_policy_loss(const void *logits, int logits_dtype, int64_t
     if (!aligned16(workspace)) return MOE_ERR_ALIGN;
     if (N == 0)
         return cudaMemsetAsync(stats, 0, 6 * sizeof(float), st) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    Ws *ws = (Ws *)workspace;
     PolicyArgs a = {old_logprobs, advantages, ref_logprobs, weights, 1.0f - clip_low, 1.0f + clip_high, kl_coef,
-                    entropy_coef, norm, grad_scale, 1.0f / temperature, ld_d, (double *)workspace};
+                    entropy_coef, norm, grad_scale, 1.0f / temperature, ld_d, stats, ws};
     const float k2 = (float)(1.4426950408889634 / (double)temperature);
-    const unsigned g = row_grid(N);
+    const int t64 = target_bits == 64;
+    policy_norm_kernel<<<1, 1024, 0, st>>>(weights, N, norm, ws);
+    if (cudaPeekAtLastError() != cudaSuccess) return launch_status();
+    cudaError_t e;
     if (logits_dtype == MOE_LOGITS_BF16)
-        token_rows_kernel<uint16_t, true><<<g, 512, 0, st>>>((const uint16_t *)logits, N, V, ld, targets,
-                                                             target_bits == 64, k2, logprobs, nullptr,
-                                                             (uint16_t *)dlogits, a, dev_status);
+        e = entropy_coef != 0.0f
+                ? launch_rows<uint16_t, true, true>((const uint16_t *)logits, N, V, ld, targets, t64, k2, logprobs,
+                                                    nullptr, (uint16_t *)dlogits, a, dev_status, st)
+                : launch_rows<uint16_t, true, false>((const uint16_t *)logits, N, V, ld, targets, t64, k2, logprobs,
+                                                     nullptr, (uint16_t *)dlogits, a, dev_status, st);
     else
-        token_rows_kernel<float, true><<<g, 512, 0, st>>>((const float *)logits, N, V, ld, targets,
-                                                          target_bits == 64, k2, logprobs, nullptr, (float *)dlogits,
-                                                          a, dev_status);
-    policy_stats_kernel<<<1, 1, 0, st>>>((const double *)workspace, (int)g, ref_logprobs ? kl_coef : 0.0f,
-                                         entropy_coef, stats);
-    return launch_status();
+        e = entropy_coef != 0.0f
+                ? launch_rows<float, true, true>((const float *)logits, N, V, ld, targets, t64, k2, logprobs, nullptr,
+                                                 (float *)dlogits, a, dev_status, st)
+                : launch_rows<float, true, false>((const float *)logits, N, V, ld, targets, t64, k2, logprobs,
+                                                  nullptr, (float *)dlogits, a, dev_status, st);
+    return e == cudaSuccess ? launch_status() : MOE_ERR_CUDA;
 }

@@ -583,7 +583,7 @@ moe_status moe_combine_slots(const uint16_t *out_slots, const int32_t *slot_to_s
  *   logprobs[t] = z[t,y_t] - LSE[t], y = targets;
  *   entropy[t]  = LSE[t] - sum_v p[t,v] z[t,v]  (nullable).
  *   Sums in fp32, in an order fixed by N and V.
- * Errors: SHAPE (N < 0, V < 1, N or V >= 2^31, ld < V, dtype, target_bits,
+ * Errors: SHAPE (N < 0, V < 1, N >= 2^28, V >= 2^31, ld < V, dtype, target_bits,
  * temperature not finite and > 0), NULL, ALIGN (logits not aligned to its
  * element), CUDA.
  *

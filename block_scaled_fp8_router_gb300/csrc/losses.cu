@@ -117,6 +117,15 @@ struct Vec<uint16_t> {
         const __nv_bfloat162 a = __hmax2(__hmax2(m[0], m[1]), __hmax2(m[2], m[3]));
         return fmaxf(__low2float(a), __high2float(a));
     }
+    // elements below -2^100 raised to it, NaN kept
+    static __device__ __forceinline__ uint4 floor100(const uint4 &v)
+    {
+        const uint32_t lo = 0xF180F180u;
+        uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; i++) asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(w[i]) : "r"(lo));
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
     // pair i (0 .. 3) as two fp32
     static __device__ __forceinline__ uint64_t pair(const uint4 &v, int i)
     {
@@ -137,6 +146,17 @@ struct Vec<float> {
     {
         return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)),
                      fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
+    }
+    static __device__ __forceinline__ uint4 floor100(const uint4 &v)
+    {
+        uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            float f = __uint_as_float(w[i]);
+            asm("max.NaN.f32 %0, %0, %1;" : "+f"(f) : "f"(-0x1p100f));
+            w[i] = __float_as_uint(f);
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
     }
     static __device__ __forceinline__ uint64_t pair(const uint4 &v, int i)
     {
@@ -163,60 +183,91 @@ __device__ __forceinline__ void store_grad(uint16_t *p, float v)
 }
 __device__ __forceinline__ void store_grad(float *p, float v) { *p = v; }
 
+// a vector at a row's ends, or past it: elements e .. e + W - 1 of the row,
+// those outside [0, V) -inf
+template <typename T>
+__device__ __noinline__ uint4 load_ends(const T *l, int64_t V, int64_t e)
+{
+    constexpr int W = Vec<T>::W;
+    float f[W];
+#pragma unroll
+    for (int u = 0; u < W; u++) f[u] = e + u >= 0 && e + u < V ? load_logit(l + e + u) : -INFINITY;
+    return Vec<T>::make(f);
+}
+
 // a row as 16-byte vectors: vector j holds the elements W j - head .. + W - 1
-// of the row, those outside [0, V) absent
+// of the row, those outside [0, V) absent; vectors lo .. hi - 1 are whole
 template <typename T>
 struct Row {
     const T *l;
-    int head, nvec;
+    const uint4 *base;
+    int head, nvec, lo, hi;
     int64_t V;
     __device__ __forceinline__ Row(const T *p, int64_t n) : l(p), V(n)
     {
         constexpr int W = Vec<T>::W;
         head = (int)((reinterpret_cast<uintptr_t>(p) & 15u) / sizeof(T));
+        base = reinterpret_cast<const uint4 *>(reinterpret_cast<uintptr_t>(p) & ~(uintptr_t)15u);
         nvec = (int)((n + head + W - 1) / W);
+        lo = head > 0;
+        hi = (int)((n + head) / W);
     }
-    __device__ __forceinline__ bool inside(int j) const
+    __device__ __forceinline__ bool inside(int j) const { return j >= lo && j < hi; }
+    __device__ __forceinline__ uint4 load_edge(int j) const
     {
-        constexpr int W = Vec<T>::W;
-        const int64_t e = (int64_t)W * j - head;
-        return e >= 0 && e + W <= V;
+        return load_ends<T>(l, V, (int64_t)Vec<T>::W * j - head);
     }
-    // absent elements read as -inf
     __device__ __forceinline__ uint4 load(int j) const
     {
-        constexpr int W = Vec<T>::W;
         constexpr uint32_t NI = Vec<T>::NINF;
-        if (j >= nvec) return make_uint4(NI, NI, NI, NI);
-        const int64_t e = (int64_t)W * j - head;
-        if (e >= 0 && e + W <= V) {
-            uint4 v;
+        uint4 v = make_uint4(NI, NI, NI, NI);
+        if (inside(j))
             asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
                          : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                         : "l"(l + e)
+                         : "l"(base + j)
                          : "memory");
-            return v;
-        }
-        float f[W];
-#pragma unroll
-        for (int u = 0; u < W; u++) f[u] = e + u >= 0 && e + u < V ? load_logit(l + e + u) : -INFINITY;
-        return Vec<T>::make(f);
+        return v;
     }
 };
 
 struct PolicyArgs {
     const float *old_lp, *adv, *ref_lp, *w;
-    float clip_lo, clip_hi, beta, eta, norm, grad_scale, inv_tau;
+    float clip_lo, clip_hi, beta, eta, inv_tau;
     int64_t ld_d;
-    float *stats;
     struct Ws *ws;
 };
 
-// workspace: the weights' sum, the rows done so far, and per row w pg, w kl,
-// w H and w [clipped]
+// a sum in two fp32 numbers (Knuth's exact sum of two, the error carried along):
+// about 48 bits, without the fp64 units, which are slow here
+struct Sum2 {
+    float hi, lo;
+};
+__device__ __forceinline__ void add(Sum2 &s, float v)
+{
+    const float t = __fadd_rn(s.hi, v), z = __fsub_rn(t, s.hi);
+    const float e = __fadd_rn(__fsub_rn(s.hi, __fsub_rn(t, z)), __fsub_rn(v, z));
+    s.hi = t;
+    s.lo = __fadd_rn(s.lo, e);
+}
+__device__ __forceinline__ void add(Sum2 &s, const Sum2 &o)
+{
+    add(s, o.hi);
+    s.lo = __fadd_rn(s.lo, o.lo);
+}
+__device__ __forceinline__ void warp_sum2(Sum2 &s)
+{
+    for (int o = 16; o; o >>= 1) {
+        Sum2 b;
+        b.hi = __shfl_xor_sync(0xFFFFFFFFu, s.hi, o);
+        b.lo = __shfl_xor_sync(0xFFFFFFFFu, s.lo, o);
+        add(s, b);
+    }
+}
+
+// workspace: the weights' sum, and per row w pg, w kl, w H and w [clipped]
 struct Ws {
-    double norm;
-    uint32_t done, pad;
+    float norm, scale;      // scale = grad_scale / (norm temperature), 0 where norm is
+    float pad[2];
     float4 row[1];
 };
 
@@ -232,28 +283,35 @@ __device__ __forceinline__ float kl_term(float q)
     return expf(q) - q - 1.0f;
 }
 
-// sum of the weights in a fixed order; resets the count of rows done
-__global__ void __launch_bounds__(1024) policy_norm_kernel(const float *__restrict__ w, int64_t N, float norm, Ws *ws)
+// sum of the weights in a fixed order
+__global__ void __launch_bounds__(1024) policy_norm_kernel(const float *__restrict__ w, int64_t N, float norm,
+                                                           float num, Ws *ws)
 {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    __shared__ double s_v[32];
+    __shared__ Sum2 s_v[32];
     const int tid = threadIdx.x;
-    double v = 0.0;
-    if (norm > 0.0f) {
-        v = tid == 0 ? (double)norm : 0.0;
-    } else if (!w) {
-        v = tid == 0 ? (double)N : 0.0;
-    } else {
-        for (int64_t i = tid; i < N; i += 1024) v += (double)__ldg(w + i);
+    if (norm == 0.0f && w) {
+        Sum2 v = {0.0f, 0.0f};
+        for (int64_t i = tid; i < N; i += 8192) {
+            float q[8];
+#pragma unroll
+            for (int u = 0; u < 8; u++) q[u] = i + 1024 * u < N ? __ldg(w + i + 1024 * u) : 0.0f;
+#pragma unroll
+            for (int u = 0; u < 8; u++) add(v, q[u]);
+        }
+        warp_sum2(v);
+        if ((tid & 31) == 0) s_v[tid >> 5] = v;
+        __syncthreads();
+        if (tid >= 32) return;
+        v = s_v[tid];
+        warp_sum2(v);
+        norm = v.hi + v.lo;
+    } else if (norm == 0.0f) {
+        norm = (float)N;
     }
-    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-    if ((tid & 31) == 0) s_v[tid >> 5] = v;
-    __syncthreads();
     if (tid == 0) {
-        v = 0.0;
-        for (int i = 0; i < 32; i++) v += s_v[i];
-        ws->norm = v;
-        ws->done = 0;
+        ws->norm = norm;
+        ws->scale = norm != 0.0f ? num / norm : 0.0f;
     }
 }
 
@@ -270,35 +328,79 @@ __device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank)
     return out;
 }
 
-constexpr int ROW_THREADS = 512;        // at most
+constexpr int ROW_THREADS = 128;
 constexpr uint64_t ROW_TIMEOUT_NS = 1000ull * 1000ull * 1000ull;
 
-// what a row's gradient needs: dl_v = 2^t_v (A0 + B0 t_v) + gy 1[v = y]
+// what a row's gradient needs: dl_v = 2^t_v (A0 + B0 t_v) + gy 1[v = y],
+// t_v = l_v k2 - ck
 struct RowGrad {
-    float c, A0, B0, gy;
+    float ck, A0, B0, gy;
 };
 
-// sums of one vector against the shift m, two elements at a time
-template <typename T>
-__device__ __forceinline__ void add_vec(const uint4 &v, uint64_t nm2, uint64_t k22, uint64_t &S, uint64_t &U)
+// whether t of a logit held above -2^100 is finite for the shift c, so that 2^t t
+// needs no other care (rows whose largest logit is beyond 2^99, or -inf, and
+// temperatures below 1e-6 take the slower form)
+__device__ __forceinline__ bool plain_range(float c, float k2) { return fabsf(c) < 0x1p99f && k2 < 0x1p20f; }
+
+// sums of one vector against the shift c = -nc, two elements at a time
+template <typename T, bool SLOW>
+__device__ __forceinline__ void add_vec(uint4 v, uint64_t nc2, uint64_t k22, uint64_t &S, uint64_t &U)
 {
+    if (!SLOW) v = Vec<T>::floor100(v);
 #pragma unroll
     for (int i = 0; i < Vec<T>::W / 2; i++) {
-        const uint64_t t = mul2(add2(Vec<T>::pair(v, i), nm2), k22);
+        uint64_t t = mul2(add2(Vec<T>::pair(v, i), nc2), k22);
         float t0, t1;
         unpack2(t, t0, t1);
         const uint64_t e = pack2(ex2(t0), ex2(t1));
         S = add2(S, e);
-        U = fma2(e, pack2(fmaxf(t0, TMIN), fmaxf(t1, TMIN)), U);
+        if (SLOW) t = pack2(fmaxf(t0, TMIN), fmaxf(t1, TMIN));
+        U = fma2(e, t, U);
     }
 }
 
-template <typename T, bool ETA>
-__device__ __forceinline__ void grad_vec(const uint4 &v, const RowGrad &g, uint64_t nm2, uint64_t k22, float *f)
+// adds NV vectors of a warp to its sums (all lanes hold the same shift)
+template <typename T, int NV>
+__device__ __forceinline__ void add_vecs(RowSum &s, const uint4 (&v)[NV], float k2)
 {
+    float m = s.c;
+#pragma unroll
+    for (int i = 0; i < NV; i++) m = fmaxf(m, Vec<T>::max(v[i]));
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    if (m > s.c) {
+        if (s.c != -INFINITY) {
+            const float d = fmaxf((s.c - m) * k2, TMIN), f = ex2(d);
+            s.U = (s.U + d * s.S) * f;
+            s.S *= f;
+        }
+        s.c = m;
+    }
+    const float nc = m == -INFINITY ? 0.0f : -m;
+    const uint64_t nc2 = pack2(nc, nc), k22 = pack2(k2, k2);
+    uint64_t S = pack2(s.S, 0.0f), U = pack2(s.U, 0.0f);
+    if (plain_range(m, k2)) {
+#pragma unroll
+        for (int i = 0; i < NV; i++) add_vec<T, false>(v[i], nc2, k22, S, U);
+    } else {
+#pragma unroll
+        for (int i = 0; i < NV; i++) add_vec<T, true>(v[i], nc2, k22, S, U);
+    }
+    float x, z;
+    unpack2(S, x, z);
+    s.S = x + z;
+    unpack2(U, x, z);
+    s.U = x + z;
+}
+
+// the gradient of one vector.  t = l k2 - ck in one step, ck = c k2 rounded:
+// the rounding is one factor for the whole row and part of A0 and B0
+template <typename T, bool ETA>
+__device__ __forceinline__ void grad_vec(const uint4 &v, const RowGrad &g, uint64_t k22, float *f)
+{
+    const uint64_t nck2 = pack2(-g.ck, -g.ck);
 #pragma unroll
     for (int i = 0; i < Vec<T>::W / 2; i++) {
-        const uint64_t t = mul2(add2(Vec<T>::pair(v, i), nm2), k22);
+        const uint64_t t = fma2(Vec<T>::pair(v, i), k22, nck2);
         float t0, t1;
         unpack2(t, t0, t1);
         const uint64_t e = pack2(ex2(t0), ex2(t1));
@@ -311,7 +413,7 @@ __device__ __forceinline__ void grad_vec(const uint4 &v, const RowGrad &g, uint6
 // Row blockIdx.x / C by a cluster of C CTAs.  POLICY: the policy loss and its
 // gradient (else log-probabilities and entropy); ETA: with an entropy bonus.
 template <typename T, int NV, bool POLICY, bool ETA>
-__global__ void __launch_bounds__(ROW_THREADS, 2)
+__global__ void __launch_bounds__(ROW_THREADS, POLICY ? 6 : 8)
     token_rows_kernel(const T *logits, int64_t N, int64_t V, int64_t ld, const void *__restrict__ targets, int t64,
                       float k2, int C, float *__restrict__ logprobs, float *__restrict__ entropy, T *dlogits,
                       const PolicyArgs a, int32_t *dev_status)
@@ -322,7 +424,6 @@ __global__ void __launch_bounds__(ROW_THREADS, 2)
     __shared__ RowGrad s_grad;
     __shared__ int s_live;
     __shared__ uint64_t s_bar;
-    __shared__ double s_tot[ROW_THREADS / 32][4];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, TH = blockDim.x, nw = TH >> 5;
     const int64_t row = blockIdx.x / (unsigned)C;
     const int rank = C > 1 ? (int)cluster_rank() : 0;
@@ -340,58 +441,37 @@ __global__ void __launch_bounds__(ROW_THREADS, 2)
     if (y >= V && w != 0.0f && tid == 0 && rank == 0) dev_flag(dev_status, MOE_DEV_BAD_IDS);
     const Row<T> R(logits + row * ld, V);
     const int j0 = rank * TH + tid, dj = C * TH;   // my vectors: j0, j0 + dj, ...
-    const uint64_t k22 = pack2(k2, k2);
+    // the row in chunks of NV vectors a thread; the last stays in registers for
+    // the gradient, which goes through the chunks backward
+    const int nch = (R.hi + NV * dj - 1) / (NV * dj);
     uint4 raw[NV];
+    auto load = [&](int c) {
+#pragma unroll
+        for (int i = 0; i < NV; i++) raw[i] = R.load((c * NV + i) * dj + j0);
+    };
     float lp = 0.0f, H = 0.0f;
     float4 st = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (live) {
-#pragma unroll
-        for (int i = 0; i < NV; i++) raw[i] = R.load(j0 + i * dj);
+        load(0);
         const float ly = warp == 0 ? load_logit(R.l + y) : 0.0f;
-        float m = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < NV; i++) m = fmaxf(m, Vec<T>::max(raw[i]));
-        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-        RowSum s = {m, 0.0f, 0.0f};
-        {
-            const float sh = m == -INFINITY ? 0.0f : -m;
-            const uint64_t nm2 = pack2(sh, sh);
-            uint64_t S = 0, U = 0;
-#pragma unroll
-            for (int i = 0; i < NV; i++) add_vec<T>(raw[i], nm2, k22, S, U);
-            float x, z;
-            unpack2(S, x, z);
-            s.S = x + z;
-            unpack2(U, x, z);
-            s.U = x + z;
-        }
-        // the rest of a row longer than the registers hold, NV vectors at a time
-        for (int jb = NV * dj; jb < R.nvec; jb += NV * dj) {
-            uint4 v[NV];
-            float mm = s.c;
-#pragma unroll
-            for (int i = 0; i < NV; i++) v[i] = R.load(jb + j0 + i * dj);
-#pragma unroll
-            for (int i = 0; i < NV; i++) mm = fmaxf(mm, Vec<T>::max(v[i]));
-            for (int o = 16; o; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xFFFFFFFFu, mm, o));
-            if (mm > s.c) {
-                if (s.c != -INFINITY) {
-                    const float d = fmaxf((s.c - mm) * k2, TMIN), f = ex2(d);
-                    s.U = (s.U + d * s.S) * f;
-                    s.S *= f;
+        RowSum s = {-INFINITY, 0.0f, 0.0f};
+        // the vectors at the row's two ends, one lane's each, if not whole
+        if (R.lo > 0 || R.hi < R.nvec) {
+            const bool first = R.lo > 0 && j0 == 0, last = R.hi < R.nvec && j0 == (R.nvec - 1) % dj;
+            if (__any_sync(0xFFFFFFFFu, first || last)) {
+                uint4 e[1];
+                e[0] = R.load_edge(first ? 0 : R.nvec);
+                add_vecs<T, 1>(s, e, k2);
+                if (R.nvec > 1 || !(R.lo > 0)) {
+                    e[0] = R.load_edge(last ? R.nvec - 1 : R.nvec);
+                    add_vecs<T, 1>(s, e, k2);
                 }
-                s.c = mm;
             }
-            const float sh = s.c == -INFINITY ? 0.0f : -s.c;
-            const uint64_t nm2 = pack2(sh, sh);
-            uint64_t S = 0, U = 0;
-#pragma unroll
-            for (int i = 0; i < NV; i++) add_vec<T>(v[i], nm2, k22, S, U);
-            float x, z;
-            unpack2(S, x, z);
-            s.S += x + z;
-            unpack2(U, x, z);
-            s.U += x + z;
+        }
+        add_vecs<T, NV>(s, raw, k2);
+        for (int c = 1; c < nch; c++) {
+            load(c);
+            add_vecs<T, NV>(s, raw, k2);
         }
         for (int o = 16; o; o >>= 1) {
             s.S += __shfl_xor_sync(0xFFFFFFFFu, s.S, o);
@@ -401,7 +481,7 @@ __global__ void __launch_bounds__(ROW_THREADS, 2)
         __syncthreads();
         if (warp == 0) {
             s = lane < nw ? s_part[lane] : RowSum{-INFINITY, 0.0f, 0.0f};
-            s = warp_join(s, nw, lane, k2);
+            s = warp_join(s, nw > C ? nw : C, lane, k2);     // lanes 0 .. C-1 all hold the CTA's
             if (C > 1) {
                 // the peers have set up their barriers; lane r sends (c, S, U,
                 // l_y) to CTA r.  l_y travels too so that it has been read
@@ -429,29 +509,31 @@ __global__ void __launch_bounds__(ROW_THREADS, 2)
                 const float ls = log2f(s.S);
                 lp = LN2 * ((ly - s.c) * k2 - ls);
                 H = LN2 * (ls - s.U / s.S);
-                RowGrad g = {s.c, 0.0f, 0.0f, 0.0f};
+                RowGrad g = {0.0f, 0.0f, 0.0f, 0.0f};
                 if (POLICY) {
                     const float A = a.adv[row];
                     float dlt = lp - a.old_lp[row];
                     dlt = dlt > 80.0f ? 80.0f : dlt;
-                    const float r = expf(dlt);
-                    const float rc = r < a.clip_lo ? a.clip_lo : (r > a.clip_hi ? a.clip_hi : r);
-                    const float p0 = -A * r, p1 = -A * rc;
+                    const float ratio = expf(dlt);
+                    const float rc = ratio < a.clip_lo ? a.clip_lo : (ratio > a.clip_hi ? a.clip_hi : ratio);
+                    const float p0 = -A * ratio, p1 = -A * rc;
                     const bool clipped = p1 > p0;
                     float gl = clipped ? 0.0f : p0, kl = 0.0f;
                     if (a.ref_lp) {
-                        float q = a.ref_lp[row] - lp;
-                        q = q > 80.0f ? 80.0f : q;
-                        kl = kl_term(q);
-                        gl = fmaf(-a.beta, expm1f(q), gl);
+                        float u = a.ref_lp[row] - lp;
+                        u = u > 80.0f ? 80.0f : u;
+                        kl = kl_term(u);
+                        gl = fmaf(-a.beta, expm1f(u), gl);
                     }
                     st = make_float4(w * (clipped ? p1 : p0), w * kl, w * H, clipped ? w : 0.0f);
                     asm volatile("griddepcontrol.wait;" ::: "memory");
-                    const double norm = __ldcg(&a.ws->norm);
-                    const float coef = norm != 0.0 ? (float)((double)w * a.grad_scale * a.inv_tau / norm) : 0.0f;
+                    const float coef = w * __ldcg(&a.ws->scale);
+                    // t here is off by r = c k2 - ck from the sums' t
+                    g.ck = s.c * k2;
+                    const float r = fmaf(s.c, k2, -g.ck), q = coef / s.S * exp2f(-r);
                     g.gy = coef * gl;
-                    g.A0 = coef * (-gl + a.eta * (H - LN2 * ls)) / s.S;
-                    g.B0 = coef * a.eta * LN2 / s.S;
+                    g.B0 = q * a.eta * LN2;
+                    g.A0 = q * (-gl + a.eta * (H - LN2 * (ls + r)));
                 }
                 if (lane == 0) s_grad = g;
             }
@@ -469,16 +551,16 @@ __global__ void __launch_bounds__(ROW_THREADS, 2)
             live = s_live != 0;
         }
         const RowGrad g = live ? s_grad : RowGrad{0.0f, 0.0f, 0.0f, 0.0f};
-        const uint64_t nm2 = pack2(-g.c, -g.c);
+        const uint64_t k22 = pack2(k2, k2);
         T *d = dlogits + row * a.ld_d;
         // vector stores where the gradient's rows are aligned as the logits' are
         const bool same = ((reinterpret_cast<uintptr_t>(d) ^ reinterpret_cast<uintptr_t>(R.l)) & 15u) == 0;
+        uint4 *dv = reinterpret_cast<uint4 *>(reinterpret_cast<uintptr_t>(d) & ~(uintptr_t)15u);
         const int jy = live ? (int)((y + R.head) / W) : -1, uy = live ? (int)((y + R.head) % W) : 0;
-        auto put = [&](int j, const uint4 &v) {
-            if (j >= R.nvec) return;
+        auto put = [&](int j, const uint4 &v, bool whole) {
             float f[W];
             if (live) {
-                grad_vec<T, ETA>(v, g, nm2, k22, f);
+                grad_vec<T, ETA>(v, g, k22, f);
                 if (j == jy) {
 #pragma unroll
                     for (int u = 0; u < W; u++) f[u] += u == uy ? g.gy : 0.0f;
@@ -487,79 +569,107 @@ __global__ void __launch_bounds__(ROW_THREADS, 2)
 #pragma unroll
                 for (int u = 0; u < W; u++) f[u] = 0.0f;
             }
-            const int64_t e = (int64_t)W * j - R.head;
-            if (same && R.inside(j)) {
-                __stcs(reinterpret_cast<uint4 *>(d + e), Vec<T>::make(f));
+            if (whole && same) {
+                __stcs(dv + j, Vec<T>::make(f));
             } else {
+                const int64_t e = (int64_t)W * j - R.head;
 #pragma unroll
                 for (int u = 0; u < W; u++)
                     if (e + u >= 0 && e + u < V) store_grad(d + e + u, f[u]);
             }
         };
+        const int j1 = (R.nvec - 1) % dj;      // the last vector's thread
+        if (R.lo > 0 && j0 == 0) put(0, live ? R.load_edge(0) : raw[0], false);
+        if (R.hi < R.nvec && j0 == j1 && (R.nvec > 1 || R.lo == 0))
+            put(R.nvec - 1, live ? R.load_edge(R.nvec - 1) : raw[0], false);
+        for (int c = nch - 1; c >= 0; c--) {
 #pragma unroll
-        for (int i = 0; i < NV; i++) put(j0 + i * dj, raw[i]);
-        for (int j = j0 + NV * dj; j < R.nvec; j += dj) put(j, live ? R.load(j) : raw[0]);
+            for (int i = 0; i < NV; i++) {
+                const int j = (c * NV + i) * dj + j0;
+                if (R.inside(j)) put(j, raw[i], true);
+            }
+            if (live && c > 0) load(c - 1);
+        }
     }
     if (rank == 0 && tid == 0) {
         if (logprobs) logprobs[row] = lp;
         if (!POLICY && entropy) entropy[row] = H;
     }
-    if (POLICY && rank == 0) {
-        // the CTA that finishes the last row sums the rows' parts in order
-        __shared__ int s_last;
-        if (tid == 0) {
-            asm volatile("griddepcontrol.wait;" ::: "memory");
-            a.ws->row[row] = st;
-            __threadfence();
-            s_last = atomicAdd(&a.ws->done, 1u) == (uint32_t)(N - 1);
-        }
-        __syncthreads();
-        if (!s_last) return;
-        __threadfence();
-        double v[4] = {0.0, 0.0, 0.0, 0.0};
-        for (int64_t i = tid; i < N; i += TH) {
-            const float4 q = __ldcg(&a.ws->row[i]);
-            v[0] += q.x;
-            v[1] += q.y;
-            v[2] += q.z;
-            v[3] += q.w;
-        }
+    if (POLICY && rank == 0 && tid == 0) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        a.ws->row[row] = st;
+    }
+}
+
+// the rows' parts added in a fixed order
+__global__ void __launch_bounds__(1024) policy_stats_kernel(const Ws *__restrict__ ws, int64_t N, float beta, float eta,
+                                                            float *__restrict__ stats)
+{
+    __shared__ Sum2 s_tot[32][4];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    Sum2 v[4] = {};
+    for (int64_t i = tid; i < N; i += 4096) {
+        float4 q[4];
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-            for (int o = 16; o; o >>= 1) v[i] += __shfl_xor_sync(0xFFFFFFFFu, v[i], o);
-            if (lane == 0) s_tot[warp][i] = v[i];
+        for (int u = 0; u < 4; u++)
+            q[u] = i + 1024 * u < N ? ws->row[i + 1024 * u] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int u = 0; u < 4; u++) {
+            add(v[0], q[u].x);
+            add(v[1], q[u].y);
+            add(v[2], q[u].z);
+            add(v[3], q[u].w);
         }
-        __syncthreads();
-        if (tid == 0) {
-            const double norm = __ldcg(&a.ws->norm);
-            double m[4];
-            for (int i = 0; i < 4; i++) {
-                m[i] = 0.0;
-                for (int k = 0; k < nw; k++) m[i] += s_tot[k][i];
-                m[i] = norm != 0.0 ? m[i] / norm : 0.0;
-                a.stats[1 + i] = (float)m[i];
-            }
-            a.stats[0] = (float)(m[0] + (a.ref_lp ? (double)a.beta : 0.0) * m[1] - (double)a.eta * m[2]);
-            a.stats[5] = (float)norm;
-        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        warp_sum2(v[i]);
+        if (lane == 0) s_tot[warp][i] = v[i];
+    }
+    __syncthreads();
+    if (warp < 4) {
+        Sum2 m = s_tot[lane][warp];
+        warp_sum2(m);
+        __syncwarp();
+        if (lane == 0) s_tot[0][warp] = m;
+    }
+    __syncthreads();
+    if (tid == 0) {
+        const float norm = ws->norm, in = norm != 0.0f ? 1.0f / norm : 0.0f;
+        const Sum2 pg = s_tot[0][0], kl = s_tot[0][1], H = s_tot[0][2], cl = s_tot[0][3];
+        // pg + beta kl - eta H, the products' errors kept
+        Sum2 l = pg;
+        const float bk = beta * kl.hi, eh = -eta * H.hi;
+        add(l, bk);
+        add(l, eh);
+        l.lo += fmaf(beta, kl.hi, -bk) + beta * kl.lo + fmaf(-eta, H.hi, -eh) - eta * H.lo;
+        stats[0] = (l.hi + l.lo) * in;
+        stats[1] = (pg.hi + pg.lo) * in;
+        stats[2] = (kl.hi + kl.lo) * in;
+        stats[3] = (H.hi + H.lo) * in;
+        stats[4] = (cl.hi + cl.lo) * in;
+        stats[5] = norm;
     }
 }
 
 // how a row is spread: threads of a CTA, CTAs of a cluster, vectors kept per
-// thread.  A CTA takes 256 threads, so that four share an SM and their phases
-// interleave; a row takes as many CTAs as it needs to stay in registers
-// (eight at most), then as many as fill the GPU when rows are few, while each
-// thread keeps a vector.
+// thread.  A CTA takes a warp per 256 vectors, four at most (8192 x 16384 bf16
+// log-probabilities: 50 us at 128 threads, 61 at 256, 58 at 64; an SM holds
+// six or eight such CTAs, whose phases interleave).  One CTA a row where the
+// rows fill the GPU: an exchange costs more than reading a long row's
+// remainder again from L2 (8192 x 131072 bf16 log-probabilities 0.32 ms, 0.34
+// at two CTAs, 0.60 at eight); two for the gradient of long rows, which keeps
+// the rows in work within L2 (4096 x 131072: 0.40 ms against 0.42).  More as
+// rows get few, while each thread keeps a vector.
 struct RowPlan {
     int threads, C, NV;
 };
-static RowPlan row_plan(int64_t N, int64_t V, int w, bool aligned)
+static RowPlan row_plan(int64_t N, int64_t V, int w, bool aligned, bool policy)
 {
     const int64_t nvec = (V + w - 1) / w + (aligned ? 0 : 1);
-    RowPlan p = {256, 1, 8};
-    while (p.C < 8 && (int64_t)p.C * p.threads * 8 < nvec) p.C *= 2;
-    if ((int64_t)p.C * p.threads * 8 < nvec) p.threads = 512;
-    const int64_t fill = 4LL * sm_count();
+    RowPlan p = {32, policy && nvec > 4096 ? 2 : 1, 8};
+    while (p.threads < ROW_THREADS && p.threads * 8 < nvec) p.threads *= 2;
+    const int64_t fill = 3LL * sm_count();
     while (p.C < 8 && N * p.C * 2 <= fill && (int64_t)p.C * p.threads < nvec) p.C *= 2;
     while (p.NV > 1 && (int64_t)p.C * p.threads * (p.NV / 2) >= nvec) p.NV /= 2;
     return p;
@@ -593,7 +703,7 @@ static cudaError_t launch_rows(const T *logits, int64_t N, int64_t V, int64_t ld
                                int32_t *dev_status, cudaStream_t st)
 {
     const bool aligned = aligned16(logits) && (N == 1 || ld % Vec<T>::W == 0);
-    const RowPlan p = row_plan(N, V, Vec<T>::W, aligned);
+    const RowPlan p = row_plan(N, V, Vec<T>::W, aligned, POLICY);
 #define MOE_ROWS(NV)                                                                                                  \
     launch_rows_nv<T, NV, POLICY, ETA>(p, logits, N, V, ld, targets, t64, k2, logprobs, entropy, dlogits, a,          \
                                        dev_status, st)
@@ -677,10 +787,10 @@ MOE_API moe_status moe_policy_loss(const void *logits, int logits_dtype, int64_t
         return cudaMemsetAsync(stats, 0, 6 * sizeof(float), st) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
     Ws *ws = (Ws *)workspace;
     PolicyArgs a = {old_logprobs, advantages, ref_logprobs, weights, 1.0f - clip_low, 1.0f + clip_high, kl_coef,
-                    entropy_coef, norm, grad_scale, 1.0f / temperature, ld_d, stats, ws};
+                    entropy_coef, 1.0f / temperature, ld_d, ws};
     const float k2 = (float)(1.4426950408889634 / (double)temperature);
     const int t64 = target_bits == 64;
-    policy_norm_kernel<<<1, 1024, 0, st>>>(weights, N, norm, ws);
+    policy_norm_kernel<<<1, 1024, 0, st>>>(weights, N, norm, grad_scale * a.inv_tau, ws);
     if (cudaPeekAtLastError() != cudaSuccess) return launch_status();
     cudaError_t e;
     if (logits_dtype == MOE_LOGITS_BF16)
@@ -695,5 +805,7 @@ MOE_API moe_status moe_policy_loss(const void *logits, int logits_dtype, int64_t
                                                  (float *)dlogits, a, dev_status, st)
                 : launch_rows<float, true, false>((const float *)logits, N, V, ld, targets, t64, k2, logprobs,
                                                   nullptr, (float *)dlogits, a, dev_status, st);
-    return e == cudaSuccess ? launch_status() : MOE_ERR_CUDA;
+    if (e != cudaSuccess) return MOE_ERR_CUDA;
+    policy_stats_kernel<<<1, 1024, 0, st>>>(ws, N, ref_logprobs ? kl_coef : 0.0f, entropy_coef, stats);
+    return launch_status();
 }

@@ -18,23 +18,15 @@
 // message to every CTA of the cluster (st.async on an mbarrier), always in the
 // same order.  So a row costs one CTA barrier, one exchange and one more CTA
 // barrier, and several CTAs per SM keep HBM busy across them.
-#include "common.cuh"
+#include "losses.cuh"
 
 #include <math.h>
 
 namespace moe {
 
-constexpr float LN2 = 0.693147180559945309f;
 // where t multiplies 2^t it is held above this: 2^t is 0 there, and 0 times
 // an infinite t (a masked logit) would be NaN
 constexpr float TMIN = -16384.0f;
-
-__device__ __forceinline__ float ex2(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 
 // the sums of one part of a row, relative to the shift c (c = -inf: no logit
 // above -inf, S = U = 0)
@@ -69,36 +61,6 @@ __device__ __forceinline__ RowSum warp_join(RowSum s, int n, int lane, float k2)
         s = (lane & o) ? join(b, s, k2) : join(s, b, k2);
     }
     return s;
-}
-
-// ---- two fp32 at a time ----
-__device__ __forceinline__ uint64_t pack2(float a, float b)
-{
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ void unpack2(uint64_t v, float &a, float &b)
-{
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
-{
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
-{
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
-{
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
 }
 
 // a 16-byte vector of logits: 8 bf16 or 4 fp32
@@ -236,33 +198,6 @@ struct PolicyArgs {
     int64_t ld_d;
     struct Ws *ws;
 };
-
-// a sum in two fp32 numbers (Knuth's exact sum of two, the error carried along):
-// about 48 bits, without the fp64 units, which are slow here
-struct Sum2 {
-    float hi, lo;
-};
-__device__ __forceinline__ void add(Sum2 &s, float v)
-{
-    const float t = __fadd_rn(s.hi, v), z = __fsub_rn(t, s.hi);
-    const float e = __fadd_rn(__fsub_rn(s.hi, __fsub_rn(t, z)), __fsub_rn(v, z));
-    s.hi = t;
-    s.lo = __fadd_rn(s.lo, e);
-}
-__device__ __forceinline__ void add(Sum2 &s, const Sum2 &o)
-{
-    add(s, o.hi);
-    s.lo = __fadd_rn(s.lo, o.lo);
-}
-__device__ __forceinline__ void warp_sum2(Sum2 &s)
-{
-    for (int o = 16; o; o >>= 1) {
-        Sum2 b;
-        b.hi = __shfl_xor_sync(0xFFFFFFFFu, s.hi, o);
-        b.lo = __shfl_xor_sync(0xFFFFFFFFu, s.lo, o);
-        add(s, b);
-    }
-}
 
 // workspace: the weights' sum, and per row w pg, w kl, w H and w [clipped]
 struct Ws {

@@ -13,12 +13,15 @@
 // fp32 registers, rounding to nearest (two or more TMEM buffers, so that the
 // next chunk's MMAs run meanwhile).
 //
-// One persistent CTA per SM: a producer warp (TMA, 128-byte swizzle), an MMA
-// warp and up to 16 epilogue warps.  The work is the list of K blocks of all
-// output tiles, cut into equal runs of blocks, one run per CTA (whole tiles
-// where there are many): a CTA has at most one tile begun by another and one
-// that another ends, which go to its two fp32 slots in the workspace;
-// reduce_kernel adds a tile's slots in order.
+// One persistent CTA per SM: eight epilogue warps, a producer warp (TMA,
+// 128-byte swizzle) and an MMA warp.  A tiles (one part, 16 KB) and B tiles
+// have rings of their own, so that a part's place is free again after its own
+// four MMAs.  The work is the list of K blocks of all output tiles, cut into
+// equal runs of blocks, one run per CTA (whole tiles where there are many): a
+// CTA has at most one tile begun by another and one that another ends, which
+// go to its two fp32 slots in the workspace; reduce_kernel adds a tile's slots
+// in order.  The launches are chained programmatically (a kernel sets itself
+// up while the one before it ends).
 #include "tcgen05.cuh"
 #include "router_dense.cuh"
 
@@ -31,6 +34,9 @@ constexpr int TM = 128;                   // tile rows
 constexpr int KB = 64;                    // K block: 128 bytes of bf16
 constexpr int CHUNK = 4;                  // K blocks per accumulator chain
 constexpr int A_TILE = TM * KB * 2;       // 16 KB
+constexpr int GEMM_EPI = 8;               // epilogue warps
+constexpr int GEMM_PRODUCER = 8, GEMM_MMA = 9;
+constexpr int GEMM_THREADS = 10 * 32;
 constexpr int MAX_CTAS = 160;
 constexpr int SLOT_COLS = 256;
 constexpr size_t SLOT_FLOATS = (size_t)TM * SLOT_COLS;
@@ -42,20 +48,20 @@ struct Cfg {
     static constexpr int P = MODE == LOGITS ? 1 : 3;              // parts of A
     static constexpr bool A_MN = MODE == DW, B_MN = MODE != LOGITS;
     static constexpr int B_TILE = BN * KB * 2;
-    static constexpr int STAGE = P * A_TILE + B_TILE;
-    static constexpr int STAGES = P == 3 ? 2 : (BN == 256 ? 3 : 4);
-    static constexpr int BUFS = BN == 256 ? 2 : 4;
-    static constexpr int CGS = BN / 32 < 4 ? BN / 32 : 4;         // column groups of the epilogue
-    static constexpr int WCOLS = BN / CGS;                        // columns of one epilogue warp
-    static constexpr int EPI = 4 * CGS;
+    static constexpr int NB = BN == 256 ? (P == 3 ? 3 : 4) : BN == 128 ? (P == 3 ? 4 : 6) : 8;   // B tiles
+    static constexpr int NA = P == 3 ? (BN == 256 ? 6 : 8) : (BN == 256 ? 4 : BN == 128 ? 6 : 8); // A tiles
+    static constexpr int BUFS = BN == 256 ? 2 : 4;                // accumulators in tensor memory
+    static constexpr int WCOLS = BN / 2;                          // columns of one epilogue warp
 };
 
 template <Mode MODE, int BN>
 struct Smem {
     using C = Cfg<MODE, BN>;
-    uint8_t ring[C::STAGES][C::STAGE];    // the parts' A tiles, then the B tile
-    float stage[C::EPI][32 * 32];         // a warp's 32 x 32 sub-tile for its TMA store
-    uint64_t full[C::STAGES], empty[C::STAGES];
+    uint8_t a[C::NA][A_TILE];
+    uint8_t b[C::NB][C::B_TILE];
+    float stage[GEMM_EPI][32 * 32];       // a warp's 32 x 32 sub-tile for its TMA store
+    uint64_t afull[C::NA], aempty[C::NA];
+    uint64_t bfull[C::NB], bempty[C::NB];
     uint64_t tfull[C::BUFS], tempty[C::BUFS];
     uint64_t mma_done;
     uint32_t tmem_base;
@@ -135,8 +141,19 @@ constexpr uint32_t idesc_bf16(int M, int N, bool a_mn, bool b_mn)
            ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
+// wait until the phase that block n's use of a ring of `size` fills (or frees)
+// is complete; each wait is bounded
+__device__ __forceinline__ void drain(uint64_t *full, int size, uint32_t n)
+{
+    for (int i = 0; i < size && (uint32_t)i < n; i++) {
+        const uint32_t last = n - 1 - ((n - 1 - i) % size);
+        const uint64_t t0 = globaltimer_ns();
+        while (!mbar_try_wait(&full[i], (last / size) & 1) && globaltimer_ns() - t0 < TIMEOUT_NS) {}
+    }
+}
+
 template <Mode MODE, int BN>
-__global__ void __launch_bounds__(THREADS, 1)
+__global__ void __launch_bounds__(GEMM_THREADS, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                 const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ CUtensorMap tm_slots, const Params p)
 {
@@ -146,82 +163,115 @@ __global__ void __launch_bounds__(THREADS, 1)
         *reinterpret_cast<Smem<MODE, BN> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < C::STAGES; i++) {
-            mbar_init(&s.full[i], 1);
-            mbar_init(&s.empty[i], 1);
+        for (int i = 0; i < C::NA; i++) {
+            mbar_init(&s.afull[i], 1);
+            mbar_init(&s.aempty[i], 1);
+        }
+        for (int i = 0; i < C::NB; i++) {
+            mbar_init(&s.bfull[i], 1);
+            mbar_init(&s.bempty[i], 1);
         }
         for (int i = 0; i < C::BUFS; i++) {
             mbar_init(&s.tfull[i], 1);
-            mbar_init(&s.tempty[i], C::EPI);
+            mbar_init(&s.tempty[i], GEMM_EPI);
         }
         mbar_init(&s.mma_done, 1);
         s.abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
-    if (warp == MMA_WARP) tmem_alloc(&s.tmem_base, TMEM_COLS);
+    if (warp == GEMM_MMA) tmem_alloc(&s.tmem_base, TMEM_COLS);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    // everything before this overlaps the kernel before; nothing it wrote is
+    // read, and nothing written, before it has ended
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const uint32_t tmem = s.tmem_base;
     volatile int *abort_flag = &s.abort_flag;
     const int64_t b0 = run_begin(p.blocks, p.gran, gridDim.x, blockIdx.x);
     const int64_t b1 = run_begin(p.blocks, p.gran, gridDim.x, blockIdx.x + 1);
 
-    if (warp == PRODUCER_WARP) {
+    if (warp == GEMM_PRODUCER) {
         if (lane == 0) {
-            uint32_t j = 0;
-            for (int64_t b = b0; b < b1; b++, j++) {
-                const int tile = (int)(b / p.nkb), kb = (int)(b - (int64_t)tile * p.nkb);
-                const int mt = tile / p.n_tiles, nt = tile - mt * p.n_tiles;
-                const int st = j % C::STAGES;
-                if (!wait_or_abort(&s.empty[st], ((j / C::STAGES) & 1) ^ 1, abort_flag, p.dev_status)) break;
-                mbar_arrive_expect_tx(&s.full[st], C::STAGE);
-#pragma unroll
-                for (int q = 0; q < C::P; q++) {
-                    if (C::A_MN)
-                        tma_load_4d(s.ring[st] + q * A_TILE, &tm_a, 0, kb * KB, mt * (TM / 64), q, &s.full[st]);
-                    else
-                        tma_load_3d(s.ring[st] + q * A_TILE, &tm_a, kb * KB * 2, mt * TM, q, &s.full[st]);
-                }
+            uint32_t ja = 0, jb = 0;
+            bool ok = true;
+            int tile = (int)(b0 / p.nkb), kb = (int)(b0 - (int64_t)tile * p.nkb);
+            int mt = tile / p.n_tiles, nt = tile - mt * p.n_tiles;
+            for (int64_t b = b0; ok && b < b1; b++) {
+                const int sb = jb % C::NB;
+                if (!wait_or_abort(&s.bempty[sb], ((jb / C::NB) & 1) ^ 1, abort_flag, p.dev_status)) break;
+                mbar_arrive_expect_tx(&s.bfull[sb], C::B_TILE);
                 if (C::B_MN)
-                    tma_load_3d(s.ring[st] + C::P * A_TILE, &tm_b, 0, kb * KB, nt * (BN / 64), &s.full[st]);
+                    tma_load_3d(s.b[sb], &tm_b, 0, kb * KB, nt * (BN / 64), &s.bfull[sb]);
                 else
-                    tma_load_2d(s.ring[st] + C::P * A_TILE, &tm_b, kb * KB * 2, nt * BN, &s.full[st]);
+                    tma_load_2d(s.b[sb], &tm_b, kb * KB * 2, nt * BN, &s.bfull[sb]);
+                jb++;
+#pragma unroll
+                for (int q = C::P - 1; q >= 0; q--) {
+                    const int sa = ja % C::NA;
+                    if (!wait_or_abort(&s.aempty[sa], ((ja / C::NA) & 1) ^ 1, abort_flag, p.dev_status)) {
+                        ok = false;
+                        break;
+                    }
+                    mbar_arrive_expect_tx(&s.afull[sa], A_TILE);
+                    if (C::A_MN)
+                        tma_load_4d(s.a[sa], &tm_a, 0, kb * KB, mt * (TM / 64), q, &s.afull[sa]);
+                    else
+                        tma_load_3d(s.a[sa], &tm_a, kb * KB * 2, mt * TM, q, &s.afull[sa]);
+                    ja++;
+                }
+                if (++kb == p.nkb) {
+                    kb = 0;
+                    if (++nt == p.n_tiles) {
+                        nt = 0;
+                        mt++;
+                    }
+                }
             }
             // no copy may still be in flight when the CTA exits
-            for (int i = 0; i < C::STAGES && (uint32_t)i < j; i++) {
-                const uint32_t last = j - 1 - ((j - 1 - i) % C::STAGES);
-                const uint64_t t0 = globaltimer_ns();
-                while (!mbar_try_wait(&s.full[i], (last / C::STAGES) & 1) && globaltimer_ns() - t0 < TIMEOUT_NS) {}
-            }
+            drain(s.afull, C::NA, ja);
+            drain(s.bfull, C::NB, jb);
         }
-    } else if (warp == MMA_WARP) {
+    } else if (warp == GEMM_MMA) {
         if (lane == 0) {
             constexpr uint32_t IDESC = idesc_bf16(TM, BN, C::A_MN, C::B_MN);
             constexpr int A_STEP = C::A_MN ? 2048 >> 4 : 32 >> 4, B_STEP = C::B_MN ? 2048 >> 4 : 32 >> 4;
-            uint32_t j = 0, jc = 0;
-            int in_chunk = 0;
-            for (int64_t b = b0; b < b1; b++, j++) {
-                const int st = j % C::STAGES, buf = jc % C::BUFS;
+            uint32_t ja = 0, jb = 0, jc = 0;
+            int in_chunk = 0, kb = (int)(b0 % p.nkb);
+            bool ok = true;
+            for (int64_t b = b0; ok && b < b1; b++) {
+                const int sb = jb % C::NB, buf = jc % C::BUFS;
                 if ((in_chunk == 0 &&
                      !wait_or_abort(&s.tempty[buf], ((jc / C::BUFS) & 1) ^ 1, abort_flag, p.dev_status)) ||
-                    !wait_or_abort(&s.full[st], (j / C::STAGES) & 1, abort_flag, p.dev_status))
+                    !wait_or_abort(&s.bfull[sb], (jb / C::NB) & 1, abort_flag, p.dev_status))
                     break;
-                tc_fence_after();
-                const uint32_t ring = smem_u32(s.ring[st]);
-                const uint64_t bdesc = C::B_MN ? sw128_desc_mn(ring + C::P * A_TILE) : sw128_desc(ring + C::P * A_TILE);
+                const uint32_t baddr = smem_u32(s.b[sb]);
+                const uint64_t bdesc = C::B_MN ? sw128_desc_mn(baddr) : sw128_desc(baddr);
 #pragma unroll
                 for (int q = C::P - 1; q >= 0; q--) {      // the small parts first
-                    const uint64_t adesc = C::A_MN ? sw128_desc_mn(ring + q * A_TILE) : sw128_desc(ring + q * A_TILE);
+                    const int sa = ja % C::NA;
+                    if (!wait_or_abort(&s.afull[sa], (ja / C::NA) & 1, abort_flag, p.dev_status)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t aaddr = smem_u32(s.a[sa]);
+                    const uint64_t adesc = C::A_MN ? sw128_desc_mn(aaddr) : sw128_desc(aaddr);
 #pragma unroll
                     for (int ks = 0; ks < KB / 16; ks++)
                         mma_bf16(tmem + buf * BN, adesc + A_STEP * ks, bdesc + B_STEP * ks, IDESC,
                                  in_chunk > 0 || q < C::P - 1 || ks > 0);
+                    mma_commit(&s.aempty[sa]);
+                    ja++;
                 }
-                mma_commit(&s.empty[st]);
+                if (!ok) break;
+                mma_commit(&s.bempty[sb]);
+                jb++;
                 in_chunk++;
-                if (in_chunk == CHUNK || (b + 1) % p.nkb == 0 || b + 1 == b1) {
+                if (++kb == p.nkb) kb = 0;
+                if (in_chunk == CHUNK || kb == 0 || b + 1 == b1) {
                     mma_commit(&s.tfull[buf]);
                     jc++;
                     in_chunk = 0;
@@ -232,9 +282,9 @@ __global__ void __launch_bounds__(THREADS, 1)
             while (!mbar_try_wait(&s.mma_done, 0) && globaltimer_ns() - t0 < TIMEOUT_NS) {}
         }
         __syncwarp();
-    } else if (warp < C::EPI) {
-        // warp (q, cg): TMEM lanes 32q .. 32q+31 (tile rows), columns WCOLS cg ..
-        const int q = warp & 3, cg = warp >> 2;
+    } else {
+        // warp (q, half): TMEM lanes 32q .. 32q+31 (tile rows), columns WCOLS half ..
+        const int q = warp & 3, half = warp >> 2;
         const uint32_t lane_addr = (uint32_t)(q * 32) << 16;
         float *stg = s.stage[warp];
         uint32_t jc = 0;
@@ -257,7 +307,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                 for (int h = 0; h < C::WCOLS / 16; h++) {
                     float v[16];
-                    tmem_ld16(tmem + lane_addr + buf * BN + C::WCOLS * cg + 16 * h, v);
+                    tmem_ld16(tmem + lane_addr + buf * BN + C::WCOLS * half + 16 * h, v);
 #pragma unroll
                     for (int i = 0; i < 16; i++) acc[16 * h + i] += v[i];
                 }
@@ -271,7 +321,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             const bool slot0 = b == b0;
 #pragma unroll
             for (int h = 0; h < C::WCOLS / 32; h++) {
-                const int col_t = C::WCOLS * cg + 32 * h, col0 = nt * BN + col_t;
+                const int col_t = C::WCOLS * half + 32 * h, col0 = nt * BN + col_t;
                 if (row0 >= p.M || col0 >= p.N) break;
                 if (whole && !p.direct_tma) {
                     if (row0 + lane < p.M)
@@ -305,39 +355,50 @@ __global__ void __launch_bounds__(THREADS, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == MMA_WARP) tmem_dealloc(tmem, TMEM_COLS);
+    if (warp == GEMM_MMA) tmem_dealloc(tmem, TMEM_COLS);
 }
 
 // C tiles that several CTAs have parts of: the parts added in order of K.
-// grid (tile, 8 row groups), 256 threads over 16 rows x BN columns
+// grid (tile, row group of 8), 256 threads, four columns each
 template <int BN>
 __global__ void __launch_bounds__(256) reduce_kernel(const float *__restrict__ slots, Params p, int ctas)
 {
+    __shared__ int s_slot[MAX_CTAS];
     const int tile = blockIdx.x, mt = tile / p.n_tiles, nt = tile - mt * p.n_tiles;
     const int64_t k0 = (int64_t)tile * p.nkb, k1 = k0 + p.nkb;
     const int64_t ub = p.blocks / p.gran;
     const int c0 = (int)(((k0 / p.gran + 1) * ctas - 1) / ub), c1 = (int)((((k1 - 1) / p.gran + 1) * ctas - 1) / ub);
-    if (c0 == c1) return;
-    const int rows = min(16, p.M - mt * TM - 16 * (int)blockIdx.y), cols = min(BN, p.N - nt * BN);
-    if (rows <= 0) return;
+    const int rows = min(8, p.M - mt * TM - 8 * (int)blockIdx.y), cols = min(BN, p.N - nt * BN), n = c1 - c0 + 1;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (n == 1 || rows <= 0) return;
+    for (int i = threadIdx.x; i < n; i += 256)
+        s_slot[i] = 2 * (c0 + i) + (run_begin(p.blocks, p.gran, ctas, c0 + i) >= k0 ? 0 : 1);
+    __syncthreads();
     const int tc = threadIdx.x % (BN / 4), tr = threadIdx.x / (BN / 4);
+    if (4 * tc >= cols) return;
     for (int r = tr; r < rows; r += 256 / (BN / 4)) {
-        if (4 * tc >= cols) continue;
+        const float *src = slots + (size_t)(8 * blockIdx.y + r) * SLOT_COLS + 4 * tc;
         float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        for (int c = c0; c <= c1; c++) {
-            const int slot = 2 * c + (run_begin(p.blocks, p.gran, ctas, c) >= k0 ? 0 : 1);
-            const float4 v = __ldcs(reinterpret_cast<const float4 *>(
-                slots + (size_t)slot * SLOT_FLOATS + (size_t)(16 * blockIdx.y + r) * SLOT_COLS + 4 * tc));
-            acc.x += v.x;
-            acc.y += v.y;
-            acc.z += v.z;
-            acc.w += v.w;
+        for (int c = 0; c < n; c += 8) {
+            float4 v[8];
+#pragma unroll
+            for (int u = 0; u < 8; u++)
+                v[u] = c + u < n ? __ldcs(reinterpret_cast<const float4 *>(src + (size_t)s_slot[c + u] * SLOT_FLOATS))
+                                 : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int u = 0; u < 8; u++) {
+                acc.x += v[u].x;
+                acc.y += v[u].y;
+                acc.z += v[u].z;
+                acc.w += v[u].w;
+            }
         }
-        float *o = p.c + (int64_t)(mt * TM + 16 * blockIdx.y + r) * p.N + nt * BN + 4 * tc;
-        const float v[4] = {acc.x, acc.y, acc.z, acc.w};
+        float *o = p.c + (int64_t)(mt * TM + 8 * blockIdx.y + r) * p.N + nt * BN + 4 * tc;
         if (p.direct_tma) {
             *reinterpret_cast<float4 *>(o) = acc;
         } else {
+            const float v[4] = {acc.x, acc.y, acc.z, acc.w};
             for (int i = 0; i < 4; i++)
                 if (4 * tc + i < cols) o[i] = v[i];
         }
@@ -349,6 +410,7 @@ __global__ void __launch_bounds__(256) reduce_kernel(const float *__restrict__ s
 __global__ void __launch_bounds__(256) split_kernel(const float *__restrict__ dl, int T, int E, int Ep,
                                                     uint16_t *__restrict__ parts)
 {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int per = Ep / 8;
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i >= (int64_t)T * per) return;
@@ -440,13 +502,32 @@ static bool map_mn_major(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap *m, 
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// a launch that may begin while the kernel before it on the stream ends (pdl:
+// that kernel is one of this file's, which lets it)
+template <typename... Args>
+static cudaError_t launch_chained(void (*kernel)(Args...), dim3 grid, int threads, size_t smem, bool pdl,
+                                  cudaStream_t st, Args... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 template <Mode MODE, int BN>
 static moe_status launch(const void *a, const void *b, float *c, int M, int N, int K, float *slots,
-                         int32_t *dev_status, cudaStream_t st)
+                         int32_t *dev_status, bool pdl, cudaStream_t st)
 {
     using C = Cfg<MODE, BN>;
     const Plan pl = plan(M, N, K, BN);
-    auto enc = encode_fn();
+    static const auto enc = encode_fn();      // the driver's encoder: looked up once
     if (!enc) return MOE_ERR_CUDA;
     CUtensorMap ma, mb, mc, ms;
     const bool ok_a = C::A_MN ? map_mn_major(enc, &ma, a, pad64(M), K, C::P, TM / 64, 4)
@@ -475,12 +556,16 @@ static moe_status launch(const void *a, const void *b, float *c, int M, int N, i
     if (!p.direct_tma) mc = ms;          // not used
     constexpr size_t smem = sizeof(Smem<MODE, BN>) + 1024;
     static_assert(smem <= 227 * 1024, "shared memory");
-    if (cudaFuncSetAttribute(gemm_kernel<MODE, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
+    static const cudaError_t attr =
+        cudaFuncSetAttribute(gemm_kernel<MODE, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (attr != cudaSuccess) return MOE_ERR_CUDA;
+    if (launch_chained(gemm_kernel<MODE, BN>, dim3(pl.ctas), GEMM_THREADS, smem, pdl, st, (const CUtensorMap)ma,
+                       (const CUtensorMap)mb, (const CUtensorMap)mc, (const CUtensorMap)ms, (const Params)p) !=
         cudaSuccess)
         return MOE_ERR_CUDA;
-    gemm_kernel<MODE, BN><<<pl.ctas, THREADS, smem, st>>>(ma, mb, mc, ms, p);
-    if (pl.slots)
-        reduce_kernel<BN><<<dim3((unsigned)(pl.m_tiles * pl.n_tiles), 8), 256, 0, st>>>(slots, p, pl.ctas);
+    if (pl.slots && launch_chained(reduce_kernel<BN>, dim3((unsigned)(pl.m_tiles * pl.n_tiles), TM / 8), 256, 0, true,
+                                   st, (const float *)slots, p, pl.ctas) != cudaSuccess)
+        return MOE_ERR_CUDA;
     return launch_status();
 }
 
@@ -500,9 +585,9 @@ moe_status router_logits(const uint16_t *x, const uint16_t *w, int T, int d, int
     using namespace rg;
     float *slots = (float *)ws;
     switch (logits_bn(E)) {
-    case 64: return launch<LOGITS, 64>(x, w, logits, T, E, d, slots, dev_status, st);
-    case 128: return launch<LOGITS, 128>(x, w, logits, T, E, d, slots, dev_status, st);
-    default: return launch<LOGITS, 256>(x, w, logits, T, E, d, slots, dev_status, st);
+    case 64: return launch<LOGITS, 64>(x, w, logits, T, E, d, slots, dev_status, false, st);
+    case 128: return launch<LOGITS, 128>(x, w, logits, T, E, d, slots, dev_status, false, st);
+    default: return launch<LOGITS, 256>(x, w, logits, T, E, d, slots, dev_status, false, st);
     }
 }
 
@@ -525,13 +610,13 @@ moe_status router_backward(const uint16_t *x, const uint16_t *w, const float *dl
     moe_status s = launch_status();
     if (s != MOE_OK) return s;
     if (dx) {
-        s = hidden_bn(d) == 256 ? launch<DX, 256>(parts, w, dx, T, d, E, slots, dev_status, st)
-                                : launch<DX, 128>(parts, w, dx, T, d, E, slots, dev_status, st);
+        s = hidden_bn(d) == 256 ? launch<DX, 256>(parts, w, dx, T, d, E, slots, dev_status, true, st)
+                                : launch<DX, 128>(parts, w, dx, T, d, E, slots, dev_status, true, st);
         if (s != MOE_OK) return s;
     }
     if (dw)
-        s = hidden_bn(d) == 256 ? launch<DW, 256>(parts, x, dw, E, d, T, slots, dev_status, st)
-                                : launch<DW, 128>(parts, x, dw, E, d, T, slots, dev_status, st);
+        s = hidden_bn(d) == 256 ? launch<DW, 256>(parts, x, dw, E, d, T, slots, dev_status, true, st)
+                                : launch<DW, 128>(parts, x, dw, E, d, T, slots, dev_status, true, st);
     return s;
 }
 

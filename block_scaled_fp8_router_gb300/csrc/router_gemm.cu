@@ -43,20 +43,24 @@ constexpr size_t SLOT_FLOATS = (size_t)TM * SLOT_COLS;
 
 enum Mode { LOGITS, DX, DW };
 
-template <Mode MODE, int BN>
+// CL = 2: a pair of CTAs takes two row tiles of one column tile.  Each loads its
+// own A tile and half of the B tile; one thread of the first CTA issues MMAs of
+// 256 rows over both SMs (cta_group::2), each accumulating its 128 rows.
+template <Mode MODE, int BN, int CL>
 struct Cfg {
     static constexpr int P = MODE == LOGITS ? 1 : 3;              // parts of A
     static constexpr bool A_MN = MODE == DW, B_MN = MODE != LOGITS;
-    static constexpr int B_TILE = BN * KB * 2;
-    static constexpr int NB = BN == 256 ? (P == 3 ? 3 : 4) : BN == 128 ? (P == 3 ? 4 : 6) : 8;   // B tiles
-    static constexpr int NA = P == 3 ? (BN == 256 ? 6 : 8) : (BN == 256 ? 4 : BN == 128 ? 6 : 8); // A tiles
+    static constexpr int B_TILE = BN / CL * KB * 2;               // this CTA's share
+    // places of the rings, 192 KB in all at most: a block needs one B and P A tiles
+    static constexpr int NB = B_TILE == 32768 ? (P == 3 ? 3 : 4) : B_TILE == 16384 ? (P == 3 ? 4 : 6) : 8;
+    static constexpr int NA = P == 3 ? (B_TILE == 32768 ? 6 : 8) : (B_TILE == 32768 ? 4 : B_TILE == 16384 ? 6 : 8);
     static constexpr int BUFS = BN == 256 ? 2 : 4;                // accumulators in tensor memory
     static constexpr int WCOLS = BN / 2;                          // columns of one epilogue warp
 };
 
-template <Mode MODE, int BN>
+template <Mode MODE, int BN, int CL>
 struct Smem {
-    using C = Cfg<MODE, BN>;
+    using C = Cfg<MODE, BN, CL>;
     uint8_t a[C::NA][A_TILE];
     uint8_t b[C::NB][C::B_TILE];
     float stage[GEMM_EPI][32 * 32];       // a warp's 32 x 32 sub-tile for its TMA store
@@ -79,7 +83,7 @@ struct Params {
     int32_t *dev_status;
 };
 
-// first K block of CTA c's run
+// first K block of run c (a CTA's, or a cluster's)
 __host__ __device__ __forceinline__ int64_t run_begin(int64_t blocks, int gran, int ctas, int64_t c)
 {
     return c * (blocks / gran) / ctas * gran;
@@ -99,6 +103,69 @@ __device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *tm, in
                  "%3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
                  "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
                  : "memory");
+}
+
+// ---- the pair's forms (cta_group::2) ----
+// loads to this CTA that complete at a barrier of the pair's first CTA (bar:
+// its shared::cluster address)
+__device__ __forceinline__ void tma_load_2d_pair(void *dst, const CUtensorMap *tm, int x, int y, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], "
+                 "[%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+                 "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ void tma_load_3d_pair(void *dst, const CUtensorMap *tm, int x, int y, int z, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], "
+                 "[%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+                 "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(z), "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ void tma_load_4d_pair(void *dst, const CUtensorMap *tm, int x, int y, int z, int w,
+                                                 uint32_t bar)
+{
+    asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], "
+                 "[%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
+                 "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t *dst, uint32_t ncols)
+{
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "r"(ncols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols)
+{
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+__device__ __forceinline__ void mma_bf16_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                              uint32_t accumulate)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+                 "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+                 : "memory");
+}
+// arrive at the barrier at this place in both CTAs when the MMAs so far are done
+__device__ __forceinline__ void mma_commit_pair(uint64_t *bar)
+{
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                     smem_u32(bar)),
+                 "h"((uint16_t)3)
+                 : "memory");
+}
+// this barrier's address in the pair's first CTA
+__device__ __forceinline__ uint32_t first_cta(const uint64_t *bar)
+{
+    uint32_t out;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(out) : "r"(smem_u32(bar)));
+    return out;
+}
+__device__ __forceinline__ void arrive_remote(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap *tm, const void *src, int x, int y)
@@ -141,8 +208,8 @@ constexpr uint32_t idesc_bf16(int M, int N, bool a_mn, bool b_mn)
            ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-// wait until the phase that block n's use of a ring of `size` fills (or frees)
-// is complete; each wait is bounded
+// waits (each bounded) until the last of the n uses of each place of a ring is
+// complete at its barrier
 __device__ __forceinline__ void drain(uint64_t *full, int size, uint32_t n)
 {
     for (int i = 0; i < size && (uint32_t)i < n; i++) {
@@ -152,15 +219,16 @@ __device__ __forceinline__ void drain(uint64_t *full, int size, uint32_t n)
     }
 }
 
-template <Mode MODE, int BN>
+template <Mode MODE, int BN, int CL>
 __global__ void __launch_bounds__(GEMM_THREADS, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                 const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ CUtensorMap tm_slots, const Params p)
 {
-    using C = Cfg<MODE, BN>;
+    using C = Cfg<MODE, BN, CL>;
     extern __shared__ uint8_t smem_raw[];
-    Smem<MODE, BN> &s =
-        *reinterpret_cast<Smem<MODE, BN> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    Smem<MODE, BN, CL> &s =
+        *reinterpret_cast<Smem<MODE, BN, CL> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int rank = CL > 1 ? (int)(blockIdx.x % CL) : 0;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::NA; i++) {
@@ -173,16 +241,22 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
         }
         for (int i = 0; i < C::BUFS; i++) {
             mbar_init(&s.tfull[i], 1);
-            mbar_init(&s.tempty[i], GEMM_EPI);
+            mbar_init(&s.tempty[i], CL * GEMM_EPI);
         }
         mbar_init(&s.mma_done, 1);
         s.abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
-    if (warp == GEMM_MMA) tmem_alloc(&s.tmem_base, TMEM_COLS);
+    if (warp == GEMM_MMA) {
+        if (CL > 1) tmem_alloc_pair(&s.tmem_base, TMEM_COLS);
+        else tmem_alloc(&s.tmem_base, TMEM_COLS);
+    }
     tc_fence_before();
     __syncthreads();
+    __syncwarp();
+    if (CL > 1)      // both CTAs barriers are set up
+        asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
     tc_fence_after();
     // everything before this overlaps the kernel before; nothing it wrote is
     // read, and nothing written, before it has ended
@@ -190,8 +264,8 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const uint32_t tmem = s.tmem_base;
     volatile int *abort_flag = &s.abort_flag;
-    const int64_t b0 = run_begin(p.blocks, p.gran, gridDim.x, blockIdx.x);
-    const int64_t b1 = run_begin(p.blocks, p.gran, gridDim.x, blockIdx.x + 1);
+    const int64_t b0 = run_begin(p.blocks, p.gran, gridDim.x / CL, blockIdx.x / CL);
+    const int64_t b1 = run_begin(p.blocks, p.gran, gridDim.x / CL, blockIdx.x / CL + 1);
 
     if (warp == GEMM_PRODUCER) {
         if (lane == 0) {
@@ -199,14 +273,20 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
             bool ok = true;
             int tile = (int)(b0 / p.nkb), kb = (int)(b0 - (int64_t)tile * p.nkb);
             int mt = tile / p.n_tiles, nt = tile - mt * p.n_tiles;
+            mt = mt * CL + rank;
             for (int64_t b = b0; ok && b < b1; b++) {
                 const int sb = jb % C::NB;
                 if (!wait_or_abort(&s.bempty[sb], ((jb / C::NB) & 1) ^ 1, abort_flag, p.dev_status)) break;
-                mbar_arrive_expect_tx(&s.bfull[sb], C::B_TILE);
-                if (C::B_MN)
-                    tma_load_3d(s.b[sb], &tm_b, 0, kb * KB, nt * (BN / 64), &s.bfull[sb]);
-                else
-                    tma_load_2d(s.b[sb], &tm_b, kb * KB * 2, nt * BN, &s.bfull[sb]);
+                if (rank == 0) mbar_arrive_expect_tx(&s.bfull[sb], CL * C::B_TILE);
+                const int bt = nt * CL + rank;           // this CTA's share of the column tile
+                if (CL > 1) {
+                    const uint32_t bar = first_cta(&s.bfull[sb]);
+                    if (C::B_MN) tma_load_3d_pair(s.b[sb], &tm_b, 0, kb * KB, bt * (BN / CL / 64), bar);
+                    else tma_load_2d_pair(s.b[sb], &tm_b, kb * KB * 2, bt * (BN / CL), bar);
+                } else {
+                    if (C::B_MN) tma_load_3d(s.b[sb], &tm_b, 0, kb * KB, bt * (BN / 64), &s.bfull[sb]);
+                    else tma_load_2d(s.b[sb], &tm_b, kb * KB * 2, bt * BN, &s.bfull[sb]);
+                }
                 jb++;
 #pragma unroll
                 for (int q = C::P - 1; q >= 0; q--) {
@@ -215,28 +295,45 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
                         ok = false;
                         break;
                     }
-                    mbar_arrive_expect_tx(&s.afull[sa], A_TILE);
-                    if (C::A_MN)
-                        tma_load_4d(s.a[sa], &tm_a, 0, kb * KB, mt * (TM / 64), q, &s.afull[sa]);
-                    else
-                        tma_load_3d(s.a[sa], &tm_a, kb * KB * 2, mt * TM, q, &s.afull[sa]);
+                    if (rank == 0) mbar_arrive_expect_tx(&s.afull[sa], CL * A_TILE);
+                    if (CL > 1) {
+                        const uint32_t bar = first_cta(&s.afull[sa]);
+                        if (C::A_MN) tma_load_4d_pair(s.a[sa], &tm_a, 0, kb * KB, mt * (TM / 64), q, bar);
+                        else tma_load_3d_pair(s.a[sa], &tm_a, kb * KB * 2, mt * TM, q, bar);
+                    } else {
+                        if (C::A_MN) tma_load_4d(s.a[sa], &tm_a, 0, kb * KB, mt * (TM / 64), q, &s.afull[sa]);
+                        else tma_load_3d(s.a[sa], &tm_a, kb * KB * 2, mt * TM, q, &s.afull[sa]);
+                    }
                     ja++;
                 }
                 if (++kb == p.nkb) {
                     kb = 0;
                     if (++nt == p.n_tiles) {
                         nt = 0;
-                        mt++;
+                        mt += CL;
                     }
                 }
             }
-            // no copy may still be in flight when the CTA exits
-            drain(s.afull, C::NA, ja);
-            drain(s.bfull, C::NB, jb);
+            // no copy may still be in flight when the CTA exits (the pair's
+            // copies all complete at the first CTA's barriers)
+            if (rank == 0) {
+                drain(s.afull, C::NA, ja);
+                drain(s.bfull, C::NB, jb);
+            }
+            // nor an arrival at this CTA's barriers from the other
+            if (CL > 1 && !*abort_flag) {
+                drain(s.aempty, C::NA, ja);
+                drain(s.bempty, C::NB, jb);
+            }
         }
+        __syncwarp();
     } else if (warp == GEMM_MMA) {
-        if (lane == 0) {
-            constexpr uint32_t IDESC = idesc_bf16(TM, BN, C::A_MN, C::B_MN);
+        if (lane == 0 && rank == 0) {
+            constexpr uint32_t IDESC = idesc_bf16(CL * TM, BN, C::A_MN, C::B_MN);
+            auto commit = [](uint64_t *bar) {
+                if (CL > 1) mma_commit_pair(bar);
+                else mma_commit(bar);
+            };
             constexpr int A_STEP = C::A_MN ? 2048 >> 4 : 32 >> 4, B_STEP = C::B_MN ? 2048 >> 4 : 32 >> 4;
             uint32_t ja = 0, jb = 0, jc = 0;
             int in_chunk = 0, kb = (int)(b0 % p.nkb);
@@ -260,26 +357,33 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
                     const uint32_t aaddr = smem_u32(s.a[sa]);
                     const uint64_t adesc = C::A_MN ? sw128_desc_mn(aaddr) : sw128_desc(aaddr);
 #pragma unroll
-                    for (int ks = 0; ks < KB / 16; ks++)
-                        mma_bf16(tmem + buf * BN, adesc + A_STEP * ks, bdesc + B_STEP * ks, IDESC,
-                                 in_chunk > 0 || q < C::P - 1 || ks > 0);
-                    mma_commit(&s.aempty[sa]);
+                    for (int ks = 0; ks < KB / 16; ks++) {
+                        const uint32_t add = in_chunk > 0 || q < C::P - 1 || ks > 0;
+                        if (CL > 1)
+                            mma_bf16_pair(tmem + buf * BN, adesc + A_STEP * ks, bdesc + B_STEP * ks, IDESC, add);
+                        else
+                            mma_bf16(tmem + buf * BN, adesc + A_STEP * ks, bdesc + B_STEP * ks, IDESC, add);
+                    }
+                    commit(&s.aempty[sa]);
                     ja++;
                 }
                 if (!ok) break;
-                mma_commit(&s.bempty[sb]);
+                commit(&s.bempty[sb]);
                 jb++;
                 in_chunk++;
                 if (++kb == p.nkb) kb = 0;
                 if (in_chunk == CHUNK || kb == 0 || b + 1 == b1) {
-                    mma_commit(&s.tfull[buf]);
+                    commit(&s.tfull[buf]);
                     jc++;
                     in_chunk = 0;
                 }
             }
-            mma_commit(&s.mma_done);
+            commit(&s.mma_done);
+        }
+        // (the second CTA too: the arrival at its barrier has then come)
+        if (lane == 0) {
             const uint64_t t0 = globaltimer_ns();
-            while (!mbar_try_wait(&s.mma_done, 0) && globaltimer_ns() - t0 < TIMEOUT_NS) {}
+            while (!mbar_try_wait(&s.mma_done, 0) && globaltimer_ns() - t0 < 4 * TIMEOUT_NS) {}
         }
         __syncwarp();
     } else {
@@ -291,7 +395,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
         bool aborted = false;
         for (int64_t b = b0; b < b1 && !aborted;) {
             const int tile = (int)(b / p.nkb), kb0 = (int)(b - (int64_t)tile * p.nkb);
-            const int mt = tile / p.n_tiles, nt = tile - mt * p.n_tiles;
+            const int mp = tile / p.n_tiles, nt = tile - mp * p.n_tiles, mt = mp * CL + rank;
             const int64_t left = b1 - b;
             const int n = (int)(left < p.nkb - kb0 ? left : p.nkb - kb0);   // K blocks of this tile here
             float acc[C::WCOLS];
@@ -313,7 +417,10 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&s.tempty[buf]);
+                if (lane == 0) {
+                    if (CL > 1) arrive_remote(first_cta(&s.tempty[buf]));
+                    else mbar_arrive(&s.tempty[buf]);
+                }
             }
             if (aborted) break;
             const bool whole = n == p.nkb;
@@ -355,16 +462,24 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == GEMM_MMA) tmem_dealloc(tmem, TMEM_COLS);
+    __syncwarp();
+    if (CL > 1)      // no CTA leaves while the other may still use its memory or barriers
+        asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (warp == GEMM_MMA) {
+        if (CL > 1) tmem_dealloc_pair(tmem, TMEM_COLS);
+        else tmem_dealloc(tmem, TMEM_COLS);
+    }
 }
 
 // C tiles that several CTAs have parts of: the parts added in order of K.
 // grid (tile, row group of 8), 256 threads, four columns each
 template <int BN>
-__global__ void __launch_bounds__(256) reduce_kernel(const float *__restrict__ slots, Params p, int ctas)
+__global__ void __launch_bounds__(256) reduce_kernel(const float *__restrict__ slots, Params p, int ctas, int cl)
 {
     __shared__ int s_slot[MAX_CTAS];
-    const int tile = blockIdx.x, mt = tile / p.n_tiles, nt = tile - mt * p.n_tiles;
+    // ctas: runs; cl CTAs each, for the row tiles mp cl .. mp cl + cl - 1
+    const int tile = blockIdx.x / cl, mp = tile / p.n_tiles, nt = tile - mp * p.n_tiles;
+    const int rank = blockIdx.x % cl, mt = mp * cl + rank;
     const int64_t k0 = (int64_t)tile * p.nkb, k1 = k0 + p.nkb;
     const int64_t ub = p.blocks / p.gran;
     const int c0 = (int)(((k0 / p.gran + 1) * ctas - 1) / ub), c1 = (int)((((k1 - 1) / p.gran + 1) * ctas - 1) / ub);
@@ -373,7 +488,7 @@ __global__ void __launch_bounds__(256) reduce_kernel(const float *__restrict__ s
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (n == 1 || rows <= 0) return;
     for (int i = threadIdx.x; i < n; i += 256)
-        s_slot[i] = 2 * (c0 + i) + (run_begin(p.blocks, p.gran, ctas, c0 + i) >= k0 ? 0 : 1);
+        s_slot[i] = 2 * ((c0 + i) * cl + rank) + (run_begin(p.blocks, p.gran, ctas, c0 + i) >= k0 ? 0 : 1);
     __syncthreads();
     const int tc = threadIdx.x % (BN / 4), tr = threadIdx.x / (BN / 4);
     if (4 * tc >= cols) return;
@@ -446,7 +561,7 @@ __global__ void __launch_bounds__(256) split_kernel(const float *__restrict__ dl
 static inline int pad64(int v) { return (v + 63) / 64 * 64; }
 
 struct Plan {
-    int ctas, gran, m_tiles, n_tiles, nkb;
+    int cl, runs, gran, m_tiles, n_tiles, nkb;     // m_tiles: groups of cl row tiles
     int64_t blocks;
     bool slots;          // some tile is cut
 };
@@ -454,23 +569,27 @@ struct Plan {
 static Plan plan(int M, int N, int K, int bn)
 {
     Plan r;
-    r.m_tiles = (M + TM - 1) / TM;
+    const int rows = (M + TM - 1) / TM;
+    // pairs of row tiles where few are wasted
+    r.cl = bn >= 128 && rows > 1 && (rows % 2 == 0 || rows >= 7) ? 2 : 1;
+    r.m_tiles = (rows + r.cl - 1) / r.cl;
     r.n_tiles = (N + bn - 1) / bn;
     r.nkb = (K + KB - 1) / KB;
     const int64_t tiles = (int64_t)r.m_tiles * r.n_tiles;
     r.blocks = tiles * r.nkb;
     int sms = sm_count();
     if (sms > MAX_CTAS) sms = MAX_CTAS;
-    // whole tiles where every CTA has four or more (the last ones then cost a
-    // quarter at most), else cut tiles, CHUNK blocks a CTA at the least
-    r.gran = tiles >= 4 * sms || r.nkb == 1 ? r.nkb : 1;
+    const int most = sms / r.cl > 0 ? sms / r.cl : 1;
+    // whole tiles where every run has four or more (the last ones then cost a
+    // quarter at most), else cut tiles, CHUNK blocks a run at the least
+    r.gran = tiles >= 4 * most || r.nkb == 1 ? r.nkb : 1;
     const int64_t units = r.gran == 1 && r.nkb > 1 ? (r.blocks + CHUNK - 1) / CHUNK : tiles;
-    r.ctas = (int)(units < sms ? units : sms);
+    r.runs = (int)(units < most ? units : most);
     r.slots = r.gran != r.nkb;
     return r;
 }
 
-static size_t slots_bytes(const Plan &r) { return r.slots ? (size_t)r.ctas * 2 * SLOT_FLOATS * sizeof(float) : 0; }
+static size_t slots_bytes(const Plan &r) { return r.slots ? (size_t)r.runs * r.cl * 2 * SLOT_FLOATS * sizeof(float) : 0; }
 
 static int logits_bn(int E) { return E <= 64 ? 64 : E <= 128 ? 128 : 256; }
 static int hidden_bn(int d) { return d % 256 == 0 ? 256 : 128; }
@@ -505,35 +624,38 @@ static bool map_mn_major(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap *m, 
 // a launch that may begin while the kernel before it on the stream ends (pdl:
 // that kernel is one of this file's, which lets it)
 template <typename... Args>
-static cudaError_t launch_chained(void (*kernel)(Args...), dim3 grid, int threads, size_t smem, bool pdl,
+static cudaError_t launch_chained(void (*kernel)(Args...), dim3 grid, int cluster, int threads, size_t smem, bool pdl,
                                   cudaStream_t st, Args... args)
 {
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cluster;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cfg.attrs = attr;
-    cfg.numAttrs = pdl ? 1 : 0;
+    cfg.numAttrs = pdl ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-template <Mode MODE, int BN>
-static moe_status launch(const void *a, const void *b, float *c, int M, int N, int K, float *slots,
-                         int32_t *dev_status, bool pdl, cudaStream_t st)
+template <Mode MODE, int BN, int CL>
+static moe_status launch_cl(const Plan &pl, const void *a, const void *b, float *c, int M, int N, int K, float *slots,
+                            int32_t *dev_status, bool pdl, cudaStream_t st)
 {
-    using C = Cfg<MODE, BN>;
-    const Plan pl = plan(M, N, K, BN);
+    using C = Cfg<MODE, BN, CL>;
     static const auto enc = encode_fn();      // the driver's encoder: looked up once
     if (!enc) return MOE_ERR_CUDA;
     CUtensorMap ma, mb, mc, ms;
     const bool ok_a = C::A_MN ? map_mn_major(enc, &ma, a, pad64(M), K, C::P, TM / 64, 4)
                               : map_k_major(enc, &ma, a, MODE == DX ? pad64(K) : K, M, C::P, TM);
-    const bool ok_b = C::B_MN ? map_mn_major(enc, &mb, b, N, K, 1, BN / 64, 3)
-                              : make_map(enc, &mb, b, (uint64_t)K * 2, N, BN);
+    const bool ok_b = C::B_MN ? map_mn_major(enc, &mb, b, N, K, 1, BN / 64 / CL, 3)
+                              : make_map(enc, &mb, b, (uint64_t)K * 2, N, BN / CL);
     if (!ok_a || !ok_b) return MOE_ERR_CUDA;
     Params p;
     p.M = M;
@@ -548,25 +670,37 @@ static moe_status launch(const void *a, const void *b, float *c, int M, int N, i
     if (p.direct_tma) {
         if (!make_map_f32_store(enc, &mc, c, (uint64_t)N, (uint64_t)M)) return MOE_ERR_CUDA;
     }
+    const int ctas = pl.runs * CL;
     if (pl.slots) {
-        if (!make_map_f32_store(enc, &ms, slots, SLOT_COLS, (uint64_t)pl.ctas * 2 * TM)) return MOE_ERR_CUDA;
+        if (!make_map_f32_store(enc, &ms, slots, SLOT_COLS, (uint64_t)ctas * 2 * TM)) return MOE_ERR_CUDA;
     } else {
         ms = p.direct_tma ? mc : ma;     // not used
     }
     if (!p.direct_tma) mc = ms;          // not used
-    constexpr size_t smem = sizeof(Smem<MODE, BN>) + 1024;
+    constexpr size_t smem = sizeof(Smem<MODE, BN, CL>) + 1024;
     static_assert(smem <= 227 * 1024, "shared memory");
     static const cudaError_t attr =
-        cudaFuncSetAttribute(gemm_kernel<MODE, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        cudaFuncSetAttribute(gemm_kernel<MODE, BN, CL>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (attr != cudaSuccess) return MOE_ERR_CUDA;
-    if (launch_chained(gemm_kernel<MODE, BN>, dim3(pl.ctas), GEMM_THREADS, smem, pdl, st, (const CUtensorMap)ma,
+    if (launch_chained(gemm_kernel<MODE, BN, CL>, dim3(ctas), CL, GEMM_THREADS, smem, pdl, st, (const CUtensorMap)ma,
                        (const CUtensorMap)mb, (const CUtensorMap)mc, (const CUtensorMap)ms, (const Params)p) !=
         cudaSuccess)
         return MOE_ERR_CUDA;
-    if (pl.slots && launch_chained(reduce_kernel<BN>, dim3((unsigned)(pl.m_tiles * pl.n_tiles), TM / 8), 256, 0, true,
-                                   st, (const float *)slots, p, pl.ctas) != cudaSuccess)
+    if (pl.slots && launch_chained(reduce_kernel<BN>, dim3((unsigned)(pl.m_tiles * pl.n_tiles * CL), TM / 8), 1, 256, 0,
+                                   true, st, (const float *)slots, p, pl.runs, CL) != cudaSuccess)
         return MOE_ERR_CUDA;
     return launch_status();
+}
+
+template <Mode MODE, int BN>
+static moe_status launch(const void *a, const void *b, float *c, int M, int N, int K, float *slots,
+                         int32_t *dev_status, bool pdl, cudaStream_t st)
+{
+    const Plan pl = plan(M, N, K, BN);
+    if constexpr (BN >= 128) {
+        if (pl.cl == 2) return launch_cl<MODE, BN, 2>(pl, a, b, c, M, N, K, slots, dev_status, pdl, st);
+    }
+    return launch_cl<MODE, BN, 1>(pl, a, b, c, M, N, K, slots, dev_status, pdl, st);
 }
 
 static size_t align_up(size_t v) { return (v + 255) & ~(size_t)255; }

@@ -78,6 +78,7 @@ struct Params {
     int n_tiles;              // tiles along N
     int64_t blocks;           // K blocks in all
     int gran;                 // cuts fall on multiples of this many blocks
+    int split;                // CTAs that share a tile's K blocks
     float *c;                 // [M, N]
     int direct_tma;           // whole tiles may be stored through tm_c
     int32_t *dev_status;
@@ -219,7 +220,9 @@ __device__ __forceinline__ void drain(uint64_t *full, int size, uint32_t n)
     }
 }
 
-template <Mode MODE, int BN, int CL>
+// SPLIT: a cluster of p.split CTAs per tile, each a share of its K blocks; the
+// partial tiles meet in shared memory (CL = 1)
+template <Mode MODE, int BN, int CL, bool SPLIT>
 __global__ void __launch_bounds__(GEMM_THREADS, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                 const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ CUtensorMap tm_slots, const Params p)
@@ -228,6 +231,8 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
     extern __shared__ uint8_t smem_raw[];
     Smem<MODE, BN, CL> &s =
         *reinterpret_cast<Smem<MODE, BN, CL> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    static_assert(CL == 1 || !SPLIT, "one or the other");
+    static_assert(sizeof(s.a) + sizeof(s.b) >= (size_t)TM * BN * 4, "a partial tile fits the rings");
     const int rank = CL > 1 ? (int)(blockIdx.x % CL) : 0;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -264,8 +269,16 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const uint32_t tmem = s.tmem_base;
     volatile int *abort_flag = &s.abort_flag;
-    const int64_t b0 = run_begin(p.blocks, p.gran, gridDim.x / CL, blockIdx.x / CL);
-    const int64_t b1 = run_begin(p.blocks, p.gran, gridDim.x / CL, blockIdx.x / CL + 1);
+    int64_t b0, b1;
+    const int share = SPLIT ? (int)(blockIdx.x % (unsigned)p.split) : 0;
+    if (SPLIT) {
+        const int64_t t0 = (int64_t)(blockIdx.x / (unsigned)p.split) * p.nkb;
+        b0 = t0 + (int64_t)p.nkb * share / p.split;
+        b1 = t0 + (int64_t)p.nkb * (share + 1) / p.split;
+    } else {
+        b0 = run_begin(p.blocks, p.gran, gridDim.x / CL, blockIdx.x / CL);
+        b1 = run_begin(p.blocks, p.gran, gridDim.x / CL, blockIdx.x / CL + 1);
+    }
 
     if (warp == GEMM_PRODUCER) {
         if (lane == 0) {
@@ -423,6 +436,16 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
                 }
             }
             if (aborted) break;
+            if (SPLIT) {
+                // this CTA's partial tile over the rings, which nothing uses any
+                // more: row r's 16-byte chunk c at chunk c ^ (r & 15)
+                float4 *part = reinterpret_cast<float4 *>(s.a) + (32 * q + lane) * (BN / 4);
+#pragma unroll
+                for (int i = 0; i < C::WCOLS / 4; i++)
+                    part[(C::WCOLS / 4 * half + i) ^ (lane & 15)] =
+                        make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
+                break;
+            }
             const bool whole = n == p.nkb;
             const int row0 = mt * TM + 32 * q;
             const bool slot0 = b == b0;
@@ -463,7 +486,48 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
     __syncthreads();
     tc_fence_after();
     __syncwarp();
-    if (CL > 1)      // no CTA leaves while the other may still use its memory or barriers
+    if constexpr (SPLIT) {
+        // every CTA's partial tile is there: each adds up a share of the rows,
+        // the partial tiles in order of K
+        asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+        const int tile = (int)(blockIdx.x / (unsigned)p.split), mt = tile / p.n_tiles, nt = tile - mt * p.n_tiles;
+        const int r0 = TM * share / p.split, r1 = min(TM * (share + 1) / p.split, p.M - mt * TM);
+        const uint32_t base = smem_u32(s.a);
+        for (int i = r0 * (BN / 4) + threadIdx.x; i < r1 * (BN / 4) && !*abort_flag; i += GEMM_THREADS) {
+            const int r = i / (BN / 4), c = i % (BN / 4), col = nt * BN + 4 * c;
+            if (col >= p.N) continue;
+            const uint32_t at = base + (uint32_t)(r * (BN / 4) + (c ^ (r & 15))) * 16;
+            float4 v[8];
+#pragma unroll
+            for (int u = 0; u < 8; u++) {
+                v[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (u < p.split) {
+                    uint32_t a;
+                    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(at), "r"(u));
+                    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                                 : "=f"(v[u].x), "=f"(v[u].y), "=f"(v[u].z), "=f"(v[u].w)
+                                 : "r"(a));
+                }
+            }
+#pragma unroll
+            for (int u = 1; u < 8; u++) {
+                v[0].x += v[u].x;
+                v[0].y += v[u].y;
+                v[0].z += v[u].z;
+                v[0].w += v[u].w;
+            }
+            float *o = p.c + (int64_t)(mt * TM + r) * p.N + col;
+            if (p.direct_tma) {
+                *reinterpret_cast<float4 *>(o) = v[0];
+            } else {
+                const float x[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+                for (int u = 0; u < 4; u++)
+                    if (col + u < p.N) o[u] = x[u];
+            }
+        }
+        __syncwarp();
+    }
+    if (CL > 1 || SPLIT)      // no CTA leaves while another may still use its memory or barriers
         asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
     if (warp == GEMM_MMA) {
         if (CL > 1) tmem_dealloc_pair(tmem, TMEM_COLS);
@@ -560,32 +624,89 @@ __global__ void __launch_bounds__(256) split_kernel(const float *__restrict__ dl
 
 static inline int pad64(int v) { return (v + 63) / 64 * 64; }
 
+// clusters of 2, 4 or 8 of these CTAs (one fills an SM) that the device holds
+// at once: SMs come in groups of uneven size, so fewer than SMs / size
+static int clusters_at_once(int size)
+{
+    static const struct Held {
+        int n[4];
+        Held()
+        {
+            constexpr size_t smem = sizeof(Smem<LOGITS, 256, 1>) + 1024;
+            auto *kernel = gemm_kernel<LOGITS, 256, 1, true>;
+            const bool ok =
+                cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) == cudaSuccess;
+            for (int i = 1; i < 4; i++) {
+                cudaLaunchConfig_t cfg = {};
+                cudaLaunchAttribute attr[1];
+                attr[0].id = cudaLaunchAttributeClusterDimension;
+                attr[0].val.clusterDim.x = 1 << i;
+                attr[0].val.clusterDim.y = 1;
+                attr[0].val.clusterDim.z = 1;
+                cfg.gridDim = dim3(1 << i);
+                cfg.blockDim = dim3(GEMM_THREADS);
+                cfg.dynamicSmemBytes = smem;
+                cfg.attrs = attr;
+                cfg.numAttrs = 1;
+                if (!ok || cudaOccupancyMaxActiveClusters(&n[i], kernel, &cfg) != cudaSuccess || n[i] < 1) n[i] = 1;
+            }
+            cudaGetLastError();
+        }
+    } held;
+    return held.n[size == 2 ? 1 : size == 4 ? 2 : 3];
+}
+
+// How the work is cut, by an estimate in clocks.  A K block takes parts x 2 BN
+// clocks on the tensor cores, or 700 where a CTA's share of HBM is slower (one
+// part: the A tile's 16 KB).  Whole tiles; or a cluster of 2, 4 or 8 CTAs per
+// tile (about 4000 clocks for the exchange; 8192 x 7168 x 256 logits 40 us
+// against 44 cut into runs); or all blocks cut into equal runs (about 16000
+// for the slots and their reduction: only long sums, weight gradients of
+// thousands of tokens, win by it: 65 us against 79 at 8192 x 7168 x 256).
 struct Plan {
-    int cl, runs, gran, m_tiles, n_tiles, nkb;     // m_tiles: groups of cl row tiles
+    int cl, split, runs, gran, m_tiles, n_tiles, nkb;     // m_tiles: groups of cl row tiles
     int64_t blocks;
-    bool slots;          // some tile is cut
+    bool slots;          // some tile is cut into runs
 };
 
-static Plan plan(int M, int N, int K, int bn)
+static Plan plan(int M, int N, int K, int bn, int parts)
 {
     Plan r;
     const int rows = (M + TM - 1) / TM;
-    // pairs of row tiles where few are wasted
-    r.cl = bn >= 128 && rows > 1 && (rows % 2 == 0 || rows >= 7) ? 2 : 1;
-    r.m_tiles = (rows + r.cl - 1) / r.cl;
     r.n_tiles = (N + bn - 1) / bn;
     r.nkb = (K + KB - 1) / KB;
-    const int64_t tiles = (int64_t)r.m_tiles * r.n_tiles;
-    r.blocks = tiles * r.nkb;
     int sms = sm_count();
     if (sms > MAX_CTAS) sms = MAX_CTAS;
+    const int64_t t = 2 * bn * parts > 700 ? 2 * bn * parts : 700;
+    const int64_t tiles1 = (int64_t)rows * r.n_tiles;
+    int64_t best = (tiles1 + sms - 1) / sms * r.nkb * t;
+    int kind = 1;                                          // whole tiles
+    for (int s = 2; s <= 8 && s <= r.nkb; s *= 2) {
+        const int64_t cap = clusters_at_once(s);
+        const int64_t e = (tiles1 + cap - 1) / cap * ((r.nkb + s - 1) / s * t + 4000);
+        if (e < best) {
+            best = e;
+            kind = s;
+        }
+    }
+    const int64_t cut = tiles1 * r.nkb * t / sms + 16000;
+    if (cut < best && r.nkb > 1) {
+        best = cut;
+        kind = 0;
+    }
+    r.split = kind > 1 ? kind : 1;
+    // pairs of row tiles (two-SM MMAs) for long work where few tiles are
+    // wasted: 8192 x 7168 x 256 backward 125 us against 129, but dx of 5000 x
+    // 4096 x 128 29 us against 25
+    r.cl = kind <= 1 && best > 50000 && bn >= 128 && rows > 1 && (rows % 2 == 0 || rows >= 7) ? 2 : 1;
+    r.m_tiles = (rows + r.cl - 1) / r.cl;
+    const int64_t tiles = (int64_t)r.m_tiles * r.n_tiles;
     const int most = sms / r.cl > 0 ? sms / r.cl : 1;
-    // whole tiles where every run has four or more (the last ones then cost a
-    // quarter at most), else cut tiles, CHUNK blocks a run at the least
-    r.gran = tiles >= 4 * most || r.nkb == 1 ? r.nkb : 1;
-    const int64_t units = r.gran == 1 && r.nkb > 1 ? (r.blocks + CHUNK - 1) / CHUNK : tiles;
-    r.runs = (int)(units < most ? units : most);
-    r.slots = r.gran != r.nkb;
+    r.blocks = tiles * r.nkb;
+    r.gran = kind == 0 ? 1 : r.nkb;
+    const int64_t units = kind == 0 ? (r.blocks + CHUNK - 1) / CHUNK : tiles;
+    r.runs = kind > 1 ? (int)(tiles * kind) : (int)(units < most ? units : most);
+    r.slots = kind == 0;
     return r;
 }
 
@@ -644,7 +765,7 @@ static cudaError_t launch_chained(void (*kernel)(Args...), dim3 grid, int cluste
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-template <Mode MODE, int BN, int CL>
+template <Mode MODE, int BN, int CL, bool SPLIT>
 static moe_status launch_cl(const Plan &pl, const void *a, const void *b, float *c, int M, int N, int K, float *slots,
                             int32_t *dev_status, bool pdl, cudaStream_t st)
 {
@@ -664,6 +785,7 @@ static moe_status launch_cl(const Plan &pl, const void *a, const void *b, float 
     p.n_tiles = pl.n_tiles;
     p.blocks = pl.blocks;
     p.gran = pl.gran;
+    p.split = pl.split;
     p.c = c;
     p.direct_tma = N % 4 == 0 && aligned16(c);
     p.dev_status = dev_status;
@@ -680,9 +802,9 @@ static moe_status launch_cl(const Plan &pl, const void *a, const void *b, float 
     constexpr size_t smem = sizeof(Smem<MODE, BN, CL>) + 1024;
     static_assert(smem <= 227 * 1024, "shared memory");
     static const cudaError_t attr =
-        cudaFuncSetAttribute(gemm_kernel<MODE, BN, CL>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        cudaFuncSetAttribute(gemm_kernel<MODE, BN, CL, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (attr != cudaSuccess) return MOE_ERR_CUDA;
-    if (launch_chained(gemm_kernel<MODE, BN, CL>, dim3(ctas), CL, GEMM_THREADS, smem, pdl, st, (const CUtensorMap)ma,
+    if (launch_chained(gemm_kernel<MODE, BN, CL, SPLIT>, dim3(ctas), SPLIT ? pl.split : CL, GEMM_THREADS, smem, pdl, st, (const CUtensorMap)ma,
                        (const CUtensorMap)mb, (const CUtensorMap)mc, (const CUtensorMap)ms, (const Params)p) !=
         cudaSuccess)
         return MOE_ERR_CUDA;
@@ -696,11 +818,12 @@ template <Mode MODE, int BN>
 static moe_status launch(const void *a, const void *b, float *c, int M, int N, int K, float *slots,
                          int32_t *dev_status, bool pdl, cudaStream_t st)
 {
-    const Plan pl = plan(M, N, K, BN);
+    const Plan pl = plan(M, N, K, BN, Cfg<MODE, BN, 1>::P);
+    if (pl.split > 1) return launch_cl<MODE, BN, 1, true>(pl, a, b, c, M, N, K, slots, dev_status, pdl, st);
     if constexpr (BN >= 128) {
-        if (pl.cl == 2) return launch_cl<MODE, BN, 2>(pl, a, b, c, M, N, K, slots, dev_status, pdl, st);
+        if (pl.cl == 2) return launch_cl<MODE, BN, 2, false>(pl, a, b, c, M, N, K, slots, dev_status, pdl, st);
     }
-    return launch_cl<MODE, BN, 1>(pl, a, b, c, M, N, K, slots, dev_status, pdl, st);
+    return launch_cl<MODE, BN, 1, false>(pl, a, b, c, M, N, K, slots, dev_status, pdl, st);
 }
 
 static size_t align_up(size_t v) { return (v + 255) & ~(size_t)255; }
@@ -710,7 +833,7 @@ static size_t align_up(size_t v) { return (v + 255) & ~(size_t)255; }
 size_t router_logits_workspace(int T, int d, int E)
 {
     using namespace rg;
-    return 256 + slots_bytes(plan(T, E, d, logits_bn(E)));
+    return 256 + slots_bytes(plan(T, E, d, logits_bn(E), 1));
 }
 
 moe_status router_logits(const uint16_t *x, const uint16_t *w, int T, int d, int E, float *logits, void *ws,
@@ -728,7 +851,7 @@ moe_status router_logits(const uint16_t *x, const uint16_t *w, int T, int d, int
 size_t router_backward_workspace(int T, int d, int E)
 {
     using namespace rg;
-    const size_t sx = slots_bytes(plan(T, d, E, hidden_bn(d))), sw = slots_bytes(plan(E, d, T, hidden_bn(d)));
+    const size_t sx = slots_bytes(plan(T, d, E, hidden_bn(d), 3)), sw = slots_bytes(plan(E, d, T, hidden_bn(d), 3));
     return 256 + align_up((size_t)3 * T * pad64(E) * 2) + (sx > sw ? sx : sw);
 }
 

@@ -209,6 +209,14 @@ constexpr uint32_t idesc_bf16(int M, int N, bool a_mn, bool b_mn)
            ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
+// true in one thread of the (converged) warp
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+    return e != 0;
+}
+
 // waits (each bounded) until the last of the n uses of each place of a ring is
 // complete at its barrier
 __device__ __forceinline__ void drain(uint64_t *full, int size, uint32_t n)
@@ -341,57 +349,77 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
         }
         __syncwarp();
     } else if (warp == GEMM_MMA) {
-        if (lane == 0 && rank == 0) {
+        // the whole warp goes through the loop (addresses and descriptors stay
+        // in uniform registers), one elected thread issues
+        if (rank == 0) {
             constexpr uint32_t IDESC = idesc_bf16(CL * TM, BN, C::A_MN, C::B_MN);
             auto commit = [](uint64_t *bar) {
                 if (CL > 1) mma_commit_pair(bar);
                 else mma_commit(bar);
             };
-            constexpr int A_STEP = C::A_MN ? 2048 >> 4 : 32 >> 4, B_STEP = C::B_MN ? 2048 >> 4 : 32 >> 4;
-            uint32_t ja = 0, jb = 0, jc = 0;
+            auto wait = [&](uint64_t *bar, uint32_t parity) {
+                return __all_sync(0xFFFFFFFFu, wait_or_abort(bar, parity, abort_flag, p.dev_status));
+            };
+            const bool leader = elect_one();
+            constexpr uint64_t A_STEP = C::A_MN ? 2048 >> 4 : 32 >> 4, B_STEP = C::B_MN ? 2048 >> 4 : 32 >> 4;
+            const uint32_t a0 = smem_u32(s.a[0]), bb0 = smem_u32(s.b[0]);
+            const uint64_t adesc0 = C::A_MN ? sw128_desc_mn(a0) : sw128_desc(a0);
+            const uint64_t bdesc0 = C::B_MN ? sw128_desc_mn(bb0) : sw128_desc(bb0);
+            int sa = 0, sb = 0, buf = 0;                 // places in the rings, and their phases
+            uint32_t pa = 0, pb = 0, pt = 1;
             int in_chunk = 0, kb = (int)(b0 % p.nkb);
             bool ok = true;
-            for (int64_t b = b0; ok && b < b1; b++) {
-                const int sb = jb % C::NB, buf = jc % C::BUFS;
-                if ((in_chunk == 0 &&
-                     !wait_or_abort(&s.tempty[buf], ((jc / C::BUFS) & 1) ^ 1, abort_flag, p.dev_status)) ||
-                    !wait_or_abort(&s.bfull[sb], (jb / C::NB) & 1, abort_flag, p.dev_status))
-                    break;
-                const uint32_t baddr = smem_u32(s.b[sb]);
-                const uint64_t bdesc = C::B_MN ? sw128_desc_mn(baddr) : sw128_desc(baddr);
+            for (int left = (int)(b1 - b0); ok && left > 0; left--) {
+                if ((in_chunk == 0 && !wait(&s.tempty[buf], pt)) || !wait(&s.bfull[sb], pb)) break;
+                const uint64_t bdesc = bdesc0 + (uint64_t)sb * (C::B_TILE >> 4);
 #pragma unroll
                 for (int q = C::P - 1; q >= 0; q--) {      // the small parts first
-                    const int sa = ja % C::NA;
-                    if (!wait_or_abort(&s.afull[sa], (ja / C::NA) & 1, abort_flag, p.dev_status)) {
+                    if (!wait(&s.afull[sa], pa)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t aaddr = smem_u32(s.a[sa]);
-                    const uint64_t adesc = C::A_MN ? sw128_desc_mn(aaddr) : sw128_desc(aaddr);
+                    const uint64_t adesc = adesc0 + (uint64_t)sa * (A_TILE >> 4);
+                    if (leader) {
 #pragma unroll
-                    for (int ks = 0; ks < KB / 16; ks++) {
-                        const uint32_t add = in_chunk > 0 || q < C::P - 1 || ks > 0;
-                        if (CL > 1)
-                            mma_bf16_pair(tmem + buf * BN, adesc + A_STEP * ks, bdesc + B_STEP * ks, IDESC, add);
-                        else
-                            mma_bf16(tmem + buf * BN, adesc + A_STEP * ks, bdesc + B_STEP * ks, IDESC, add);
+                        for (int ks = 0; ks < KB / 16; ks++) {
+                            const uint32_t add = in_chunk > 0 || q < C::P - 1 || ks > 0;
+                            if (CL > 1)
+                                mma_bf16_pair(tmem + buf * BN, adesc + A_STEP * ks, bdesc + B_STEP * ks, IDESC, add);
+                            else
+                                mma_bf16(tmem + buf * BN, adesc + A_STEP * ks, bdesc + B_STEP * ks, IDESC, add);
+                        }
+                        commit(&s.aempty[sa]);
                     }
-                    commit(&s.aempty[sa]);
-                    ja++;
+                    __syncwarp();
+                    if (++sa == C::NA) {
+                        sa = 0;
+                        pa ^= 1;
+                    }
                 }
                 if (!ok) break;
-                commit(&s.bempty[sb]);
-                jb++;
                 in_chunk++;
                 if (++kb == p.nkb) kb = 0;
-                if (in_chunk == CHUNK || kb == 0 || b + 1 == b1) {
-                    commit(&s.tfull[buf]);
-                    jc++;
+                const bool end = in_chunk == CHUNK || kb == 0 || left == 1;
+                if (leader) {
+                    commit(&s.bempty[sb]);
+                    if (end) commit(&s.tfull[buf]);
+                }
+                __syncwarp();
+                if (++sb == C::NB) {
+                    sb = 0;
+                    pb ^= 1;
+                }
+                if (end) {
                     in_chunk = 0;
+                    if (++buf == C::BUFS) {
+                        buf = 0;
+                        pt ^= 1;
+                    }
                 }
             }
-            commit(&s.mma_done);
+            if (leader) commit(&s.mma_done);
+            __syncwarp();
         }
         // (the second CTA too: the arrival at its barrier has then come)
         if (lane == 0) {

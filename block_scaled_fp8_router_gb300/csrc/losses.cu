@@ -266,8 +266,8 @@ __device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank)
 constexpr int ROW_THREADS = 128;
 constexpr uint64_t ROW_TIMEOUT_NS = 1000ull * 1000ull * 1000ull;
 
-// what a row's gradient needs: dl_v = 2^t_v (A0 + B0 t_v) + gy 1[v = y],
-// t_v = l_v k2 - ck
+// what a row's gradient needs: dl_v = 2^t_v (A0 + B0 t_v), t_v = l_v k2 - ck, and
+// gy, the whole of dl_y
 struct RowGrad {
     float ck, A0, B0, gy;
 };
@@ -466,9 +466,10 @@ __global__ void __launch_bounds__(ROW_THREADS, POLICY ? 6 : 8)
                     // t here is off by r = c k2 - ck from the sums' t
                     g.ck = s.c * k2;
                     const float r = fmaf(s.c, k2, -g.ck), q = coef / s.S * exp2f(-r);
-                    g.gy = coef * gl;
                     g.B0 = q * a.eta * LN2;
                     g.A0 = q * (-gl + a.eta * (H - LN2 * (ls + r)));
+                    const float ty = fmaf(ly, k2, -g.ck);
+                    g.gy = fmaf(ex2(ty), fmaf(g.B0, fmaxf(ty, TMIN), g.A0), coef * gl);
                 }
                 if (lane == 0) s_grad = g;
             }
@@ -491,19 +492,7 @@ __global__ void __launch_bounds__(ROW_THREADS, POLICY ? 6 : 8)
         // vector stores where the gradient's rows are aligned as the logits' are
         const bool same = ((reinterpret_cast<uintptr_t>(d) ^ reinterpret_cast<uintptr_t>(R.l)) & 15u) == 0;
         uint4 *dv = reinterpret_cast<uint4 *>(reinterpret_cast<uintptr_t>(d) & ~(uintptr_t)15u);
-        const int jy = live ? (int)((y + R.head) / W) : -1, uy = live ? (int)((y + R.head) % W) : 0;
-        auto put = [&](int j, const uint4 &v, bool whole) {
-            float f[W];
-            if (live) {
-                grad_vec<T, ETA>(v, g, k22, f);
-                if (j == jy) {
-#pragma unroll
-                    for (int u = 0; u < W; u++) f[u] += u == uy ? g.gy : 0.0f;
-                }
-            } else {
-#pragma unroll
-                for (int u = 0; u < W; u++) f[u] = 0.0f;
-            }
+        auto store = [&](int j, const float *f, bool whole) {
             if (whole && same) {
                 __stcs(dv + j, Vec<T>::make(f));
             } else {
@@ -513,17 +502,33 @@ __global__ void __launch_bounds__(ROW_THREADS, POLICY ? 6 : 8)
                     if (e + u >= 0 && e + u < V) store_grad(d + e + u, f[u]);
             }
         };
-        const int j1 = (R.nvec - 1) % dj;      // the last vector's thread
-        if (R.lo > 0 && j0 == 0) put(0, live ? R.load_edge(0) : raw[0], false);
-        if (R.hi < R.nvec && j0 == j1 && (R.nvec > 1 || R.lo == 0))
-            put(R.nvec - 1, live ? R.load_edge(R.nvec - 1) : raw[0], false);
-        for (int c = nch - 1; c >= 0; c--) {
+        const bool first = R.lo > 0 && j0 == 0;
+        const bool last = R.hi < R.nvec && j0 == (R.nvec - 1) % dj && (R.nvec > 1 || R.lo == 0);
+        if (live) {
+            auto put = [&](int j, const uint4 &v, bool whole) {
+                float f[W];
+                grad_vec<T, ETA>(v, g, k22, f);
+                store(j, f, whole);
+            };
+            if (first) put(0, R.load_edge(0), false);
+            if (last) put(R.nvec - 1, R.load_edge(R.nvec - 1), false);
+            for (int c = nch - 1; c >= 0; c--) {
+                const int jc = c * NV * dj + j0;
 #pragma unroll
-            for (int i = 0; i < NV; i++) {
-                const int j = (c * NV + i) * dj + j0;
-                if (R.inside(j)) put(j, raw[i], true);
+                for (int i = 0; i < NV; i++)
+                    if (R.inside(jc + i * dj)) put(jc + i * dj, raw[i], true);
+                if (c > 0) load(c - 1);
             }
-            if (live && c > 0) load(c - 1);
+            // the target's entry again, by the thread that has just written its vector
+            if ((int)((y + R.head) / W) % dj == j0) store_grad(d + y, g.gy);
+        } else {
+            float f[W];
+#pragma unroll
+            for (int u = 0; u < W; u++) f[u] = 0.0f;
+            if (first) store(0, f, false);
+            if (last) store(R.nvec - 1, f, false);
+            for (int j = j0; j < R.hi; j += dj)
+                if (j >= R.lo) store(j, f, true);
         }
     }
     if (rank == 0 && tid == 0) {

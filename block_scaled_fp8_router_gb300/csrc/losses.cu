@@ -263,7 +263,7 @@ __device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank)
     return out;
 }
 
-constexpr int ROW_THREADS = 128;
+constexpr int RING_DEPTH = 2;           // chunks of a thread in shared memory
 constexpr uint64_t ROW_TIMEOUT_NS = 1000ull * 1000ull * 1000ull;
 
 // what a row's gradient needs: dl_v = 2^t_v (A0 + B0 t_v), t_v = l_v k2 - ck, and
@@ -345,21 +345,23 @@ __device__ __forceinline__ void grad_vec(const uint4 &v, const RowGrad &g, uint6
     }
 }
 
-// Row blockIdx.x / C by a cluster of C CTAs.  POLICY: the policy loss and its
-// gradient (else log-probabilities and entropy); ETA: with an entropy bonus.
-template <typename T, int NV, bool POLICY, bool ETA>
-__global__ void __launch_bounds__(ROW_THREADS, POLICY ? 6 : 8)
+// Row blockIdx.x / C by a cluster of C CTAs of TH threads at most.  POLICY: the
+// policy loss and its gradient (else log-probabilities and entropy); RING: that
+// of a row with more than one chunk of NV vectors a thread; ETA: with an
+// entropy bonus.
+template <typename T, int TH, int NV, bool RING, bool POLICY, bool ETA>
+__global__ void __launch_bounds__(TH, TH == 256 ? (POLICY ? 3 : 4) : POLICY ? 5 : 8)
     token_rows_kernel(const T *logits, int64_t N, int64_t V, int64_t ld, const void *__restrict__ targets, int t64,
                       float k2, int C, float *__restrict__ logprobs, float *__restrict__ entropy, T *dlogits,
                       const PolicyArgs a, int32_t *dev_status)
 {
     constexpr int W = Vec<T>::W;
-    __shared__ RowSum s_part[ROW_THREADS / 32];
+    __shared__ RowSum s_part[TH / 32];
     __shared__ float4 s_msg[8];
     __shared__ RowGrad s_grad;
     __shared__ int s_live;
     __shared__ uint64_t s_bar;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, TH = blockDim.x, nw = TH >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x, nw = nt >> 5;
     const int64_t row = blockIdx.x / (unsigned)C;
     const int rank = C > 1 ? (int)cluster_rank() : 0;
     if (C > 1) {
@@ -375,19 +377,50 @@ __global__ void __launch_bounds__(ROW_THREADS, POLICY ? 6 : 8)
     bool live = y >= 0 && y < V && w != 0.0f;
     if (y >= V && w != 0.0f && tid == 0 && rank == 0) dev_flag(dev_status, MOE_DEV_BAD_IDS);
     const Row<T> R(logits + row * ld, V);
-    const int j0 = rank * TH + tid, dj = C * TH;   // my vectors: j0, j0 + dj, ...
-    // the row in chunks of NV vectors a thread; the last stays in registers for
-    // the gradient, which goes through the chunks backward
-    const int nch = (R.hi + NV * dj - 1) / (NV * dj);
+    const int j0 = rank * nt + tid, dj = C * nt;   // my vectors: j0, j0 + dj, ...
+    // The row in chunks of NV vectors a thread.  For a gradient, one chunk stays
+    // in registers; of more, the next RING_DEPTH are on their way to the
+    // thread's own places in shared memory (chunk c at c mod RING_DEPTH) while
+    // one is worked on, and the gradient goes through them backward: the last
+    // are still there, the others come again from L2.
+    const int nch = POLICY && !RING ? 1 : (R.hi + NV * dj - 1) / (NV * dj);
+    extern __shared__ uint4 s_ring[];
     uint4 raw[NV];
+    auto fetch = [&](int c) {            // always one group, empty outside 0 .. nch - 1
+        if (c >= 0 && c < nch) {
+            uint4 *place = s_ring + (c % RING_DEPTH) * (NV * TH) + tid;
+#pragma unroll
+            for (int i = 0; i < NV; i++) {
+                const int j = (c * NV + i) * dj + j0;
+                if (R.inside(j))
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(place + i * TH)),
+                                 "l"(R.base + j)
+                                 : "memory");
+            }
+        }
+        cp_async_commit();
+    };
     auto load = [&](int c) {
 #pragma unroll
         for (int i = 0; i < NV; i++) raw[i] = R.load((c * NV + i) * dj + j0);
     };
+    auto take = [&](int c) {             // chunk c to registers, absent vectors as -inf
+        constexpr uint32_t NI = Vec<T>::NINF;
+        cp_async_wait<RING_DEPTH - 1>();
+        const uint4 *place = s_ring + (c % RING_DEPTH) * (NV * TH) + tid;
+#pragma unroll
+        for (int i = 0; i < NV; i++)
+            raw[i] = R.inside((c * NV + i) * dj + j0) ? place[i * TH] : make_uint4(NI, NI, NI, NI);
+    };
     float lp = 0.0f, H = 0.0f;
     float4 st = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (live) {
-        load(0);
+        if (RING) {
+#pragma unroll
+            for (int c = 0; c < RING_DEPTH; c++) fetch(c);
+        } else {
+            load(0);
+        }
         const float ly = warp == 0 ? load_logit(R.l + y) : 0.0f;
         RowSum s = {-INFINITY, 0.0f, 0.0f};
         // the vectors at the row's two ends, one lane's each, if not whole
@@ -403,9 +436,13 @@ __global__ void __launch_bounds__(ROW_THREADS, POLICY ? 6 : 8)
                 }
             }
         }
-        add_vecs<T, NV>(s, raw, k2);
-        for (int c = 1; c < nch; c++) {
-            load(c);
+        for (int c = 0; c < nch; c++) {
+            if (RING) {
+                take(c);
+                fetch(c + RING_DEPTH);
+            } else if (c > 0) {
+                load(c);
+            }
             add_vecs<T, NV>(s, raw, k2);
         }
         for (int o = 16; o; o >>= 1) {
@@ -514,10 +551,13 @@ __global__ void __launch_bounds__(ROW_THREADS, POLICY ? 6 : 8)
             if (last) put(R.nvec - 1, R.load_edge(R.nvec - 1), false);
             for (int c = nch - 1; c >= 0; c--) {
                 const int jc = c * NV * dj + j0;
+                if (RING) {
+                    take(c);
+                    fetch(c - RING_DEPTH);
+                }
 #pragma unroll
                 for (int i = 0; i < NV; i++)
                     if (R.inside(jc + i * dj)) put(jc + i * dj, raw[i], true);
-                if (c > 0) load(c - 1);
             }
             // the target's entry again, by the thread that has just written its vector
             if ((int)((y + R.head) / W) % dj == j0) store_grad(d + y, g.gy);
@@ -592,34 +632,42 @@ __global__ void __launch_bounds__(1024) policy_stats_kernel(const Ws *__restrict
     }
 }
 
-// how a row is spread: threads of a CTA, CTAs of a cluster, vectors kept per
-// thread.  A CTA takes a warp per 256 vectors, four at most (8192 x 16384 bf16
-// log-probabilities: 50 us at 128 threads, 61 at 256, 58 at 64; an SM holds
-// six or eight such CTAs, whose phases interleave).  One CTA a row where the
-// rows fill the GPU: an exchange costs more than reading a long row's
-// remainder again from L2 (8192 x 131072 bf16 log-probabilities 0.32 ms, 0.34
-// at two CTAs, 0.60 at eight); two for the gradient of long rows, which keeps
-// the rows in work within L2 (4096 x 131072: 0.40 ms against 0.42).  More as
-// rows get few, while each thread keeps a vector.
+// How a row is spread: threads of a CTA, CTAs of a cluster, vectors of a chunk.
+// A CTA takes a warp per 256 vectors: up to four for log-probabilities (8192 x
+// 16384 bf16: 50 us, 61 with eight warps, 58 with two), up to eight for
+// gradients.  A longer row streams, one CTA a row where the rows fill the GPU:
+// an exchange costs more than it saves (8192 x 131072 log-probabilities 0.31
+// ms, 0.34 with two CTAs, 0.60 with eight); two for the gradient of long rows,
+// so that the rows in work stay within L2 until they are read again (4096 x
+// 131072: 0.32 ms against 0.37).  More CTAs as rows get few, while each thread
+// keeps a vector.
 struct RowPlan {
     int threads, C, NV;
+    bool ring;
 };
 static RowPlan row_plan(int64_t N, int64_t V, int w, bool aligned, bool policy)
 {
     const int64_t nvec = (V + w - 1) / w + (aligned ? 0 : 1);
-    RowPlan p = {32, policy && nvec > 4096 ? 2 : 1, 8};
-    while (p.threads < ROW_THREADS && p.threads * 8 < nvec) p.threads *= 2;
+    RowPlan p = {32, policy && nvec > 4096 ? 2 : 1, 8, false};
     const int64_t fill = 3LL * sm_count();
+    const int most = policy || 8 * N <= fill ? 256 : 128;
+    while (p.threads < most && p.threads * 8 < nvec) p.threads *= 2;
     while (p.C < 8 && N * p.C * 2 <= fill && (int64_t)p.C * p.threads < nvec) p.C *= 2;
+    p.ring = policy && (int64_t)p.C * p.threads * p.NV < nvec;      // (then there are 256 threads)
     while (p.NV > 1 && (int64_t)p.C * p.threads * (p.NV / 2) >= nvec) p.NV /= 2;
     return p;
 }
 
-template <typename T, int NV, bool POLICY, bool ETA>
+template <typename T, int TH, int NV, bool RING, bool POLICY, bool ETA>
 static cudaError_t launch_rows_nv(const RowPlan &p, const T *logits, int64_t N, int64_t V, int64_t ld,
                                   const void *targets, int t64, float k2, float *logprobs, float *entropy, T *dlogits,
                                   const PolicyArgs &a, int32_t *dev_status, cudaStream_t st)
 {
+    auto *kernel = token_rows_kernel<T, TH, NV, RING, POLICY, ETA>;
+    constexpr int smem = RING ? RING_DEPTH * NV * TH * 16 : 0;
+    static const cudaError_t set =
+        RING ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) : cudaSuccess;
+    if (set != cudaSuccess) return set;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -630,11 +678,12 @@ static cudaError_t launch_rows_nv(const RowPlan &p, const T *logits, int64_t N, 
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.gridDim = dim3((unsigned)(N * p.C));
     cfg.blockDim = dim3(p.threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = POLICY ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, token_rows_kernel<T, NV, POLICY, ETA>, logits, N, V, ld, targets, t64, k2, p.C,
-                              logprobs, entropy, dlogits, a, dev_status);
+    return cudaLaunchKernelEx(&cfg, kernel, logits, N, V, ld, targets, t64, k2, p.C, logprobs, entropy, dlogits, a,
+                              dev_status);
 }
 
 template <typename T, bool POLICY, bool ETA>
@@ -644,15 +693,19 @@ static cudaError_t launch_rows(const T *logits, int64_t N, int64_t V, int64_t ld
 {
     const bool aligned = aligned16(logits) && (N == 1 || ld % Vec<T>::W == 0);
     const RowPlan p = row_plan(N, V, Vec<T>::W, aligned, POLICY);
-#define MOE_ROWS(NV)                                                                                                  \
-    launch_rows_nv<T, NV, POLICY, ETA>(p, logits, N, V, ld, targets, t64, k2, logprobs, entropy, dlogits, a,          \
-                                       dev_status, st)
-    switch (p.NV) {
-    case 1: return MOE_ROWS(1);
-    case 2: return MOE_ROWS(2);
-    case 4: return MOE_ROWS(4);
-    default: return MOE_ROWS(8);
+#define MOE_ROWS(TH, NV, RING)                                                                                        \
+    launch_rows_nv<T, TH, NV, RING, POLICY, ETA>(p, logits, N, V, ld, targets, t64, k2, logprobs, entropy, dlogits,   \
+                                                 a, dev_status, st)
+#define MOE_ROWS_NV(TH)                                                                                               \
+    p.NV == 1 ? MOE_ROWS(TH, 1, false)                                                                                \
+    : p.NV == 2 ? MOE_ROWS(TH, 2, false)                                                                              \
+    : p.NV == 4 ? MOE_ROWS(TH, 4, false)                                                                              \
+                : MOE_ROWS(TH, 8, false)
+    if constexpr (POLICY) {
+        if (p.ring) return MOE_ROWS(256, 8, true);
     }
+    return p.threads > 128 ? (MOE_ROWS_NV(256)) : (MOE_ROWS_NV(128));
+#undef MOE_ROWS_NV
 #undef MOE_ROWS
 }
 

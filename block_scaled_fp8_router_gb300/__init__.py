@@ -16,6 +16,9 @@ _BINDING = {
     "moe_route_topk", "moe_route_replay", "fp8_block_quant", "moe_dispatch", "moe_dispatch_workspace_size",
     "moe_grouped_ffn_fp8", "moe_grouped_ffn_workspace_size", "moe_combine", "moe_status_str",
     "moe_debug_bounded_wait", "moe_device_sm_count", "check_status", "MoEError",
+    "moe_token_logprobs", "moe_policy_loss", "moe_policy_loss_workspace_size", "moe_router_logits",
+    "moe_router_logits_workspace_size", "moe_balance_loss", "moe_balance_loss_workspace_size",
+    "moe_router_backward_dense", "moe_router_backward_dense_workspace_size",
 }
 _LAYER = {"MoELayerFP8", "MoEWeightsFP8", "quantize_weights"}
 

@@ -506,7 +506,9 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
             }
             b += n;
         }
-        if (lane == 0) bulk_wait_all();
+        // the stores have read their staging tiles (they are complete when the
+        // grid is)
+        if (lane == 0) bulk_wait_read_all();
         __syncwarp();
     }
 
@@ -685,8 +687,9 @@ static int clusters_at_once(int size)
 }
 
 // How the work is cut, by an estimate in clocks.  A K block takes parts x 2 BN
-// clocks on the tensor cores, or 700 where a CTA's share of HBM is slower (one
-// part: the A tile's 16 KB).  Whole tiles; or a cluster of 2, 4 or 8 CTAs per
+// clocks on the tensor cores and about 400 more (measured: 128 clocks per MMA
+// of N = 256, 960 per block of four, 1960 per block of twelve), and 700 at
+// least, where a CTA's share of HBM is slower.  Whole tiles; or a cluster of 2, 4 or 8 CTAs per
 // tile (about 4000 clocks for the exchange; 8192 x 7168 x 256 logits 40 us
 // against 44 cut into runs); or all blocks cut into equal runs (about 16000
 // for the slots and their reduction: only long sums, weight gradients of
@@ -695,17 +698,20 @@ struct Plan {
     int cl, split, runs, gran, m_tiles, n_tiles, nkb;     // m_tiles: groups of cl row tiles
     int64_t blocks;
     bool slots;          // some tile is cut into runs
+    int bn;              // columns of a tile
+    int64_t clocks;
 };
 
-static Plan plan(int M, int N, int K, int bn, int parts)
+static Plan plan_bn(int M, int N, int K, int bn, int parts)
 {
     Plan r;
+    r.bn = bn;
     const int rows = (M + TM - 1) / TM;
     r.n_tiles = (N + bn - 1) / bn;
     r.nkb = (K + KB - 1) / KB;
     int sms = sm_count();
     if (sms > MAX_CTAS) sms = MAX_CTAS;
-    const int64_t t = 2 * bn * parts > 700 ? 2 * bn * parts : 700;
+    const int64_t t = 2 * bn * parts + 400 > 700 ? 2 * bn * parts + 400 : 700;
     const int64_t tiles1 = (int64_t)rows * r.n_tiles;
     int64_t best = (tiles1 + sms - 1) / sms * r.nkb * t;
     int kind = 1;                                          // whole tiles
@@ -735,13 +741,25 @@ static Plan plan(int M, int N, int K, int bn, int parts)
     const int64_t units = kind == 0 ? (r.blocks + CHUNK - 1) / CHUNK : tiles;
     r.runs = kind > 1 ? (int)(tiles * kind) : (int)(units < most ? units : most);
     r.slots = kind == 0;
+    r.clocks = best;
+    return r;
+}
+
+// the tile width by the same estimate: narrower tiles where wide ones are too
+// few for the SMs
+static Plan plan(Mode mode, int M, int N, int K)
+{
+    const int parts = mode == LOGITS ? 1 : 3;
+    Plan r = plan_bn(M, N, K, 256, parts);
+    for (int bn = 128; bn >= (mode == LOGITS ? 64 : 128); bn /= 2) {
+        const Plan q = plan_bn(M, N, K, bn, parts);
+        if (q.clocks < r.clocks || N <= bn) r = q;
+    }
     return r;
 }
 
 static size_t slots_bytes(const Plan &r) { return r.slots ? (size_t)r.runs * r.cl * 2 * SLOT_FLOATS * sizeof(float) : 0; }
 
-static int logits_bn(int E) { return E <= 64 ? 64 : E <= 128 ? 128 : 256; }
-static int hidden_bn(int d) { return d % 256 == 0 ? 256 : 128; }
 
 // [parts][rows][k] bf16, k contiguous: box 64 k x box_rows rows of one part
 static bool map_k_major(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap *m, const void *base, uint64_t k,
@@ -843,15 +861,26 @@ static moe_status launch_cl(const Plan &pl, const void *a, const void *b, float 
 }
 
 template <Mode MODE, int BN>
-static moe_status launch(const void *a, const void *b, float *c, int M, int N, int K, float *slots,
-                         int32_t *dev_status, bool pdl, cudaStream_t st)
+static moe_status launch_bn(const Plan &pl, const void *a, const void *b, float *c, int M, int N, int K, float *slots,
+                            int32_t *dev_status, bool pdl, cudaStream_t st)
 {
-    const Plan pl = plan(M, N, K, BN, Cfg<MODE, BN, 1>::P);
     if (pl.split > 1) return launch_cl<MODE, BN, 1, true>(pl, a, b, c, M, N, K, slots, dev_status, pdl, st);
     if constexpr (BN >= 128) {
         if (pl.cl == 2) return launch_cl<MODE, BN, 2, false>(pl, a, b, c, M, N, K, slots, dev_status, pdl, st);
     }
     return launch_cl<MODE, BN, 1, false>(pl, a, b, c, M, N, K, slots, dev_status, pdl, st);
+}
+
+template <Mode MODE>
+static moe_status launch(const void *a, const void *b, float *c, int M, int N, int K, float *slots,
+                         int32_t *dev_status, bool pdl, cudaStream_t st)
+{
+    const Plan pl = plan(MODE, M, N, K);
+    if (pl.bn == 256) return launch_bn<MODE, 256>(pl, a, b, c, M, N, K, slots, dev_status, pdl, st);
+    if constexpr (MODE == LOGITS) {
+        if (pl.bn == 64) return launch_bn<MODE, 64>(pl, a, b, c, M, N, K, slots, dev_status, pdl, st);
+    }
+    return launch_bn<MODE, 128>(pl, a, b, c, M, N, K, slots, dev_status, pdl, st);
 }
 
 static size_t align_up(size_t v) { return (v + 255) & ~(size_t)255; }
@@ -861,25 +890,19 @@ static size_t align_up(size_t v) { return (v + 255) & ~(size_t)255; }
 size_t router_logits_workspace(int T, int d, int E)
 {
     using namespace rg;
-    return 256 + slots_bytes(plan(T, E, d, logits_bn(E), 1));
+    return 256 + slots_bytes(plan(LOGITS, T, E, d));
 }
 
 moe_status router_logits(const uint16_t *x, const uint16_t *w, int T, int d, int E, float *logits, void *ws,
                          int32_t *dev_status, cudaStream_t st)
 {
-    using namespace rg;
-    float *slots = (float *)ws;
-    switch (logits_bn(E)) {
-    case 64: return launch<LOGITS, 64>(x, w, logits, T, E, d, slots, dev_status, false, st);
-    case 128: return launch<LOGITS, 128>(x, w, logits, T, E, d, slots, dev_status, false, st);
-    default: return launch<LOGITS, 256>(x, w, logits, T, E, d, slots, dev_status, false, st);
-    }
+    return rg::launch<rg::LOGITS>(x, w, logits, T, E, d, (float *)ws, dev_status, false, st);
 }
 
 size_t router_backward_workspace(int T, int d, int E)
 {
     using namespace rg;
-    const size_t sx = slots_bytes(plan(T, d, E, hidden_bn(d), 3)), sw = slots_bytes(plan(E, d, T, hidden_bn(d), 3));
+    const size_t sx = slots_bytes(plan(DX, T, d, E)), sw = slots_bytes(plan(DW, E, d, T));
     return 256 + align_up((size_t)3 * T * pad64(E) * 2) + (sx > sw ? sx : sw);
 }
 
@@ -893,15 +916,8 @@ moe_status router_backward(const uint16_t *x, const uint16_t *w, const float *dl
     const int64_t n = (int64_t)T * (Ep / 8);
     split_kernel<<<(unsigned)((n + 255) / 256), 256, 0, st>>>(dl, T, E, Ep, parts);
     moe_status s = launch_status();
-    if (s != MOE_OK) return s;
-    if (dx) {
-        s = hidden_bn(d) == 256 ? launch<DX, 256>(parts, w, dx, T, d, E, slots, dev_status, true, st)
-                                : launch<DX, 128>(parts, w, dx, T, d, E, slots, dev_status, true, st);
-        if (s != MOE_OK) return s;
-    }
-    if (dw)
-        s = hidden_bn(d) == 256 ? launch<DW, 256>(parts, x, dw, E, d, T, slots, dev_status, true, st)
-                                : launch<DW, 128>(parts, x, dw, E, d, T, slots, dev_status, true, st);
+    if (s == MOE_OK && dx) s = launch<DX>(parts, w, dx, T, d, E, slots, dev_status, true, st);
+    if (s == MOE_OK && dw) s = launch<DW>(parts, x, dw, E, d, T, slots, dev_status, true, st);
     return s;
 }
 

@@ -6,6 +6,8 @@
 #include <cuda_fp8.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "moe_r3.h"
 
 #define MOE_API extern "C" __attribute__((visibility("default")))
@@ -22,6 +24,21 @@ static inline int sm_count()
     if (cudaGetDevice(&dev) != cudaSuccess) return 1;
     if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 1;
     return n > 0 ? n : 1;
+}
+
+// Allows a kernel `bytes` of dynamic shared memory on the current device, once
+// per device: `done` (one bit each, a static of the launching function) saves
+// later calls the runtime's look-up.  Devices past 63 are set every time.
+static inline cudaError_t allow_smem(const void *kernel, int bytes, std::atomic<uint64_t> &done)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
 }
 
 static inline moe_status launch_status()

@@ -266,10 +266,10 @@ __device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank)
 constexpr int RING_DEPTH = 2;           // chunks of a thread in shared memory
 constexpr uint64_t ROW_TIMEOUT_NS = 1000ull * 1000ull * 1000ull;
 
-// what a row's gradient needs: dl_v = 2^t_v (A0 + B0 t_v), t_v = l_v k2 - ck, and
+// what a row's gradient needs: dl_v = 2^t_v (A0 + B0 t_v), t_v = (l_v - c) k2, and
 // gy, the whole of dl_y
 struct RowGrad {
-    float ck, A0, B0, gy;
+    float c, A0, B0, gy;
 };
 
 // whether t of a logit held above -2^100 is finite for the shift c, so that 2^t t
@@ -327,15 +327,14 @@ __device__ __forceinline__ void add_vecs(RowSum &s, const uint4 (&v)[NV], float 
     s.U = x + z;
 }
 
-// the gradient of one vector.  t = l k2 - ck in one step, ck = c k2 rounded:
-// the rounding is one factor for the whole row and part of A0 and B0
+// the gradient of one vector, t as in the sums
 template <typename T, bool ETA>
 __device__ __forceinline__ void grad_vec(const uint4 &v, const RowGrad &g, uint64_t k22, float *f)
 {
-    const uint64_t nck2 = pack2(-g.ck, -g.ck);
+    const uint64_t nc2 = pack2(-g.c, -g.c);
 #pragma unroll
     for (int i = 0; i < Vec<T>::W / 2; i++) {
-        const uint64_t t = fma2(Vec<T>::pair(v, i), k22, nck2);
+        const uint64_t t = mul2(add2(Vec<T>::pair(v, i), nc2), k22);
         float t0, t1;
         unpack2(t, t0, t1);
         const uint64_t e = pack2(ex2(t0), ex2(t1));
@@ -500,12 +499,11 @@ __global__ void __launch_bounds__(TH, TH == 256 ? (POLICY ? 3 : 4) : POLICY ? 5 
                     st = make_float4(w * (clipped ? p1 : p0), w * kl, w * H, clipped ? w : 0.0f);
                     asm volatile("griddepcontrol.wait;" ::: "memory");
                     const float coef = w * __ldcg(&a.ws->scale);
-                    // t here is off by r = c k2 - ck from the sums' t
-                    g.ck = s.c * k2;
-                    const float r = fmaf(s.c, k2, -g.ck), q = coef / s.S * exp2f(-r);
+                    const float q = coef / s.S;
+                    g.c = s.c;
                     g.B0 = q * a.eta * LN2;
-                    g.A0 = q * (-gl + a.eta * (H - LN2 * (ls + r)));
-                    const float ty = fmaf(ly, k2, -g.ck);
+                    g.A0 = q * (-gl + a.eta * (H - LN2 * ls));
+                    const float ty = (ly - s.c) * k2;
                     g.gy = fmaf(ex2(ty), fmaf(g.B0, fmaxf(ty, TMIN), g.A0), coef * gl);
                 }
                 if (lane == 0) s_grad = g;
@@ -665,9 +663,11 @@ static cudaError_t launch_rows_nv(const RowPlan &p, const T *logits, int64_t N, 
 {
     auto *kernel = token_rows_kernel<T, TH, NV, RING, POLICY, ETA>;
     constexpr int smem = RING ? RING_DEPTH * NV * TH * 16 : 0;
-    static const cudaError_t set =
-        RING ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) : cudaSuccess;
-    if (set != cudaSuccess) return set;
+    if (RING) {
+        static std::atomic<uint64_t> done{0};
+        const cudaError_t e = allow_smem((const void *)kernel, smem, done);
+        if (e != cudaSuccess) return e;
+    }
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;

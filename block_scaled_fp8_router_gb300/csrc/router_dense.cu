@@ -86,6 +86,7 @@ __global__ void __launch_bounds__(1024) balance_count_kernel(const int32_t *__re
         for (int b = tid; b < B; b += 1024)
             if (off[b] < 0 || off[b + 1] < off[b] || off[b + 1] > T) dev_flag(dev_status, MOE_DEV_ROWS);
     const bool one = B == 1 && !off;
+    const bool v4 = k % 4 == 0 && (reinterpret_cast<uintptr_t>(ids) & 15u) == 0;
     if (!one) asm volatile("griddepcontrol.wait;" ::: "memory");
     for (int t = t0; t < t1;) {
         const int b = seq_of(off, B, t);
@@ -93,21 +94,29 @@ __global__ void __launch_bounds__(1024) balance_count_kernel(const int32_t *__re
         e1 = e1 < t1 ? e1 : t1;
         if (b >= 0) {
             int32_t mine = 0;
-            const int n = (e1 - t) * k;               // <= T k < 2^31
-            for (int i0 = tid; i0 < n; i0 += 4096) {
-                int32_t e[4];
-                bool on[4];
+            for (int i = t + tid; i < e1; i += 1024) {          // a token a thread
+                if (mask && !__ldg(mask + i)) continue;
+                mine++;
+                const int32_t *p = ids + (int64_t)i * k;
+                for (int j = 0; j < k; j += 8) {
+                    int32_t e[8];
+                    if (v4) {
 #pragma unroll
-                for (int u = 0; u < 4; u++) {
-                    const int i = i0 + 1024 * u;
-                    on[u] = i < n && (!mask || __ldg(mask + t + i / k));
-                    e[u] = i < n ? __ldg(ids + (int64_t)t * k + i) : -1;
-                }
+                        for (int h = 0; h < 2; h++) {
+                            const int4 q = j + 4 * h < k ? __ldg(reinterpret_cast<const int4 *>(p + j + 4 * h))
+                                                         : make_int4(-1, -1, -1, -1);
+                            e[4 * h] = q.x;
+                            e[4 * h + 1] = q.y;
+                            e[4 * h + 2] = q.z;
+                            e[4 * h + 3] = q.w;
+                        }
+                    } else {
 #pragma unroll
-                for (int u = 0; u < 4; u++) {
-                    if (!on[u]) continue;
-                    mine += (i0 + 1024 * u) % k == 0;
-                    if (e[u] >= 0 && e[u] < E) atomicAdd(&s_hist[e[u]], 1);
+                        for (int u = 0; u < 8; u++) e[u] = j + u < k ? __ldg(p + j + u) : -1;
+                    }
+#pragma unroll
+                    for (int u = 0; u < 8; u++)
+                        if ((uint32_t)e[u] < (uint32_t)E) atomicAdd(&s_hist[e[u]], 1);
                 }
             }
             mine = __reduce_add_sync(0xFFFFFFFFu, mine);

@@ -847,9 +847,8 @@ static moe_status launch_cl(const Plan &pl, const void *a, const void *b, float 
     if (!p.direct_tma) mc = ms;          // not used
     constexpr size_t smem = sizeof(Smem<MODE, BN, CL>) + 1024;
     static_assert(smem <= 227 * 1024, "shared memory");
-    static const cudaError_t attr =
-        cudaFuncSetAttribute(gemm_kernel<MODE, BN, CL, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (attr != cudaSuccess) return MOE_ERR_CUDA;
+    static std::atomic<uint64_t> done{0};
+    if (allow_smem((const void *)gemm_kernel<MODE, BN, CL, SPLIT>, (int)smem, done) != cudaSuccess) return MOE_ERR_CUDA;
     if (launch_chained(gemm_kernel<MODE, BN, CL, SPLIT>, dim3(ctas), SPLIT ? pl.split : CL, GEMM_THREADS, smem, pdl, st, (const CUtensorMap)ma,
                        (const CUtensorMap)mb, (const CUtensorMap)mc, (const CUtensorMap)ms, (const Params)p) !=
         cudaSuccess)

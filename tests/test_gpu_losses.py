@@ -134,6 +134,18 @@ def test_logprobs_hard_rows(L, dt, V):
     _close(H[keep], wH[keep], (rel * (2 * wH + 4) + at)[keep], "entropy")
 
 
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("tau,scale", [(1e-7, 1e-7), (1e5, 3e4), (1.0, 1e30), (3e-3, 0.02)])
+def test_logprobs_extreme_scales(L, dt, tau, scale):
+    """Temperatures and logits far from 1, a policy gradient among them."""
+    x, g = _rows(6, 3001, dt, 77, scale=scale)
+    y, _ = _inputs(6, 3001, g)
+    lp, H = _check_logprobs(L, x, y, tau)
+    assert torch.isfinite(H).all()
+    old = lp.clamp(min=-50.0)
+    _check_policy(L, x, y, old, torch.ones(6, device="cuda"), None, None, tau=tau, eta=0.01)
+
+
 def test_logprobs_target_out_of_range(L):
     x, g = _rows(4, 100, F32, 1)
     y = torch.tensor([5, 100, -7, 2 ** 40], device="cuda")

@@ -385,31 +385,53 @@ __global__ void __launch_bounds__(TH, TH == 256 ? (POLICY ? 3 : 4) : POLICY ? 5 
     const int nch = POLICY && !RING ? 1 : (R.hi + NV * dj - 1) / (NV * dj);
     extern __shared__ uint4 s_ring[];
     uint4 raw[NV];
+    // chunk c whole for every thread: no vector of it needs a look
+    auto full = [&](int c) { return c * NV * dj >= R.lo && (c + 1) * NV * dj <= R.hi; };
     auto fetch = [&](int c) {            // always one group, empty outside 0 .. nch - 1
         if (c >= 0 && c < nch) {
-            uint4 *place = s_ring + (c % RING_DEPTH) * (NV * TH) + tid;
+            const uint32_t place = smem_u32(s_ring + (c % RING_DEPTH) * (NV * TH) + tid);
+            const uint4 *src = R.base + (c * NV * dj + j0);
+            auto copy = [&](int i) {
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(place + i * TH * 16), "l"(src + i * dj)
+                             : "memory");
+            };
+            if (full(c)) {
 #pragma unroll
-            for (int i = 0; i < NV; i++) {
-                const int j = (c * NV + i) * dj + j0;
-                if (R.inside(j))
-                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(place + i * TH)),
-                                 "l"(R.base + j)
-                                 : "memory");
+                for (int i = 0; i < NV; i++) copy(i);
+            } else {
+#pragma unroll
+                for (int i = 0; i < NV; i++)
+                    if (R.inside((c * NV + i) * dj + j0)) copy(i);
             }
         }
         cp_async_commit();
     };
     auto load = [&](int c) {
+        if (full(c)) {
+            const uint4 *src = R.base + (c * NV * dj + j0);
 #pragma unroll
-        for (int i = 0; i < NV; i++) raw[i] = R.load((c * NV + i) * dj + j0);
+            for (int i = 0; i < NV; i++)
+                asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(raw[i].x), "=r"(raw[i].y), "=r"(raw[i].z), "=r"(raw[i].w)
+                             : "l"(src + i * dj)
+                             : "memory");
+        } else {
+#pragma unroll
+            for (int i = 0; i < NV; i++) raw[i] = R.load((c * NV + i) * dj + j0);
+        }
     };
     auto take = [&](int c) {             // chunk c to registers, absent vectors as -inf
         constexpr uint32_t NI = Vec<T>::NINF;
         cp_async_wait<RING_DEPTH - 1>();
         const uint4 *place = s_ring + (c % RING_DEPTH) * (NV * TH) + tid;
+        if (full(c)) {
 #pragma unroll
-        for (int i = 0; i < NV; i++)
-            raw[i] = R.inside((c * NV + i) * dj + j0) ? place[i * TH] : make_uint4(NI, NI, NI, NI);
+            for (int i = 0; i < NV; i++) raw[i] = place[i * TH];
+        } else {
+#pragma unroll
+            for (int i = 0; i < NV; i++)
+                raw[i] = R.inside((c * NV + i) * dj + j0) ? place[i * TH] : make_uint4(NI, NI, NI, NI);
+        }
     };
     float lp = 0.0f, H = 0.0f;
     float4 st = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -553,9 +575,19 @@ __global__ void __launch_bounds__(TH, TH == 256 ? (POLICY ? 3 : 4) : POLICY ? 5 
                     take(c);
                     fetch(c - RING_DEPTH);
                 }
+                if (same && full(c)) {
+                    uint4 *dst = dv + jc;
 #pragma unroll
-                for (int i = 0; i < NV; i++)
-                    if (R.inside(jc + i * dj)) put(jc + i * dj, raw[i], true);
+                    for (int i = 0; i < NV; i++) {
+                        float f[W];
+                        grad_vec<T, ETA>(raw[i], g, k22, f);
+                        __stcs(dst + i * dj, Vec<T>::make(f));
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < NV; i++)
+                        if (R.inside(jc + i * dj)) put(jc + i * dj, raw[i], true);
+                }
             }
             // the target's entry again, by the thread that has just written its vector
             if ((int)((y + R.head) / W) % dj == j0) store_grad(d + y, g.gy);

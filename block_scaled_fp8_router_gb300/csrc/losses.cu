@@ -679,7 +679,7 @@ static RowPlan row_plan(int64_t N, int64_t V, int w, bool aligned, bool policy)
 {
     const int64_t nvec = (V + w - 1) / w + (aligned ? 0 : 1);
     RowPlan p = {32, policy && nvec > 4096 ? 2 : 1, 8, false};
-    const int64_t fill = 3LL * sm_count();
+    const int64_t fill = 4LL * sm_count();
     const int most = policy || 8 * N <= fill ? 256 : 128;
     while (p.threads < most && p.threads * 8 < nvec) p.threads *= 2;
     while (p.C < 8 && N * p.C * 2 <= fill && (int64_t)p.C * p.threads < nvec) p.C *= 2;

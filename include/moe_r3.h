@@ -604,7 +604,8 @@ moe_status moe_combine_slots(const uint16_t *out_slots, const int32_t *slot_to_s
  *     g = (0 if clipped else -A r) + kl_coef (1 - exp(q)),
  *   in the logits' type (bf16: rounded once, to nearest even), row stride
  *   ld_d.  dlogits may be logits itself (the gradient replaces them).
- *   The row is read from memory once where the chip can hold it.
+ *   The row is read from memory once; a long row's second reading comes
+ *   from L2.
  * workspace: moe_policy_loss_workspace_size(N, V) bytes, 16-byte aligned; its
  * contents need no initialisation.  N may be 0: stats are 0.
  * Errors: as above, and SHAPE (clip_low, clip_high, kl_coef, entropy_coef,

@@ -41,7 +41,8 @@ constexpr int MAX_CTAS = 160;
 constexpr int SLOT_COLS = 256;
 constexpr size_t SLOT_FLOATS = (size_t)TM * SLOT_COLS;
 
-enum Mode { LOGITS, DX, DW };
+// BOTH: DW's tiles by the first CTAs, DX's by the others, in one launch
+enum Mode { LOGITS, DX, DW, BOTH };
 
 // CL = 2: a pair of CTAs takes two row tiles of one column tile.  Each loads its
 // own A tile and half of the B tile; one thread of the first CTA issues MMAs of
@@ -49,7 +50,7 @@ enum Mode { LOGITS, DX, DW };
 template <Mode MODE, int BN, int CL>
 struct Cfg {
     static constexpr int P = MODE == LOGITS ? 1 : 3;              // parts of A
-    static constexpr bool A_MN = MODE == DW, B_MN = MODE != LOGITS;
+    static constexpr bool A_MN = MODE == DW, B_MN = MODE != LOGITS;  // (BOTH: A as the CTA's product has it)
     static constexpr int B_TILE = BN / CL * KB * 2;               // this CTA's share
     // places of the rings, 192 KB in all at most: a block needs one B and P A tiles
     static constexpr int NB = B_TILE == 32768 ? (P == 3 ? 3 : 4) : B_TILE == 16384 ? (P == 3 ? 4 : 6) : 8;
@@ -79,6 +80,7 @@ struct Params {
     int64_t blocks;           // K blocks in all
     int gran;                 // cuts fall on multiples of this many blocks
     int split;                // CTAs that share a tile's K blocks
+    int first;                // BOTH: CTAs of this product, the grid's first
     float *c;                 // [M, N]
     int direct_tma;           // whole tiles may be stored through tm_c
     int32_t *dev_status;
@@ -203,7 +205,7 @@ __device__ __forceinline__ uint64_t sw128_desc_mn(uint32_t saddr)
 }
 
 // fp32 accumulate, A = B = bf16, majorness bits 15 / 16 (1 = MN-major)
-constexpr uint32_t idesc_bf16(int M, int N, bool a_mn, bool b_mn)
+__host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool a_mn, bool b_mn)
 {
     return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) |
            ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
@@ -232,14 +234,24 @@ __device__ __forceinline__ void drain(uint64_t *full, int size, uint32_t n)
 // partial tiles meet in shared memory (CL = 1)
 template <Mode MODE, int BN, int CL, bool SPLIT>
 __global__ void __launch_bounds__(GEMM_THREADS, 1)
-    gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
-                const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ CUtensorMap tm_slots, const Params p)
+    gemm_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ CUtensorMap tm_b0,
+                const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ CUtensorMap tm_slots,
+                const __grid_constant__ CUtensorMap tm_b1, const __grid_constant__ Params p0,
+                const __grid_constant__ Params p1)
 {
     using C = Cfg<MODE, BN, CL>;
     extern __shared__ uint8_t smem_raw[];
     Smem<MODE, BN, CL> &s =
         *reinterpret_cast<Smem<MODE, BN, CL> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     static_assert(CL == 1 || !SPLIT, "one or the other");
+    static_assert(MODE != BOTH || SPLIT, "clusters for DW");
+    // BOTH: CTAs below p1.first take DW (p1, A through tm_slots, B through
+    // tm_b1) in clusters of p1.split, the others DX (p0), in the same clusters
+    // but each on its own tiles
+    const bool second = MODE == BOTH && (int)blockIdx.x < p1.first;
+    const Params &p = second ? p1 : p0;
+    const CUtensorMap &tm_a = second ? tm_slots : tm_a0, &tm_b = second ? tm_b1 : tm_b0;
+    const bool a_mn = MODE == BOTH ? second : C::A_MN, split = MODE == BOTH ? second : SPLIT;
     static_assert(sizeof(s.a) + sizeof(s.b) >= (size_t)TM * BN * 4, "a partial tile fits the rings");
     const int rank = CL > 1 ? (int)(blockIdx.x % CL) : 0;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -278,14 +290,15 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
     const uint32_t tmem = s.tmem_base;
     volatile int *abort_flag = &s.abort_flag;
     int64_t b0, b1;
-    const int share = SPLIT ? (int)(blockIdx.x % (unsigned)p.split) : 0;
-    if (SPLIT) {
+    const int share = split ? (int)(blockIdx.x % (unsigned)p.split) : 0;
+    if (split) {
         const int64_t t0 = (int64_t)(blockIdx.x / (unsigned)p.split) * p.nkb;
         b0 = t0 + (int64_t)p.nkb * share / p.split;
         b1 = t0 + (int64_t)p.nkb * (share + 1) / p.split;
     } else {
-        b0 = run_begin(p.blocks, p.gran, gridDim.x / CL, blockIdx.x / CL);
-        b1 = run_begin(p.blocks, p.gran, gridDim.x / CL, blockIdx.x / CL + 1);
+        const int first = MODE == BOTH ? p1.first : 0;
+        b0 = run_begin(p.blocks, p.gran, (gridDim.x - first) / CL, (blockIdx.x - first) / CL);
+        b1 = run_begin(p.blocks, p.gran, (gridDim.x - first) / CL, (blockIdx.x - first) / CL + 1);
     }
 
     if (warp == GEMM_PRODUCER) {
@@ -319,10 +332,10 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
                     if (rank == 0) mbar_arrive_expect_tx(&s.afull[sa], CL * A_TILE);
                     if (CL > 1) {
                         const uint32_t bar = first_cta(&s.afull[sa]);
-                        if (C::A_MN) tma_load_4d_pair(s.a[sa], &tm_a, 0, kb * KB, mt * (TM / 64), q, bar);
+                        if (a_mn) tma_load_4d_pair(s.a[sa], &tm_a, 0, kb * KB, mt * (TM / 64), q, bar);
                         else tma_load_3d_pair(s.a[sa], &tm_a, kb * KB * 2, mt * TM, q, bar);
                     } else {
-                        if (C::A_MN) tma_load_4d(s.a[sa], &tm_a, 0, kb * KB, mt * (TM / 64), q, &s.afull[sa]);
+                        if (a_mn) tma_load_4d(s.a[sa], &tm_a, 0, kb * KB, mt * (TM / 64), q, &s.afull[sa]);
                         else tma_load_3d(s.a[sa], &tm_a, kb * KB * 2, mt * TM, q, &s.afull[sa]);
                     }
                     ja++;
@@ -352,7 +365,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
         // the whole warp goes through the loop (addresses and descriptors stay
         // in uniform registers), one elected thread issues
         if (rank == 0) {
-            constexpr uint32_t IDESC = idesc_bf16(CL * TM, BN, C::A_MN, C::B_MN);
+            const uint32_t IDESC = idesc_bf16(CL * TM, BN, a_mn, C::B_MN);
             auto commit = [](uint64_t *bar) {
                 if (CL > 1) mma_commit_pair(bar);
                 else mma_commit(bar);
@@ -361,9 +374,10 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
                 return __all_sync(0xFFFFFFFFu, wait_or_abort(bar, parity, abort_flag, p.dev_status));
             };
             const bool leader = elect_one();
-            constexpr uint64_t A_STEP = C::A_MN ? 2048 >> 4 : 32 >> 4, B_STEP = C::B_MN ? 2048 >> 4 : 32 >> 4;
+            const uint64_t A_STEP = a_mn ? 2048 >> 4 : 32 >> 4;
+            constexpr uint64_t B_STEP = C::B_MN ? 2048 >> 4 : 32 >> 4;
             const uint32_t a0 = smem_u32(s.a[0]), bb0 = smem_u32(s.b[0]);
-            const uint64_t adesc0 = C::A_MN ? sw128_desc_mn(a0) : sw128_desc(a0);
+            const uint64_t adesc0 = a_mn ? sw128_desc_mn(a0) : sw128_desc(a0);
             const uint64_t bdesc0 = C::B_MN ? sw128_desc_mn(bb0) : sw128_desc(bb0);
             int sa = 0, sb = 0, buf = 0;                 // places in the rings, and their phases
             uint32_t pa = 0, pb = 0, pt = 1;
@@ -464,7 +478,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
                 }
             }
             if (aborted) break;
-            if (SPLIT) {
+            if (split) {
                 // this CTA's partial tile over the rings, which nothing uses any
                 // more: row r's 16-byte chunk c at chunk c ^ (r & 15)
                 float4 *part = reinterpret_cast<float4 *>(s.a) + (32 * q + lane) * (BN / 4);
@@ -523,7 +537,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
         const int tile = (int)(blockIdx.x / (unsigned)p.split), mt = tile / p.n_tiles, nt = tile - mt * p.n_tiles;
         const int r0 = TM * share / p.split, r1 = min(TM * (share + 1) / p.split, p.M - mt * TM);
         const uint32_t base = smem_u32(s.a);
-        for (int i = r0 * (BN / 4) + threadIdx.x; i < r1 * (BN / 4) && !*abort_flag; i += GEMM_THREADS) {
+        for (int i = r0 * (BN / 4) + threadIdx.x; split && i < r1 * (BN / 4) && !*abort_flag; i += GEMM_THREADS) {
             const int r = i / (BN / 4), c = i % (BN / 4), col = nt * BN + 4 * c;
             if (col >= p.N) continue;
             const uint32_t at = base + (uint32_t)(r * (BN / 4) + (c ^ (r & 15))) * 16;
@@ -788,11 +802,16 @@ static bool map_mn_major(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap *m, 
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+template <typename T>
+struct Same {
+    using type = T;
+};
+
 // a launch that may begin while the kernel before it on the stream ends (pdl:
 // that kernel is one of this file's, which lets it)
 template <typename... Args>
 static cudaError_t launch_chained(void (*kernel)(Args...), dim3 grid, int cluster, int threads, size_t smem, bool pdl,
-                                  cudaStream_t st, Args... args)
+                                  cudaStream_t st, typename Same<Args>::type... args)
 {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
@@ -811,19 +830,8 @@ static cudaError_t launch_chained(void (*kernel)(Args...), dim3 grid, int cluste
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-template <Mode MODE, int BN, int CL, bool SPLIT>
-static moe_status launch_cl(const Plan &pl, const void *a, const void *b, float *c, int M, int N, int K, float *slots,
-                            int32_t *dev_status, bool pdl, cudaStream_t st)
+static Params params(const Plan &pl, float *c, int M, int N, int32_t *dev_status)
 {
-    using C = Cfg<MODE, BN, CL>;
-    static const auto enc = encode_fn();      // the driver's encoder: looked up once
-    if (!enc) return MOE_ERR_CUDA;
-    CUtensorMap ma, mb, mc, ms;
-    const bool ok_a = C::A_MN ? map_mn_major(enc, &ma, a, pad64(M), K, C::P, TM / 64, 4)
-                              : map_k_major(enc, &ma, a, MODE == DX ? pad64(K) : K, M, C::P, TM);
-    const bool ok_b = C::B_MN ? map_mn_major(enc, &mb, b, N, K, 1, BN / 64 / CL, 3)
-                              : make_map(enc, &mb, b, (uint64_t)K * 2, N, BN / CL);
-    if (!ok_a || !ok_b) return MOE_ERR_CUDA;
     Params p;
     p.M = M;
     p.N = N;
@@ -832,31 +840,129 @@ static moe_status launch_cl(const Plan &pl, const void *a, const void *b, float 
     p.blocks = pl.blocks;
     p.gran = pl.gran;
     p.split = pl.split;
+    p.first = 0;
     p.c = c;
     p.direct_tma = N % 4 == 0 && aligned16(c);
     p.dev_status = dev_status;
-    if (p.direct_tma) {
-        if (!make_map_f32_store(enc, &mc, c, (uint64_t)N, (uint64_t)M)) return MOE_ERR_CUDA;
-    }
-    const int ctas = pl.runs * CL;
-    if (pl.slots) {
-        if (!make_map_f32_store(enc, &ms, slots, SLOT_COLS, (uint64_t)ctas * 2 * TM)) return MOE_ERR_CUDA;
-    } else {
-        ms = p.direct_tma ? mc : ma;     // not used
-    }
-    if (!p.direct_tma) mc = ms;          // not used
+    return p;
+}
+
+// the maps of A ([parts][rows][k] for logits and dx, [parts][k][rows] for dW_r)
+// and of one CTA's share of B ([N][K] for logits, else [K][N])
+static bool map_a(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap *m, Mode mode, const void *a, int M, int K)
+{
+    if (mode == DW) return map_mn_major(enc, m, a, pad64(M), K, 3, TM / 64, 4);
+    return map_k_major(enc, m, a, mode == DX ? pad64(K) : K, M, mode == DX ? 3 : 1, TM);
+}
+static bool map_b(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap *m, Mode mode, const void *b, int N, int K, int share)
+{
+    return mode == LOGITS ? make_map(enc, m, b, (uint64_t)K * 2, N, share) : map_mn_major(enc, m, b, N, K, 1, share / 64, 3);
+}
+
+static PFN_cuTensorMapEncodeTiled_v12000 encoder()
+{
+    static const auto enc = encode_fn();      // the driver's: looked up once
+    return enc;
+}
+
+template <Mode MODE, int BN, int CL, bool SPLIT>
+static cudaError_t start(int ctas, int cluster, const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &c,
+                         const CUtensorMap &slots, const CUtensorMap &b1, const Params &p0, const Params &p1, bool pdl,
+                         cudaStream_t st)
+{
     constexpr size_t smem = sizeof(Smem<MODE, BN, CL>) + 1024;
     static_assert(smem <= 227 * 1024, "shared memory");
     static std::atomic<uint64_t> done{0};
-    if (allow_smem((const void *)gemm_kernel<MODE, BN, CL, SPLIT>, (int)smem, done) != cudaSuccess) return MOE_ERR_CUDA;
-    if (launch_chained(gemm_kernel<MODE, BN, CL, SPLIT>, dim3(ctas), SPLIT ? pl.split : CL, GEMM_THREADS, smem, pdl, st, (const CUtensorMap)ma,
-                       (const CUtensorMap)mb, (const CUtensorMap)mc, (const CUtensorMap)ms, (const Params)p) !=
-        cudaSuccess)
+    const cudaError_t e = allow_smem((const void *)gemm_kernel<MODE, BN, CL, SPLIT>, (int)smem, done);
+    if (e != cudaSuccess) return e;
+    return launch_chained(gemm_kernel<MODE, BN, CL, SPLIT>, dim3(ctas), cluster, GEMM_THREADS, smem, pdl, st, a, b, c,
+                          slots, b1, p0, p1);
+}
+
+template <Mode MODE, int BN, int CL, bool SPLIT>
+static moe_status launch_cl(const Plan &pl, const void *a, const void *b, float *c, int M, int N, int K, float *slots,
+                            int32_t *dev_status, bool pdl, cudaStream_t st)
+{
+    const auto enc = encoder();
+    if (!enc) return MOE_ERR_CUDA;
+    const Params p = params(pl, c, M, N, dev_status);
+    const int ctas = pl.runs * CL;
+    CUtensorMap ma, mb, mc, ms;
+    if (!map_a(enc, &ma, MODE, a, M, K) || !map_b(enc, &mb, MODE, b, N, K, BN / CL)) return MOE_ERR_CUDA;
+    mc = ms = ma;                         // where not used
+    if (!SPLIT && p.direct_tma && !make_map_f32_store(enc, &mc, c, (uint64_t)N, (uint64_t)M)) return MOE_ERR_CUDA;
+    if (pl.slots && !make_map_f32_store(enc, &ms, slots, SLOT_COLS, (uint64_t)ctas * 2 * TM)) return MOE_ERR_CUDA;
+    if (start<MODE, BN, CL, SPLIT>(ctas, SPLIT ? pl.split : CL, ma, mb, mc, ms, mb, p, p, pdl, st) != cudaSuccess)
         return MOE_ERR_CUDA;
     if (pl.slots && launch_chained(reduce_kernel<BN>, dim3((unsigned)(pl.m_tiles * pl.n_tiles * CL), TM / 8), 1, 256, 0,
                                    true, st, (const float *)slots, p, pl.runs, CL) != cudaSuccess)
         return MOE_ERR_CUDA;
     return launch_status();
+}
+
+// dx and dW_r in one launch where neither fills the GPU for long: clusters of
+// pw.split CTAs on dW_r's tiles, the other CTAs on whole tiles of dx, all
+// resident at once.  False where two launches are estimated to be shorter.
+// Measured, one launch against two (split_kernel included): 4093 x 2048 x 64
+// 23.6 us against 30, 5000 x 4096 x 128 39.5 against 49, 4096 x 5120 x 160 48
+// against 60, 1 x 2048 x 64 11 against 13; dW_r alone, which keeps the same cut
+// so that its bits do not depend on what else is asked for, 31.7 against 25.5
+// at 5000 x 4096 x 128.
+static bool plan_both(int T, int d, int E, Plan *px, Plan *pw, int *first, int *ctas)
+{
+    int64_t best = plan(DX, T, d, E).clocks + plan(DW, E, d, T).clocks;
+    bool found = false;
+    for (int bn = 256; bn >= 128; bn /= 2)
+        for (int s = 1; s <= 8; s *= 2) {
+            Plan x = plan_bn(T, d, E, bn, 3), w = plan_bn(E, d, T, bn, 3);
+            const int64_t tx = (int64_t)((T + TM - 1) / TM) * x.n_tiles, tw = (int64_t)((E + TM - 1) / TM) * w.n_tiles;
+            const int64_t cap = (s == 1 ? sm_count() : clusters_at_once(s)) * (int64_t)s;
+            int64_t nx = (cap - tw * s) / s * s;
+            if (s > w.nkb || nx < s) continue;
+            if (nx > (tx + s - 1) / s * s) nx = (tx + s - 1) / s * s;
+            const int64_t t = 6 * bn + 400;
+            const int64_t cw = (w.nkb + s - 1) / s * t + (s > 1 ? 4000 : 0), cx = (tx + nx - 1) / nx * (x.nkb * t + 600);
+            if ((cw > cx ? cw : cx) >= best) continue;
+            best = cw > cx ? cw : cx;
+            found = true;
+            x.cl = w.cl = 1;
+            x.m_tiles = (T + TM - 1) / TM;
+            w.m_tiles = (E + TM - 1) / TM;
+            x.blocks = tx * x.nkb;
+            w.blocks = tw * w.nkb;
+            x.gran = x.nkb;
+            w.gran = w.nkb;
+            x.split = 1;
+            w.split = s;
+            x.slots = w.slots = false;
+            x.runs = (int)(tx < sm_count() ? tx : sm_count());     // on its own
+            w.runs = (int)(tw * s);
+            *px = x;
+            *pw = w;
+            *first = (int)(tw * s);
+            *ctas = (int)(tw * s + nx);
+        }
+    return found;
+}
+
+template <int BN>
+static moe_status launch_both(const Plan &px, const Plan &pw, int first, int ctas, const uint16_t *parts,
+                              const uint16_t *x, const uint16_t *w, int T, int d, int E, float *dx, float *dw,
+                              int32_t *dev_status, cudaStream_t st)
+{
+    const auto enc = encoder();
+    if (!enc) return MOE_ERR_CUDA;
+    CUtensorMap xa, xb, xc, wa, wb;
+    if (!map_a(enc, &xa, DX, parts, T, E) || !map_b(enc, &xb, DX, w, d, E, BN) ||
+        !make_map_f32_store(enc, &xc, dx, (uint64_t)d, (uint64_t)T) || !map_a(enc, &wa, DW, parts, E, T) ||
+        !map_b(enc, &wb, DW, x, d, T, BN))
+        return MOE_ERR_CUDA;
+    const Params p0 = params(px, dx, T, d, dev_status);
+    Params p1 = params(pw, dw, E, d, dev_status);
+    p1.first = first;
+    return start<BOTH, BN, 1, true>(ctas, pw.split, xa, xb, xc, wa, wb, p0, p1, true, st) == cudaSuccess
+               ? launch_status()
+               : MOE_ERR_CUDA;
 }
 
 template <Mode MODE, int BN>
@@ -871,10 +977,9 @@ static moe_status launch_bn(const Plan &pl, const void *a, const void *b, float 
 }
 
 template <Mode MODE>
-static moe_status launch(const void *a, const void *b, float *c, int M, int N, int K, float *slots,
+static moe_status launch(const Plan &pl, const void *a, const void *b, float *c, int M, int N, int K, float *slots,
                          int32_t *dev_status, bool pdl, cudaStream_t st)
 {
-    const Plan pl = plan(MODE, M, N, K);
     if (pl.bn == 256) return launch_bn<MODE, 256>(pl, a, b, c, M, N, K, slots, dev_status, pdl, st);
     if constexpr (MODE == LOGITS) {
         if (pl.bn == 64) return launch_bn<MODE, 64>(pl, a, b, c, M, N, K, slots, dev_status, pdl, st);
@@ -895,7 +1000,7 @@ size_t router_logits_workspace(int T, int d, int E)
 moe_status router_logits(const uint16_t *x, const uint16_t *w, int T, int d, int E, float *logits, void *ws,
                          int32_t *dev_status, cudaStream_t st)
 {
-    return rg::launch<rg::LOGITS>(x, w, logits, T, E, d, (float *)ws, dev_status, false, st);
+    return rg::launch<rg::LOGITS>(rg::plan(rg::LOGITS, T, E, d), x, w, logits, T, E, d, (float *)ws, dev_status, false, st);
 }
 
 size_t router_backward_workspace(int T, int d, int E)
@@ -915,8 +1020,20 @@ moe_status router_backward(const uint16_t *x, const uint16_t *w, const float *dl
     const int64_t n = (int64_t)T * (Ep / 8);
     split_kernel<<<(unsigned)((n + 255) / 256), 256, 0, st>>>(dl, T, E, Ep, parts);
     moe_status s = launch_status();
-    if (s == MOE_OK && dx) s = launch<DX>(parts, w, dx, T, d, E, slots, dev_status, true, st);
-    if (s == MOE_OK && dw) s = launch<DW>(parts, x, dw, E, d, T, slots, dev_status, true, st);
+    Plan px, pw;
+    int first, ctas;
+    if (s != MOE_OK) return s;
+    // (one output alone is summed in the same order as beside the other)
+    if (!plan_both(T, d, E, &px, &pw, &first, &ctas)) {
+        px = plan(DX, T, d, E);
+        pw = plan(DW, E, d, T);
+    } else if (dx && dw) {
+        return px.bn == 256
+                   ? launch_both<256>(px, pw, first, ctas, parts, x, w, T, d, E, dx, dw, dev_status, st)
+                   : launch_both<128>(px, pw, first, ctas, parts, x, w, T, d, E, dx, dw, dev_status, st);
+    }
+    if (dx) s = launch<DX>(px, parts, w, dx, T, d, E, slots, dev_status, true, st);
+    if (s == MOE_OK && dw) s = launch<DW>(pw, parts, x, dw, E, d, T, slots, dev_status, true, st);
     return s;
 }
 

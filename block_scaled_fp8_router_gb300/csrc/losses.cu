@@ -194,10 +194,15 @@ struct Row {
 
 struct PolicyArgs {
     const float *old_lp, *adv, *ref_lp, *w;
-    float clip_lo, clip_hi, beta, eta, inv_tau;
+    float clip_lo, clip_hi, beta, eta;
     int64_t ld_d;
     struct Ws *ws;
+    float num, norm;        // the gradient's scale is num / norm; norm 0: the rows' CTAs add up w; below: scale is in ws
 };
+
+// Up to this many weights each row's CTA adds them up itself, which saves a
+// launch (256 rows of 32768: 28 us a call against 31, most of it the host's).
+constexpr int64_t NORM_ROWS = 512;
 
 // workspace: the weights' sum, and per row w pg, w kl, w H and w [clipped]
 struct Ws {
@@ -219,35 +224,50 @@ __device__ __forceinline__ float kl_term(float q)
 }
 
 // sum of the weights in a fixed order
-__global__ void __launch_bounds__(1024) policy_norm_kernel(const float *__restrict__ w, int64_t N, float norm,
-                                                           float num, Ws *ws)
+__global__ void __launch_bounds__(1024) policy_norm_kernel(const float *__restrict__ w, int64_t N, float num, Ws *ws)
 {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     __shared__ Sum2 s_v[32];
     const int tid = threadIdx.x;
-    if (norm == 0.0f && w) {
-        Sum2 v = {0.0f, 0.0f};
-        for (int64_t i = tid; i < N; i += 8192) {
-            float q[8];
+    Sum2 v = {0.0f, 0.0f};
+    for (int64_t i = tid; i < N; i += 8192) {
+        float q[8];
 #pragma unroll
-            for (int u = 0; u < 8; u++) q[u] = i + 1024 * u < N ? __ldg(w + i + 1024 * u) : 0.0f;
+        for (int u = 0; u < 8; u++) q[u] = i + 1024 * u < N ? __ldg(w + i + 1024 * u) : 0.0f;
 #pragma unroll
-            for (int u = 0; u < 8; u++) add(v, q[u]);
-        }
-        warp_sum2(v);
-        if ((tid & 31) == 0) s_v[tid >> 5] = v;
-        __syncthreads();
-        if (tid >= 32) return;
-        v = s_v[tid];
-        warp_sum2(v);
-        norm = v.hi + v.lo;
-    } else if (norm == 0.0f) {
-        norm = (float)N;
+        for (int u = 0; u < 8; u++) add(v, q[u]);
     }
+    warp_sum2(v);
+    if ((tid & 31) == 0) s_v[tid >> 5] = v;
+    __syncthreads();
+    if (tid >= 32) return;
+    v = s_v[tid];
+    warp_sum2(v);
+    const float norm = v.hi + v.lo;
     if (tid == 0) {
         ws->norm = norm;
         ws->scale = norm != 0.0f ? num / norm : 0.0f;
     }
+}
+
+// the scale of the gradients, by a whole warp
+__device__ __forceinline__ float grad_scale_of(const PolicyArgs &a, int64_t N, int lane)
+{
+    if (a.norm < 0.0f) return __ldcg(&a.ws->scale);
+    float norm = a.norm;
+    if (norm == 0.0f) {
+        Sum2 v = {0.0f, 0.0f};
+        for (int64_t i = lane; i < N; i += 256) {
+            float q[8];
+#pragma unroll
+            for (int u = 0; u < 8; u++) q[u] = i + 32 * u < N ? __ldg(a.w + i + 32 * u) : 0.0f;
+#pragma unroll
+            for (int u = 0; u < 8; u++) add(v, q[u]);
+        }
+        warp_sum2(v);
+        norm = v.hi + v.lo;
+    }
+    return norm != 0.0f ? a.num / norm : 0.0f;
 }
 
 __device__ __forceinline__ uint32_t cluster_rank()
@@ -520,7 +540,7 @@ __global__ void __launch_bounds__(TH, TH == 256 ? (POLICY ? 3 : 4) : POLICY ? 5 
                     }
                     st = make_float4(w * (clipped ? p1 : p0), w * kl, w * H, clipped ? w : 0.0f);
                     asm volatile("griddepcontrol.wait;" ::: "memory");
-                    const float coef = w * __ldcg(&a.ws->scale);
+                    const float coef = w * grad_scale_of(a, N, lane);
                     const float q = coef / s.S;
                     g.c = s.c;
                     g.B0 = q * a.eta * LN2;
@@ -611,15 +631,20 @@ __global__ void __launch_bounds__(TH, TH == 256 ? (POLICY ? 3 : 4) : POLICY ? 5 
     }
 }
 
-// the rows' parts added in a fixed order
-__global__ void __launch_bounds__(1024) policy_stats_kernel(const Ws *__restrict__ ws, int64_t N, float beta, float eta,
+// the rows' parts, and the weights w where given, added in a fixed order
+// (norm 0: the weights' sum; below: it is in ws)
+__global__ void __launch_bounds__(1024) policy_stats_kernel(const Ws *__restrict__ ws, const float *__restrict__ w,
+                                                            int64_t N, float norm, float beta, float eta,
                                                             float *__restrict__ stats)
 {
-    __shared__ Sum2 s_tot[32][4];
+    __shared__ Sum2 s_tot[32][5];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    Sum2 v[4] = {};
+    Sum2 v[5] = {};
     for (int64_t i = tid; i < N; i += 4096) {
         float4 q[4];
+        float x[4];
+#pragma unroll
+        for (int u = 0; u < 4; u++) x[u] = w && i + 1024 * u < N ? __ldg(w + i + 1024 * u) : 0.0f;
 #pragma unroll
         for (int u = 0; u < 4; u++)
             q[u] = i + 1024 * u < N ? ws->row[i + 1024 * u] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -629,15 +654,16 @@ __global__ void __launch_bounds__(1024) policy_stats_kernel(const Ws *__restrict
             add(v[1], q[u].y);
             add(v[2], q[u].z);
             add(v[3], q[u].w);
+            add(v[4], x[u]);
         }
     }
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
+    for (int i = 0; i < 5; i++) {
         warp_sum2(v[i]);
         if (lane == 0) s_tot[warp][i] = v[i];
     }
     __syncthreads();
-    if (warp < 4) {
+    if (warp < 5) {
         Sum2 m = s_tot[lane][warp];
         warp_sum2(m);
         __syncwarp();
@@ -645,7 +671,9 @@ __global__ void __launch_bounds__(1024) policy_stats_kernel(const Ws *__restrict
     }
     __syncthreads();
     if (tid == 0) {
-        const float norm = ws->norm, in = norm != 0.0f ? 1.0f / norm : 0.0f;
+        if (norm == 0.0f) norm = s_tot[0][4].hi + s_tot[0][4].lo;
+        else if (norm < 0.0f) norm = ws->norm;
+        const float in = norm != 0.0f ? 1.0f / norm : 0.0f;
         const Sum2 pg = s_tot[0][0], kl = s_tot[0][1], H = s_tot[0][2], cl = s_tot[0][3];
         // pg + beta kl - eta H, the products' errors kept
         Sum2 l = pg;
@@ -713,7 +741,7 @@ static cudaError_t launch_rows_nv(const RowPlan &p, const T *logits, int64_t N, 
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cfg.attrs = attr;
-    cfg.numAttrs = POLICY ? 2 : 1;
+    cfg.numAttrs = POLICY && a.norm < 0.0f ? 2 : 1;     // after policy_norm_kernel
     return cudaLaunchKernelEx(&cfg, kernel, logits, N, V, ld, targets, t64, k2, p.C, logprobs, entropy, dlogits, a,
                               dev_status);
 }
@@ -812,11 +840,16 @@ MOE_API moe_status moe_policy_loss(const void *logits, int logits_dtype, int64_t
         return cudaMemsetAsync(stats, 0, 6 * sizeof(float), st) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
     Ws *ws = (Ws *)workspace;
     PolicyArgs a = {old_logprobs, advantages, ref_logprobs, weights, 1.0f - clip_low, 1.0f + clip_high, kl_coef,
-                    entropy_coef, 1.0f / temperature, ld_d, ws};
+                    entropy_coef, ld_d, ws, grad_scale * (1.0f / temperature), norm};
+    const bool sum = norm == 0.0f && weights, first = sum && N > NORM_ROWS;
+    if (!sum && norm == 0.0f) a.norm = (float)N;
+    if (first) a.norm = -1.0f;
     const float k2 = (float)(1.4426950408889634 / (double)temperature);
     const int t64 = target_bits == 64;
-    policy_norm_kernel<<<1, 1024, 0, st>>>(weights, N, norm, grad_scale * a.inv_tau, ws);
-    if (cudaPeekAtLastError() != cudaSuccess) return launch_status();
+    if (first) {
+        policy_norm_kernel<<<1, 1024, 0, st>>>(weights, N, a.num, ws);
+        if (cudaPeekAtLastError() != cudaSuccess) return launch_status();
+    }
     cudaError_t e;
     if (logits_dtype == MOE_LOGITS_BF16)
         e = entropy_coef != 0.0f
@@ -831,6 +864,7 @@ MOE_API moe_status moe_policy_loss(const void *logits, int logits_dtype, int64_t
                 : launch_rows<float, true, false>((const float *)logits, N, V, ld, targets, t64, k2, logprobs,
                                                   nullptr, (float *)dlogits, a, dev_status, st);
     if (e != cudaSuccess) return MOE_ERR_CUDA;
-    policy_stats_kernel<<<1, 1024, 0, st>>>(ws, N, ref_logprobs ? kl_coef : 0.0f, entropy_coef, stats);
+    policy_stats_kernel<<<1, 1024, 0, st>>>(ws, sum && !first ? weights : nullptr, N, a.norm,
+                                            ref_logprobs ? kl_coef : 0.0f, entropy_coef, stats);
     return launch_status();
 }

@@ -358,3 +358,28 @@ def test_rows_beyond_32_bit_offsets(L, V):
     assert torch.equal(L.moe_token_logprobs(src, y)[0], L.moe_token_logprobs(x, y)[0])
     L.moe_policy_loss(x, y, old, adv, weights=w, dlogits=x)
     assert torch.equal(x, a[2])
+
+
+@pytest.mark.parametrize("N", [1, 33, 511, 512, 513, 2100])
+def test_policy_norm_at_every_row_count(L, N):
+    """The weights' sum as the norm, by the rows or before them: the stats and
+    the gradient equal those of the call that is given it; a negative sum and
+    one of zero hold too."""
+    x, y, old, adv, ref, w = _policy_case(N, 100, F32, 70 + N)
+    for v in (w, -w, torch.zeros_like(w)):
+        norm = v.double().sum()
+        st, lp, dl = L.moe_policy_loss(x, y, old, adv, ref_logprobs=ref, weights=v, kl_coef=0.1, entropy_coef=0.02)
+        assert abs(st[5].double() - norm) <= 2.0 ** -23 * abs(norm)
+        if v is w:
+            st1, lp1, dl1 = L.moe_policy_loss(x, y, old, adv, ref_logprobs=ref, weights=v, kl_coef=0.1,
+                                              entropy_coef=0.02, norm=float(st[5]))
+            assert torch.equal(st, st1) and torch.equal(lp, lp1)
+            keep = st, dl
+            # norms one step apart and five roundings after them, 6 * 2^-23;
+            # the target's entry cancels, so 2^-18 of the largest
+            assert (dl - dl1).abs().max() <= 2.0 ** -18 * dl.abs().max()
+        elif v.any():
+            # numerators and norm change their signs together
+            assert torch.equal(st[:5], keep[0][:5]) and (dl - keep[1]).abs().max() <= 2.0 ** -18 * dl.abs().max()
+        else:
+            assert st.eq(0).all() and dl.eq(0).all()

@@ -693,12 +693,15 @@ __global__ void __launch_bounds__(1024) policy_stats_kernel(const Ws *__restrict
 // How a row is spread: threads of a CTA, CTAs of a cluster, vectors of a chunk.
 // A CTA takes a warp per 256 vectors: up to four for log-probabilities (8192 x
 // 16384 bf16: 50 us, 61 with eight warps, 58 with two), up to eight for
-// gradients.  A longer row streams, one CTA a row where the rows fill the GPU:
-// an exchange costs more than it saves (8192 x 131072 log-probabilities 0.31
-// ms, 0.34 with two CTAs, 0.60 with eight); two for the gradient of long rows,
-// so that the rows in work stay within L2 until they are read again (4096 x
-// 131072: 0.32 ms against 0.37).  More CTAs as rows get few, while each thread
-// keeps a vector.
+// gradients.  A longer row streams in even chunks of at most eight vectors a
+// thread (chunks of eight and the rest: 4096 x 20000 bf16 gradients 91 us
+// against 73, 4096 x 10000 log-probabilities 24 against 19: an absent vector
+// costs its exponentials), one CTA a row where the rows fill the GPU: an
+// exchange costs more than it saves (8192 x 131072 log-probabilities 0.30 ms,
+// 0.34 with two CTAs, 0.60 with eight); two for the gradient of rows beyond
+// 8192 vectors, so that the rows in work stay within L2 until they are read
+// again (4096 x 131072: 0.32 ms against 0.37; but 4096 x 60000 0.16 with one,
+// 0.19 with two).  More CTAs as rows get few, while each thread keeps a vector.
 struct RowPlan {
     int threads, C, NV;
     bool ring;
@@ -706,13 +709,16 @@ struct RowPlan {
 static RowPlan row_plan(int64_t N, int64_t V, int w, bool aligned, bool policy)
 {
     const int64_t nvec = (V + w - 1) / w + (aligned ? 0 : 1);
-    RowPlan p = {32, policy && nvec > 4096 ? 2 : 1, 8, false};
+    RowPlan p = {32, policy && nvec > 8192 ? 2 : 1, 8, false};
     const int64_t fill = 4LL * sm_count();
     const int most = policy || 8 * N <= fill ? 256 : 128;
     while (p.threads < most && p.threads * 8 < nvec) p.threads *= 2;
     while (p.C < 8 && N * p.C * 2 <= fill && (int64_t)p.C * p.threads < nvec) p.C *= 2;
-    p.ring = policy && (int64_t)p.C * p.threads * p.NV < nvec;      // (then there are 256 threads)
-    while (p.NV > 1 && (int64_t)p.C * p.threads * (p.NV / 2) >= nvec) p.NV /= 2;
+    const int64_t v = (nvec + p.C * p.threads - 1) / (p.C * p.threads), chunks = (v + 7) / 8;     // of a thread
+    p.ring = policy && chunks > 1;                                  // (then there are 256 threads)
+    p.NV = (int)((v + chunks - 1) / chunks);
+    if (p.NV == 3) p.NV = 4;
+    if (p.NV > 4 && (policy ? !p.ring : p.threads > 128)) p.NV += p.NV % 2;     // (no kernel of five or seven)
     return p;
 }
 
@@ -760,9 +766,16 @@ static cudaError_t launch_rows(const T *logits, int64_t N, int64_t V, int64_t ld
     p.NV == 1 ? MOE_ROWS(TH, 1, false)                                                                                \
     : p.NV == 2 ? MOE_ROWS(TH, 2, false)                                                                              \
     : p.NV == 4 ? MOE_ROWS(TH, 4, false)                                                                              \
+    : p.NV == 6 ? MOE_ROWS(TH, 6, false)                                                                              \
                 : MOE_ROWS(TH, 8, false)
     if constexpr (POLICY) {
-        if (p.ring) return MOE_ROWS(256, 8, true);
+        if (p.ring)
+            return p.NV == 5 ? MOE_ROWS(256, 5, true)
+                 : p.NV == 6 ? MOE_ROWS(256, 6, true)
+                 : p.NV == 7 ? MOE_ROWS(256, 7, true)
+                             : MOE_ROWS(256, 8, true);
+    } else if (p.NV == 5 || p.NV == 7) {
+        return p.NV == 5 ? MOE_ROWS(128, 5, false) : MOE_ROWS(128, 7, false);
     }
     return p.threads > 128 ? (MOE_ROWS_NV(256)) : (MOE_ROWS_NV(128));
 #undef MOE_ROWS_NV

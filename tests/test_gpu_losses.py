@@ -383,3 +383,21 @@ def test_policy_norm_at_every_row_count(L, N):
             assert torch.equal(st[:5], keep[0][:5]) and (dl - keep[1]).abs().max() <= 2.0 ** -18 * dl.abs().max()
         else:
             assert st.eq(0).all() and dl.eq(0).all()
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("v", [1, 2, 3, 5, 6, 7, 9, 11, 13, 15, 17, 19, 25])
+def test_rows_of_every_chunk(L, dt, v):
+    """v vectors of 16 bytes a thread of 128 (log-probabilities) or 256
+    (gradients), the last one short, rows on odd starts and on vectors."""
+    W = 8 if dt == BF else 4
+    N = 320
+    for V, ld, off in ((128 * W * v - W - 1, None, 3), (128 * W * v, None, 0)):
+        x, g = _rows(N, V, dt, v, ld=ld, off=off)
+        y, _ = _inputs(N, V, g)
+        y[::7] = V - 1
+        y[1::7] = 0
+        _check_logprobs(L, x, y, 1.1)
+    for V, off, eta in ((256 * W * v - W - 1, 3, 0.01), (256 * W * v, 0, 0.0)):
+        x, y, old, adv, ref, w = _policy_case(N, V, dt, v, 1.0, None, off, 1)
+        _check_policy(L, x, y, old, adv, ref, w, 1.0, 0.1, eta)

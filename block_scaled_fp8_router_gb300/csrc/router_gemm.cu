@@ -628,6 +628,12 @@ __global__ void __launch_bounds__(256) reduce_kernel(const float *__restrict__ s
     }
 }
 
+__device__ __forceinline__ float rest(float v, float part)
+{
+    const float r = v - part;
+    return r == r ? r : 0.0f;
+}
+
 // dl [T, E] fp32 -> parts [3][T][Ep] bf16 by truncation, zeros in columns E ..
 // Ep - 1; one thread per eight columns
 __global__ void __launch_bounds__(256) split_kernel(const float *__restrict__ dl, int T, int E, int Ep,
@@ -650,6 +656,10 @@ __global__ void __launch_bounds__(256) split_kernel(const float *__restrict__ dl
         for (int u = 0; u < 8; u++) v[u] = e + u < E ? __ldg(dl + t * E + e + u) : 0.0f;
     }
     const int64_t plane = (int64_t)T * Ep;
+    // infinities and NaN are their first part, the others 0 (NaN made quiet:
+    // a low payload would be cut off)
+#pragma unroll
+    for (int u = 0; u < 8; u++) v[u] = v[u] == v[u] ? v[u] : __uint_as_float(0x7FC00000u);
 #pragma unroll
     for (int q = 0; q < 3; q++) {
         uint32_t w[4];
@@ -657,8 +667,8 @@ __global__ void __launch_bounds__(256) split_kernel(const float *__restrict__ dl
         for (int u = 0; u < 4; u++) {
             const uint32_t lo = __float_as_uint(v[2 * u]) & 0xFFFF0000u, hi = __float_as_uint(v[2 * u + 1]) & 0xFFFF0000u;
             w[u] = (lo >> 16) | hi;
-            v[2 * u] -= __uint_as_float(lo);
-            v[2 * u + 1] -= __uint_as_float(hi);
+            v[2 * u] = rest(v[2 * u], __uint_as_float(lo));
+            v[2 * u + 1] = rest(v[2 * u + 1], __uint_as_float(hi));
         }
         *reinterpret_cast<uint4 *>(parts + q * plane + t * Ep + e) = make_uint4(w[0], w[1], w[2], w[3]);
     }

@@ -107,6 +107,30 @@ def test_router_backward_dense_keeps_24_bits(L):
     assert not torch.isfinite(dw[3]).any() and not torch.isfinite(dw[5]).any()
 
 
+@pytest.mark.parametrize("T,d,E", [(200, 256, 64), (1500, 512, 256), (4000, 7168, 256)])
+def test_router_backward_dense_infinities(L, T, d, E):
+    """Infinite and NaN gradients give what the fp32 product gives: the sign of
+    the infinity, NaN where two meet, a NaN of any payload."""
+    g = torch.Generator(device="cuda").manual_seed(T)
+    dl = torch.randn(T, E, device="cuda", generator=g)
+    inf = float("inf")
+    dl[9, 5], dl[20, 2], dl[30, 1], dl[30, 2] = inf, -inf, inf, -inf
+    dl.view(torch.int32)[7, 3] = 0x7F800001
+    x = torch.ones(T, d, device="cuda", dtype=torch.bfloat16)
+    w = torch.ones(E, d, device="cuda", dtype=torch.bfloat16)
+    w[:, 1::2] = -1
+    dx, dw = L.moe_router_backward_dense(x, w, dl)
+    sign = w[0].float()
+    assert torch.equal(dx[9], inf * sign) and torch.equal(dx[20], -inf * sign)
+    assert dx[30].isnan().all() and dx[7].isnan().all()
+    assert dw[5].eq(inf).all() and dw[1].eq(inf).all() and dw[2].eq(-inf).all() and dw[3].isnan().all()
+    rest = torch.ones(T, dtype=torch.bool, device="cuda")
+    rest[[7, 9, 20, 30]] = False
+    cols = torch.ones(E, dtype=torch.bool, device="cuda")
+    cols[[1, 2, 3, 5]] = False
+    assert dx[rest].isfinite().all() and dw[cols].isfinite().all()
+
+
 def test_dense_empty(L):
     x, w, _ = _xw(0, 128, 8, 1)
     assert L.moe_router_logits(x, w).shape == (0, 8)

@@ -11,13 +11,20 @@
 // (l_v - c) k2 and not l_v k2 - c k2: the largest logit's t is then exactly 0.
 //
 // token_rows_kernel: one cluster of C CTAs per row.  A row's 16-byte vectors
-// are dealt to the threads of the cluster, up to NV of them kept in registers
-// from the one read to the gradient's write (a longer row's remainder is read
-// again, from L2).  A warp takes its maximum, sums 2^t and 2^t t against it;
+// are dealt to the threads of the cluster, NV of them kept in registers from
+// the one read to the gradient's write; a longer row goes through a ring of
+// asynchronous copies in shared memory, and its gradient reads it again, from
+// L2.  A warp takes its maximum, sums 2^t and 2^t t against it;
 // the warps' sums are joined in shared memory, the CTAs' through one 16-byte
 // message to every CTA of the cluster (st.async on an mbarrier), always in the
 // same order.  So a row costs one CTA barrier, one exchange and one more CTA
 // barrier, and several CTAs per SM keep HBM busy across them.
+//
+// Bound: HBM for long rows, one exponential a logit (two with a gradient) close
+// behind.  Measured: log-probabilities of 8192 x 131072 bf16 0.30 ms (7.1
+// TB/s read), the gradient of as many rows, a quarter without weight, 0.61 ms
+// (6.1 TB/s read once and written); short or few rows by latency, 7 x 50001
+// fp32 4.6 us, 256 x 32768 13 us (back to back in a CUDA graph).
 #include "losses.cuh"
 
 #include <math.h>

@@ -22,6 +22,12 @@
 // go to its two fp32 slots in the workspace; reduce_kernel adds a tile's slots
 // in order.  The launches are chained programmatically (a kernel sets itself
 // up while the one before it ends).
+//
+// Bound: the rate at which MMAs of 128 x 256 x 16 issue (128 clocks each at
+// best; blocks of four take 730 to 830, of twelve 1960 or, over two SMs, 1820).
+// Measured at 8192 x 7168 x 256: logits 36 us (0.83 PFLOP/s), both gradients 122 us
+// (0.49 PFLOP/s of fp32 products, three times that in MMAs); 4093 x 2048 x 64:
+// 9 and 20 us.
 #include "tcgen05.cuh"
 #include "router_dense.cuh"
 

@@ -376,7 +376,7 @@ __device__ __forceinline__ void grad_vec(const uint4 &v, const RowGrad &g, uint6
 // of a row with more than one chunk of NV vectors a thread; ETA: with an
 // entropy bonus.
 template <typename T, int TH, int NV, bool RING, bool POLICY, bool ETA>
-__global__ void __launch_bounds__(TH, TH == 256 ? (POLICY ? 3 : 4) : POLICY ? 5 : 8)
+__global__ void __launch_bounds__(TH, TH == 256 ? (POLICY ? 3 : 4) : POLICY ? (RING ? 6 : 5) : 8)
     token_rows_kernel(const T *logits, int64_t N, int64_t V, int64_t ld, const void *__restrict__ targets, int t64,
                       float k2, int C, float *__restrict__ logprobs, float *__restrict__ entropy, T *dlogits,
                       const PolicyArgs a, int32_t *dev_status)
@@ -700,7 +700,9 @@ __global__ void __launch_bounds__(1024) policy_stats_kernel(const Ws *__restrict
 // How a row is spread: threads of a CTA, CTAs of a cluster, vectors of a chunk.
 // A CTA takes a warp per 256 vectors: up to four for log-probabilities (8192 x
 // 16384 bf16: 50 us, 61 with eight warps, 58 with two), up to eight for
-// gradients.  A longer row streams in even chunks of at most eight vectors a
+// gradients of rows beyond 2048 vectors or few in number (4096 x 10000: four
+// warps 44 us, eight 53, where three rows an SM wait for their joins; 4096 x
+// 32768: 100 and 96).  A longer row streams in even chunks of at most eight vectors a
 // thread (chunks of eight and the rest: 4096 x 20000 bf16 gradients 91 us
 // against 73, 4096 x 10000 log-probabilities 24 against 19: an absent vector
 // costs its exponentials), one CTA a row where the rows fill the GPU: an
@@ -718,11 +720,11 @@ static RowPlan row_plan(int64_t N, int64_t V, int w, bool aligned, bool policy)
     const int64_t nvec = (V + w - 1) / w + (aligned ? 0 : 1);
     RowPlan p = {32, policy && nvec > 8192 ? 2 : 1, 8, false};
     const int64_t fill = 4LL * sm_count();
-    const int most = policy || 8 * N <= fill ? 256 : 128;
+    const int most = (policy && nvec > 2048) || 8 * N <= fill ? 256 : 128;
     while (p.threads < most && p.threads * 8 < nvec) p.threads *= 2;
     while (p.C < 8 && N * p.C * 2 <= fill && (int64_t)p.C * p.threads < nvec) p.C *= 2;
     const int64_t v = (nvec + p.C * p.threads - 1) / (p.C * p.threads), chunks = (v + 7) / 8;     // of a thread
-    p.ring = policy && chunks > 1;                                  // (then there are 256 threads)
+    p.ring = policy && chunks > 1;                                  // (then there are 128 or 256 threads)
     p.NV = (int)((v + chunks - 1) / chunks);
     if (p.NV == 3) p.NV = 4;
     if (p.NV > 4 && (policy ? !p.ring : p.threads > 128)) p.NV += p.NV % 2;     // (no kernel of five or seven)
@@ -775,16 +777,18 @@ static cudaError_t launch_rows(const T *logits, int64_t N, int64_t V, int64_t ld
     : p.NV == 4 ? MOE_ROWS(TH, 4, false)                                                                              \
     : p.NV == 6 ? MOE_ROWS(TH, 6, false)                                                                              \
                 : MOE_ROWS(TH, 8, false)
+#define MOE_ROWS_RING(TH)                                                                                             \
+    p.NV == 5 ? MOE_ROWS(TH, 5, true)                                                                                 \
+    : p.NV == 6 ? MOE_ROWS(TH, 6, true)                                                                               \
+    : p.NV == 7 ? MOE_ROWS(TH, 7, true)                                                                               \
+                : MOE_ROWS(TH, 8, true)
     if constexpr (POLICY) {
-        if (p.ring)
-            return p.NV == 5 ? MOE_ROWS(256, 5, true)
-                 : p.NV == 6 ? MOE_ROWS(256, 6, true)
-                 : p.NV == 7 ? MOE_ROWS(256, 7, true)
-                             : MOE_ROWS(256, 8, true);
+        if (p.ring) return p.threads > 128 ? (MOE_ROWS_RING(256)) : (MOE_ROWS_RING(128));
     } else if (p.NV == 5 || p.NV == 7) {
         return p.NV == 5 ? MOE_ROWS(128, 5, false) : MOE_ROWS(128, 7, false);
     }
     return p.threads > 128 ? (MOE_ROWS_NV(256)) : (MOE_ROWS_NV(128));
+#undef MOE_ROWS_RING
 #undef MOE_ROWS_NV
 #undef MOE_ROWS
 }

@@ -410,7 +410,8 @@ __global__ void __launch_bounds__(256) balance_rows_kernel(const BalanceArgs a)
             uint64_t sa = 0, da = 0;
 #pragma unroll
             for (int i = 0; i < NP; i++) {
-                // e = exp(-l) up to 2^127, where s is 0; s = 1 / (1 + e), s (1 - s) = e s s
+                // e = exp(-l) up to 2^127, where s is 0; s = 1 / (1 + e), s (1 - s) = s (s e),
+                // in this order: s s underflows where the slope is still about s
                 float x, y;
                 unpack2(mul2(l2[i], nk2), x, y);
                 asm("min.NaN.f32 %0, %0, %1;" : "+f"(x) : "f"(127.0f));
@@ -420,7 +421,23 @@ __global__ void __launch_bounds__(256) balance_rows_kernel(const BalanceArgs a)
                 const uint64_t s = pack2(rcp(x), rcp(y));
                 sa = add2(sa, s);
                 da = fma2(pack2(f[2 * i], f[2 * i + 1]), s, da);
-                s2[i] = mul2(mul2(s, s), e);
+                s2[i] = mul2(s, mul2(s, e));
+            }
+            if (m <= 0.0f) {
+                // all scores e^m and less, and their sum underflows with them: up to
+                // e^-m, s = a / (1 + a e^m) with a = e^(l - m), and 1 - s = 1 / (1 + a e^m)
+                const float em = ex2(sh * LOG2E);
+                const uint64_t em2 = pack2(em, em);
+                sa = da = 0;
+#pragma unroll
+                for (int i = 0; i < NP; i++) {
+                    float x, y;
+                    unpack2(fma2(e2[i], em2, one2), x, y);
+                    const uint64_t r = pack2(rcp(x), rcp(y)), s = mul2(e2[i], r);
+                    sa = add2(sa, s);
+                    da = fma2(pack2(f[2 * i], f[2 * i + 1]), s, da);
+                    s2[i] = mul2(s, r);
+                }
             }
             tot = gsum<G>(sum_pair(acc));
             unpack2(gsum2<G>(pack2(sum_pair(sa), sum_pair(da))), S, dot);

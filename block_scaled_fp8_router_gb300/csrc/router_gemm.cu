@@ -662,21 +662,27 @@ __global__ void __launch_bounds__(256) split_kernel(const float *__restrict__ dl
         for (int u = 0; u < 8; u++) v[u] = e + u < E ? __ldg(dl + t * E + e + u) : 0.0f;
     }
     const int64_t plane = (int64_t)T * Ep;
-    // infinities and NaN are their first part, the others 0 (NaN made quiet:
-    // a low payload would be cut off)
+    // infinities and NaN are their first part (NaN made quiet: a low payload
+    // would be cut off).  A part that comes out 0 where dl is not is the least
+    // bf16 of dl's sign, 2^-133: 0 times an infinity of x or W_r would be a NaN
+    // beside the other parts' infinity, this gives the same infinity
+    uint32_t least[8];
 #pragma unroll
-    for (int u = 0; u < 8; u++) v[u] = v[u] == v[u] ? v[u] : __uint_as_float(0x7FC00000u);
+    for (int u = 0; u < 8; u++) {
+        v[u] = v[u] == v[u] ? v[u] : __uint_as_float(0x7FC00000u);
+        least[u] = (__float_as_uint(v[u]) & 0x80000000u) | (v[u] != 0.0f ? 0x00010000u : 0u);
+    }
 #pragma unroll
     for (int q = 0; q < 3; q++) {
-        uint32_t w[4];
+        uint32_t w[8];
 #pragma unroll
-        for (int u = 0; u < 4; u++) {
-            const uint32_t lo = __float_as_uint(v[2 * u]) & 0xFFFF0000u, hi = __float_as_uint(v[2 * u + 1]) & 0xFFFF0000u;
-            w[u] = (lo >> 16) | hi;
-            v[2 * u] = rest(v[2 * u], __uint_as_float(lo));
-            v[2 * u + 1] = rest(v[2 * u + 1], __uint_as_float(hi));
+        for (int u = 0; u < 8; u++) {
+            w[u] = __float_as_uint(v[u]) & 0xFFFF0000u;
+            v[u] = rest(v[u], __uint_as_float(w[u]));
+            if ((w[u] & 0x7FFFFFFFu) == 0) w[u] = least[u];
         }
-        *reinterpret_cast<uint4 *>(parts + q * plane + t * Ep + e) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4 *>(parts + q * plane + t * Ep + e) =
+            make_uint4((w[0] >> 16) | w[1], (w[2] >> 16) | w[3], (w[4] >> 16) | w[5], (w[6] >> 16) | w[7]);
     }
 }
 

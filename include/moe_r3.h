@@ -662,7 +662,8 @@ moe_status moe_policy_loss(const void *logits, int logits_dtype, int64_t N, int6
  *   dw_router[e,i] = sum_t d_logits[t,e] x[t,i]  (nullable), both fp32.
  *   d_logits enters the tensor cores as three bf16 parts whose sum holds its
  *   24 significant bits (parts below the smallest normal bf16 excepted), so
- *   the products are those of fp32, infinities and NaN included.
+ *   the products are those of fp32, infinities and NaN of d_logits, x and
+ *   w_router included (0 times an infinity is NaN where d_logits is 0).
  * x [T,d], w_router [E,d] bf16; logits, d_logits [T,E], dx [T,d], dw_router
  * [E,d], losses [2] fp32; topk_ids [T,k], counts [B,E], seq_offsets [B+1]
  * int32; token_mask [T] uint8.  x, w_router, dx, dw_router 16-byte aligned.

@@ -62,3 +62,36 @@ def test_balance_sigmoid_low_experts(L):
     l[:, 5] = 1.0
     ids = torch.rand(T, E, device="cuda", generator=g).topk(3, 1).indices.int()
     _check_sigmoid(L, l, ids)
+
+
+# ---------------------------------------------------------- dense backward
+
+@pytest.mark.parametrize("T,d,E", [(200, 256, 64), (333, 384, 37), (1500, 512, 256), (4000, 7168, 256)])
+def test_router_backward_dense_infinite_operands(L, T, d, E):
+    """Infinities and NaN in x and W_r give what the products of fp32 give, also
+    against gradients of few bits (a part of theirs that is 0 times an infinity
+    is no NaN) and exact zeros (where it is one)."""
+    g = torch.Generator(device="cuda").manual_seed(T + E)
+    inf, nan = float("inf"), float("nan")
+    dl = torch.randn(T, E, device="cuda", generator=g)
+    dl[:, ::2] = dl[:, ::2].bfloat16().float()
+    dl[10:20] = 1.0
+    dl[20:25] = -0.5
+    dl[26] = 2.0 ** -100
+    dl[27] = -2.0 ** -126
+    dl[::7, 2] = 0.0
+    dl[40, 6] = inf
+    x = torch.randn(T, d, device="cuda", generator=g).bfloat16()
+    w = (0.05 * torch.randn(E, d, device="cuda", generator=g)).bfloat16()
+    x[12, 5], x[22, 9], x[26, 70], x[27, 71], x[30, 3], x[7, 100], x[40, 101] = inf, -inf, inf, inf, nan, inf, -inf
+    x[10, 200], x[21, 200] = inf, inf
+    w[2, 4], w[6, 8], w[2, 10], w[7, 10], w[8, 20] = inf, -inf, inf, inf, nan
+    dx, dw = L.moe_router_backward_dense(x, w, dl)
+    for got, a, b in ((dx, dl.double(), w.double()), (dw, dl.double().t(), x.double())):
+        want = a @ b
+        assert not want.isfinite().all()
+        assert torch.equal(got.isnan(), want.isnan())
+        assert torch.equal(got == inf, want == inf) and torch.equal(got == -inf, want == -inf)
+        fin = want.isfinite()
+        bound = (a.shape[1] + 64) * 2.0 ** -24 * (a.abs() @ b.abs()) + 2.0 ** -126
+        assert bool(((got.double() - want).abs()[fin] <= bound[fin]).all())

@@ -300,9 +300,13 @@ struct RowGrad {
 };
 
 // whether t of a logit held above -2^100 is finite for the shift c, so that 2^t t
-// needs no other care (rows whose largest logit is beyond 2^99, or -inf, and
-// temperatures below 1e-6 take the slower form)
-__device__ __forceinline__ bool plain_range(float c, float k2) { return fabsf(c) < 0x1p99f && k2 < 0x1p20f; }
+// needs no other care, and below -512, so that 2^t is still 0 (rows whose largest
+// logit is beyond 2^99, or -inf, and temperatures below 1e-6 or above 1e27 take
+// the slower form)
+__device__ __forceinline__ bool plain_range(float c, float k2)
+{
+    return fabsf(c) < 0x1p99f && k2 > 0x1p-90f && k2 < 0x1p20f;
+}
 
 // sums of one vector against the shift c = -nc, two elements at a time
 template <typename T, bool SLOW>

@@ -3,6 +3,8 @@ those of the operators' own tests, where they are derived."""
 import pytest
 import torch
 
+from tests import loss_refs as R
+
 pytestmark = pytest.mark.gpu
 SIGMOID = 1
 
@@ -95,3 +97,25 @@ def test_router_backward_dense_infinite_operands(L, T, d, E):
         fin = want.isfinite()
         bound = (a.shape[1] + 64) * 2.0 ** -24 * (a.abs() @ b.abs()) + 2.0 ** -126
         assert bool(((got.double() - want).abs()[fin] <= bound[fin]).all())
+
+
+# --------------------------------------------------------- vocabulary rows
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("tau", [1e20, 1e27, 1e30, 3e38])
+@pytest.mark.parametrize("V", [64, 5000])
+def test_masked_logits_at_high_temperatures(L, dt, tau, V):
+    """A logit of -inf has probability 0 whatever the temperature: the others
+    are uniform."""
+    g = torch.Generator(device="cuda").manual_seed(V)
+    x = (3 * torch.randn(6, V, device="cuda", generator=g)).to(dt)
+    x[:, 1::3] = float("-inf")
+    y = torch.tensor([0, 2, 3, 5, 6, 8], device="cuda")
+    lp, H = L.moe_token_logprobs(x, y, temperature=tau, entropy=True)
+    want, wH, _, _, _ = R.token_rows(x, y, tau)
+    # the rows' bound with a range of 0: 2^-22 8 + (V / 128 + 16) 2^-24 and lp's own roundings
+    rel = 2.0 ** -22 * 8 + (V / 128 + 16) * 2.0 ** -24
+    assert bool(((lp.double() - want).abs() <= rel + 2.0 ** -23 * want.abs()).all())
+    assert bool(((H.double() - wH).abs() <= rel * (2 * wH + 5) + 2.0 ** -23 * wH).all())
+    d = L.moe_policy_loss(x, y, lp, torch.ones(6, device="cuda"), temperature=tau, grad_scale=1e30)[2]
+    assert d[:, 1::3].eq(0).all() and d.isfinite().all()

@@ -799,13 +799,16 @@ static cudaError_t launch_rows(const T *logits, int64_t N, int64_t V, int64_t ld
 #undef MOE_ROWS
 }
 
+// log2(e) / temperature, infinite below 4.24e-39 (where every row would be NaN)
+static float scale_of(float temperature) { return (float)(1.4426950408889634 / (double)temperature); }
+
 static moe_status check_rows(const void *logits, int dtype, int64_t N, int64_t V, int64_t ld, const void *targets,
                              int target_bits, float temperature)
 {
     if (N < 0 || V < 1 || N >= (1LL << 28) || V >= (1LL << 31) || ld < V) return MOE_ERR_SHAPE;
     if (dtype != MOE_LOGITS_BF16 && dtype != MOE_LOGITS_F32) return MOE_ERR_SHAPE;
     if (target_bits != 32 && target_bits != 64) return MOE_ERR_SHAPE;
-    if (!isfinite(temperature) || !(temperature > 0.0f)) return MOE_ERR_SHAPE;
+    if (!isfinite(temperature) || !(temperature > 0.0f) || !isfinite(scale_of(temperature))) return MOE_ERR_SHAPE;
     if (N == 0) return MOE_OK;
     if (!logits || !targets) return MOE_ERR_NULL;
     const uintptr_t es = dtype == MOE_LOGITS_BF16 ? 2 : 4, ts = target_bits / 8;
@@ -825,7 +828,7 @@ MOE_API moe_status moe_token_logprobs(const void *logits, int logits_dtype, int6
     if (s != MOE_OK) return s;
     if (N == 0) return MOE_OK;
     if (!logprobs) return MOE_ERR_NULL;
-    const float k2 = (float)(1.4426950408889634 / (double)temperature);
+    const float k2 = scale_of(temperature);
     PolicyArgs a = {};
     cudaStream_t st = as_stream(stream);
     const int t64 = target_bits == 64;
@@ -874,7 +877,7 @@ MOE_API moe_status moe_policy_loss(const void *logits, int logits_dtype, int64_t
     const bool sum = norm == 0.0f && weights, first = sum && N > NORM_ROWS;
     if (!sum && norm == 0.0f) a.norm = (float)N;
     if (first) a.norm = -1.0f;
-    const float k2 = (float)(1.4426950408889634 / (double)temperature);
+    const float k2 = scale_of(temperature);
     const int t64 = target_bits == 64;
     if (first) {
         policy_norm_kernel<<<1, 1024, 0, st>>>(weights, N, a.num, ws);

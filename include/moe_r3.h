@@ -584,8 +584,8 @@ moe_status moe_combine_slots(const uint16_t *out_slots, const int32_t *slot_to_s
  *   entropy[t]  = LSE[t] - sum_v p[t,v] z[t,v]  (nullable).
  *   Sums in fp32, in an order fixed by N and V.
  * Errors: SHAPE (N < 0, V < 1, N >= 2^28, V >= 2^31, ld < V, dtype, target_bits,
- * temperature not finite and > 0), NULL, ALIGN (logits not aligned to its
- * element), CUDA.
+ * temperature not finite and > 0, or below 4.24e-39, where log2(e) / temperature
+ * is infinite), NULL, ALIGN (logits not aligned to its element), CUDA.
  *
  * moe_policy_loss -- the clipped policy loss with a KL term, and its gradient
  *   With lp = logprobs, H = entropy as above and, per token, old_logprobs,

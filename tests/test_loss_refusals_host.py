@@ -1,0 +1,40 @@
+"""Calls of the training-step losses that are refused on the host, before any
+CUDA call."""
+import ctypes
+
+import pytest
+
+
+@pytest.fixture(scope="module")
+def L():
+    import __graft_entry__
+    __graft_entry__.build()
+    from block_scaled_fp8_router_gb300 import moe_r3
+    return moe_r3
+
+
+NULL, SHAPE, ALIGN, WORKSPACE = 1, 2, 3, 4
+BASE = 0x100000
+
+
+def _at(off):
+    return ctypes.c_void_p(BASE + off)
+
+
+def _logprobs(L, N=4, tau=1.0, logprobs=_at(0x3000)):
+    return L._lib.moe_token_logprobs(_at(0), 1, N, 64, 64, _at(0x2000), 64, tau, logprobs, None, None, None)
+
+
+def _policy(L, N=4, V=64, ld=64, ldd=64, tau=1.0, bits=64, logits=_at(0), targets=_at(0x2000), old=_at(0x3000),
+            adv=_at(0x4000), ref=_at(0x5000), w=_at(0x6000), stats=_at(0x7000), logprobs=_at(0x8000), d=_at(0x9000),
+            work=_at(0x20000)):
+    return L._lib.moe_policy_loss(logits, 1, N, V, ld, targets, bits, old, adv, ref, w, tau, 0.2, 0.2, 0.0, 0.0, 0.0, 1.0,
+                                  stats, logprobs, d, ldd, work, 1 << 20, None, None)
+
+
+@pytest.mark.parametrize("tau", [4.2e-39, 1e-45, 0.0, -1.0, float("inf"), float("nan")])
+def test_temperatures_without_a_scale(L, tau):
+    """log2(e) / temperature has to be finite in fp32: every row would be NaN."""
+    assert _logprobs(L, tau=tau) == SHAPE and _policy(L, tau=tau) == SHAPE
+    assert _logprobs(L, N=0, tau=tau) == SHAPE
+    assert _logprobs(L, N=0, tau=4.3e-39) == 0

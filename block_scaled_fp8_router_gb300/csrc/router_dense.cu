@@ -666,7 +666,8 @@ MOE_API moe_status moe_balance_loss(const float *logits, const int32_t *topk_ids
 {
     if (T < 0 || E < 1 || E > 1024 || k < 1 || k > 32 || k > E || B < 1 || B > 65535) return MOE_ERR_SHAPE;
     if (B > 1 && !seq_offsets) return MOE_ERR_SHAPE;
-    if ((int64_t)T * k >= (1LL << 31)) return MOE_ERR_SHAPE;
+    // (the kernels step through the tokens in strides of up to 1024, in 32 bits)
+    if ((int64_t)T * k >= (1LL << 31) - 4096) return MOE_ERR_SHAPE;
     if (score_fn != MOE_SCORE_SOFTMAX && score_fn != MOE_SCORE_SIGMOID) return MOE_ERR_SHAPE;
     if (!isfinite(route_scale) || !isfinite(balance_coef) || !isfinite(z_coef) || !isfinite(grad_scale))
         return MOE_ERR_SHAPE;

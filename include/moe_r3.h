@@ -671,7 +671,7 @@ moe_status moe_policy_loss(const void *logits, int logits_dtype, int64_t N, int6
  * need no initialisation.  T may be 0: counts, losses and dw_router, where
  * given, are zeroed and the [T, .] arrays may be NULL.
  * Errors: NULL, SHAPE (also B < 1, B > 65535, B > 1 without seq_offsets,
- * coefficients not finite), ALIGN, WORKSPACE, CUDA.
+ * T k >= 2^31 - 4096, coefficients not finite), ALIGN, WORKSPACE, CUDA.
  * ---------------------------------------------------------------------- */
 size_t moe_router_logits_workspace_size(int T, int d, int E);
 moe_status moe_router_logits(const uint16_t *x, const uint16_t *w_router, int T, int d, int E, float *logits,

@@ -38,3 +38,11 @@ def test_temperatures_without_a_scale(L, tau):
     assert _logprobs(L, tau=tau) == SHAPE and _policy(L, tau=tau) == SHAPE
     assert _logprobs(L, N=0, tau=tau) == SHAPE
     assert _logprobs(L, N=0, tau=4.3e-39) == 0
+
+
+@pytest.mark.parametrize("T,k", [((1 << 31) - 1, 1), ((1 << 31) - 1024, 1), ((1 << 30) - 1, 2), ((1 << 28) - 500, 8)])
+def test_balance_loss_token_limit(L, T, k):
+    """Token numbers stay below 2^31 when a kernel steps past the last one."""
+    size = L.moe_balance_loss_workspace_size(T, 8, 1)
+    assert L._lib.moe_balance_loss(_at(0), _at(0), None, None, T, 8, k, 1, 0, 1, 1.0, 0.1, 0.0, 1.0, None, _at(0), _at(0),
+                                   _at(0), _at(0), size, None, None) == SHAPE

@@ -816,6 +816,22 @@ static moe_status check_rows(const void *logits, int dtype, int64_t N, int64_t V
     return MOE_OK;
 }
 
+static bool overlap(const void *a, int64_t na, const void *b, int64_t nb)
+{
+    const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+    return a && b && x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
+}
+
+// whether the gradient's rows lie over the logits' in a way other than row on
+// row: a row's CTAs would write what another row has yet to read
+static bool rows_clash(const void *logits, int64_t ld, const void *d, int64_t ld_d, int64_t N, int64_t V, int64_t es)
+{
+    if (logits == d) return N > 1 && ld != ld_d;
+    if (!d || ld != ld_d || !overlap(logits, ((N - 1) * ld + V) * es, d, ((N - 1) * ld + V) * es)) return false;
+    const int64_t off = ((int64_t)((intptr_t)d - (intptr_t)logits) / es % ld + ld) % ld;
+    return off < V || ld - off < V;
+}
+
 } // namespace moe
 
 using namespace moe;
@@ -865,10 +881,17 @@ MOE_API moe_status moe_policy_loss(const void *logits, int logits_dtype, int64_t
     cudaStream_t st = as_stream(stream);
     if (N > 0) {
         if (!old_logprobs || !advantages) return MOE_ERR_NULL;
-        if (dlogits && (uintptr_t)dlogits % (logits_dtype == MOE_LOGITS_BF16 ? 2 : 4)) return MOE_ERR_ALIGN;
+        const int es = logits_dtype == MOE_LOGITS_BF16 ? 2 : 4;
+        if (dlogits && (uintptr_t)dlogits % es) return MOE_ERR_ALIGN;
+        if (rows_clash(logits, ld, dlogits, ld_d, N, V, es)) return MOE_ERR_UNSUPPORTED;
     }
     if (!workspace || workspace_bytes < moe_policy_loss_workspace_size(N, V)) return MOE_ERR_WORKSPACE;
     if (!aligned16(workspace)) return MOE_ERR_ALIGN;
+    // every CTA of a row reads its numbers, one of them writes the log-probability
+    const float *in[4] = {old_logprobs, advantages, ref_logprobs, weights};
+    for (const float *p : in)
+        if (overlap(logprobs, 4 * N, p, 4 * N)) return MOE_ERR_UNSUPPORTED;
+    if (overlap(logprobs, 4 * N, targets, target_bits / 8 * N)) return MOE_ERR_UNSUPPORTED;
     if (N == 0)
         return cudaMemsetAsync(stats, 0, 6 * sizeof(float), st) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
     Ws *ws = (Ws *)workspace;

@@ -603,14 +603,16 @@ moe_status moe_combine_slots(const uint16_t *out_slots, const int32_t *slot_to_s
  *     (g (1[v = y] - p_v) + entropy_coef p_v (log p_v + H)),
  *     g = (0 if clipped else -A r) + kl_coef (1 - exp(q)),
  *   in the logits' type (bf16: rounded once, to nearest even), row stride
- *   ld_d.  dlogits may be logits itself (the gradient replaces them).
+ *   ld_d.  dlogits may be logits itself, with ld_d = ld (the gradient replaces
+ *   them); else no output overlaps an input or another output.
  *   The row is read from memory once; a long row's second reading comes
  *   from L2.
  * workspace: moe_policy_loss_workspace_size(N, V) bytes, 16-byte aligned; its
  * contents need no initialisation.  N may be 0: stats are 0.
  * Errors: as above, and SHAPE (clip_low, clip_high, kl_coef, entropy_coef,
  * norm or grad_scale not finite, clip bounds negative, norm < 0, ld_d < V),
- * WORKSPACE.
+ * WORKSPACE, UNSUPPORTED (logprobs over old_logprobs, advantages, ref_logprobs,
+ * weights or targets; dlogits over logits other than row on row).
  * ---------------------------------------------------------------------- */
 #define MOE_LOGITS_BF16 0
 #define MOE_LOGITS_F32 1

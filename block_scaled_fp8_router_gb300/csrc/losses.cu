@@ -250,7 +250,7 @@ __global__ void __launch_bounds__(1024) policy_norm_kernel(const float *__restri
     if (tid >= 32) return;
     v = s_v[tid];
     warp_sum2(v);
-    const float norm = v.hi + v.lo;
+    const float norm = total(v);
     if (tid == 0) {
         ws->norm = norm;
         ws->scale = norm != 0.0f ? num / norm : 0.0f;
@@ -272,7 +272,7 @@ __device__ __forceinline__ float grad_scale_of(const PolicyArgs &a, int64_t N, i
             for (int u = 0; u < 8; u++) add(v, q[u]);
         }
         warp_sum2(v);
-        norm = v.hi + v.lo;
+        norm = total(v);
     }
     return norm != 0.0f ? a.num / norm : 0.0f;
 }
@@ -684,21 +684,26 @@ __global__ void __launch_bounds__(1024) policy_stats_kernel(const Ws *__restrict
     }
     __syncthreads();
     if (tid == 0) {
-        if (norm == 0.0f) norm = s_tot[0][4].hi + s_tot[0][4].lo;
+        if (norm == 0.0f) norm = total(s_tot[0][4]);
         else if (norm < 0.0f) norm = ws->norm;
         const float in = norm != 0.0f ? 1.0f / norm : 0.0f;
         const Sum2 pg = s_tot[0][0], kl = s_tot[0][1], H = s_tot[0][2], cl = s_tot[0][3];
-        // pg + beta kl - eta H, the products' errors kept
+        // pg + beta kl - eta H, the products' errors kept (no kl in it for beta 0,
+        // where kl may be infinite)
         Sum2 l = pg;
-        const float bk = beta * kl.hi, eh = -eta * H.hi;
-        add(l, bk);
+        const float eh = -eta * H.hi;
+        if (beta != 0.0f) {
+            const float bk = beta * kl.hi;
+            add(l, bk);
+            l.lo += fmaf(beta, kl.hi, -bk) + beta * kl.lo;
+        }
         add(l, eh);
-        l.lo += fmaf(beta, kl.hi, -bk) + beta * kl.lo + fmaf(-eta, H.hi, -eh) - eta * H.lo;
-        stats[0] = (l.hi + l.lo) * in;
-        stats[1] = (pg.hi + pg.lo) * in;
-        stats[2] = (kl.hi + kl.lo) * in;
-        stats[3] = (H.hi + H.lo) * in;
-        stats[4] = (cl.hi + cl.lo) * in;
+        l.lo += fmaf(-eta, H.hi, -eh) - eta * H.lo;
+        stats[0] = total(l) * in;
+        stats[1] = total(pg) * in;
+        stats[2] = total(kl) * in;
+        stats[3] = total(H) * in;
+        stats[4] = total(cl) * in;
         stats[5] = norm;
     }
 }

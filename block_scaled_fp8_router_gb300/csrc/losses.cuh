@@ -89,6 +89,12 @@ __device__ __forceinline__ void add(Sum2 &s, const Sum2 &o)
     add(s, o.hi);
     s.lo = __fadd_rn(s.lo, o.lo);
 }
+// the sum: infinite (not NaN, as the error term then is) where it is beyond fp32
+__device__ __forceinline__ float total(const Sum2 &s)
+{
+    const float t = s.hi + s.lo;
+    return t == t ? t : s.hi;
+}
 __device__ __forceinline__ void warp_sum2(Sum2 &s)
 {
     for (int o = 16; o; o >>= 1) {

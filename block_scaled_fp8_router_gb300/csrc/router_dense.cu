@@ -203,11 +203,12 @@ __device__ __forceinline__ float sum_pair(uint64_t v)
     return x + y;
 }
 
-// running sum with its error (Kahan): s - c is the sum
+// running sum with its error (Kahan): s - c is the sum; the limit on c, which
+// has no effect while s is finite, lets a sum beyond fp32 stay infinite
 __device__ __forceinline__ void kahan(float &s, float &c, float v)
 {
     const float y = __fsub_rn(v, c), t = __fadd_rn(s, y);
-    c = __fsub_rn(__fsub_rn(t, s), y);
+    c = fminf(__fsub_rn(__fsub_rn(t, s), y), 0x1p126f);
     s = t;
 }
 
@@ -581,7 +582,7 @@ __global__ void __launch_bounds__(256) balance_rows_kernel(const BalanceArgs a)
             add(v, o);
         }
         warp_sum2(v);
-        if (lane == 0) a.losses[warp] = warp == 0 ? v.hi + v.lo : s_n > 0 ? (v.hi + v.lo) * (a.zeta / (float)s_n) : 0.0f;
+        if (lane == 0) a.losses[warp] = warp == 0 ? total(v) : s_n > 0 ? total(v) * (a.zeta / (float)s_n) : 0.0f;
     }
 }
 

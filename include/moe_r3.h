@@ -607,6 +607,7 @@ moe_status moe_combine_slots(const uint16_t *out_slots, const int32_t *slot_to_s
  *   them); else no output overlaps an input or another output.
  *   The row is read from memory once; a long row's second reading comes
  *   from L2.
+ *   A sum over the rows that is beyond fp32 gives an infinity.
  * workspace: moe_policy_loss_workspace_size(N, V) bytes, 16-byte aligned; its
  * contents need no initialisation.  N may be 0: stats are 0.
  * Errors: as above, and SHAPE (clip_low, clip_high, kl_coef, entropy_coef,
@@ -658,7 +659,8 @@ moe_status moe_policy_loss(const void *logits, int logits_dtype, int64_t N, int6
  *   token that is not counted and whose d_gates are all 0 gets zeros whatever
  *   its logits hold.  seq_offsets that decrease or leave [0,T] set
  *   MOE_DEV_ROWS (a token is then in some sequence or in none).
- *   Sums run in an order fixed by T, E, B and the device; counts are exact.
+ *   Sums run in an order fixed by T, E, B and the device; one beyond fp32 gives
+ *   an infinity.  Counts are exact.
  * moe_router_backward_dense  from d_logits [T,E]:
  *   dx[t,i] = sum_e d_logits[t,e] w_router[e,i]  (nullable),
  *   dw_router[e,i] = sum_t d_logits[t,e] x[t,i]  (nullable), both fp32.

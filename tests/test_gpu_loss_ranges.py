@@ -6,7 +6,7 @@ import torch
 from tests import loss_refs as R
 
 pytestmark = pytest.mark.gpu
-SIGMOID = 1
+SOFTMAX, SIGMOID = 0, 1
 
 
 @pytest.fixture(scope="module")
@@ -66,6 +66,19 @@ def test_balance_sigmoid_low_experts(L):
     _check_sigmoid(L, l, ids)
 
 
+def test_balance_sums_beyond_fp32(L):
+    """A z loss beyond fp32 is an infinity; the balance loss beside it stays."""
+    for T in (40, 3000):
+        g = torch.Generator(device="cuda").manual_seed(2)
+        l = torch.randn(T, 64, device="cuda", generator=g)
+        l[3, 4] = l[9, 1] = 1e30
+        ids = torch.rand(T, 64, device="cuda", generator=g).topk(2, 1).indices.int()
+        losses, _, d = L.moe_balance_loss(l, ids, SOFTMAX, 0.1, z_coef=1e-4)
+        want = R.balance(l, ids, SOFTMAX, 0.1)[0]
+        assert losses[1] == torch.inf and not d.isnan().any()
+        assert abs(float(losses[0]) - float(want[0])) <= 2.0 ** -18 * float(want[0])
+
+
 # ---------------------------------------------------------- dense backward
 
 @pytest.mark.parametrize("T,d,E", [(200, 256, 64), (333, 384, 37), (1500, 512, 256), (4000, 7168, 256)])
@@ -119,3 +132,23 @@ def test_masked_logits_at_high_temperatures(L, dt, tau, V):
     assert bool(((H.double() - wH).abs() <= rel * (2 * wH + 5) + 2.0 ** -23 * wH).all())
     d = L.moe_policy_loss(x, y, lp, torch.ones(6, device="cuda"), temperature=tau, grad_scale=1e30)[2]
     assert d[:, 1::3].eq(0).all() and d.isfinite().all()
+
+
+@pytest.mark.parametrize("N", [40, 1100])
+def test_policy_sums_beyond_fp32(L, N):
+    """A policy term that sums beyond fp32 is an infinity, not a NaN; the other means stay."""
+    g = torch.Generator(device="cuda").manual_seed(N)
+    x = torch.randn(N, 100, device="cuda", generator=g)
+    y = torch.randint(0, 100, (N,), device="cuda", generator=g)
+    lp, H = L.moe_token_logprobs(x, y, entropy=True)
+    adv = torch.full((N,), 1e38, device="cuda")
+    for s in (1, -1):
+        st = L.moe_policy_loss(x, y, lp, s * adv, weights=torch.ones(N, device="cuda"))[0]
+        assert st[0] == -s * torch.inf and st[1] == -s * torch.inf
+        assert st[2] == 0 and st[4] == 0 and st[5] == N
+        # a KL mean beyond fp32 stays out of the loss where its coefficient is 0
+        st2 = L.moe_policy_loss(x, y, lp, s * torch.ones(N, device="cuda"), ref_logprobs=lp + 100,
+                                weights=torch.full((N,), 1e4, device="cuda"))[0]
+        assert st2[2] == torch.inf and abs(float(st2[0]) + s) <= 2.0 ** -20
+        # N entropies summed in two fp32 numbers, one division, against their own fp32 values
+        assert abs(float(st[3]) - float(H.double().mean())) <= 2.0 ** -22 * float(H.double().mean())

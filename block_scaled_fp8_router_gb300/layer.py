@@ -244,37 +244,45 @@ class MoELayerFP8:
         fp32; dW_r [E, d] fp32).  Takes the place of router_backward where a
         loss reaches experts that were not chosen.  token_mask [T] and
         seq_offsets [B+1] as moe_balance_loss takes them.  The results stay
-        the layer's buffers until the next call."""
+        the layer's buffers until the next call.  They are made at the first
+        call and stay where they are; only counts moves when B exceeds all
+        before (at least doubled; the old memory is kept, so a CUDA graph
+        captured earlier stays valid)."""
         T = getattr(self, "_T_train", None)
         if T is None or self.mx or self.gathered:
             raise ValueError("router_losses needs a forward(train=True) of the fp32-scale sorted form")
-        E, d = self.w.E, self.w.d
         B = 1 if seq_offsets is None else seq_offsets.numel() - 1
-        r = getattr(self, "_rl", None)
-        if r is None or r["counts"].shape[0] != B:
-            e = lambda shape, dt: torch.empty(shape, dtype=dt, device=self.ids.device)
-            ws = max(L.moe_router_logits_workspace_size(self.T_max, d, E),
-                     L.moe_balance_loss_workspace_size(self.T_max, E, B),
-                     L.moe_router_backward_dense_workspace_size(self.T_max, d, E))
-            self._rl = r = dict(logits=e((self.T_max, E), torch.float32), dl=e((self.T_max, E), torch.float32),
-                                losses=e((2,), torch.float32), counts=e((B, E), torch.int32),
-                                dx=e((self.T_max, d), torch.float32), dw=e((E, d), torch.float32),
-                                ws=e((ws,), torch.uint8), ws_T=self.T_max)
-        if r["ws_T"] != T:      # the cut of the work, and with it the workspace, depends on T
-            need = max(L.moe_router_logits_workspace_size(T, d, E), L.moe_balance_loss_workspace_size(T, E, B),
-                       L.moe_router_backward_dense_workspace_size(T, d, E))
-            if need > r["ws"].numel():
-                r["ws"] = torch.empty((need,), dtype=torch.uint8, device=self.ids.device)
-            r["ws_T"] = T
+        r = self._router_loss_buffers(B)
+        counts = r["counts"][:B]
         x = self._x_train
         L.moe_router_logits(x, self.w.w_router, logits=r["logits"][:T], workspace=r["ws"], dev_status=self.dev_status)
         L.moe_balance_loss(r["logits"][:T], self.ids[:T], self.score_fn, balance_coef, z_coef=z_coef,
                            token_mask=token_mask, seq_offsets=seq_offsets, d_gates=d_gates, renorm=self.renorm,
-                           route_scale=self.route_scale, grad_scale=grad_scale, counts=r["counts"],
+                           route_scale=self.route_scale, grad_scale=grad_scale, counts=counts,
                            losses=r["losses"], d_logits=r["dl"][:T], workspace=r["ws"], dev_status=self.dev_status)
         L.moe_router_backward_dense(x, self.w.w_router, r["dl"][:T], dx=r["dx"][:T], dw_router=r["dw"],
                                     workspace=r["ws"], dev_status=self.dev_status)
-        return r["losses"], r["counts"], r["dx"][:T], r["dw"]
+        return r["losses"], counts, r["dx"][:T], r["dw"]
+
+    def _router_loss_buffers(self, B: int) -> dict:
+        """router_losses' buffers, kept for the layer's life: made for every T
+        up to T_max, counts for B sequences or more."""
+        E, d = self.w.E, self.w.d
+        e = lambda shape, dt: torch.empty(shape, dtype=dt, device=self.ids.device)
+        r = getattr(self, "_rl", None)
+        if r is None:
+            ws = L.moe_balance_loss_workspace_size(self.T_max, E, 65535)     # the most sequences of a call
+            for T in (*range(64, self.T_max, 64), self.T_max):               # the products' cuts go by tiles of 64 tokens
+                ws = max(ws, L.moe_router_logits_workspace_size(T, d, E),
+                         L.moe_router_backward_dense_workspace_size(T, d, E))
+            self._rl = r = dict(logits=e((self.T_max, E), torch.float32), dl=e((self.T_max, E), torch.float32),
+                                losses=e((2,), torch.float32), counts=e((max(B, 1), E), torch.int32),
+                                dx=e((self.T_max, d), torch.float32), dw=e((E, d), torch.float32),
+                                ws=e((ws,), torch.uint8), outgrown=[])
+        if r["counts"].shape[0] < B:
+            r["outgrown"].append(r["counts"])        # a captured graph may still write it
+            r["counts"] = e((max(B, 2 * r["counts"].shape[0]), E), torch.int32)
+        return r
 
     def _weight_grads(self, dy: torch.Tensor, T: int, events=None):
         """dW13, dW2 of the last train forward; `events` (seven CUDA events, for

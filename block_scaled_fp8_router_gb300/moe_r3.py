@@ -127,6 +127,16 @@ def _empty(shape, dtype, like: torch.Tensor) -> torch.Tensor:
     return torch.empty(shape, dtype=dtype, device=like.device)
 
 
+def _workspace(nbytes: int, like: torch.Tensor, stream) -> torch.Tensor:
+    """A call's own workspace, from the memory of the stream that the call runs
+    on: it is free again when the call returns, and only what follows on that
+    stream may have it then."""
+    if stream is None:
+        return _empty((nbytes,), torch.uint8, like)
+    with torch.cuda.stream(stream):
+        return _empty((nbytes,), torch.uint8, like)
+
+
 def moe_status_str(status: int) -> str:
     return _lib.moe_status_str(status).decode()
 
@@ -346,7 +356,7 @@ def moe_dispatch(topk_ids, E, rows=None, row_scales=None, expert_counts=None, ex
             _want(scales_sorted, torch.float32, (A, spr), "scales_sorted")
     need = moe_dispatch_workspace_size(T, k, E)
     if workspace is None:
-        workspace = _empty((need,), torch.uint8, dev)
+        workspace = _workspace(need, dev, stream)
     _check("moe_dispatch", _lib.moe_dispatch(
         _ptr(topk_ids), T, k, E, _ptr(rows), row_bytes, _ptr(row_scales), spr, _ptr(expert_counts),
         _ptr(expert_offsets), _ptr(sorted_to_slot), _ptr(slot_to_sorted), _ptr(rows_sorted),
@@ -418,7 +428,7 @@ def moe_grouped_ffn_fp8(xq_sorted, xs_sorted, expert_offsets, w13_q, w13_s, w2_q
     _want(out_sorted, torch.bfloat16, (max_rows, d), "out_sorted")
     need = moe_grouped_ffn_workspace_size(max_rows, d, F)
     if workspace is None:
-        workspace = _empty((need,), torch.uint8, xq_sorted)
+        workspace = _workspace(need, xq_sorted, stream)
     _check("moe_grouped_ffn_fp8", _lib.moe_grouped_ffn_fp8(
         _ptr(xq_sorted), _ptr(xs_sorted), _ptr(expert_offsets), max_rows, E, d, F, _ptr(w13_q), _ptr(w13_s),
         _ptr(w2_q), _ptr(w2_s), _ptr(out_sorted), _ptr(workspace), workspace.numel() * workspace.element_size(),
@@ -445,7 +455,7 @@ def moe_grouped_ffn_fp8_gathered(xq, xs, top_k, sorted_to_slot, expert_offsets, 
     out_slots = _empty((T * k, d), torch.bfloat16, xq) if out_slots is None else out_slots
     _want(out_slots, torch.bfloat16, (T * k, d), "out_slots")
     if workspace is None:
-        workspace = _empty((moe_grouped_ffn_workspace_size(T * k, d, F),), torch.uint8, xq)
+        workspace = _workspace(moe_grouped_ffn_workspace_size(T * k, d, F), xq, stream)
     _check("moe_grouped_ffn_fp8_gathered", _lib.moe_grouped_ffn_fp8_gathered(
         _ptr(xq), _ptr(xs), T, k, _ptr(sorted_to_slot), _ptr(expert_offsets), E, d, F, _ptr(w13_q), _ptr(w13_s),
         _ptr(w2_q), _ptr(w2_s), _ptr(out_slots), _ptr(workspace), workspace.numel() * workspace.element_size(),
@@ -476,7 +486,7 @@ def moe_grouped_ffn_mx(xq_sorted, x_exp, sorted_to_slot, top_k, expert_offsets, 
     out_sorted = _empty((max_rows, d), torch.bfloat16, xq_sorted) if out_sorted is None else out_sorted
     _want(out_sorted, torch.bfloat16, (max_rows, d), "out_sorted")
     if workspace is None:
-        workspace = _empty((moe_grouped_ffn_mx_workspace_size(max_rows, d, F),), torch.uint8, xq_sorted)
+        workspace = _workspace(moe_grouped_ffn_mx_workspace_size(max_rows, d, F), xq_sorted, stream)
     _check("moe_grouped_ffn_mx", _lib.moe_grouped_ffn_mx(
         _ptr(xq_sorted), _ptr(x_exp), _ptr(sorted_to_slot), T, top_k, _ptr(expert_offsets), max_rows, E, d, F,
         _ptr(w13_q), _ptr(w13_exp), _ptr(w2_q), _ptr(w2_exp), _ptr(out_sorted), _ptr(workspace),
@@ -528,7 +538,7 @@ def moe_grouped_ffn_nvfp4(xq_sorted, xs_sorted, x_enc, expert_offsets, w13_q, w1
     out_sorted = _empty((max_rows, d), torch.bfloat16, xq_sorted) if out_sorted is None else out_sorted
     _want(out_sorted, torch.bfloat16, (max_rows, d), "out_sorted")
     if workspace is None:
-        workspace = _empty((moe_grouped_ffn_nvfp4_workspace_size(max_rows, d, F),), torch.uint8, xq_sorted)
+        workspace = _workspace(moe_grouped_ffn_nvfp4_workspace_size(max_rows, d, F), xq_sorted, stream)
     _check("moe_grouped_ffn_nvfp4", _lib.moe_grouped_ffn_nvfp4(
         _ptr(xq_sorted), _ptr(xs_sorted), _ptr(x_enc), _ptr(expert_offsets), max_rows, E, d, F, _ptr(w13_q),
         _ptr(w13_sf_tiled), _ptr(w13_enc), _ptr(w2_q), _ptr(w2_sf_tiled), _ptr(w2_enc), _ptr(out_sorted),
@@ -549,7 +559,7 @@ def moe_grouped_ffn_fp8_train(xq_sorted, xs_sorted, expert_offsets, w13_q, w13_s
     out_sorted = _empty((max_rows, d), torch.bfloat16, xq_sorted) if out_sorted is None else out_sorted
     _want(out_sorted, torch.bfloat16, (max_rows, d), "out_sorted")
     if workspace is None:
-        workspace = _empty((moe_grouped_ffn_workspace_size(max_rows, d, F),), torch.uint8, xq_sorted)
+        workspace = _workspace(moe_grouped_ffn_workspace_size(max_rows, d, F), xq_sorted, stream)
     _check("moe_grouped_ffn_fp8_train", _lib.moe_grouped_ffn_fp8_train(
         _ptr(xq_sorted), _ptr(xs_sorted), _ptr(expert_offsets), max_rows, E, d, F, _ptr(w13_q), _ptr(w13_s),
         _ptr(w2_q), _ptr(w2_s), _ptr(out_sorted), _ptr(h_out), _ptr(workspace),
@@ -805,7 +815,7 @@ def moe_policy_loss(logits, targets, old_logprobs, advantages, ref_logprobs=None
     else:
         dlogits = None
     if workspace is None:
-        workspace = _empty((moe_policy_loss_workspace_size(N, V),), torch.uint8, logits)
+        workspace = _workspace(moe_policy_loss_workspace_size(N, V), logits, stream)
     if dev_status is not None:
         _want(dev_status, torch.int32, (1,), "dev_status")
     _check("moe_policy_loss", _lib.moe_policy_loss(
@@ -831,7 +841,7 @@ def moe_router_logits(x, w_router, logits=None, workspace=None, dev_status=None,
     else:
         _want(logits, torch.float32, (T, E), "logits")
     if workspace is None:
-        workspace = _empty((moe_router_logits_workspace_size(T, d, E),), torch.uint8, x)
+        workspace = _workspace(moe_router_logits_workspace_size(T, d, E), x, stream)
     if dev_status is not None:
         _want(dev_status, torch.int32, (1,), "dev_status")
     _check("moe_router_logits", _lib.moe_router_logits(
@@ -881,7 +891,7 @@ def moe_balance_loss(logits, topk_ids, score_fn, balance_coef, z_coef=0.0, token
     else:
         d_logits = None
     if workspace is None:
-        workspace = _empty((moe_balance_loss_workspace_size(T, E, B),), torch.uint8, logits)
+        workspace = _workspace(moe_balance_loss_workspace_size(T, E, B), logits, stream)
     if dev_status is not None:
         _want(dev_status, torch.int32, (1,), "dev_status")
     _check("moe_balance_loss", _lib.moe_balance_loss(
@@ -918,7 +928,7 @@ def moe_router_backward_dense(x, w_router, d_logits, dx=True, dw_router=True, wo
     else:
         dw_router = None
     if workspace is None:
-        workspace = _empty((moe_router_backward_dense_workspace_size(T, d, E),), torch.uint8, x)
+        workspace = _workspace(moe_router_backward_dense_workspace_size(T, d, E), x, stream)
     if dev_status is not None:
         _want(dev_status, torch.int32, (1,), "dev_status")
     _check("moe_router_backward_dense", _lib.moe_router_backward_dense(

@@ -13,8 +13,9 @@
 // token_rows_kernel: one cluster of C CTAs per row.  A row's 16-byte vectors
 // are dealt to the threads of the cluster, NV of them kept in registers from
 // the one read to the gradient's write; a longer row goes through a ring of
-// asynchronous copies in shared memory, and its gradient reads it again, from
-// L2.  A warp takes its maximum, sums 2^t and 2^t t against it;
+// asynchronous copies in shared memory, and its gradient reads it again, mostly
+// from L2 (a seventh misses at 131072 logits).  A warp takes its maximum, sums
+// 2^t and 2^t t against it;
 // the warps' sums are joined in shared memory, the CTAs' through one 16-byte
 // message to every CTA of the cluster (st.async on an mbarrier), always in the
 // same order.  So a row costs one CTA barrier, one exchange and one more CTA
@@ -22,9 +23,9 @@
 //
 // Bound: HBM for long rows, one exponential a logit (two with a gradient) close
 // behind.  Measured: log-probabilities of 8192 x 131072 bf16 0.30 ms (7.1
-// TB/s read), the gradient of as many rows, a quarter without weight, 0.61 ms
-// (6.1 TB/s read once and written); short or few rows by latency, 7 x 50001
-// fp32 4.6 us, 256 x 32768 13 us (back to back in a CUDA graph).
+// TB/s read; 4096 x 131072 fp32 0.31), the gradient of 8192 rows, a quarter
+// without weight, 0.61 ms (6.1 TB/s read once and written); short or few rows by
+// latency, 7 x 50001 fp32 4.6 us, 256 x 32768 13 us (back to back in a CUDA graph).
 #include "losses.cuh"
 
 #include <math.h>
@@ -580,6 +581,7 @@ __global__ void __launch_bounds__(TH, TH == 256 ? (POLICY ? 3 : 4) : POLICY ? (R
         const uint64_t k22 = pack2(k2, k2);
         T *d = dlogits + row * a.ld_d;
         // vector stores where the gradient's rows are aligned as the logits' are
+        // (else elements: 4096 x 131072 bf16 1.15 ms against 0.36)
         const bool same = ((reinterpret_cast<uintptr_t>(d) ^ reinterpret_cast<uintptr_t>(R.l)) & 15u) == 0;
         uint4 *dv = reinterpret_cast<uint4 *>(reinterpret_cast<uintptr_t>(d) & ~(uintptr_t)15u);
         auto store = [&](int j, const float *f, bool whole) {

@@ -606,7 +606,10 @@ moe_status moe_combine_slots(const uint16_t *out_slots, const int32_t *slot_to_s
  *   ld_d.  dlogits may be logits itself, with ld_d = ld (the gradient replaces
  *   them); else no output overlaps an input or another output.
  *   The row is read from memory once; a long row's second reading comes
- *   from L2.
+ *   mostly from L2 (2048 x 131072 bf16: 73 of its 537 MB from memory).  Rows
+ *   of the gradient whose start differs from the logits' modulo 16 bytes are
+ *   written element by element, up to 3.2 times slower (4096 x 131072 bf16
+ *   1.15 ms against 0.36; fp32 1.2 times).
  *   A sum over the rows that is beyond fp32 gives an infinity.
  * workspace: moe_policy_loss_workspace_size(N, V) bytes, 16-byte aligned; its
  * contents need no initialisation.  N may be 0: stats are 0.
@@ -667,7 +670,11 @@ moe_status moe_policy_loss(const void *logits, int logits_dtype, int64_t N, int6
  *   d_logits enters the tensor cores as three bf16 parts whose sum holds its
  *   24 significant bits (parts below the smallest normal bf16 excepted), so
  *   the products are those of fp32, infinities and NaN of d_logits, x and
- *   w_router included (0 times an infinity is NaN where d_logits is 0).
+ *   w_router included (0 times an infinity is NaN where d_logits is 0).  The
+ *   tensor cores' running sums truncate, up to 48 additions in a row: the
+ *   error's norm is up to 8.3e-7 of the result's, where an fp32 product has
+ *   1.4e-7 to 1.6e-6 by its length (dx of 256 experts 8.3e-7 against 2.9e-7,
+ *   dw_router of 8192 tokens 8.2e-7 against 1.6e-6).
  * x [T,d], w_router [E,d] bf16; logits, d_logits [T,E], dx [T,d], dw_router
  * [E,d], losses [2] fp32; topk_ids [T,k], counts [B,E], seq_offsets [B+1]
  * int32; token_mask [T] uint8.  x, w_router, dx, dw_router 16-byte aligned.

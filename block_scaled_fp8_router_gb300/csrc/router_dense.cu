@@ -495,11 +495,16 @@ __global__ void __launch_bounds__(256) balance_rows_kernel(const BalanceArgs a)
                 for (int u = 0; u < KS; u++) dl[u] *= a.renorm ? dg[u] - dt : dg[u];
                 go = a.renorm || !gate ? 0.0f : a.route_scale * dt * it;
             } else {
+                // renormalised gates depend on the scores' ratios: for low tokens, whose
+                // scores are e^l and underflow, those of the logits moved up to -20 (1 - s
+                // is 1 there too)
+                const bool low = a.renorm && sh < -40.0f;
+                const float l0 = low ? sh : 0.0f, l1 = low ? 20.0f : 0.0f;
                 float ds[KS];
 #pragma unroll
                 for (int u = 0; u < KS; u++) {
                     const bool mine = gate && gl + G * u < k;
-                    float e = expf(-my[u]);
+                    float e = expf(l1 - (my[u] - l0));
                     asm("min.NaN.f32 %0, %0, %1;" : "+f"(e) : "f"(0x1p126f));
                     const float s = mine ? div1(1.0f, 1.0f + e) : 0.0f;
                     ds[u] = e * s * s;

@@ -66,6 +66,32 @@ def test_balance_sigmoid_low_experts(L):
     _check_sigmoid(L, l, ids)
 
 
+@pytest.mark.parametrize("E,k", [(8, 2), (64, 6), (256, 8), (300, 1), (1000, 32)])
+@pytest.mark.parametrize("base", [-40.0, -80.0, -84.0, -87.0, -88.0, -95.0, -1000.0, -1e9])
+@pytest.mark.parametrize("mixed", [False, True])
+def test_gates_gradient_of_low_tokens(L, E, k, base, mixed):
+    """Renormalised sigmoid gates of tokens whose logits are all low: from log
+    sigmoid, as their ratios are; plain ones have a derivative below fp32."""
+    T = 203
+    g = torch.Generator(device="cuda").manual_seed(E + k)
+    l = torch.randn(T, E, device="cuda", generator=g)
+    low = torch.arange(T, device="cuda") % 3 > 0 if mixed else torch.ones(T, dtype=torch.bool, device="cuda")
+    l[low] += base
+    ids = torch.rand(T, E, device="cuda", generator=g).topk(k, 1).indices
+    dg = 1e-2 * torch.randn(T, k, device="cuda", generator=g)
+    z = l.double().gather(1, ids)
+    p = torch.softmax(torch.nn.functional.logsigmoid(z), 1)
+    want = 1.5 * p * torch.sigmoid(-z) * (dg.double() - (p * dg.double()).sum(1, keepdim=True))
+    d = L.moe_balance_loss(l, ids.int(), SIGMOID, 0.0, d_gates=dg, route_scale=1.5)[2]
+    rel = 2.0 ** -24 * (24 + 2 * min(float((l.amax(1) - l.amin(1)).max()), 110) + E / 16)
+    size = 2 * 1.5 * dg.double().abs().sum(1, keepdim=True)
+    assert bool(((d.gather(1, ids).double() - want).abs() <= 4 * rel * size).all())
+    assert d.scatter(1, ids, 0.0).eq(0).all()
+    d = L.moe_balance_loss(l, ids.int(), SIGMOID, 0.0, d_gates=dg, renorm=0)[2]
+    want = torch.sigmoid(z) * torch.sigmoid(-z) * dg.double()
+    assert bool(((d.gather(1, ids).double() - want).abs() <= 4 * rel * want.abs() + 1e-35).all())
+
+
 def test_balance_sums_beyond_fp32(L):
     """A z loss beyond fp32 is an infinity; the balance loss beside it stays."""
     for T in (40, 3000):

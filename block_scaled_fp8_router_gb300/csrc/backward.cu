@@ -40,8 +40,11 @@ __device__ __forceinline__ float sigmoid_fast(float g) { return __fdividef(1.0f,
 // shuffles), written with its scale to the slot's sorted row.  The gate
 // gradient is the warp-reduced dot of dy with the slot's expert output row
 // (each lane accumulates its columns in order).
+// OUT false: no expert outputs and no gate gradients (a caller who takes them
+// from moe_swiglu_backward_ckpt).
 constexpr int CB_U = 4;
 
+template <bool OUT>
 __global__ void __launch_bounds__(256) combine_backward_kernel(const uint16_t *__restrict__ dy,
                                                                const float *__restrict__ gates,
                                                                const uint16_t *__restrict__ out_sorted,
@@ -61,7 +64,7 @@ __global__ void __launch_bounds__(256) combine_backward_kernel(const uint16_t *_
     for (int64_t p = gw; p < n; p += nw) {
         const int32_t r = __ldg(slot_to_sorted + p);
         if (r < 0 || r >= A) {
-            if (lane == 0) d_gates[p] = 0.0f;
+            if (OUT && lane == 0) d_gates[p] = 0.0f;
             continue;
         }
         const int64_t t = p / k;
@@ -78,7 +81,7 @@ __global__ void __launch_bounds__(256) combine_backward_kernel(const uint16_t *_
                 b[u] = make_uint4(0u, 0u, 0u, 0u);
                 if (v < nvec) {
                     a[u] = __ldg(dyr + v);
-                    b[u] = __ldcs(outr + v);
+                    if (OUT) b[u] = __ldcs(outr + v);
                 }
             }
 #pragma unroll
@@ -91,7 +94,7 @@ __global__ void __launch_bounds__(256) combine_backward_kernel(const uint16_t *_
                 float amax = 0.0f;
 #pragma unroll
                 for (int i = 0; i < 8; i++) {
-                    dot = fmaf(f[i], o[i], dot);
+                    if (OUT) dot = fmaf(f[i], o[i], dot);
                     f[i] = g * f[i];
                     amax = fmaxf(amax, fabsf(f[i]));
                 }
@@ -105,9 +108,11 @@ __global__ void __launch_bounds__(256) combine_backward_kernel(const uint16_t *_
                 }
             }
         }
+        if (OUT) {
 #pragma unroll
-        for (int off = 16; off >= 1; off >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, off);
-        if (lane == 0) d_gates[p] = dot;
+            for (int off = 16; off >= 1; off >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, off);
+            if (lane == 0) d_gates[p] = dot;
+        }
     }
 }
 
@@ -164,6 +169,7 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volati
     return __all_sync(0xFFFFFFFFu, ok);
 }
 
+template <bool OUT>
 __global__ void __launch_bounds__(CBT_THREADS, 2)
     combine_backward_tma_kernel(const uint16_t *__restrict__ dy, const float *__restrict__ gates,
                                 const uint16_t *__restrict__ out_sorted, const int32_t *__restrict__ slot_to_sorted,
@@ -216,7 +222,7 @@ __global__ void __launch_bounds__(CBT_THREADS, 2)
             }
             mbar_arrive_expect_tx(&hd.dy_full[db], row_bytes);
             ffn::bulk_load_1d(dyb + (int64_t)db * d, dy + t * d, row_bytes, &hd.dy_full[db]);
-            for (int j = 0; j < k; j++) {
+            for (int j = 0; OUT && j < k; j++) {
                 const int64_t p = t * k + j;
                 const int32_t r = __ldg(slot_to_sorted + p);
                 if (r < 0 || r >= A) {
@@ -282,7 +288,7 @@ __global__ void __launch_bounds__(CBT_THREADS, 2)
             const int32_t r = __ldg(slot_to_sorted + p);
             if (r < 0 || r >= A) continue;
             const int st = (int)(sc % CBT_STAGES);
-            if (!warp_wait(&hd.out_full[st], (uint32_t)((sc / CBT_STAGES) & 1), abort_flag, dev_status)) return;
+            if (OUT && !warp_wait(&hd.out_full[st], (uint32_t)((sc / CBT_STAGES) & 1), abort_flag, dev_status)) return;
             sc++;
             const float g = __ldg(gates + p), ag = fabsf(g);
             const uint16_t *outr = outb + (int64_t)st * d;
@@ -292,10 +298,10 @@ __global__ void __launch_bounds__(CBT_THREADS, 2)
                 const int blk = h + 2 * CBT_WARPS * u;
                 if (blk < nb) {
                     float o[8], f[8];
-                    unpack_bf16x8(*reinterpret_cast<const uint4 *>(outr + blk * 128 + sub * 8), o);
+                    if (OUT) unpack_bf16x8(*reinterpret_cast<const uint4 *>(outr + blk * 128 + sub * 8), o);
 #pragma unroll
                     for (int i = 0; i < 8; i++) {
-                        dot = fmaf(dv[u][i], o[i], dot);
+                        if (OUT) dot = fmaf(dv[u][i], o[i], dot);
                         f[i] = g * dv[u][i];
                     }
                     const float s = block_scale(__fmul_rn(ag, am[u]));
@@ -304,6 +310,7 @@ __global__ void __launch_bounds__(CBT_THREADS, 2)
                     if (sub == 0) d_out_s[(int64_t)r * nb + blk] = s;
                 }
             }
+            if (!OUT) continue;
 #pragma unroll
             for (int off = 16; off >= 1; off >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, off);
             if (lane == 0) {
@@ -835,28 +842,28 @@ MOE_API moe_status moe_combine_backward(const uint16_t *dy, const float *gates, 
 {
     if (T < 0 || k < 1 || k > 32 || d <= 0 || d % 128 != 0 || A < 0) return MOE_ERR_SHAPE;
     if (T == 0) return MOE_OK;
-    if (!dy || !gates || !out_sorted || !slot_to_sorted || !d_out_q || !d_out_s || !d_gates) return MOE_ERR_NULL;
+    if (!dy || !gates || !out_sorted != !d_gates || !slot_to_sorted || !d_out_q || !d_out_s) return MOE_ERR_NULL;
     if (!aligned16(dy) || !aligned16(out_sorted) || !aligned16(d_out_q)) return MOE_ERR_ALIGN;
     cudaStream_t st = as_stream(stream);
     if (d <= CBT_MAX_D) {
-        const size_t smem = CBT_HDR + (size_t)(2 + CBT_STAGES) * d * 2;
-        if (cudaFuncSetAttribute(combine_backward_tma_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)smem) != cudaSuccess)
+        const auto kernel = out_sorted ? combine_backward_tma_kernel<true> : combine_backward_tma_kernel<false>;
+        const size_t smem = CBT_HDR + (size_t)(2 + (out_sorted ? CBT_STAGES : 0)) * d * 2;
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
             return MOE_ERR_CUDA;
         // two CTAs per SM (both fit in the SM's shared memory for every
         // d <= CBT_MAX_D), persistent over tokens
         const int per_sm = smem * 2 <= 227 * 1024 ? 2 : 1;
         int64_t grid = (int64_t)sm_count() * per_sm;
         if (grid > T) grid = T;
-        combine_backward_tma_kernel<<<(unsigned)grid, CBT_THREADS, smem, st>>>(
-            dy, gates, out_sorted, slot_to_sorted, T, k, d, A, d_out_q, d_out_s, d_gates, dev_status);
+        kernel<<<(unsigned)grid, CBT_THREADS, smem, st>>>(dy, gates, out_sorted, slot_to_sorted, T, k, d, A, d_out_q,
+                                                          d_out_s, d_gates, dev_status);
         return launch_status();
     }
     int64_t grid = ((int64_t)T * k + 7) / 8;                  // one warp per (token, slot)
     const int64_t cap = (int64_t)sm_count() * 8;
     if (grid > cap) grid = cap;
-    combine_backward_kernel<<<(unsigned)grid, 256, 0, st>>>(dy, gates, out_sorted, slot_to_sorted, T, k, d, A,
-                                                           d_out_q, d_out_s, d_gates);
+    const auto kernel = out_sorted ? combine_backward_kernel<true> : combine_backward_kernel<false>;
+    kernel<<<(unsigned)grid, 256, 0, st>>>(dy, gates, out_sorted, slot_to_sorted, T, k, d, A, d_out_q, d_out_s, d_gates);
     return launch_status();
 }
 

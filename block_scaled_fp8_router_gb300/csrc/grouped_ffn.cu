@@ -52,6 +52,8 @@ struct Params {
     int32_t *dev_status;
     const int32_t *sorted_to_slot;  // gathered form: sorted row -> slot t*top_k + j
     float *h_out;                   // GEMM1, nullable: pre-activations [max_rows, 2F] for the backward
+    uint8_t *h_q;                   // GEMM1 (H8): the pre-activations' 1x128 codes [max_rows, 2F]
+    float *h_s;                     //   and their scales [max_rows, 2F/128]
     int64_t max_rows;
     int E, d, F;
     int top_k;
@@ -98,6 +100,7 @@ struct SmemF {
     float sa[FT_SLOTS][BM];             // K block j's row scales in slot j % FT_SLOTS
     float sb[FT_SLOTS][4];              //   and its two weight-block scales
     float red[2][2][BM];                // GEMM1: per-half partial amax (by tile parity)
+    float2 redh[2][BM];                 // GEMM1 (H8): per-half amax of gate and up
     uint4 ostage[FT_EPI_WARPS][32 * 4]; // GEMM2: a warp's 32 rows x 32 bf16 columns on their way out
     uint64_t full[STAGES];
     uint64_t empty[STAGES];
@@ -187,6 +190,19 @@ __device__ __forceinline__ bool pair_bar_or(int q, bool pred)
     return out != 0;
 }
 
+// Codes of a pre-activation block: E4M3(h RN(1 / s)), as the act codes below;
+// a scale too small for a finite reciprocal takes both up by 2^64 (uniform
+// over the row, and of no cost elsewhere: the factor is 1).
+struct H8Recip {
+    float lift, y;
+    __device__ __forceinline__ explicit H8Recip(float s)
+    {
+        lift = s < 0x1p-126f ? 0x1p64f : 1.0f;
+        y = __frcp_rn(s * lift);
+    }
+    __device__ __forceinline__ float operator()(float v) const { return v * lift * y; }
+};
+
 // GATHER (the gathered form): GEMM1 loads its A rows straight from the
 // token-major activation codes (row = sorted_to_slot[r] / top_k, four rows
 // per tile::gather4, one per producer lane) and takes their scales from the
@@ -194,7 +210,9 @@ __device__ __forceinline__ bool pair_bar_or(int q, bool pred)
 // (row sorted_to_slot[r] of a [T*top_k, d] array) instead of its sorted
 // position.  A slot outside [0, max_rows) marks its row as not routed: it
 // gathers token 0, stores nothing and sets MOE_DEV_ROWS.
-template <int MODE, bool GATHER>
+// H8 (GEMM1): the pre-activations leave as 1x128 codes and scales for the
+// backward (a kernel of its own, so that the others keep their code).
+template <int MODE, bool GATHER, bool H8 = false>
 __global__ void __launch_bounds__(FT_THREADS, 1)
     grouped_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                         const Params p)
@@ -453,7 +471,46 @@ __global__ void __launch_bounds__(FT_THREADS, 1)
                 }
             }
             if (MODE == 1) {
-                if (p.h_out != nullptr && row_ok && !aborted) {
+                if constexpr (H8) {
+                    // gate and up, 64 of the tile's 128 columns each: the
+                    // largest of both halves by the pair's barrier, as for act
+                    // below.  One exchange buffer is enough: the act exchange's
+                    // barrier lies between this tile's reads and the next
+                    // tile's writes
+                    float mg = 0.0f, mu = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < 64; i++) {
+                        mg = fmaxf(mg, fabsf(acc[i]));
+                        mu = fmaxf(mu, fabsf(acc[64 + i]));
+                    }
+                    s.redh[cg][r_in] = make_float2(mg, mu);
+                    if (pair_bar_or(q, aborted || *abort_flag)) aborted = true;
+                    const float2 m0 = s.redh[0][r_in], m1 = s.redh[1][r_in];
+                    const float sg = block_scale(fmaxf(m0.x, m1.x)), su = block_scale(fmaxf(m0.y, m1.y));
+                    if (row_ok && !aborted) {
+                        uint8_t *dst = p.h_q + row * 2 * p.F + tl.n_blk * 128 + 64 * cg;
+#pragma unroll
+                        for (int half = 0; half < 2; half++) {
+                            const H8Recip y(half ? su : sg);
+#pragma unroll
+                            for (int u = 0; u < 4; u++) {
+                                uint32_t w[4];
+#pragma unroll
+                                for (int i = 0; i < 4; i++) {
+                                    const float *a = acc + 64 * half + 16 * u + 4 * i;
+                                    w[i] = (uint32_t)pack_e4m3x2(y(a[0]), y(a[1])) |
+                                           ((uint32_t)pack_e4m3x2(y(a[2]), y(a[3])) << 16);
+                                }
+                                reinterpret_cast<uint4 *>(dst + half * p.F)[u] = make_uint4(w[0], w[1], w[2], w[3]);
+                            }
+                        }
+                        if (cg == 0) {
+                            p.h_s[row * (p.F / 64) + tl.n_blk] = sg;
+                            p.h_s[row * (p.F / 64) + p.F / 128 + tl.n_blk] = su;
+                        }
+                    }
+                }
+                if (!H8 && p.h_out != nullptr && row_ok && !aborted) {
                     // the pre-activations, kept for the backward: gate then up columns
                     float4 *hg = reinterpret_cast<float4 *>(p.h_out + row * 2 * p.F + tl.n_blk * 128 + 64 * cg);
                     float4 *hu = reinterpret_cast<float4 *>(p.h_out + row * 2 * p.F + p.F + tl.n_blk * 128 + 64 * cg);
@@ -560,12 +617,12 @@ __global__ void __launch_bounds__(FT_THREADS, 1)
 // setmaxnreg split inside it assumes exactly FT_LAUNCH_REGS: with fewer, the
 // promotion warps' setmaxnreg.inc could not be satisfied and would wait, so
 // the host refuses to launch unless the count matches.
-template <int MODE, bool GATHER>
+template <int MODE, bool GATHER, bool H8 = false>
 static bool forward_kernel_regs_ok()
 {
     static const bool ok = [] {
         cudaFuncAttributes a;
-        if (cudaFuncGetAttributes(&a, grouped_gemm_kernel<MODE, GATHER>) != cudaSuccess) return false;
+        if (cudaFuncGetAttributes(&a, grouped_gemm_kernel<MODE, GATHER, H8>) != cudaSuccess) return false;
         return a.numRegs == FT_LAUNCH_REGS;
     }();
     return ok;
@@ -1218,13 +1275,13 @@ namespace moe {
 namespace ffn {
 
 // both GEMMs; GATHER: A rows of GEMM1 from the token-major x (T rows) by
-// sorted_to_slot / top_k, outputs of GEMM2 to their slots
-template <bool GATHER>
+// sorted_to_slot / top_k, outputs of GEMM2 to their slots; H8: h in 8 bits
+template <bool GATHER, bool H8 = false>
 static moe_status ffn_launch(const uint8_t *xq, int64_t x_rows, const float *xs, const int32_t *sorted_to_slot,
                              int top_k, const int32_t *expert_offsets, int64_t max_rows, int E, int d, int F,
                              const uint8_t *w13_q, const float *w13_s, const uint8_t *w2_q, const float *w2_s,
                              uint16_t *out, void *workspace, size_t workspace_bytes, int32_t *dev_status,
-                             void *stream, float *h_out = nullptr)
+                             void *stream, float *h_out = nullptr, uint8_t *h_q = nullptr, float *h_s = nullptr)
 {
     if (max_rows < 0 || max_rows >= (1LL << 31) || E < 1 || E > MAX_E || d <= 0 || F <= 0 || d % 128 != 0 ||
         F % 128 != 0)
@@ -1255,13 +1312,15 @@ static moe_status ffn_launch(const uint8_t *xq, int64_t x_rows, const float *xs,
     prm.dev_status = dev_status;
     prm.sorted_to_slot = sorted_to_slot;
     prm.h_out = nullptr;
+    prm.h_q = nullptr;
+    prm.h_s = nullptr;
     prm.max_rows = max_rows;
     prm.E = E;
     prm.d = d;
     prm.F = F;
     prm.top_k = top_k;
-    if (!forward_kernel_regs_ok<1, GATHER>() || !forward_kernel_regs_ok<2, GATHER>()) return MOE_ERR_UNSUPPORTED;
-    if (cudaFuncSetAttribute(grouped_gemm_kernel<1, GATHER>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (!forward_kernel_regs_ok<1, GATHER, H8>() || !forward_kernel_regs_ok<2, GATHER>()) return MOE_ERR_UNSUPPORTED;
+    if (cudaFuncSetAttribute(grouped_gemm_kernel<1, GATHER, H8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)SMEM_F_BYTES) != cudaSuccess ||
         cudaFuncSetAttribute(grouped_gemm_kernel<2, GATHER>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)SMEM_F_BYTES) != cudaSuccess)
@@ -1272,7 +1331,9 @@ static moe_status ffn_launch(const uint8_t *xq, int64_t x_rows, const float *xs,
     p1.a_scales = xs;
     p1.b_scales = w13_s;
     p1.h_out = h_out;
-    grouped_gemm_kernel<1, GATHER><<<grid, FT_THREADS, SMEM_F_BYTES, st>>>(ma1, mb1, p1);
+    p1.h_q = h_q;
+    p1.h_s = h_s;
+    grouped_gemm_kernel<1, GATHER, H8><<<grid, FT_THREADS, SMEM_F_BYTES, st>>>(ma1, mb1, p1);
     Params p2 = prm;
     p2.a_scales = act_s;
     p2.b_scales = w2_s;
@@ -1305,6 +1366,19 @@ MOE_API moe_status moe_grouped_ffn_fp8_train(const uint8_t *xq_sorted, const flo
                              w13_s, w2_q, w2_s, out_sorted, workspace, workspace_bytes, dev_status, stream, h_out);
 }
 
+MOE_API moe_status moe_grouped_ffn_fp8_ckpt(const uint8_t *xq_sorted, const float *xs_sorted,
+                                            const int32_t *expert_offsets, int64_t max_rows, int E, int d, int F,
+                                            const uint8_t *w13_q, const float *w13_s, const uint8_t *w2_q,
+                                            const float *w2_s, uint16_t *out_sorted, uint8_t *h_q, float *h_s,
+                                            void *workspace, size_t workspace_bytes, int32_t *dev_status, void *stream)
+{
+    if (max_rows != 0 && (!h_q || !h_s)) return MOE_ERR_NULL;
+    if (!aligned16(h_q)) return MOE_ERR_ALIGN;
+    return ffn_launch<false, true>(xq_sorted, max_rows, xs_sorted, nullptr, 1, expert_offsets, max_rows, E, d, F, w13_q,
+                                   w13_s, w2_q, w2_s, out_sorted, workspace, workspace_bytes, dev_status, stream,
+                                   nullptr, h_q, h_s);
+}
+
 MOE_API moe_status moe_grouped_gemm_fp8(const uint8_t *a_q, const float *a_s, const int32_t *expert_offsets,
                                         int64_t max_rows, int E, int K, int N, const uint8_t *b_q, const float *b_s,
                                         uint16_t *out, int32_t *dev_status, void *stream)
@@ -1331,6 +1405,8 @@ MOE_API moe_status moe_grouped_gemm_fp8(const uint8_t *a_q, const float *a_s, co
     prm.dev_status = dev_status;
     prm.sorted_to_slot = nullptr;
     prm.h_out = nullptr;
+    prm.h_q = nullptr;
+    prm.h_s = nullptr;
     prm.max_rows = max_rows;
     prm.E = E;
     prm.d = N;

@@ -69,6 +69,12 @@ _SIGS = {
     "moe_balance_loss": (I, [P, P, P, P, I, I, I, I, I, I, F, F, F, F, P, P, P, P, P, SZ, P, P]),
     "moe_router_backward_dense_workspace_size": (SZ, [I, I, I]),
     "moe_router_backward_dense": (I, [P, P, P, I, I, I, P, P, P, SZ, P, P]),
+    "moe_layer_norm": (I, [P, I, I64, I64, I64, P, P, I, F, I, P, I64, P, P, P, P, P, P, P]),
+    "moe_layer_norm_backward_workspace_size": (SZ, [I64, I64]),
+    "moe_layer_norm_backward": (I, [P, I, I64, I64, I64, P, P, I64, P, P, P, I, P, P, I, P, I64, P, I64, P, P, P, SZ, P]),
+    "moe_grouped_ffn_fp8_ckpt": (I, [P, P, P, I64, I, I, I, P, P, P, P, P, P, P, P, SZ, P, P]),
+    "moe_swiglu_backward_ckpt_workspace_size": (SZ, [I64, I]),
+    "moe_swiglu_backward_ckpt": (I, [P, P, P, I64, I, P, P, I64, P, P, P, P, P, I, I64, P, P, P, P, P, SZ, P]),
     "moe_debug_bounded_wait": (I, [I64, P, P]),
     "moe_device_sm_count": (I, []),
 }
@@ -600,19 +606,25 @@ def fp8_weight_transpose(q, s, qt=None, st=None, stream=None):
 
 def moe_combine_backward(dy, gates, out_sorted, slot_to_sorted, d_out_q=None, d_out_s=None, d_gates=None,
                          dev_status=None, stream=None):
-    """-> (d_out_q [A, d] e4m3, d_out_s [A, d/128], d_gates [T, k])."""
+    """-> (d_out_q [A, d] e4m3, d_out_s [A, d/128], d_gates [T, k]).  out_sorted
+    None (A = T k rows): the rows alone, d_gates is None."""
     T, k = gates.shape
-    A, d = out_sorted.shape
+    A, d = (T * k, dy.shape[1]) if out_sorted is None else out_sorted.shape
     _want(dy, torch.bfloat16, (T, d), "dy")
     _want(gates, torch.float32, (T, k), "gates")
-    _want(out_sorted, torch.bfloat16, (A, d), "out_sorted")
+    if out_sorted is not None:
+        _want(out_sorted, torch.bfloat16, (A, d), "out_sorted")
+    elif d_gates is not None:
+        raise ValueError("d_gates needs out_sorted")
     _want(slot_to_sorted, torch.int32, (T * k,), "slot_to_sorted")
     d_out_q = _empty((A, d), torch.uint8, dy) if d_out_q is None else d_out_q
     d_out_s = _empty((A, d // 128), torch.float32, dy) if d_out_s is None else d_out_s
-    d_gates = _empty((T, k), torch.float32, dy) if d_gates is None else d_gates
+    if d_gates is None and out_sorted is not None:
+        d_gates = _empty((T, k), torch.float32, dy)
     _want(d_out_q, torch.uint8, (A, d), "d_out_q")
     _want(d_out_s, torch.float32, (A, d // 128), "d_out_s")
-    _want(d_gates, torch.float32, (T, k), "d_gates")
+    if d_gates is not None:
+        _want(d_gates, torch.float32, (T, k), "d_gates")
     _check("moe_combine_backward", _lib.moe_combine_backward(
         _ptr(dy), _ptr(gates), _ptr(out_sorted), _ptr(slot_to_sorted), T, k, d, A, _ptr(d_out_q), _ptr(d_out_s),
         _ptr(d_gates), _ptr(dev_status), _stream(stream)))
@@ -935,6 +947,217 @@ def moe_router_backward_dense(x, w_router, d_logits, dx=True, dw_router=True, wo
         _ptr(x), _ptr(w_router), _ptr(d_logits), T, d, E, _ptr(dx), _ptr(dw_router), _ptr(workspace),
         workspace.numel() * workspace.element_size(), _ptr(dev_status), _stream(stream)))
     return dx, dw_router
+
+
+MOE_TYPE_BF16, MOE_TYPE_F32 = 0, 1
+
+
+def _pair(v, q_shape, s_shape, name, like):
+    """(codes, scales) of an optional output: True allocates, a pair of tensors
+    is written, False / None skips."""
+    if v is None or v is False:
+        return None
+    if v is True:
+        return _empty(q_shape, torch.uint8, like), _empty(s_shape, torch.float32, like)
+    q, s = v
+    _want(q, torch.uint8, q_shape, name + " codes")
+    _want(s, torch.float32, s_shape, name + " scales")
+    return q, s
+
+
+def _vector(v, n, name, like):
+    """An optional fp32 output [n]: True allocates, a tensor is written, False / None skips."""
+    if v is None or v is False:
+        return None
+    if v is True:
+        return _empty((n,), torch.float32, like)
+    _want(v, torch.float32, (n,), name)
+    return v
+
+
+def _half(pair, i):
+    return None if pair is None else pair[i].data_ptr()
+
+
+def _weights(weight, bias, cols, like) -> int:
+    """The type code of a norm's weight and bias (one type, [cols])."""
+    dt = None
+    for t, name in ((weight, "weight"), (bias, "bias")):
+        if t is None:
+            continue
+        if t.dtype not in (torch.bfloat16, torch.float32) or dt not in (None, t.dtype):
+            raise TypeError(f"{name}: expected torch.bfloat16 or torch.float32, the same for weight and bias, got {t.dtype}")
+        dt = t.dtype
+        _want(t, dt, (cols,), name)
+    return MOE_TYPE_F32 if dt == torch.float32 else MOE_TYPE_BF16
+
+
+def _one_device(like, *tensors) -> None:
+    """Every tensor on like's device, and that the current one (the launches go there)."""
+    dev = like.get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"expected every tensor on {like.device}, got one on {t.device}")
+    if dev != torch._C._cuda_getDevice():
+        raise ValueError(f"the tensors are on {like.device}, which is not the current device")
+
+
+def moe_layer_norm(x, weight=None, bias=None, eps=1e-5, center=True, y=None, mean=None, rstd=None, codes=None,
+                   ckpt=None, stream=None):
+    """Norm of the rows of x [rows, cols] (bf16 or fp32, any row stride;
+    center=False: RMS) -> (y, mean, rstd, codes, ckpt).  mean, rstd [rows]
+    fp32; codes: y's 1x128 (codes, scales); ckpt: those of the normalised rows,
+    for moe_layer_norm_backward.  Each of the four: True allocates, tensors are
+    written, False / None skips.  y may be x."""
+    dt, ld = _logit_rows(x, "x")
+    rows, cols = x.shape
+    w_dt = _weights(weight, bias, cols, x)
+    if y is None:
+        y = _empty((rows, cols), x.dtype, x)
+    _, ld_y = _logit_rows(y, "y", like=x)
+    mean, rstd = _vector(mean, rows, "mean", x), _vector(rstd, rows, "rstd", x)
+    codes = _pair(codes, (rows, cols), (rows, cols // 128), "codes", x)
+    ckpt = _pair(ckpt, (rows, cols), (rows, cols // 128), "ckpt", x)
+    _one_device(x, weight, bias, y, mean, rstd, *(codes or ()), *(ckpt or ()))
+    _check("moe_layer_norm", _lib.moe_layer_norm(
+        _ptr(x), dt, rows, cols, ld, _ptr(weight), _ptr(bias), w_dt, eps, int(center), _ptr(y), ld_y, _ptr(mean),
+        _ptr(rstd), _half(codes, 0), _half(codes, 1), _half(ckpt, 0), _half(ckpt, 1), _stream(stream)))
+    return y, mean, rstd, codes, ckpt
+
+
+def moe_layer_norm_backward_workspace_size(rows: int, cols: int) -> int:
+    return int(_lib.moe_layer_norm_backward_workspace_size(rows, cols))
+
+
+def moe_layer_norm_backward(dy, rstd, x=None, mean=None, ckpt=None, weight=None, center=True, dy_add=None, dx_add=None,
+                            dx=True, dweight=True, dbias=False, workspace=None, stream=None):
+    """Backward of moe_layer_norm from x (with mean, if center) or from ckpt =
+    (codes, scales) -> (dx in dy's type, dweight [cols] fp32, dbias [cols]
+    fp32; each or None).  dy_add [rows, cols] fp32 adds to dy, dx_add (dy's
+    type) to dx.  dx, dweight, dbias: True allocates, a tensor is written
+    (dx may be dy, x or dx_add), False / None skips."""
+    dt, ld = _logit_rows(dy, "dy")
+    rows, cols = dy.shape
+    _want(rstd, torch.float32, (rows,), "rstd")
+    if (x is None) == (ckpt is None):
+        raise ValueError("one of x and ckpt")
+    ld_x = ld_add = ld_dx = cols
+    if x is not None:
+        _, ld_x = _logit_rows(x, "x", like=dy)
+        if center:
+            if mean is None:
+                raise ValueError("mean: needed with x and center")
+            _want(mean, torch.float32, (rows,), "mean")
+    else:
+        ckpt = _pair(ckpt, (rows, cols), (rows, cols // 128), "ckpt", dy)
+        mean = None
+    w_dt = _weights(weight, None, cols, dy)
+    if dy_add is not None:
+        _want(dy_add, torch.float32, (rows, cols), "dy_add")
+    if dx is True:
+        dx = _empty((rows, cols), dy.dtype, dy)
+    elif dx is False:
+        dx = None
+    if dx is not None:
+        _, ld_dx = _logit_rows(dx, "dx", like=dy)
+    if dx_add is not None:
+        if dx is None:
+            raise ValueError("dx_add needs dx")
+        _, ld_add = _logit_rows(dx_add, "dx_add", like=dy)
+    dweight, dbias = _vector(dweight, cols, "dweight", dy), _vector(dbias, cols, "dbias", dy)
+    if workspace is None and (dweight is not None or dbias is not None):
+        workspace = _workspace(moe_layer_norm_backward_workspace_size(rows, cols), dy, stream)
+    _one_device(dy, rstd, x, mean, *(ckpt or ()), weight, dy_add, dx_add, dx, dweight, dbias, workspace)
+    _check("moe_layer_norm_backward", _lib.moe_layer_norm_backward(
+        _ptr(dy), dt, rows, cols, ld, _ptr(dy_add), _ptr(x), ld_x, _half(ckpt, 0), _half(ckpt, 1), _ptr(weight), w_dt,
+        _ptr(mean if center else None), _ptr(rstd), int(center), _ptr(dx_add), ld_add, _ptr(dx), ld_dx, _ptr(dweight),
+        _ptr(dbias), _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(),
+        _stream(stream)))
+    return dx, dweight, dbias
+
+
+def moe_grouped_ffn_fp8_ckpt(xq_sorted, xs_sorted, expert_offsets, w13_q, w13_s, w2_q, w2_s, h_q=None, h_s=None,
+                             out_sorted=None, workspace=None, dev_status=None, stream=None):
+    """moe_grouped_ffn_fp8 that also keeps GEMM1's pre-activations in 8 bits ->
+    (out_sorted, h_q [max_rows, 2F] e4m3, h_s [max_rows, 2F/128] fp32)."""
+    max_rows, d = xq_sorted.shape
+    E, twoF, _ = w13_q.shape
+    F = twoF // 2
+    _want(xq_sorted, torch.uint8, (max_rows, d), "xq_sorted")
+    _want(xs_sorted, torch.float32, (max_rows, d // 128), "xs_sorted")
+    _want(expert_offsets, torch.int32, (E + 1,), "expert_offsets")
+    _want(w13_q, torch.uint8, (E, twoF, d), "w13_q")
+    _want(w13_s, torch.float32, (E, twoF // 128, d // 128), "w13_s")
+    _want(w2_q, torch.uint8, (E, d, F), "w2_q")
+    _want(w2_s, torch.float32, (E, d // 128, F // 128), "w2_s")
+    h_q = _empty((max_rows, twoF), torch.uint8, xq_sorted) if h_q is None else h_q
+    h_s = _empty((max_rows, twoF // 128), torch.float32, xq_sorted) if h_s is None else h_s
+    _want(h_q, torch.uint8, (max_rows, twoF), "h_q")
+    _want(h_s, torch.float32, (max_rows, twoF // 128), "h_s")
+    out_sorted = _empty((max_rows, d), torch.bfloat16, xq_sorted) if out_sorted is None else out_sorted
+    _want(out_sorted, torch.bfloat16, (max_rows, d), "out_sorted")
+    if workspace is None:
+        workspace = _workspace(moe_grouped_ffn_workspace_size(max_rows, d, F), xq_sorted, stream)
+    if dev_status is not None:
+        _want(dev_status, torch.int32, (1,), "dev_status")
+    _one_device(xq_sorted, xs_sorted, expert_offsets, w13_q, w13_s, w2_q, w2_s, h_q, h_s, out_sorted, workspace,
+                 dev_status)
+    _check("moe_grouped_ffn_fp8_ckpt", _lib.moe_grouped_ffn_fp8_ckpt(
+        _ptr(xq_sorted), _ptr(xs_sorted), _ptr(expert_offsets), max_rows, E, d, F, _ptr(w13_q), _ptr(w13_s),
+        _ptr(w2_q), _ptr(w2_s), _ptr(out_sorted), _ptr(h_q), _ptr(h_s), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _ptr(dev_status), _stream(stream)))
+    return out_sorted, h_q, h_s
+
+
+def moe_swiglu_backward_ckpt_workspace_size(rows: int, F: int) -> int:
+    return int(_lib.moe_swiglu_backward_ckpt_workspace_size(rows, F))
+
+
+def moe_swiglu_backward_ckpt(d_act, h_q, h_s, gates=None, slot_to_sorted=None, expert_offsets=None, pad=None, ld=0,
+                             dh=True, d_gates=None, dhT=None, actT=None, workspace=None, stream=None):
+    """SwiGLU backward from pre-activations kept in 8 bits (h_q, h_s as
+    moe_grouped_ffn_fp8_ckpt writes them) -> (dh, d_gates, dhT, actT): dh
+    (codes [rows, 2F], scales [rows, 2F/128]); d_gates in gates' shape (needs
+    gates and slot_to_sorted); dhT (codes [2F, ld], scales [ld/128, 2F]) and
+    actT (codes [F, ld], scales [ld/128, F]), the weight gradients' operands
+    (need expert_offsets, pad and ld).  Each: True allocates, tensors are
+    written, False / None skips."""
+    rows, F = d_act.shape
+    _want(d_act, torch.bfloat16, (rows, F), "d_act")
+    _want(h_q, torch.uint8, (rows, 2 * F), "h_q")
+    _want(h_s, torch.float32, (rows, 2 * F // 128), "h_s")
+    dh = _pair(dh, (rows, 2 * F), (rows, 2 * F // 128), "dh", d_act)
+    slots = 0
+    if d_gates is False:
+        d_gates = None
+    if d_gates is not None:
+        if gates is None or slot_to_sorted is None:
+            raise ValueError("d_gates needs gates and slot_to_sorted")
+        slots = gates.numel()
+        _want(gates, torch.float32, gates.shape, "gates")
+        _want(slot_to_sorted, torch.int32, (slots,), "slot_to_sorted")
+        if d_gates is True:
+            d_gates = _empty(gates.shape, torch.float32, d_act)
+        _want(d_gates, torch.float32, gates.shape, "d_gates")
+        if workspace is None and slots:
+            workspace = _workspace(moe_swiglu_backward_ckpt_workspace_size(rows, F), d_act, stream)
+    E = 0
+    dhT = _pair(dhT, (2 * F, ld), (ld // 128, 2 * F), "dhT", d_act)
+    actT = _pair(actT, (F, ld), (ld // 128, F), "actT", d_act)
+    if dhT is not None or actT is not None:
+        if expert_offsets is None or pad is None:
+            raise ValueError("dhT and actT need expert_offsets and pad")
+        E = expert_offsets.numel() - 1
+        _want(expert_offsets, torch.int32, (E + 1,), "expert_offsets")
+        _want(pad, torch.int32, (E + 1,), "pad")
+    _one_device(d_act, h_q, h_s, *(dh or ()), gates, slot_to_sorted, d_gates, expert_offsets, pad, *(dhT or ()),
+                 *(actT or ()), workspace)
+    _check("moe_swiglu_backward_ckpt", _lib.moe_swiglu_backward_ckpt(
+        _ptr(d_act), _ptr(h_q), _ptr(h_s), rows, F, _ptr(gates), _ptr(slot_to_sorted), slots, _half(dh, 0),
+        _half(dh, 1), _ptr(d_gates), _ptr(expert_offsets), _ptr(pad), E, ld, _half(dhT, 0), _half(dhT, 1),
+        _half(actT, 0), _half(actT, 1), _ptr(workspace),
+        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream)))
+    return dh, d_gates, dhT, actT
 
 
 def moe_debug_bounded_wait(timeout_ns, dev_status, stream=None):

@@ -447,7 +447,10 @@ moe_status moe_grouped_ffn_mx(const uint8_t *xq_sorted, const uint8_t *x_exp, co
  *                          slot's sorted row r = slot_to_sorted[t*k+j];
  *                          d_gates[t,j] = <dy[t], out_sorted[r]> (fp32
  *                          accumulation in a fixed order), 0 for an
- *                          unrouted slot.  For d <= 8192 the rows are
+ *                          unrouted slot.  out_sorted and d_gates may both
+ *                          be NULL: the rows alone (the gates' gradient then
+ *                          comes from moe_swiglu_backward_ckpt, and the
+ *                          experts' outputs need not be kept).  For d <= 8192 the rows are
  *                          staged by bulk copies and every wait is bounded:
  *                          one that runs out ORs MOE_DEV_TIMEOUT into
  *                          dev_status (nullable) and the call's outputs are
@@ -697,6 +700,100 @@ size_t moe_router_backward_dense_workspace_size(int T, int d, int E);
 moe_status moe_router_backward_dense(const uint16_t *x, const uint16_t *w_router, const float *d_logits, int T,
                                      int d, int E, float *dx, float *dw_router, void *workspace,
                                      size_t workspace_bytes, int32_t *dev_status, void *stream);
+
+/* ------------------------------------------------------------------------
+ * The norm before the layer, and pre-activations kept in 8 bits ("RL at 1T
+ * Scale": the trainer of large MoE models; "FP8 training": block-scaled E4M3
+ * operands).  What a training step of the block keeps between forward and
+ * backward, and the backward from it.
+ *
+ * moe_layer_norm  per row t of x [rows, cols]:
+ *   mu = mean(x[t]) if center, else 0 (the RMS form),
+ *   r  = 1 / sqrt(mean((x[t] - mu)^2) + eps),
+ *   xhat = (x[t] - mu) r,   y[t,c] = xhat[c] weight[c] + bias[c]
+ *   (weight, bias nullable: 1 and 0), in fp32, y rounded once to x's type.
+ *   mean[t] = mu, rstd[t] = r (nullable, fp32).
+ *   y_q, y_s (nullable pair): y's 1 x 128 codes and scales by
+ *   fp8_block_quant's rule, from y in fp32 before its rounding to x's type
+ *   (the experts' operand); xhat_q, xhat_s (nullable pair): xhat's, the
+ *   checkpoint that moe_layer_norm_backward reads in place of x.
+ *   y may be x itself with ld_y = ld_x; else no output overlaps an input or
+ *   another output.  Infinities and NaN act on their own row only, as the
+ *   formulas have it in fp32; squares beyond fp32 give r = 0.
+ * moe_layer_norm_backward  from dy [rows, cols] and x with mean (if center)
+ * and rstd as moe_layer_norm wrote them, or (x NULL) xhat_q, xhat_s and rstd:
+ *   a = dy + dy_add,  g = a weight,  m1 = mean(g) if center, else 0,
+ *   m2 = mean(g xhat),
+ *   dx = r (g - m1 - xhat m2) + dx_add   (nullable; rounded once),
+ *   dweight[c] = sum_t a xhat,  dbias[c] = sum_t a   (nullable, fp32).
+ *   dy_add [rows, cols] fp32 (nullable): a second gradient of y, as the
+ *   router's; dx_add (nullable, x's type, needs dx): the residual's.  dx may
+ *   be dy, x or dx_add itself, row on row; else it overlaps none of the
+ *   inputs.  Sums over rows run in an order fixed by the sizes and the
+ *   device.  rows may be 0: dweight and dbias are zeroed.
+ * Rows x, y, dy, dx, dx_add are all bf16 (MOE_TYPE_BF16) or all fp32
+ * (MOE_TYPE_F32) as dtype says, unit column stride, row stride ld >= cols
+ * elements, no alignment beyond the element's (whole 16-byte vectors are
+ * faster); weight and bias [cols] are of type w_dtype.  1 <= cols <= 16384,
+ * rows < 2^31.  Codes and checkpoints [rows, cols] and [rows, cols/128] need
+ * cols % 128 = 0, rows and vectors aligned to 16 bytes.
+ * workspace (with dweight or dbias): moe_layer_norm_backward_workspace_size
+ * bytes, 16-byte aligned, no initialisation.
+ * Errors: SHAPE (also eps < 0 or not finite), NULL, ALIGN, WORKSPACE,
+ * UNSUPPORTED (an output over an input other than row on row), CUDA.
+ *
+ * moe_grouped_ffn_fp8_ckpt  moe_grouped_ffn_fp8 that also writes GEMM1's
+ *   pre-activations h (gate columns, then up) as 1 x 128 codes h_q
+ *   [max_rows, 2F] and scales h_s [max_rows, 2F/128]: s = amax / 448 (1 where
+ *   that is 0), codes E4M3(h RN(1/s)).  act is formed from h itself.
+ * moe_swiglu_backward_ckpt  from d_act [rows, F] bf16 and that checkpoint,
+ *   with g = code * scale of the gate columns, u of the up columns, a = d_act,
+ *   s(g) = 1 / (1 + exp(-g)):
+ *     dh  = [ a u (s(g) + g s(g) (1 - s(g))) | a g s(g) ],  act = g s(g) u;
+ *     dh_q, dh_s (nullable pair): dh in 1 x 128 codes [rows, 2F], scales
+ *       [rows, 2F/128] (the dgrad operand, as moe_swiglu_backward's);
+ *     d_gates[p] (nullable, [slots]): for slot p with row r =
+ *       slot_to_sorted[p], <d_act[r], act[r]> / gates[p]; 0 where r is
+ *       outside [0, rows) or the gate is 0.  With d_act = W2^T (gate dy) that
+ *       is <dy, W2 act>;
+ *     dhT_q, dhT_s and actT_q, actT_s (nullable pairs): dh and act in 128 x 1
+ *       codes, channel-major [2F, max_pad] and [F, max_pad], scales
+ *       [max_pad/128, 2F] and [max_pad/128, F] (what moe_wgrad_quant writes
+ *       for src 2 and 1 with ld = max_pad and scales_kb_major).  They need
+ *       expert_offsets and pad (moe_dispatch's and moe_wgrad_pad_offsets');
+ *       all outputs then cover the rows those name.
+ *   Codes are E4M3(v RN(1/s)).  Columns at and behind pad[E] are not written.
+ *   Rows that expert_offsets names outside [0, rows) are not read or written.
+ *   No output overlaps an input or another output.  Any of rows, slots and
+ *   max_pad may be 0.
+ *   workspace (with d_gates): moe_swiglu_backward_ckpt_workspace_size bytes,
+ *   16-byte aligned, no initialisation.
+ * Errors: NULL, SHAPE, ALIGN (codes, d_act not 16-byte aligned), WORKSPACE,
+ * CUDA.
+ * ---------------------------------------------------------------------- */
+#define MOE_TYPE_BF16 0
+#define MOE_TYPE_F32 1
+moe_status moe_layer_norm(const void *x, int dtype, int64_t rows, int64_t cols, int64_t ld_x, const void *weight,
+                          const void *bias, int w_dtype, float eps, int center, void *y, int64_t ld_y, float *mean,
+                          float *rstd, uint8_t *y_q, float *y_s, uint8_t *xhat_q, float *xhat_s, void *stream);
+size_t moe_layer_norm_backward_workspace_size(int64_t rows, int64_t cols);
+moe_status moe_layer_norm_backward(const void *dy, int dtype, int64_t rows, int64_t cols, int64_t ld_dy,
+                                   const float *dy_add, const void *x, int64_t ld_x, const uint8_t *xhat_q,
+                                   const float *xhat_s, const void *weight, int w_dtype, const float *mean,
+                                   const float *rstd, int center, const void *dx_add, int64_t ld_add, void *dx,
+                                   int64_t ld_dx, float *dweight, float *dbias, void *workspace,
+                                   size_t workspace_bytes, void *stream);
+moe_status moe_grouped_ffn_fp8_ckpt(const uint8_t *xq_sorted, const float *xs_sorted,
+                                    const int32_t *expert_offsets, int64_t max_rows, int E, int d, int F,
+                                    const uint8_t *w13_q, const float *w13_s, const uint8_t *w2_q,
+                                    const float *w2_s, uint16_t *out_sorted, uint8_t *h_q, float *h_s,
+                                    void *workspace, size_t workspace_bytes, int32_t *dev_status, void *stream);
+size_t moe_swiglu_backward_ckpt_workspace_size(int64_t rows, int F);
+moe_status moe_swiglu_backward_ckpt(const uint16_t *d_act, const uint8_t *h_q, const float *h_s, int64_t rows, int F,
+                                    const float *gates, const int32_t *slot_to_sorted, int64_t slots, uint8_t *dh_q,
+                                    float *dh_s, float *d_gates, const int32_t *expert_offsets, const int32_t *pad,
+                                    int E, int64_t max_pad, uint8_t *dhT_q, float *dhT_s, uint8_t *actT_q,
+                                    float *actT_s, void *workspace, size_t workspace_bytes, void *stream);
 
 /* ------------------------------------------------------------------------
  * moe_debug_bounded_wait -- exercises the bounded device wait that every

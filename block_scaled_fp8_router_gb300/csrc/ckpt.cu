@@ -29,19 +29,15 @@ struct Args {
 };
 
 constexpr int TILE = 128;       // rows and columns of a tile
-constexpr int WARPS = 8;        // each with 16 of the rows; a lane four columns
+constexpr int WARPS = 16;       // each with eight of the rows; a lane four columns
 constexpr int RW = TILE / WARPS;
+constexpr int THREADS = WARPS * 32;
+constexpr int MAX_E = 1024;
 
-// 2^64 brings the reciprocal of a subnormal scale into range
-constexpr float LIFT = 0x1p64f;
-
-// A block scale's reciprocal; `lift` says that the values are multiplied by
-// LIFT first.  A code is E4M3(v RN(1 / s)), as the act codes of GEMM1.
-__device__ __forceinline__ float recip(float s, bool &lift)
-{
-    lift = s < 0x1p-126f;
-    return __frcp_rn(lift ? s * LIFT : s);
-}
+// A block's scale: amax / 448 (1 where that is 0), not below 2^-126, so that
+// its reciprocal is finite.  A code is E4M3(v RN(1 / s)), as the act codes of
+// GEMM1 are.
+__device__ __forceinline__ float scale_of(float amax) { return fmaxf(block_scale(amax), 0x1p-126f); }
 
 // four codes (value 0 in the low byte), two at a time to fp32, times the scale
 __device__ __forceinline__ void decode4(uint32_t q, uint64_t s2, uint64_t (&v)[2])
@@ -55,14 +51,15 @@ __device__ __forceinline__ void decode4(uint32_t q, uint64_t s2, uint64_t (&v)[2
 }
 
 // one row's four columns: a (bf16), gate and up codes -> d_gate, d_up, act,
-// two columns in each 64-bit pair
+// two columns in each 64-bit pair, and a act summed into dot
 __device__ __forceinline__ void swiglu4(uint2 a, uint32_t gq, uint32_t uq, float gs, float us, uint64_t (&dg)[2],
-                                        uint64_t (&du)[2], uint64_t (&act)[2])
+                                        uint64_t (&du)[2], uint64_t (&act)[2], uint64_t &dot)
 {
     uint64_t g[2], u[2];
     decode4(gq, pack2(gs, gs), g);
     decode4(uq, pack2(us, us), u);
     const uint32_t aw[2] = {a.x, a.y};
+    dot = 0;
 #pragma unroll
     for (int i = 0; i < 2; i++) {
         const uint64_t a2 = pack2(__uint_as_float(aw[i] << 16), __uint_as_float(aw[i] & 0xFFFF0000u));
@@ -75,15 +72,23 @@ __device__ __forceinline__ void swiglu4(uint2 a, uint32_t gq, uint32_t uq, float
         du[i] = mul2(a2, p);
         dg[i] = mul2(mul2(a2, u[i]), fma2(p, rest, sg));
         act[i] = mul2(p, u[i]);
+        dot = fma2(a2, act[i], dot);
     }
 }
 
+// the largest magnitude of three (a NaN is passed over)
+__device__ __forceinline__ float amax3(float a, float b, float c)
+{
+    float m;
+    asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
+    return m;
+}
 __device__ __forceinline__ float amax4(const uint64_t (&v)[2])
 {
     float a, b, c, d;
     unpack2(v[0], a, b);
     unpack2(v[1], c, d);
-    return fmaxf(fmaxf(fabsf(a), fabsf(b)), fmaxf(fabsf(c), fabsf(d)));
+    return amax3(amax3(a, b, c), d, 0.0f);
 }
 
 // the warp's largest of non-negative numbers (their bits order as integers do)
@@ -92,222 +97,262 @@ __device__ __forceinline__ float warp_max(float v)
     return __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(v)));
 }
 
-__device__ __forceinline__ uint32_t encode4(const uint64_t (&v)[2], float y, bool lift)
+__device__ __forceinline__ uint32_t encode4(const uint64_t (&v)[2], float y)
 {
-    float f[4];
-    unpack2(mul2(v[0], pack2(lift ? LIFT : 1.0f, lift ? LIFT : 1.0f)), f[0], f[1]);
-    unpack2(mul2(v[1], pack2(lift ? LIFT : 1.0f, lift ? LIFT : 1.0f)), f[2], f[3]);
-    return (uint32_t)pack_e4m3x2(f[0] * y, f[1] * y) | ((uint32_t)pack_e4m3x2(f[2] * y, f[3] * y) << 16);
+    float a, b, c, d;
+    unpack2(mul2(v[0], pack2(y, y)), a, b);
+    unpack2(mul2(v[1], pack2(y, y)), c, d);
+    return (uint32_t)pack_e4m3x2(a, b) | ((uint32_t)pack_e4m3x2(c, d) << 16);
 }
 
-// shared memory of the column side: the codes of 3 x 128 channels, 128 rows each
-constexpr int CODES = 3 * TILE * TILE;
-constexpr int SMEM_COL = CODES + 3 * TILE * 2 * (int)sizeof(float);
+// eight sums of a warp's lanes, sum i left in every lane with lane / 4 = i:
+// each step keeps half of the sums
+__device__ __forceinline__ float sums8(const float (&v)[8], int lane)
+{
+    float a[4], b[2], c;
+    const bool h4 = lane & 16, h3 = lane & 8, h2 = lane & 4;
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+        a[i] = (h4 ? v[4 + i] : v[i]) + __shfl_xor_sync(0xFFFFFFFFu, h4 ? v[i] : v[4 + i], 16);
+#pragma unroll
+    for (int i = 0; i < 2; i++)
+        b[i] = (h3 ? a[2 + i] : a[i]) + __shfl_xor_sync(0xFFFFFFFFu, h3 ? a[i] : a[2 + i], 8);
+    c = (h2 ? b[1] : b[0]) + __shfl_xor_sync(0xFFFFFFFFu, h2 ? b[0] : b[1], 4);
+    c += __shfl_xor_sync(0xFFFFFFFFu, c, 2);
+    return c + __shfl_xor_sync(0xFFFFFFFFu, c, 1);
+}
 
-// One 128 x 128 tile of (rows, columns of F): with COL the rows of one padded
-// 128-row block of an expert, else any 128 rows.  Lane l of warp w holds
-// columns 4 l .. 4 l + 3 of rows 16 w .. 16 w + 15 as they came from memory
-// (one 32-bit register a pair of gate and up with its d_act), so the two
-// passes over them (largest values, then codes) recompute rather than keep
-// three fp32 numbers each.  A row's largest value is one warp reduction; its
-// scales are formed by one lane each.  The columns' largest values go through
-// shared memory.  A lane's sixteen codes of a channel are the 16-byte piece w
-// of its row of the code tile (at piece w ^ (l & 7): no bank conflicts either
-// way), and a channel leaves as one 128-byte run.
+// sixteen / four bytes to shared memory, asynchronously; `in` false: zeros, and
+// nothing is read
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool in)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void *src, bool in)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(in ? 4 : 0) : "memory");
+}
+
+// shared memory: two stages of a tile as it comes from memory (a row's 128
+// columns of d_act, gate codes and up codes are 512 bytes; then each warp's
+// scales), then for the column side the codes of 3 x 128 channels of 128 rows,
+// the warps' largest values of a channel, the reciprocals, and the experts'
+// maps
+constexpr int ROW_BYTES = 4 * TILE;
+constexpr int SCALES = TILE * ROW_BYTES;
+constexpr int STAGE = SCALES + TILE * 8;
+constexpr int CODES = 3 * TILE * TILE;
+constexpr int RED = WARPS * 3 * TILE * 4;
+constexpr int SMEM_ROW = 2 * STAGE;
+constexpr int SMEM_COL = 2 * STAGE + CODES + RED + 3 * TILE * 4 + 2 * (MAX_E + 1) * 4;
+static_assert(SMEM_COL <= 227 * 1024, "shared memory of a tile");
+
+struct Where {
+    int kb, cb;                 // the tile
+    int row;                    // the warp's first row
+    int n;                      // how many of its eight are there
+};
+
+// Tiles of 128 rows x 128 columns of F, a contiguous run of them for each CTA
+// (one per SM): with COL the rows of a tile are a padded 128-row block of one
+// expert, else any 128 rows.  Warp w has rows 8 w .. 8 w + 7; it copies them
+// asynchronously two tiles ahead into shared memory of its own (a row is one
+// instruction: lanes 0-15 its d_act, 16-23 its gate and 24-31 its up codes,
+// whose rows are all 2 F bytes apart).  Lane l takes columns 4 l .. 4 l + 3
+// and holds their d_gate, d_up and act in registers from there on (96 of
+// them; two passes that each recomputed them from the codes took 2.2 times as
+// long).  A row's largest
+// value is one warp reduction, its scale is formed by one lane.  The columns'
+// largest values meet in shared memory.  A lane's eight codes of a channel
+// are an 8-byte piece of the channel's row of the code tile (piece w at
+// w ^ (l & 15): no bank conflicts either way); a channel leaves as one
+// 128-byte run.
 template <bool ROW, bool COL>
-__global__ void __launch_bounds__(WARPS * 32, 2) swiglu_ckpt_kernel(Args p)
+__global__ void __launch_bounds__(THREADS, 1) swiglu_ckpt_kernel(Args p)
 {
     extern __shared__ __align__(16) uint8_t sm[];
-    float *red = reinterpret_cast<float *>(sm);                   // [WARPS][3][TILE], before the codes take its place
-    float *col_y = reinterpret_cast<float *>(sm + CODES);         // [3][TILE] reciprocals, then which are lifted
-    __shared__ int64_t s_r0, s_rend;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int nb = p.F >> 7;
-    const int64_t kb = blockIdx.x / nb;
-    const int cb = blockIdx.x - (int)kb * nb;
-    int64_t r0 = kb * TILE, rend = p.rows;
+    uint8_t *codes = sm + 2 * STAGE;
+    float *red = reinterpret_cast<float *>(codes + CODES);              // [WARPS][3][TILE]
+    float *col_y = red + WARPS * 3 * TILE;                              // [3][TILE]
+    int32_t *s_pad = reinterpret_cast<int32_t *>(col_y + 3 * TILE), *s_off = s_pad + MAX_E + 1;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int nb = p.F >> 7, c0 = 4 * lane;
+    int blocks = (int)((p.rows + TILE - 1) / TILE);
     if (COL) {
-        if (kb * TILE >= p.pad[p.E] || kb * TILE >= p.ld) return;
-        if (threadIdx.x == 0) s_r0 = s_rend = 0;
-        __syncthreads();
-        for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
-            const int32_t p0 = __ldg(p.pad + e), p1 = __ldg(p.pad + e + 1);
-            if (p0 <= kb * TILE && kb * TILE < p1) {
-                s_r0 = __ldg(p.offsets + e) + (kb * TILE - p0);
-                s_rend = __ldg(p.offsets + e + 1);
-            }
+        for (int e = tid; e <= p.E; e += THREADS) {
+            s_pad[e] = __ldg(p.pad + e);
+            s_off[e] = __ldg(p.offsets + e);
         }
         __syncthreads();
-        r0 = s_r0;
-        rend = s_rend < p.rows ? s_rend : p.rows;
-        if (r0 < 0) rend = 0;
+        const int64_t P = s_pad[p.E] < p.ld ? s_pad[p.E] : p.ld;
+        blocks = P > 0 ? (int)(P / TILE) : 0;
     }
-    const int64_t row0 = r0 + warp * RW;
-    const int c0 = 4 * lane;
-    uint2 a[RW];
-    uint32_t gq[RW], uq[RW];
-#pragma unroll
-    for (int i = 0; i < RW; i++) {
-        const int64_t r = row0 + i;
-        a[i] = make_uint2(0u, 0u);
-        gq[i] = uq[i] = 0u;
-        if (r < rend) {
-            a[i] = __ldcs(reinterpret_cast<const uint2 *>(p.d_act + r * p.F + cb * TILE + c0));
-            gq[i] = __ldcs(reinterpret_cast<const uint32_t *>(p.h_q + r * 2 * p.F + cb * TILE + c0));
-            uq[i] = __ldcs(reinterpret_cast<const uint32_t *>(p.h_q + r * 2 * p.F + p.F + cb * TILE + c0));
-        }
-    }
-    // lane 2 i + 0 / 1 holds row i's gate / up scale
-    float hs = 0.0f;
-    if (row0 + (lane >> 1) < rend) hs = __ldg(p.h_s + (row0 + (lane >> 1)) * 2 * nb + (lane & 1) * nb + cb);
+    // this CTA's tiles: the same number each, the first ones one more
+    const int total = blocks * nb, each = total / (int)gridDim.x, more = total - each * (int)gridDim.x;
+    const int t0 = (int)blockIdx.x * each + ((int)blockIdx.x < more ? (int)blockIdx.x : more);
+    const int t1 = t0 + each + ((int)blockIdx.x < more ? 1 : 0);
+    // the warp's rows of a stage; this lane's piece of a row, there and in memory
+    const uint32_t stage0 = smem_u32(sm) + warp * RW * ROW_BYTES + lane * 16;
+    const uint8_t *piece = lane < 16 ? reinterpret_cast<const uint8_t *>(p.d_act) + lane * 16
+                                     : p.h_q + (lane < 24 ? (lane - 16) * 16 : p.F + (lane - 24) * 16);
+    const int piece_tile = lane < 16 ? 2 * TILE : TILE;
+    const uint32_t scale0 = smem_u32(sm) + SCALES + warp * RW * 8 + lane * 4;
 
-    float cm[3][4] = {};                                          // the lane's columns: largest d_gate, d_up, act
-    float rm = 0.0f, dot = 0.0f;                                  // lane 2 i + 0 / 1: row i's largest d_gate / d_up; lane i: its dot
-#pragma unroll
-    for (int i = 0; i < RW; i++) {
-        uint64_t dg[2], du[2], act[2];
-        swiglu4(a[i], gq[i], uq[i], __shfl_sync(0xFFFFFFFFu, hs, 2 * i), __shfl_sync(0xFFFFFFFFu, hs, 2 * i + 1), dg,
-                du, act);
-        if (ROW) {
-            const float mg = warp_max(amax4(dg)), mu = warp_max(amax4(du));
-            if ((lane >> 1) == i) rm = lane & 1 ? mu : mg;
-        }
-        if (COL) {
-#pragma unroll
-            for (int j = 0; j < 2; j++) {
-                float x, y;
-                unpack2(dg[j], x, y);
-                cm[0][2 * j] = fmaxf(cm[0][2 * j], fabsf(x));
-                cm[0][2 * j + 1] = fmaxf(cm[0][2 * j + 1], fabsf(y));
-                unpack2(du[j], x, y);
-                cm[1][2 * j] = fmaxf(cm[1][2 * j], fabsf(x));
-                cm[1][2 * j + 1] = fmaxf(cm[1][2 * j + 1], fabsf(y));
-                unpack2(act[j], x, y);
-                cm[2][2 * j] = fmaxf(cm[2][2 * j], fabsf(x));
-                cm[2][2 * j + 1] = fmaxf(cm[2][2 * j + 1], fabsf(y));
+    int f_kb = t0 / nb, f_cb = t0 - f_kb * nb, f_t = t0;               // the tile that is fetched next
+    int k_r0 = 0, k_n = 0, k_at = -1;                                  // its block's first row and rows
+    auto fetch = [&](int stage) -> Where {
+        Where w{f_kb, f_cb, 0, 0};
+        if (f_t < t1) {
+            if (f_kb != k_at) {
+                k_at = f_kb;
+                int64_t r0 = (int64_t)f_kb * TILE, rend = p.rows;
+                if (COL) {
+                    int lo = 0, hi = p.E;                              // pad[lo] <= 128 kb, 128 kb < pad[hi]
+                    while (hi - lo > 1) {
+                        const int mid = (lo + hi) >> 1;
+                        if (s_pad[mid] <= f_kb * TILE) lo = mid;
+                        else hi = mid;
+                    }
+                    r0 = (int64_t)s_off[lo] + (f_kb * TILE - s_pad[lo]);
+                    rend = s_off[lo + 1] < p.rows ? s_off[lo + 1] : p.rows;
+                    if (r0 < 0) rend = 0;
+                }
+                k_n = rend <= r0 ? 0 : rend - r0 < TILE ? (int)(rend - r0) : TILE;
+                k_r0 = k_n ? (int)r0 : 0;
             }
+            w.row = k_r0 + warp * RW;
+            w.n = k_n - warp * RW < RW ? k_n - warp * RW : RW;
+            const uint8_t *src = piece + (int64_t)w.row * 2 * p.F + f_cb * piece_tile;
+#pragma unroll
+            for (int i = 0; i < RW; i++, src += 2 * p.F) copy16(stage0 + stage * STAGE + i * ROW_BYTES, src, i < w.n);
+            if (lane < 2 * RW)
+                copy4(scale0 + stage * STAGE, p.h_s + (int64_t)(w.row + (lane >> 1)) * 2 * nb + (lane & 1) * nb + f_cb,
+                      (lane >> 1) < w.n);
+            f_t++;
+            if (++f_cb == nb) f_cb = 0, f_kb++;
         }
-        if (p.dots) {
-            const float a0 = __uint_as_float(a[i].x << 16), a1 = __uint_as_float(a[i].x & 0xFFFF0000u);
-            const float a2 = __uint_as_float(a[i].y << 16), a3 = __uint_as_float(a[i].y & 0xFFFF0000u);
-            float x, y, z, w;
-            unpack2(act[0], x, y);
-            unpack2(act[1], z, w);
-            float s = fmaf(a0, x, a1 * y) + fmaf(a2, z, a3 * w);
+        cp_async_commit();
+        return w;
+    };
+    Where now = fetch(0), next = fetch(1);
+    int stage = 0;
+    for (int t = t0; t < t1; t++, stage ^= 1) {
+        cp_async_wait<1>();
+        __syncwarp();
+        const uint8_t *st = sm + stage * STAGE + warp * RW * ROW_BYTES;
+        const float2 *hs = reinterpret_cast<const float2 *>(sm + stage * STAGE + SCALES) + warp * RW;
+        uint64_t v[3][RW][2];
+        float rm = 0.0f, dots[RW];
 #pragma unroll
-            for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-            if (lane == i) dot = s;
-        }
-    }
-    if (p.dots && lane < RW && row0 + lane < rend) p.dots[(row0 + lane) * nb + cb] = dot;
-    float ry = 0.0f;
-    bool rlift = false;
-    if (ROW) {
-        const float s = block_scale(rm);
-        ry = recip(s, rlift);
-        if (row0 + (lane >> 1) < rend) p.dh_s[(row0 + (lane >> 1)) * 2 * nb + (lane & 1) * nb + cb] = s;
-    }
-    const unsigned rl = __ballot_sync(0xFFFFFFFFu, rlift);
-    float cy[3][4];
-    unsigned cl = 0;
-    if (COL) {
-#pragma unroll
-        for (int k = 0; k < 3; k++)
-            *reinterpret_cast<float4 *>(red + (warp * 3 + k) * TILE + c0) = make_float4(cm[k][0], cm[k][1], cm[k][2], cm[k][3]);
-        __syncthreads();
-        for (int c = threadIdx.x; c < 3 * TILE; c += WARPS * 32) {
-            float m = red[c];
-#pragma unroll
-            for (int w = 1; w < WARPS; w++) m = fmaxf(m, red[w * 3 * TILE + c]);
-            const float s = block_scale(m);
-            bool lift;
-            col_y[c] = recip(s, lift);
-            col_y[3 * TILE + c] = lift ? 1.0f : 0.0f;
-            const int k = c >> 7, ch = cb * TILE + (c & 127);
-            if (k == 2) {
-                if (p.actT_s) p.actT_s[kb * p.F + ch] = s;
-            } else if (p.dhT_s) {
-                p.dhT_s[kb * 2 * p.F + k * p.F + ch] = s;
-            }
-        }
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < 3; k++) {
-#pragma unroll
-            for (int j = 0; j < 4; j++) {
-                cy[k][j] = col_y[k * TILE + c0 + j];
-                if (col_y[3 * TILE + k * TILE + c0 + j] != 0.0f) cl |= 1u << (4 * k + j);
-            }
-        }
-    }
-    // the second pass starts from what was loaded: without this the compiler
-    // keeps the first one's results and spills them
-#pragma unroll
-    for (int i = 0; i < RW; i++) asm volatile("" : "+r"(a[i].x), "+r"(a[i].y), "+r"(gq[i]), "+r"(uq[i]));
-    uint32_t words[3][4][RW / 4];
-#pragma unroll
-    for (int i4 = 0; i4 < RW; i4 += 4) {
-        float v[3][4][4];                                          // [array][column][row]
-#pragma unroll
-        for (int ii = 0; ii < 4; ii++) {
-            const int i = i4 + ii;
-            uint64_t dg[2], du[2], act[2];
-            swiglu4(a[i], gq[i], uq[i], __shfl_sync(0xFFFFFFFFu, hs, 2 * i), __shfl_sync(0xFFFFFFFFu, hs, 2 * i + 1),
-                    dg, du, act);
+        for (int i = 0; i < RW; i++) {
+            uint64_t dot;
+            const float2 s = hs[i];
+            swiglu4(*reinterpret_cast<const uint2 *>(st + i * ROW_BYTES + lane * 8),
+                    *reinterpret_cast<const uint32_t *>(st + i * ROW_BYTES + 2 * TILE + lane * 4),
+                    *reinterpret_cast<const uint32_t *>(st + i * ROW_BYTES + 3 * TILE + lane * 4), s.x, s.y, v[0][i],
+                    v[1][i], v[2][i], dot);
+            float x, y;
+            unpack2(dot, x, y);
+            dots[i] = x + y;
             if (ROW) {
-                const float yg = __shfl_sync(0xFFFFFFFFu, ry, 2 * i), yu = __shfl_sync(0xFFFFFFFFu, ry, 2 * i + 1);
-                if (row0 + i < rend) {
-                    uint8_t *q = p.dh_q + (row0 + i) * 2 * p.F + cb * TILE + c0;
-                    *reinterpret_cast<uint32_t *>(q) = encode4(dg, yg, rl >> (2 * i) & 1);
-                    *reinterpret_cast<uint32_t *>(q + p.F) = encode4(du, yu, rl >> (2 * i + 1) & 1);
-                }
+                const float mg = warp_max(amax4(v[0][i])), mu = warp_max(amax4(v[1][i]));
+                if ((lane >> 1) == i) rm = lane & 1 ? mu : mg;
             }
-            if (COL) {
-#pragma unroll
-                for (int j = 0; j < 2; j++) {
-                    unpack2(dg[j], v[0][2 * j][ii], v[0][2 * j + 1][ii]);
-                    unpack2(du[j], v[1][2 * j][ii], v[1][2 * j + 1][ii]);
-                    unpack2(act[j], v[2][2 * j][ii], v[2][2 * j + 1][ii]);
-                }
-            }
+        }
+        const Where at = now;
+        now = next;
+        __syncwarp();                                                  // the warp has read the stage
+        next = fetch(stage);
+        if (p.dots) {
+            const float d = sums8(dots, lane);
+            if ((lane & 3) == 0 && (lane >> 2) < at.n) p.dots[(int64_t)(at.row + (lane >> 2)) * nb + at.cb] = d;
         }
         if (COL) {
 #pragma unroll
             for (int k = 0; k < 3; k++) {
+                float m[4] = {};
 #pragma unroll
-                for (int j = 0; j < 4; j++) {
-                    float *x = v[k][j];
-                    if (cl) {
-                        const float f = cl >> (4 * k + j) & 1 ? LIFT : 1.0f;
+                for (int i = 0; i < RW; i += 2) {
 #pragma unroll
-                        for (int ii = 0; ii < 4; ii++) x[ii] *= f;
+                    for (int j = 0; j < 2; j++) {
+                        float x0, y0, x1, y1;
+                        unpack2(v[k][i][j], x0, y0);
+                        unpack2(v[k][i + 1][j], x1, y1);
+                        m[2 * j] = amax3(x0, x1, m[2 * j]);
+                        m[2 * j + 1] = amax3(y0, y1, m[2 * j + 1]);
                     }
-                    const float y = cy[k][j];
-                    words[k][j][i4 / 4] = (uint32_t)pack_e4m3x2(x[0] * y, x[1] * y) |
-                                          ((uint32_t)pack_e4m3x2(x[2] * y, x[3] * y) << 16);
+                }
+                *reinterpret_cast<float4 *>(red + (warp * 3 + k) * TILE + c0) = make_float4(m[0], m[1], m[2], m[3]);
+            }
+            __syncthreads();
+            if (tid < 3 * TILE) {
+                float m = red[tid];
+#pragma unroll
+                for (int w = 1; w < WARPS; w++) m = fmaxf(m, red[w * 3 * TILE + tid]);
+                const float s = scale_of(m);
+                col_y[tid] = __frcp_rn(s);
+                const int k = tid >> 7, ch = at.cb * TILE + (tid & 127);
+                if (k == 2) {
+                    if (p.actT_s) p.actT_s[(int64_t)at.kb * p.F + ch] = s;
+                } else if (p.dhT_s) {
+                    p.dhT_s[(int64_t)at.kb * 2 * p.F + k * p.F + ch] = s;
                 }
             }
         }
-    }
-    if (!COL) return;
-    uint4 *tile = reinterpret_cast<uint4 *>(sm);                   // [3 * TILE channels][8 pieces]
+        if (ROW) {
+            const float s = scale_of(rm), ry = __frcp_rn(s);
+            if ((lane >> 1) < at.n) p.dh_s[(int64_t)(at.row + (lane >> 1)) * 2 * nb + (lane & 1) * nb + at.cb] = s;
+            uint8_t *q = p.dh_q + (int64_t)at.row * 2 * p.F + at.cb * TILE + c0;
 #pragma unroll
-    for (int k = 0; k < 3; k++) {
+            for (int i = 0; i < RW; i++, q += 2 * p.F) {
+                const uint32_t g = encode4(v[0][i], __shfl_sync(0xFFFFFFFFu, ry, 2 * i));
+                const uint32_t u = encode4(v[1][i], __shfl_sync(0xFFFFFFFFu, ry, 2 * i + 1));
+                if (i < at.n) {
+                    *reinterpret_cast<uint32_t *>(q) = g;
+                    *reinterpret_cast<uint32_t *>(q + p.F) = u;
+                }
+            }
+        }
+        if (COL) {
+            __syncthreads();                                           // the reciprocals; the last tile's codes have left
 #pragma unroll
-        for (int j = 0; j < 4; j++)
-            tile[(k * TILE + c0 + j) * 8 + (warp ^ (lane & 7))] =
-                make_uint4(words[k][j][0], words[k][j][1], words[k][j][2], words[k][j][3]);
+            for (int k = 0; k < 3; k++) {
+                const float4 y4 = *reinterpret_cast<const float4 *>(col_y + k * TILE + c0);
+                const uint64_t y[2] = {pack2(y4.x, y4.y), pack2(y4.z, y4.w)};
+#pragma unroll
+                for (int j = 0; j < 2; j++) {
+                    uint32_t lo[2], hi[2];                             // the two columns' eight codes
+#pragma unroll
+                    for (int i = 0; i < RW; i += 4) {
+                        float a[4], b[4];
+#pragma unroll
+                        for (int r = 0; r < 4; r++) unpack2(mul2(v[k][i + r][j], y[j]), a[r], b[r]);
+                        lo[i / 4] = (uint32_t)pack_e4m3x2(a[0], a[1]) | ((uint32_t)pack_e4m3x2(a[2], a[3]) << 16);
+                        hi[i / 4] = (uint32_t)pack_e4m3x2(b[0], b[1]) | ((uint32_t)pack_e4m3x2(b[2], b[3]) << 16);
+                    }
+                    uint2 *dst = reinterpret_cast<uint2 *>(codes + (k * TILE + c0 + 2 * j) * TILE) + (warp ^ (lane & 15));
+                    dst[0] = make_uint2(lo[0], lo[1]);
+                    dst[TILE / 8] = make_uint2(hi[0], hi[1]);
+                }
+            }
+            __syncthreads();
+            // sixteen bytes a thread, eight threads a channel, 64 channels at a
+            // time: channel tid / 8 + 64 i of the tile's 3 x 128, whose lane's
+            // l & 15 above was this warp's number
+            const int ch = tid >> 3, pc = tid & 7;
+            const uint8_t *src = codes + ch * TILE + (((2 * pc) ^ warp) & ~1) * 8;
+            const int64_t off = ((int64_t)at.cb * TILE + ch) * p.ld + (int64_t)at.kb * TILE + 16 * pc;
+#pragma unroll
+            for (int i = 0; i < 6; i++) {
+                uint4 w = *reinterpret_cast<const uint4 *>(src + i * 64 * TILE);
+                if (warp & 1) w = make_uint4(w.z, w.w, w.x, w.y);
+                uint8_t *base = i < 4 ? p.dhT_q : p.actT_q;
+                const int64_t more_rows = (int64_t)((i & 1) * 64 + (i == 2 || i == 3 ? p.F : 0));
+                if (base) *reinterpret_cast<uint4 *>(base + off + more_rows * p.ld) = w;
+            }
+        }
     }
-    __syncthreads();
-#pragma unroll 4
-    for (int u = threadIdx.x; u < 3 * TILE * 8; u += WARPS * 32) {
-        const int c = u >> 3, piece = u & 7;
-        const int k = c >> 7, cc = c & 127;
-        const uint4 w = tile[c * 8 + (piece ^ (cc >> 2 & 7))];
-        uint8_t *base = k == 2 ? p.actT_q : p.dhT_q;
-        if (base)
-            *reinterpret_cast<uint4 *>(base + ((int64_t)(k & 1) * p.F + cb * TILE + cc) * p.ld + kb * TILE + 16 * piece) = w;
-    }
+    cp_async_wait<0>();
 }
 
 // d_gates[slot]: the blocks' dots of the slot's row in order, over its gate; 0
@@ -334,13 +379,12 @@ __global__ void __launch_bounds__(256) gate_kernel(const float *__restrict__ dot
 template <bool ROW, bool COL>
 static cudaError_t launch(const Args &p, int64_t blocks, cudaStream_t st)
 {
-    constexpr int smem = COL ? SMEM_COL : 0;
-    if (COL) {
-        static std::atomic<uint64_t> done{0};
-        const cudaError_t e = allow_smem(reinterpret_cast<const void *>(swiglu_ckpt_kernel<ROW, COL>), smem, done);
-        if (e != cudaSuccess) return e;
-    }
-    swiglu_ckpt_kernel<ROW, COL><<<(unsigned)(blocks * (p.F / TILE)), WARPS * 32, smem, st>>>(p);
+    constexpr int smem = COL ? SMEM_COL : SMEM_ROW;
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = allow_smem(reinterpret_cast<const void *>(swiglu_ckpt_kernel<ROW, COL>), smem, done);
+    if (e != cudaSuccess) return e;
+    const int64_t tiles = blocks * (p.F / TILE), sms = sm_count();
+    swiglu_ckpt_kernel<ROW, COL><<<(unsigned)(tiles < sms ? tiles : sms), THREADS, smem, st>>>(p);
     return cudaGetLastError();
 }
 
@@ -366,7 +410,7 @@ MOE_API moe_status moe_swiglu_backward_ckpt(const uint16_t *d_act, const uint8_t
     const bool col = dhT_q || dhT_s || actT_q || actT_s;
     if (rows < 0 || rows >= (1LL << 31) || F <= 0 || F % 128 != 0 || slots < 0 || slots >= (1LL << 31)) return MOE_ERR_SHAPE;
     if (col && (E < 1 || E > 1024 || max_pad < 0 || max_pad % 128 != 0)) return MOE_ERR_SHAPE;
-    if ((col ? max_pad / 128 : (rows + 127) / 128) * (F / 128) >= (1LL << 31)) return MOE_ERR_SHAPE;
+    if ((col ? max_pad / 128 : (rows + 127) / 128) * (F / 128) >= (1LL << 31) || max_pad >= (1LL << 31)) return MOE_ERR_SHAPE;
     if (!dh_q != !dh_s || !dhT_q != !dhT_s || !actT_q != !actT_s) return MOE_ERR_NULL;
     if (col && (!expert_offsets || !pad)) return MOE_ERR_NULL;
     if (d_gates && slots && (!gates || !slot_to_sorted)) return MOE_ERR_NULL;

@@ -190,19 +190,6 @@ __device__ __forceinline__ bool pair_bar_or(int q, bool pred)
     return out != 0;
 }
 
-// Codes of a pre-activation block: E4M3(h RN(1 / s)), as the act codes below;
-// a scale too small for a finite reciprocal takes both up by 2^64 (uniform
-// over the row, and of no cost elsewhere: the factor is 1).
-struct H8Recip {
-    float lift, y;
-    __device__ __forceinline__ explicit H8Recip(float s)
-    {
-        lift = s < 0x1p-126f ? 0x1p64f : 1.0f;
-        y = __frcp_rn(s * lift);
-    }
-    __device__ __forceinline__ float operator()(float v) const { return v * lift * y; }
-};
-
 // GATHER (the gathered form): GEMM1 loads its A rows straight from the
 // token-major activation codes (row = sorted_to_slot[r] / top_k, four rows
 // per tile::gather4, one per producer lane) and takes their scales from the
@@ -486,20 +473,22 @@ __global__ void __launch_bounds__(FT_THREADS, 1)
                     s.redh[cg][r_in] = make_float2(mg, mu);
                     if (pair_bar_or(q, aborted || *abort_flag)) aborted = true;
                     const float2 m0 = s.redh[0][r_in], m1 = s.redh[1][r_in];
-                    const float sg = block_scale(fmaxf(m0.x, m1.x)), su = block_scale(fmaxf(m0.y, m1.y));
+                    // not below 2^-126, so that the reciprocals are finite
+                    const float sg = fmaxf(block_scale(fmaxf(m0.x, m1.x)), 0x1p-126f);
+                    const float su = fmaxf(block_scale(fmaxf(m0.y, m1.y)), 0x1p-126f);
                     if (row_ok && !aborted) {
                         uint8_t *dst = p.h_q + row * 2 * p.F + tl.n_blk * 128 + 64 * cg;
 #pragma unroll
                         for (int half = 0; half < 2; half++) {
-                            const H8Recip y(half ? su : sg);
+                            const float y = __frcp_rn(half ? su : sg);
 #pragma unroll
                             for (int u = 0; u < 4; u++) {
                                 uint32_t w[4];
 #pragma unroll
                                 for (int i = 0; i < 4; i++) {
                                     const float *a = acc + 64 * half + 16 * u + 4 * i;
-                                    w[i] = (uint32_t)pack_e4m3x2(y(a[0]), y(a[1])) |
-                                           ((uint32_t)pack_e4m3x2(y(a[2]), y(a[3])) << 16);
+                                    w[i] = (uint32_t)pack_e4m3x2(a[0] * y, a[1] * y) |
+                                           ((uint32_t)pack_e4m3x2(a[2] * y, a[3] * y) << 16);
                                 }
                                 reinterpret_cast<uint4 *>(dst + half * p.F)[u] = make_uint4(w[0], w[1], w[2], w[3]);
                             }

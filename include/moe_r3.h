@@ -745,7 +745,8 @@ moe_status moe_router_backward_dense(const uint16_t *x, const uint16_t *w_router
  * moe_grouped_ffn_fp8_ckpt  moe_grouped_ffn_fp8 that also writes GEMM1's
  *   pre-activations h (gate columns, then up) as 1 x 128 codes h_q
  *   [max_rows, 2F] and scales h_s [max_rows, 2F/128]: s = amax / 448 (1 where
- *   that is 0), codes E4M3(h RN(1/s)).  act is formed from h itself.
+ *   that is 0), not below 2^-126, codes E4M3(h RN(1/s)).  act is formed from h
+ *   itself.
  * moe_swiglu_backward_ckpt  from d_act [rows, F] bf16 and that checkpoint,
  *   with g = code * scale of the gate columns, u of the up columns, a = d_act,
  *   s(g) = 1 / (1 + exp(-g)):
@@ -762,7 +763,7 @@ moe_status moe_router_backward_dense(const uint16_t *x, const uint16_t *w_router
  *       for src 2 and 1 with ld = max_pad and scales_kb_major).  They need
  *       expert_offsets and pad (moe_dispatch's and moe_wgrad_pad_offsets');
  *       all outputs then cover the rows those name.
- *   Codes are E4M3(v RN(1/s)).  Columns at and behind pad[E] are not written.
+ *   Scales and codes by the same rule as h_q's.  Columns at and behind pad[E] are not written.
  *   Rows that expert_offsets names outside [0, rows) are not read or written.
  *   No output overlaps an input or another output.  Any of rows, slots and
  *   max_pad may be 0.

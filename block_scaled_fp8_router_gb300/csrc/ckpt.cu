@@ -11,6 +11,8 @@
 // 128 x 1 codes along the expert's rows, channel-major (the weight gradients'
 // operands), and <d_act, act>, which over the gate is the gate's gradient:
 // d_act = W2^T (gate dy), so <d_act, act> = gate <dy, W2 act>.
+#include <type_traits>
+
 #include "losses.cuh"
 
 namespace moe {
@@ -24,8 +26,8 @@ struct Args {
     uint8_t *dh_q, *dhT_q, *actT_q;
     float *dh_s, *dhT_s, *actT_s;
     float *dots;                // [rows, F / 128]: <d_act, act> over each block of columns
-    int64_t rows, ld;
-    int F, E;
+    int64_t rows;
+    int ld, F, E;
 };
 
 constexpr int TILE = 128;       // rows and columns of a tile
@@ -39,39 +41,44 @@ constexpr int MAX_E = 1024;
 // GEMM1 are.
 __device__ __forceinline__ float scale_of(float amax) { return fmaxf(block_scale(amax), 0x1p-126f); }
 
-// four codes (value 0 in the low byte), two at a time to fp32, times the scale
-__device__ __forceinline__ void decode4(uint32_t q, uint64_t s2, uint64_t (&v)[2])
+// four codes (value 0 in the low byte) to fp32
+__device__ __forceinline__ void decode4(uint32_t q, float (&f)[4])
 {
 #pragma unroll
     for (int i = 0; i < 2; i++) {
         const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(q >> (16 * i)), __NV_E4M3);
-        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
-        v[i] = mul2(pack2(f.x, f.y), s2);
+        const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+        f[2 * i] = v.x;
+        f[2 * i + 1] = v.y;
     }
 }
 
-// one row's four columns: a (bf16), gate and up codes -> d_gate, d_up, act,
-// two columns in each 64-bit pair, and a act summed into dot
+// One row's four columns: a (bf16), gate and up codes -> d_gate, d_up, act,
+// two columns in each 64-bit pair, and a act summed into dot.  Products with
+// the row's scales and sums with constants are scalar (a packed operand
+// would have to be doubled first), the rest packed.  It is -sg that the
+// reciprocal gives: silu p = (-g)(-sg), and p - p sg comes out of one fused
+// multiply-add, exact where sg is next to 1.
 __device__ __forceinline__ void swiglu4(uint2 a, uint32_t gq, uint32_t uq, float gs, float us, uint64_t (&dg)[2],
                                         uint64_t (&du)[2], uint64_t (&act)[2], uint64_t &dot)
 {
-    uint64_t g[2], u[2];
-    decode4(gq, pack2(gs, gs), g);
-    decode4(uq, pack2(us, us), u);
+    float g_[4], u_[4];
+    decode4(gq, g_);
+    decode4(uq, u_);
     const uint32_t aw[2] = {a.x, a.y};
     dot = 0;
+    const uint64_t gs2 = pack2(-gs, -gs), us2 = pack2(us, us);
 #pragma unroll
     for (int i = 0; i < 2; i++) {
+        const uint64_t g = mul2(pack2(g_[2*i], g_[2*i+1]), gs2), u = mul2(pack2(u_[2*i], u_[2*i+1]), us2);
         const uint64_t a2 = pack2(__uint_as_float(aw[i] << 16), __uint_as_float(aw[i] & 0xFFFF0000u));
         float t0, t1;
-        unpack2(mul2(g[i], pack2(-LOG2E, -LOG2E)), t0, t1);
-        unpack2(add2(pack2(ex2(t0), ex2(t1)), pack2(1.0f, 1.0f)), t0, t1);
-        const uint64_t sg = pack2(rcp(t0), rcp(t1));
-        const uint64_t p = mul2(g[i], sg);                                    // silu
-        const uint64_t rest = fma2(sg, pack2(-1.0f, -1.0f), pack2(1.0f, 1.0f));
+        unpack2(g, t0, t1);
+        const uint64_t nsg = pack2(rcp(-1.0f - ex2(t0 * LOG2E)), rcp(-1.0f - ex2(t1 * LOG2E)));
+        const uint64_t p = mul2(g, nsg);
         du[i] = mul2(a2, p);
-        dg[i] = mul2(mul2(a2, u[i]), fma2(p, rest, sg));
-        act[i] = mul2(p, u[i]);
+        dg[i] = mul2(mul2(a2, u), sub2(fma2(p, nsg, p), nsg));
+        act[i] = mul2(p, u);
         dot = fma2(a2, act[i], dot);
     }
 }
@@ -100,9 +107,9 @@ __device__ __forceinline__ float warp_max(float v)
 __device__ __forceinline__ uint32_t encode4(const uint64_t (&v)[2], float y)
 {
     float a, b, c, d;
-    unpack2(mul2(v[0], pack2(y, y)), a, b);
-    unpack2(mul2(v[1], pack2(y, y)), c, d);
-    return (uint32_t)pack_e4m3x2(a, b) | ((uint32_t)pack_e4m3x2(c, d) << 16);
+    unpack2(v[0], a, b);
+    unpack2(v[1], c, d);
+    return (uint32_t)pack_e4m3x2(a * y, b * y) | ((uint32_t)pack_e4m3x2(c * y, d * y) << 16);
 }
 
 // eight sums of a warp's lanes, sum i left in every lane with lane / 4 = i:
@@ -184,8 +191,8 @@ __global__ void __launch_bounds__(THREADS, 1) swiglu_ckpt_kernel(Args p)
             s_off[e] = __ldg(p.offsets + e);
         }
         __syncthreads();
-        const int64_t P = s_pad[p.E] < p.ld ? s_pad[p.E] : p.ld;
-        blocks = P > 0 ? (int)(P / TILE) : 0;
+        const int P = s_pad[p.E] < p.ld ? s_pad[p.E] : p.ld;
+        blocks = P > 0 ? P / TILE : 0;
     }
     // this CTA's tiles: the same number each, the first ones one more
     const int total = blocks * nb, each = total / (int)gridDim.x, more = total - each * (int)gridDim.x;
@@ -233,6 +240,35 @@ __global__ void __launch_bounds__(THREADS, 1) swiglu_ckpt_kernel(Args p)
         }
         cp_async_commit();
         return w;
+    };
+    // A tile's codes leave while the next tile is at work (no barrier of their
+    // own: the next tile's first one has every code in place, its second one
+    // every code read).  Sixteen bytes a thread, eight threads a channel, 64
+    // channels at a time: channel tid / 8 + 64 i of the tile's 3 x 128, whose
+    // lane's l & 15 was this warp's number.
+    Where before{-1, 0, 0, 0};
+    const auto leave = [&] {
+        if (before.kb < 0) return;
+        const int ch = tid >> 3, pc = tid & 7;
+        const uint8_t *src = codes + ch * TILE + (((2 * pc) ^ warp) & ~1) * 8;
+        const int64_t off = (int64_t)(before.cb * TILE + ch) * p.ld + before.kb * TILE + 16 * pc;
+        const auto one = [&](uint8_t *q, int i) {
+            uint4 w = *reinterpret_cast<const uint4 *>(src + i * 64 * TILE);
+            if (warp & 1) w = make_uint4(w.z, w.w, w.x, w.y);
+            *reinterpret_cast<uint4 *>(q) = w;
+        };
+        const int64_t half = 64 * (int64_t)p.ld;
+        if (p.dhT_q) {
+            uint8_t *q = p.dhT_q + off, *u = q + (int64_t)p.F * p.ld;
+            one(q, 0);
+            one(q + half, 1);
+            one(u, 2);
+            one(u + half, 3);
+        }
+        if (p.actT_q) {
+            one(p.actT_q + off, 4);
+            one(p.actT_q + off + half, 5);
+        }
     };
     Where now = fetch(0), next = fetch(1);
     int stage = 0;
@@ -298,23 +334,24 @@ __global__ void __launch_bounds__(THREADS, 1) swiglu_ckpt_kernel(Args p)
                     p.dhT_s[(int64_t)at.kb * 2 * p.F + k * p.F + ch] = s;
                 }
             }
+            leave();
         }
         if (ROW) {
             const float s = scale_of(rm), ry = __frcp_rn(s);
             if ((lane >> 1) < at.n) p.dh_s[(int64_t)(at.row + (lane >> 1)) * 2 * nb + (lane & 1) * nb + at.cb] = s;
-            uint8_t *q = p.dh_q + (int64_t)at.row * 2 * p.F + at.cb * TILE + c0;
+            uint8_t *q = p.dh_q + (int64_t)at.row * 2 * p.F + at.cb * TILE + c0, *q2 = q + p.F;
 #pragma unroll
-            for (int i = 0; i < RW; i++, q += 2 * p.F) {
+            for (int i = 0; i < RW; i++, q += 2 * p.F, q2 += 2 * p.F) {
                 const uint32_t g = encode4(v[0][i], __shfl_sync(0xFFFFFFFFu, ry, 2 * i));
                 const uint32_t u = encode4(v[1][i], __shfl_sync(0xFFFFFFFFu, ry, 2 * i + 1));
                 if (i < at.n) {
                     *reinterpret_cast<uint32_t *>(q) = g;
-                    *reinterpret_cast<uint32_t *>(q + p.F) = u;
+                    *reinterpret_cast<uint32_t *>(q2) = u;
                 }
             }
         }
         if (COL) {
-            __syncthreads();                                           // the reciprocals; the last tile's codes have left
+            __syncthreads();                                           // the reciprocals; the last tile's codes were read
 #pragma unroll
             for (int k = 0; k < 3; k++) {
                 const float4 y4 = *reinterpret_cast<const float4 *>(col_y + k * TILE + c0);
@@ -335,22 +372,12 @@ __global__ void __launch_bounds__(THREADS, 1) swiglu_ckpt_kernel(Args p)
                     dst[TILE / 8] = make_uint2(hi[0], hi[1]);
                 }
             }
-            __syncthreads();
-            // sixteen bytes a thread, eight threads a channel, 64 channels at a
-            // time: channel tid / 8 + 64 i of the tile's 3 x 128, whose lane's
-            // l & 15 above was this warp's number
-            const int ch = tid >> 3, pc = tid & 7;
-            const uint8_t *src = codes + ch * TILE + (((2 * pc) ^ warp) & ~1) * 8;
-            const int64_t off = ((int64_t)at.cb * TILE + ch) * p.ld + (int64_t)at.kb * TILE + 16 * pc;
-#pragma unroll
-            for (int i = 0; i < 6; i++) {
-                uint4 w = *reinterpret_cast<const uint4 *>(src + i * 64 * TILE);
-                if (warp & 1) w = make_uint4(w.z, w.w, w.x, w.y);
-                uint8_t *base = i < 4 ? p.dhT_q : p.actT_q;
-                const int64_t more_rows = (int64_t)((i & 1) * 64 + (i == 2 || i == 3 ? p.F : 0));
-                if (base) *reinterpret_cast<uint4 *>(base + off + more_rows * p.ld) = w;
-            }
+            before = at;
         }
+    }
+    if (COL) {
+        __syncthreads();
+        leave();
     }
     cp_async_wait<0>();
 }
@@ -423,7 +450,7 @@ MOE_API moe_status moe_swiglu_backward_ckpt(const uint16_t *d_act, const uint8_t
     if (dots && !aligned16(workspace)) return MOE_ERR_ALIGN;
     cudaStream_t st = as_stream(stream);
     float *ws = dots ? static_cast<float *>(workspace) : nullptr;
-    Args p{d_act, h_q, h_s, expert_offsets, pad, dh_q, dhT_q, actT_q, dh_s, dhT_s, actT_s, ws, rows, max_pad, F, E};
+    Args p{d_act, h_q, h_s, expert_offsets, pad, dh_q, dhT_q, actT_q, dh_s, dhT_s, actT_s, ws, rows, (int)max_pad, F, E};
     const int64_t blocks = col ? max_pad / 128 : (rows + 127) / 128;
     if (blocks && (dh_q || col || dots)) {
         const cudaError_t e = dh_q ? (col ? launch<true, true>(p, blocks, st) : launch<true, false>(p, blocks, st))

@@ -36,11 +36,6 @@ constexpr int RW = TILE / WARPS;
 constexpr int THREADS = WARPS * 32;
 constexpr int MAX_E = 1024;
 
-// A block's scale: amax / 448 (1 where that is 0), not below 2^-126, so that
-// its reciprocal is finite.  A code is E4M3(v RN(1 / s)), as the act codes of
-// GEMM1 are.
-__device__ __forceinline__ float scale_of(float amax) { return fmaxf(block_scale(amax), 0x1p-126f); }
-
 // four codes (value 0 in the low byte) to fp32
 __device__ __forceinline__ void decode4(uint32_t q, float (&f)[4])
 {
@@ -83,13 +78,6 @@ __device__ __forceinline__ void swiglu4(uint2 a, uint32_t gq, uint32_t uq, float
     }
 }
 
-// the largest magnitude of three (a NaN is passed over)
-__device__ __forceinline__ float amax3(float a, float b, float c)
-{
-    float m;
-    asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
-    return m;
-}
 __device__ __forceinline__ float amax4(const uint64_t (&v)[2])
 {
     float a, b, c, d;
@@ -325,7 +313,7 @@ __global__ void __launch_bounds__(THREADS, 1) swiglu_ckpt_kernel(Args p)
                 float m = red[tid];
 #pragma unroll
                 for (int w = 1; w < WARPS; w++) m = fmaxf(m, red[w * 3 * TILE + tid]);
-                const float s = scale_of(m);
+                const float s = computed_scale(m);
                 col_y[tid] = __frcp_rn(s);
                 const int k = tid >> 7, ch = at.cb * TILE + (tid & 127);
                 if (k == 2) {
@@ -337,7 +325,7 @@ __global__ void __launch_bounds__(THREADS, 1) swiglu_ckpt_kernel(Args p)
             leave();
         }
         if (ROW) {
-            const float s = scale_of(rm), ry = __frcp_rn(s);
+            const float s = computed_scale(rm), ry = __frcp_rn(s);
             if ((lane >> 1) < at.n) p.dh_s[(int64_t)(at.row + (lane >> 1)) * 2 * nb + (lane & 1) * nb + at.cb] = s;
             uint8_t *q = p.dh_q + (int64_t)at.row * 2 * p.F + at.cb * TILE + c0, *q2 = q + p.F;
 #pragma unroll

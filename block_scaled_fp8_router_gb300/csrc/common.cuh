@@ -169,6 +169,21 @@ __device__ __forceinline__ uint16_t e4m3x2_div(float v0, float v1, float s, floa
     return pack_e4m3x2(__fdiv_rn(v0, s), __fdiv_rn(v1, s));
 }
 
+// ---- codes of computed values (a checkpoint, a gradient's operand) ----
+// The scale amax / 448 (1 where that is 0), not below 2^-126 so that its
+// reciprocal is finite; a code is E4M3(v RN(1 / s)): one product an element,
+// where the quotient of the given tensors' quantiser takes five, and no less
+// exact for a value that is itself off by some 2^-24.
+__device__ __forceinline__ float computed_scale(float amax) { return fmaxf(block_scale(amax), 0x1p-126f); }
+
+// the largest magnitude of three (a NaN is passed over)
+__device__ __forceinline__ float amax3(float a, float b, float c)
+{
+    float m;
+    asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
+    return m;
+}
+
 __device__ __forceinline__ void dev_flag(int32_t *status, int32_t bits)
 {
     if (status) atomicOr(status, bits);

@@ -10,12 +10,13 @@
 // m2 = mean(g xhat):
 //   dx = r (g - m1 - xhat m2) + dx_add,  dw = sum_rows a xhat,  db = sum_rows a.
 // Everything between the loads and the stores is fp32.
-#include "common.cuh"
+#include "losses.cuh"
 
 namespace moe {
 namespace norm {
 
 constexpr int MAX_COLS = 16384;
+constexpr int SMEM_MAX = 220 * 1024;
 
 // ---- rows of bf16 or fp32, VEC elements at a time (16 bytes, or one element) ----
 template <typename T, int VEC>
@@ -134,104 +135,185 @@ struct Fwd {
     bool center, w_f32;
 };
 
-// VEC consecutive values of a row, 128 / VEC lanes a block, to codes
-template <int VEC>
-__device__ __forceinline__ void encode(const float (&v)[VEC], bool in, int lane, int64_t at, uint8_t *q, float *s)
+// N values of each lane reduced (largest) over groups of G lanes, N <= G
+// powers of two: value i is left in the lanes of the group whose number
+// within it starts, in its log2(N) highest bits, with i.  Each step keeps
+// half of the values: 2 N shuffles fewer than a reduction of each.
+template <int N, int G>
+__device__ __forceinline__ float scatter_max(float (&v)[N], int lane)
 {
-    if constexpr (VEC >= 4) {
-        float amax = 0.0f;
+    int o = G / 2;
 #pragma unroll
-        for (int i = 0; i < VEC; i++) amax = fmaxf(amax, fabsf(v[i]));
+    for (int n = N / 2; n; n /= 2, o /= 2) {
+        const bool hi = lane & o;
 #pragma unroll
-        for (int o = 64 / VEC; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-        const float sc = block_scale(amax);
-        if (!in) return;
-        const float y = scale_recip(sc);
-        const uint32_t lo = e4m3x4_div<2>(v[0], v[1], v[2], v[3], sc, y);
-        if constexpr (VEC == 8)
-            *reinterpret_cast<uint2 *>(q + at) = make_uint2(lo, e4m3x4_div<2>(v[4], v[5], v[6], v[7], sc, y));
-        else
-            *reinterpret_cast<uint32_t *>(q + at) = lo;
-        if ((lane & (128 / VEC - 1)) == 0) s[at >> 7] = sc;
+        for (int i = 0; i < n; i++)
+            v[i] = fmaxf(hi ? v[n + i] : v[i], __shfl_xor_sync(0xFFFFFFFFu, hi ? v[i] : v[n + i], o));
+    }
+#pragma unroll
+    for (; o; o /= 2) v[0] = fmaxf(v[0], __shfl_xor_sync(0xFFFFFFFFu, v[0], o));
+    return v[0];
+}
+
+// A thread's VPT vectors of a row to codes: a 128-block is one vector of
+// 128 / VEC lanes.  Each scale is formed once, by the lanes that end up with
+// its block's largest value.  c: the thread's first column; q, s: the row's.
+template <int VEC, int VPT>
+__device__ __forceinline__ void encode(const uint64_t (&v)[VPT][VEC / 2], int c, int cols, int lane, uint8_t *q, float *s)
+{
+    constexpr int G = 128 / VEC, EACH = G / VPT;               // lanes of a block; lanes that hold one block's value
+    float m[VPT];
+#pragma unroll
+    for (int i = 0; i < VPT; i++) {
+        m[i] = 0.0f;
+#pragma unroll
+        for (int j = 0; j < VEC / 2; j++) {
+            float a, b;
+            unpack2(v[i][j], a, b);
+            m[i] = amax3(a, b, m[i]);
+        }
+    }
+    const float sc = computed_scale(scatter_max<VPT, G>(m, lane)), y = __frcp_rn(sc);
+    const int mine = (lane & (G - 1)) / EACH;                  // the vector whose scale this lane has
+    const int c_mine = c - (lane & (G - 1)) * VEC + mine * 32 * VEC;
+    if ((lane & (EACH - 1)) == 0 && c_mine < cols) s[c_mine >> 7] = sc;
+#pragma unroll
+    for (int i = 0; i < VPT; i++) {
+        const float yi = __shfl_sync(0xFFFFFFFFu, y, (lane & ~(G - 1)) + i * EACH);
+        if (c + i * 32 * VEC >= cols) continue;
+        uint32_t w[VEC / 4];
+#pragma unroll
+        for (int k = 0; k < VEC / 4; k++) {
+            float a, b, e, f;
+            unpack2(v[i][2 * k], a, b);
+            unpack2(v[i][2 * k + 1], e, f);
+            w[k] = (uint32_t)pack_e4m3x2(a * yi, b * yi) | ((uint32_t)pack_e4m3x2(e * yi, f * yi) << 16);
+        }
+        if constexpr (VEC == 8) *reinterpret_cast<uint2 *>(q + c + i * 32 * VEC) = make_uint2(w[0], w[1]);
+        else *reinterpret_cast<uint32_t *>(q + c + i * 32 * VEC) = w[0];
     }
 }
 
 // One row per group of warps, the row held in registers (EPT values a
-// thread) from its one load to the stores.  The mean is taken twice: the sum
-// of x - mu' with the first mean mu' gives what rounding left out of it, at
-// no further exchange (it rides with the sum of squares).
+// thread, two in each 64-bit pair) from its one load to the stores.  A warp's
+// vectors lie side by side, so a thread's addresses are one base and
+// constants.  The mean is taken twice: the sum of x - mu' with the first mean
+// mu' gives what rounding left out of it, at no further exchange (it rides
+// with the sum of squares).
 template <typename T, int VEC, int EPT>
-__global__ void __launch_bounds__(EPT == 8 ? 1024 : 512) norm_kernel(Fwd p)
+__global__ void __launch_bounds__(EPT == 8 ? 1024 : 512, EPT == 16 ? 2 : 1) norm_kernel(Fwd p)
 {
-    constexpr int VPT = EPT / VEC;
+    constexpr int N = VEC > 1 ? EPT / VEC : EPT / 2, H = VEC > 1 ? VEC / 2 : 1;      // vectors, or pairs of single values
+    constexpr int STEP = VEC > 1 ? 32 * VEC : 64;              // columns from one to the next
     __shared__ float2 red[2][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int group = warp / p.warps;
+    const int group = warp / p.warps, gw = warp - group * p.warps;
     const int64_t row = (int64_t)blockIdx.x * ((blockDim.x >> 5) / p.warps) + group;
     if (row >= p.rows) return;                         // only where a row is one warp: no barrier below
-    const int t = threadIdx.x - group * p.warps * 32, nth = p.warps * 32;
-    const T *x = static_cast<const T *>(p.x) + row * p.ld_x;
+    const int c = gw * 32 * EPT + lane * VEC;          // the thread's first column
+    const T *x = static_cast<const T *>(p.x) + row * p.ld_x + c;
     const float inv_n = 1.0f / (float)p.cols;
-    float v[VPT][VEC];
-    float sum = 0.0f, sq = 0.0f;
+    const auto in = [&](int i) { return c + i * STEP < p.cols; };
+    const auto in2 = [&](int i) { return c + i * STEP + 32 < p.cols; };              // a pair's second single value
+    uint64_t v[N][H];
 #pragma unroll
-    for (int i = 0; i < VPT; i++) {
-        const int c = (t + i * nth) * VEC;
-        if (c < p.cols) {
-            load<T, VEC>(x + c, v[i]);
+    for (int i = 0; i < N; i++) {
+        if constexpr (VEC > 1) {
+            float f[VEC] = {};
+            if (in(i)) load<T, VEC>(x + i * STEP, f);
+#pragma unroll
+            for (int j = 0; j < H; j++) v[i][j] = pack2(f[2 * j], f[2 * j + 1]);
         } else {
-#pragma unroll
-            for (int j = 0; j < VEC; j++) v[i][j] = 0.0f;
+            float a[1] = {0.0f}, b[1] = {0.0f};
+            if (in(i)) load<T, 1>(x + i * STEP, a);
+            if (in2(i)) load<T, 1>(x + i * STEP + 32, b);
+            v[i][0] = pack2(a[0], b[0]);
         }
     }
+    float sum = 0.0f, sq = 0.0f;
     if (p.center) {
+        uint64_t s2 = 0;
 #pragma unroll
-        for (int i = 0; i < VPT; i++) {
+        for (int i = 0; i < N; i++) {
 #pragma unroll
-            for (int j = 0; j < VEC; j++) sum += v[i][j];
+            for (int j = 0; j < H; j++) s2 = add2(s2, v[i][j]);
         }
-        row_sums(sum, sq, red[0], p.warps, warp - group * p.warps, lane, 0);
+        unpack2(s2, sum, sq);
+        sum += sq;
+        sq = 0.0f;
+        row_sums(sum, sq, red[0], p.warps, gw, lane, 0);
     }
     const float mu = sum * inv_n;
-    sum = sq = 0.0f;
+    uint64_t s2 = 0, q2 = 0;
 #pragma unroll
-    for (int i = 0; i < VPT; i++) {
-        const bool in = (t + i * nth) * VEC < p.cols;
+    for (int i = 0; i < N; i++) {
+        if (p.center) {
+            // absent columns stay 0
+            const float m0 = in(i) ? -mu : 0.0f, m1 = VEC > 1 ? m0 : in2(i) ? -mu : 0.0f;
+            const uint64_t m = pack2(m0, m1);
 #pragma unroll
-        for (int j = 0; j < VEC; j++) {
-            v[i][j] = in ? v[i][j] - mu : 0.0f;
-            sum += v[i][j];
-            sq = fmaf(v[i][j], v[i][j], sq);
+            for (int j = 0; j < H; j++) {
+                v[i][j] = add2(v[i][j], m);
+                s2 = add2(s2, v[i][j]);
+            }
         }
+#pragma unroll
+        for (int j = 0; j < H; j++) q2 = fma2(v[i][j], v[i][j], q2);
     }
-    row_sums(sum, sq, red[1], p.warps, warp - group * p.warps, lane, 0);
-    const float rest = p.center ? sum * inv_n : 0.0f;
+    float a, b;
+    unpack2(s2, a, b);
+    sum = a + b;
+    unpack2(q2, a, b);
+    sq = a + b;
+    row_sums(sum, sq, red[1], p.warps, gw, lane, 0);
+    const float rest = sum * inv_n;                    // 0 without center
     float var = fmaf(sq, inv_n, -rest * rest);
     if (var < 0.0f) var = 0.0f;                        // a NaN stays
     const float rstd = rsqrtf(var + p.eps);
-    if (t == 0) {
+    if (gw == 0 && lane == 0) {
         if (p.mean) p.mean[row] = mu + rest;
         if (p.rstd) p.rstd[row] = rstd;
     }
+    const uint64_t r2 = pack2(rstd, rstd), c2 = pack2(-rest * rstd, -rest * rstd);
 #pragma unroll
-    for (int i = 0; i < VPT; i++) {
-        const int c = (t + i * nth) * VEC;
-        const bool in = c < p.cols;
-        float w[VEC], b[VEC], y[VEC];
+    for (int i = 0; i < N; i++) {
 #pragma unroll
-        for (int j = 0; j < VEC; j++) v[i][j] = (v[i][j] - rest) * rstd;
-        if (p.h_q) encode<VEC>(v[i], in, lane, row * p.cols + c, p.h_q, p.h_s);
-        if (in) {
-            load_weight<VEC>(p.w, p.w_f32, c, 1.0f, w);
-            load_weight<VEC>(p.b, p.w_f32, c, 0.0f, b);
-        } else {
+        for (int j = 0; j < H; j++) v[i][j] = p.center ? fma2(v[i][j], r2, c2) : mul2(v[i][j], r2);
+    }
+    T *y = static_cast<T *>(p.y) + row * p.ld_y + c;
+    if constexpr (VEC > 1) {
+        const int64_t at = row * p.cols, at_s = row * (p.cols >> 7);
+        if (p.h_q) encode<VEC, N>(v, c, p.cols, lane, p.h_q + at, p.h_s + at_s);
 #pragma unroll
-            for (int j = 0; j < VEC; j++) w[j] = b[j] = 0.0f;
+        for (int i = 0; i < N; i++) {
+            float w[VEC] = {}, f[VEC] = {};
+            if (in(i)) {
+                load_weight<VEC>(p.w, p.w_f32, c + i * STEP, 1.0f, w);
+                if (p.b) load_weight<VEC>(p.b, p.w_f32, c + i * STEP, 0.0f, f);
+            }
+#pragma unroll
+            for (int j = 0; j < H; j++) {
+                v[i][j] = fma2(v[i][j], pack2(w[2 * j], w[2 * j + 1]), pack2(f[2 * j], f[2 * j + 1]));
+                unpack2(v[i][j], f[2 * j], f[2 * j + 1]);
+            }
+            if (in(i)) store<T, VEC>(y + i * STEP, f);
         }
+        if (p.y_q) encode<VEC, N>(v, c, p.cols, lane, p.y_q + at, p.y_s + at_s);
+    } else {
 #pragma unroll
-        for (int j = 0; j < VEC; j++) y[j] = fmaf(v[i][j], w[j], b[j]);
-        if (in) store<T, VEC>(static_cast<T *>(p.y) + row * p.ld_y + c, y);
-        if (p.y_q) encode<VEC>(y, in, lane, row * p.cols + c, p.y_q, p.y_s);
+        for (int i = 0; i < N; i++) {
+            float h[2];
+            unpack2(v[i][0], h[0], h[1]);
+#pragma unroll
+            for (int j = 0; j < 2; j++) {
+                if (!(j ? in2(i) : in(i))) continue;
+                float w[1], f[1];
+                load_weight<1>(p.w, p.w_f32, c + i * STEP + 32 * j, 1.0f, w);
+                load_weight<1>(p.b, p.w_f32, c + i * STEP + 32 * j, 0.0f, f);
+                f[0] = fmaf(h[j], w[0], f[0]);
+                store<T, 1>(y + i * STEP + 32 * j, f);
+            }
+        }
     }
 }
 
@@ -245,123 +327,315 @@ struct Bwd {
     const float *mean, *rstd;
     void *dx;
     float *part;                // per CTA: cols sums of a xhat, cols sums of a
-    int64_t rows, ld_dy, ld_x, ld_add, ld_dx;
-    int cols, warps, groups;
+    int64_t ld_dy, ld_x, ld_add, ld_dx;
+    int rows, cols, warps, groups, stages;
+    // a stage of a group in shared memory: dy, then x or the codes, the scales, dy_add (-1: not staged)
+    int stage_bytes, at_x, at_s, at_dya;
     bool center, w_f32, want_w, want_b;
 };
 
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void *src)
+{
+    if (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
+}
+
+// the oldest of `stages` pending groups
+__device__ __forceinline__ void wait_oldest(int stages)
+{
+    if (stages == 1) cp_async_wait<0>();
+    else if (stages == 2) cp_async_wait<1>();
+    else if (stages == 3) cp_async_wait<2>();
+    else cp_async_wait<3>();
+}
+
+// VEC values to pairs; of single values two that lie 32 apart, the second one 0 where it is absent
+template <typename T, int VEC>
+__device__ __forceinline__ void pairs(const T *p, bool second, uint64_t (&v)[(VEC + 1) / 2])
+{
+    if constexpr (VEC == 1) {
+        float a[1], b[1] = {0.0f};
+        load<T, 1>(p, a);
+        if (second) load<T, 1>(p + 32, b);
+        v[0] = pack2(a[0], b[0]);
+    } else {
+        float f[VEC];
+        load<T, VEC>(p, f);
+#pragma unroll
+        for (int j = 0; j < VEC / 2; j++) v[j] = pack2(f[2 * j], f[2 * j + 1]);
+    }
+}
+
+// VEC codes of one block to fp32, times its scale
+template <int VEC>
+__device__ __forceinline__ void decode(const uint8_t *q, float s, uint64_t (&v)[VEC / 2])
+{
+    uint32_t w[VEC / 4];
+    if constexpr (VEC == 8) {
+        const uint2 r = *reinterpret_cast<const uint2 *>(q);
+        w[0] = r.x, w[1] = r.y;
+    } else {
+        w[0] = *reinterpret_cast<const uint32_t *>(q);
+    }
+    const uint64_t s2 = pack2(s, s);
+#pragma unroll
+    for (int i = 0; i < VEC / 2; i++) {
+        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[i / 2] >> (16 * (i & 1))), __NV_E4M3);
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+        v[i] = mul2(pack2(f.x, f.y), s2);
+    }
+}
+
 // Rows over groups of warps, grid-wide in turn; a thread owns the same EPT
 // columns of every row of its group, so the sums over rows stay in registers
-// until the CTA's last row.  Then the groups' sums are joined in group order
-// through shared memory and leave as this CTA's part; reduce_kernel adds the
-// parts in CTA order (no atomics: the same bits every time).
-template <typename T, int VEC, int EPT, bool CKPT>
-__global__ void __launch_bounds__(512) dnorm_kernel(Bwd p)
+// until the CTA's last row.  Whole vectors come through a ring of rows in
+// shared memory, copied asynchronously by the thread that reads them; single
+// values are read where they are used.  With KEEP a thread holds g and xhat of
+// its columns from the row's means to dx; without (rows too long for that
+// beside the sums) it reads them again.  At the end the groups' sums are
+// joined in group order through shared memory and leave as this CTA's part;
+// reduce_kernel adds the parts in CTA order (no atomics: the same bits every
+// time).
+constexpr int BWD_THREADS = 512;                       // at up to 128 registers
+
+template <typename T, int VEC, int EPT, bool CKPT, bool BIAS>
+__global__ void __launch_bounds__(BWD_THREADS, 1) dnorm_kernel(Bwd p)
 {
-    constexpr int VPT = EPT / VEC;
-    extern __shared__ float joined[];                  // [2][cols], groups > 1
+    // vectors, or pairs of single values 32 columns apart
+    constexpr int N = VEC > 1 ? EPT / VEC : EPT / 2, H = (VEC + 1) / 2, STEP = VEC > 1 ? 32 * VEC : 64;
+    constexpr bool RING = VEC > 1, KEEP = EPT == 16;
+    extern __shared__ __align__(16) uint8_t ring[];
     __shared__ float2 red[2][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int group = warp / p.warps, gw = warp - group * p.warps;
-    const int t = threadIdx.x - group * p.warps * 32, nth = p.warps * 32;
+    const int c = gw * 32 * EPT + lane * VEC, left = p.cols - c;       // the thread's first column, and those from there on
     const float inv_n = 1.0f / (float)p.cols;
-    float w[VPT][VEC], dw[VPT][VEC], db[VPT][VEC];
+    const int first = (int)blockIdx.x * p.groups + group, step = (int)gridDim.x * p.groups;
+    uint8_t *mine = ring + group * p.stages * p.stage_bytes;
+    const uint32_t mine_u = smem_u32(mine);
+    const int half = p.cols * 2;                       // bytes of the first halves of dy_add's vectors of eight
+    const auto in = [&](int i) { return i * STEP < left; };
+    const auto in2 = [&](int i) { return i * STEP + 32 < left; };      // a pair's second single value
+
+    const auto issue = [&](int64_t row, int stage) {
+        if constexpr (RING) {
+            if (row < p.rows) {
+                const uint32_t dst = mine_u + stage * p.stage_bytes;
+                const T *dy = static_cast<const T *>(p.dy) + row * p.ld_dy + c;
+                const int64_t at = row * p.cols + c;
 #pragma unroll
-    for (int i = 0; i < VPT; i++) {
-        const int c = (t + i * nth) * VEC;
-        if (c < p.cols) load_weight<VEC>(p.w, p.w_f32, c, 1.0f, w[i]);
-#pragma unroll
-        for (int j = 0; j < VEC; j++) {
-            if (c >= p.cols) w[i][j] = 0.0f;
-            dw[i][j] = db[i][j] = 0.0f;
-        }
-    }
-    const int64_t step = (int64_t)gridDim.x * p.groups;
-    int par = 0;
-    for (int64_t row = (int64_t)blockIdx.x * p.groups + group; row < p.rows; row += step, par ^= 1) {
-        const float rs = __ldg(p.rstd + row), mu = p.center && !CKPT ? __ldg(p.mean + row) : 0.0f;
-        float g[VPT][VEC], h[VPT][VEC];
-        float s1 = 0.0f, s2 = 0.0f;
-#pragma unroll
-        for (int i = 0; i < VPT; i++) {
-            const int c = (t + i * nth) * VEC;
-            if (c < p.cols) {
-                float a[VEC];
-                load<T, VEC>(static_cast<const T *>(p.dy) + row * p.ld_dy + c, a);
-                if (p.dy_add) {
-#pragma unroll
-                    for (int j = 0; j < VEC; j++) a[j] += __ldg(p.dy_add + row * p.cols + c + j);
-                }
+                for (int i = 0; i < N; i++)
+                    if (in(i)) copy_async<16>(dst + c * (int)sizeof(T) + i * 512, dy + i * STEP);
                 if constexpr (CKPT) {
-                    const float sc = __ldg(p.h_s + ((row * p.cols + c) >> 7));
+                    const uint8_t *q = p.h_q + at;
+                    const float *s = p.h_s + (at >> 7);
 #pragma unroll
-                    for (int j = 0; j < VEC; j++) {
-                        __nv_fp8_e4m3 q;
-                        q.__x = __ldg(p.h_q + row * p.cols + c + j);
-                        h[i][j] = (float)q * sc;
+                    for (int i = 0; i < N; i++) {
+                        if (!in(i)) continue;
+                        copy_async<VEC>(dst + p.at_x + c + i * STEP, q + i * STEP);
+                        if ((lane & (128 / VEC - 1)) == 0)
+                            copy_async<4>(dst + p.at_s + (c >> 7) * 4 + i * STEP / 32, s + i * STEP / 128);
                     }
                 } else {
-                    load<T, VEC>(static_cast<const T *>(p.x) + row * p.ld_x + c, h[i]);
+                    const T *x = static_cast<const T *>(p.x) + row * p.ld_x + c;
 #pragma unroll
-                    for (int j = 0; j < VEC; j++) h[i][j] = (h[i][j] - mu) * rs;
+                    for (int i = 0; i < N; i++)
+                        if (in(i)) copy_async<16>(dst + p.at_x + c * (int)sizeof(T) + i * 512, x + i * STEP);
                 }
+                if (p.at_dya >= 0) {
+                    const float *d = p.dy_add + at;
 #pragma unroll
-                for (int j = 0; j < VEC; j++) {
-                    g[i][j] = a[j] * w[i][j];
-                    s1 += g[i][j];
-                    s2 = fmaf(g[i][j], h[i][j], s2);
-                    dw[i][j] = fmaf(a[j], h[i][j], dw[i][j]);
-                    db[i][j] += a[j];
+                    for (int i = 0; i < N; i++) {
+                        if (!in(i)) continue;
+                        copy_async<16>(dst + p.at_dya + c / VEC * 16 + i * 512, d + i * STEP);
+                        if (VEC == 8) copy_async<16>(dst + p.at_dya + half + c / VEC * 16 + i * 512, d + i * STEP + 4);
+                    }
+                }
+            }
+            cp_async_commit();
+        }
+    };
+    // vector i of the row: a = dy + dy_add and xhat = (x - mu) r, or from its codes
+    const auto get = [&](int64_t row, const uint8_t *st, int i, uint64_t rs2, uint64_t nmu2, uint64_t (&a)[H], uint64_t (&h)[H]) {
+        if constexpr (RING) {
+            pairs<T, VEC>(reinterpret_cast<const T *>(st) + c + i * STEP, false, a);
+            if constexpr (CKPT)
+                decode<VEC>(st + p.at_x + c + i * STEP,
+                            *reinterpret_cast<const float *>(st + p.at_s + (c >> 7) * 4 + i * STEP / 32), h);
+            else pairs<T, VEC>(reinterpret_cast<const T *>(st + p.at_x) + c + i * STEP, false, h);
+        } else {
+            pairs<T, VEC>(static_cast<const T *>(p.dy) + row * p.ld_dy + c + i * STEP, in2(i), a);
+            pairs<T, VEC>(static_cast<const T *>(p.x) + row * p.ld_x + c + i * STEP, in2(i), h);
+        }
+        if (!CKPT) {
+#pragma unroll
+            for (int j = 0; j < H; j++) h[j] = mul2(add2(h[j], nmu2), rs2);
+        }
+        if (p.dy_add) {
+            if constexpr (VEC > 1) {
+#pragma unroll
+                for (int k = 0; k < VEC / 4; k++) {
+                    const float4 d = p.at_dya >= 0
+                                         ? *reinterpret_cast<const float4 *>(st + p.at_dya + k * half + c / VEC * 16 + i * 512)
+                                         : __ldg(reinterpret_cast<const float4 *>(p.dy_add + row * p.cols + c + i * STEP + 4 * k));
+                    a[2 * k] = add2(a[2 * k], pack2(d.x, d.y));
+                    a[2 * k + 1] = add2(a[2 * k + 1], pack2(d.z, d.w));
                 }
             } else {
-#pragma unroll
-                for (int j = 0; j < VEC; j++) g[i][j] = h[i][j] = 0.0f;
+                const float *d = p.dy_add + row * p.cols + c + i * STEP;
+                a[0] = add2(a[0], pack2(__ldg(d), in2(i) ? __ldg(d + 32) : 0.0f));
             }
         }
-        if (!p.dx) continue;
-        // the buffer alternates by row: a warp a row ahead writes the other one
-        row_sums(s1, s2, red[par] + group * p.warps, p.warps, gw, lane, group + 1);
-        const float m1 = p.center ? s1 * inv_n : 0.0f, m2 = s2 * inv_n;
+    };
+    const auto weights = [&](int i, uint64_t (&w)[H]) {
+        float f[VEC > 1 ? VEC : 2];
+        if constexpr (VEC > 1) {
+            load_weight<VEC>(p.w, p.w_f32, c + i * STEP, 1.0f, f);
+        } else {
+            float b[1] = {0.0f}, a[1];
+            load_weight<1>(p.w, p.w_f32, c + i * STEP, 1.0f, a);
+            if (in2(i)) load_weight<1>(p.w, p.w_f32, c + i * STEP + 32, 1.0f, b);
+            f[0] = a[0], f[1] = b[0];
+        }
 #pragma unroll
-        for (int i = 0; i < VPT; i++) {
-            const int c = (t + i * nth) * VEC;
-            if (c >= p.cols) continue;
-            float d[VEC], add[VEC];
+        for (int j = 0; j < H; j++) w[j] = pack2(f[2 * j], f[2 * j + 1]);
+    };
+
+    uint64_t dw[N][H] = {}, db[BIAS ? N : 1][H] = {};
+    if constexpr (RING)
+        for (int s = 0; s < p.stages; s++) issue((int64_t)first + (int64_t)s * step, s);
+    float rs_next = 0.0f, mu_next = 0.0f;              // the next row's, loaded a row ahead
+    const bool mean = p.center && !CKPT;
+    if (first < p.rows) {
+        rs_next = __ldg(p.rstd + first);
+        if (mean) mu_next = __ldg(p.mean + first);
+    }
+    int par = 0, stage = 0;
+    for (int64_t row = first; row < p.rows; row += step, par ^= 1) {
+        const float rs = rs_next;
+        const uint64_t rs2 = pack2(rs, rs), nmu2 = pack2(-mu_next, -mu_next);
+        if (row + step < p.rows) {
+            rs_next = __ldg(p.rstd + row + step);
+            if (mean) mu_next = __ldg(p.mean + row + step);
+        }
+        typename Vec<T, VEC>::Raw add[N], more[VEC > 1 ? 1 : N];      // dx_add: on its way while the means are formed
+        if (p.dx_add) {
+            const T *src = static_cast<const T *>(p.dx_add) + row * p.ld_add + c;
 #pragma unroll
-            for (int j = 0; j < VEC; j++) d[j] = rs * (g[i][j] - fmaf(h[i][j], m2, m1));
-            if (p.dx_add) {
-                load<T, VEC>(static_cast<const T *>(p.dx_add) + row * p.ld_add + c, add);
-#pragma unroll
-                for (int j = 0; j < VEC; j++) d[j] += add[j];
+            for (int i = 0; i < N; i++) {
+                if (in(i)) add[i] = *reinterpret_cast<const typename Vec<T, VEC>::Raw *>(src + i * STEP);
+                if (VEC == 1 && in2(i)) more[VEC > 1 ? 0 : i] = *reinterpret_cast<const typename Vec<T, VEC>::Raw *>(src + i * STEP + 32);
             }
-            store<T, VEC>(static_cast<T *>(p.dx) + row * p.ld_dx + c, d);
+        }
+        const uint8_t *st = mine + stage * p.stage_bytes;
+        if constexpr (RING) {
+            wait_oldest(p.stages);
+            if (CKPT) __syncwarp();                    // a block's scale was copied by one of its lanes
+        }
+        uint64_t g[KEEP ? N : 1][H], h[KEEP ? N : 1][H];
+        uint64_t s1 = 0, s2 = 0;
+#pragma unroll
+        for (int i = 0; i < N; i++) {
+            uint64_t (&hi)[H] = h[KEEP ? i : 0], (&gi)[H] = g[KEEP ? i : 0];
+            if (in(i)) {
+                uint64_t a[H], w[H];
+                get(row, st, i, rs2, nmu2, a, hi);
+                weights(i, w);
+#pragma unroll
+                for (int j = 0; j < H; j++) {
+                    gi[j] = mul2(a[j], w[j]);
+                    s1 = add2(s1, gi[j]);
+                    s2 = fma2(gi[j], hi[j], s2);
+                    dw[i][j] = fma2(a[j], hi[j], dw[i][j]);
+                    if (BIAS) db[i][j] = add2(db[i][j], a[j]);
+                }
+            }
+        }
+        if (RING && KEEP) {
+            if (CKPT) __syncwarp();
+            issue(row + (int64_t)p.stages * step, stage);
+        }
+        if (p.dx) {
+            float m1, m2, x, y;
+            unpack2(s1, x, y);
+            m1 = x + y;
+            unpack2(s2, x, y);
+            m2 = x + y;
+            // the buffer alternates by row: a warp a row ahead writes the other one
+            row_sums(m1, m2, red[par] + group * p.warps, p.warps, gw, lane, group + 1);
+            m1 = p.center ? m1 * inv_n : 0.0f, m2 *= inv_n;
+            const uint64_t nm1 = pack2(-m1, -m1), nm2 = pack2(-m2, -m2);
+            T *dx = static_cast<T *>(p.dx) + row * p.ld_dx + c;
+#pragma unroll
+            for (int i = 0; i < N; i++) {
+                if (!in(i)) continue;
+                uint64_t (&hi)[H] = h[KEEP ? i : 0], (&gi)[H] = g[KEEP ? i : 0];
+                if (!KEEP) {
+                    uint64_t w[H];
+                    get(row, st, i, rs2, nmu2, gi, hi);
+                    weights(i, w);
+#pragma unroll
+                    for (int j = 0; j < H; j++) gi[j] = mul2(gi[j], w[j]);
+                }
+                constexpr int M = VEC > 1 ? VEC : 2;
+                float f[M], d[M] = {};
+                if (p.dx_add) {
+                    float r[VEC];
+                    Vec<T, VEC>::get(add[i], r);
+#pragma unroll
+                    for (int j = 0; j < VEC; j++) d[j] = r[j];
+                    if (VEC == 1 && in2(i)) {
+                        Vec<T, VEC>::get(more[VEC > 1 ? 0 : i], r);
+                        d[1] = r[0];
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < H; j++)
+                    unpack2(fma2(fma2(hi[j], nm2, add2(gi[j], nm1)), rs2, pack2(d[2 * j], d[2 * j + 1])), f[2 * j], f[2 * j + 1]);
+                if constexpr (VEC > 1) {
+                    store<T, VEC>(dx + i * STEP, f);
+                } else {
+                    const float lo[1] = {f[0]}, hi1[1] = {f[1]};
+                    store<T, 1>(dx + i * STEP, lo);
+                    if (in2(i)) store<T, 1>(dx + i * STEP + 32, hi1);
+                }
+            }
+        }
+        if constexpr (RING) {
+            if (!KEEP) {
+                if (CKPT) __syncwarp();
+                issue(row + (int64_t)p.stages * step, stage);
+            }
+            if (++stage == p.stages) stage = 0;
         }
     }
     if (!p.want_w && !p.want_b) return;
+    cp_async_wait<0>();
+    float *joined = reinterpret_cast<float *>(ring);   // [2][cols], groups > 1
     for (int gr = 0; gr < p.groups; gr++) {
-        if (group == gr) {
+        if (p.groups > 1) __syncthreads();             // the first one: the ring is done with
+        if (group != gr) continue;
+        float *to = gr + 1 < p.groups ? joined : p.part + (int64_t)blockIdx.x * 2 * p.cols;
 #pragma unroll
-            for (int i = 0; i < VPT; i++) {
+        for (int i = 0; i < N; i++) {
+            if (!in(i)) continue;
+            float w[2 * H], b[2 * H];
 #pragma unroll
-                for (int j = 0; j < VEC; j++) {
-                    const int c = (t + i * nth) * VEC + j;
-                    if (c >= p.cols) continue;
-                    if (gr) {
-                        dw[i][j] = joined[c] + dw[i][j];
-                        db[i][j] = joined[p.cols + c] + db[i][j];
-                    }
-                    if (gr + 1 < p.groups) {
-                        joined[c] = dw[i][j];
-                        joined[p.cols + c] = db[i][j];
-                    } else {
-                        float *out = p.part + (int64_t)blockIdx.x * 2 * p.cols;
-                        out[c] = dw[i][j];
-                        out[p.cols + c] = db[i][j];
-                    }
-                }
+            for (int j = 0; j < H; j++) {
+                unpack2(dw[i][j], w[2 * j], w[2 * j + 1]);
+                if (BIAS) unpack2(db[i][j], b[2 * j], b[2 * j + 1]);
+            }
+#pragma unroll
+            for (int j = 0; j < (VEC > 1 ? VEC : 2); j++) {
+                if (VEC == 1 && j && !in2(i)) continue;
+                const int k = c + i * STEP + (VEC > 1 ? j : 32 * j);
+                to[k] = gr ? joined[k] + w[j] : w[j];
+                if (BIAS) to[p.cols + k] = gr ? joined[p.cols + k] + b[j] : b[j];
             }
         }
-        if (p.groups > 1) __syncthreads();
     }
 }
 
@@ -428,21 +702,68 @@ static void fwd_launch(const Fwd &p, bool f32, bool vec, unsigned grid, int thre
         vec ? norm_kernel<uint16_t, 8, EPT><<<grid, threads, 0, st>>>(p) : norm_kernel<uint16_t, 1, EPT><<<grid, threads, 0, st>>>(p);
 }
 
-template <int EPT>
-static void bwd_launch(const Bwd &p, bool f32, bool vec, int grid, int threads, size_t smem, cudaStream_t st)
+template <typename T, int VEC, int EPT, bool CKPT, bool BIAS>
+static cudaError_t bwd_launch(const Bwd &p, int grid, int smem, cudaStream_t st)
 {
-    if (p.h_q) {
-        if (f32)
-            dnorm_kernel<float, 4, EPT, true><<<grid, threads, smem, st>>>(p);
-        else
-            dnorm_kernel<uint16_t, 8, EPT, true><<<grid, threads, smem, st>>>(p);
-    } else if (f32) {
-        vec ? dnorm_kernel<float, 4, EPT, false><<<grid, threads, smem, st>>>(p)
-            : dnorm_kernel<float, 1, EPT, false><<<grid, threads, smem, st>>>(p);
-    } else {
-        vec ? dnorm_kernel<uint16_t, 8, EPT, false><<<grid, threads, smem, st>>>(p)
-            : dnorm_kernel<uint16_t, 1, EPT, false><<<grid, threads, smem, st>>>(p);
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = allow_smem(reinterpret_cast<const void *>(dnorm_kernel<T, VEC, EPT, CKPT, BIAS>), SMEM_MAX, done);
+    if (e != cudaSuccess) return e;
+    dnorm_kernel<T, VEC, EPT, CKPT, BIAS><<<grid, p.warps * p.groups * 32, smem, st>>>(p);
+    return cudaGetLastError();
+}
+
+template <typename T, int VEC, int EPT, bool CKPT>
+static cudaError_t bwd_launch_bias(const Bwd &p, int grid, int smem, cudaStream_t st)
+{
+    return p.want_b ? bwd_launch<T, VEC, EPT, CKPT, true>(p, grid, smem, st) : bwd_launch<T, VEC, EPT, CKPT, false>(p, grid, smem, st);
+}
+
+template <typename T, int VEC>
+static cudaError_t bwd_launch_for(const Bwd &p, int ept, int grid, int smem, cudaStream_t st)
+{
+    if constexpr (VEC > 1) {
+        if (p.h_q)
+            return ept == 16 ? bwd_launch_bias<T, VEC, 16, true>(p, grid, smem, st) : bwd_launch_bias<T, VEC, 32, true>(p, grid, smem, st);
     }
+    return ept == 16 ? bwd_launch_bias<T, VEC, 16, false>(p, grid, smem, st) : bwd_launch_bias<T, VEC, 32, false>(p, grid, smem, st);
+}
+
+// The backward's plan: 16 values a thread (32 where a row has more than 512
+// threads would hold), as many groups a CTA as its threads allow (fewer where
+// rows are few, so that they spread over the SMs, and where each would not
+// have two stages), up to four stages; dy_add is read in place where a row
+// with it does not fit at all.
+static int bwd_plan(Bwd &p, bool vec, int es, int &ept, int &smem)
+{
+    ept = p.cols > 8192 ? 32 : 16;
+    p.warps = (p.cols + 32 * ept - 1) / (32 * ept);
+    int groups = BWD_THREADS / 32 / p.warps;
+    const int per_sm = (p.rows + sm_count() - 1) / sm_count();
+    if (groups > 8) groups = 8;                        // named barriers, and the parts joined one after another
+    if (groups > per_sm) groups = per_sm;
+    p.stages = p.stage_bytes = 0;
+    p.at_x = p.at_s = p.at_dya = -1;
+    if (vec) {
+        const auto lay = [&](bool dya) {
+            int n = p.cols * es;
+            p.at_x = n;
+            n += p.h_q ? p.cols : p.cols * es;
+            p.at_s = n;
+            if (p.h_q) n = (n + p.cols / 128 * 4 + 15) & ~15;
+            p.at_dya = dya ? n : -1;
+            if (dya) n += p.cols * 4;
+            p.stage_bytes = n;
+        };
+        lay(p.dy_add != nullptr);
+        if (p.stage_bytes > SMEM_MAX) lay(false);
+        while (groups > 1 && 2 * groups * p.stage_bytes > SMEM_MAX) groups--;
+        p.stages = SMEM_MAX / (groups * p.stage_bytes);
+        if (p.stages > 4) p.stages = 4;
+    }
+    p.groups = groups;
+    const int ring = groups * p.stages * p.stage_bytes, join = groups > 1 ? 2 * p.cols * (int)sizeof(float) : 0;
+    smem = ring > join ? ring : join;
+    return bwd_ctas(p.rows, groups);
 }
 
 } // namespace norm
@@ -473,11 +794,10 @@ MOE_API moe_status moe_layer_norm(const void *x, int dtype, int64_t rows, int64_
     if (clash(y, ld_y, x, ld_x, rows, (int)cols, es)) return MOE_ERR_UNSUPPORTED;
     Fwd p{x, weight, bias, y, mean, rstd, y_q, xhat_q, y_s, xhat_s, rows, ld_x, ld_y, (int)cols, 1, eps,
           center != 0, w_dtype == MOE_TYPE_F32};
-    // 8 values a thread where rows are few (a row's latency), 32 where there
-    // are enough to fill the GPU; 16 in between
-    const int ept = rows < sm_count() && cols <= 8192 ? 8 : cols > 8192 || rows >= 8 * sm_count() ? 32 : 16;
-    const int nvec = (int)((cols + (vec ? per : 1) - 1) / (vec ? per : 1)), vpt = ept / (vec ? per : 1);
-    p.warps = (nvec + 32 * vpt - 1) / (32 * vpt);
+    // 8 values a thread where rows are few (a row's latency), 16 where they
+    // fill the GPU, 32 where a CTA would not hold the row else
+    const int ept = cols > 8192 ? 32 : rows < sm_count() ? 8 : 16;
+    p.warps = (int)((cols + 32 * ept - 1) / (32 * ept));
     const int per_cta = p.warps == 1 ? 4 : 1;
     const unsigned grid = (unsigned)((rows + per_cta - 1) / per_cta);
     const int threads = p.warps * per_cta * 32;
@@ -535,19 +855,13 @@ MOE_API moe_status moe_layer_norm_backward(const void *dy, int dtype, int64_t ro
     if (sums && !aligned16(workspace)) return MOE_ERR_ALIGN;
     if (!sums && !dx) return MOE_OK;
     Bwd p{dy, x, dx_add, weight, dy_add, xhat_q, xhat_s, mean, rstd, dx, static_cast<float *>(workspace),
-          rows, ld_dy, ld_x, ld_add, ld_dx, (int)cols, 1, 1, center != 0, w_dtype == MOE_TYPE_F32, dweight != nullptr,
-          dbias != nullptr};
-    const int ept = cols > 8192 ? 32 : 16;
-    const int unit = vec ? per : 1, nvec = (int)((cols + unit - 1) / unit), vpt = ept / unit;
-    p.warps = (nvec + 32 * vpt - 1) / (32 * vpt);
-    p.groups = 16 / p.warps;
-    if (p.groups > 8) p.groups = 8;
-    if (p.groups > rows) p.groups = (int)rows;
-    const int grid = bwd_ctas(rows, p.groups);
-    const size_t smem = p.groups > 1 ? (size_t)2 * cols * sizeof(float) : 0;
-    if (ept == 16) bwd_launch<16>(p, f32, vec, grid, p.warps * p.groups * 32, smem, st);
-    else bwd_launch<32>(p, f32, vec, grid, p.warps * p.groups * 32, smem, st);
-    if (launch_status() != MOE_OK) return MOE_ERR_CUDA;
+          ld_dy, ld_x, ld_add, ld_dx, (int)rows, (int)cols, 1, 1, 0, 0, 0, 0, 0, center != 0, w_dtype == MOE_TYPE_F32,
+          dweight != nullptr, dbias != nullptr};
+    int ept, smem;
+    const int grid = bwd_plan(p, vec, es, ept, smem);
+    const cudaError_t e = f32 ? (vec ? bwd_launch_for<float, 4>(p, ept, grid, smem, st) : bwd_launch_for<float, 1>(p, ept, grid, smem, st))
+                              : (vec ? bwd_launch_for<uint16_t, 8>(p, ept, grid, smem, st) : bwd_launch_for<uint16_t, 1>(p, ept, grid, smem, st));
+    if (e != cudaSuccess) return MOE_ERR_CUDA;
     if (sums) {
         reduce_kernel<<<dim3((unsigned)((cols + 31) / 32), 2), 256, 0, st>>>(p.part, grid, (int)cols, dweight, dbias);
         return launch_status();

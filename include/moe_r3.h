@@ -713,10 +713,11 @@ moe_status moe_router_backward_dense(const uint16_t *x, const uint16_t *w_router
  *   xhat = (x[t] - mu) r,   y[t,c] = xhat[c] weight[c] + bias[c]
  *   (weight, bias nullable: 1 and 0), in fp32, y rounded once to x's type.
  *   mean[t] = mu, rstd[t] = r (nullable, fp32).
- *   y_q, y_s (nullable pair): y's 1 x 128 codes and scales by
- *   fp8_block_quant's rule, from y in fp32 before its rounding to x's type
- *   (the experts' operand); xhat_q, xhat_s (nullable pair): xhat's, the
- *   checkpoint that moe_layer_norm_backward reads in place of x.
+ *   y_q, y_s (nullable pair): y's 1 x 128 codes and scales (the experts'
+ *   operand), from y in fp32 before its rounding to x's type; xhat_q, xhat_s
+ *   (nullable pair): xhat's, the checkpoint that moe_layer_norm_backward reads
+ *   in place of x.  Scales s = amax / 448 (1 where that is 0), not below
+ *   2^-126, codes E4M3(v RN(1/s)).
  *   y may be x itself with ld_y = ld_x; else no output overlaps an input or
  *   another output.  Infinities and NaN act on their own row only, as the
  *   formulas have it in fp32; squares beyond fp32 give r = 0.
@@ -744,9 +745,8 @@ moe_status moe_router_backward_dense(const uint16_t *x, const uint16_t *w_router
  *
  * moe_grouped_ffn_fp8_ckpt  moe_grouped_ffn_fp8 that also writes GEMM1's
  *   pre-activations h (gate columns, then up) as 1 x 128 codes h_q
- *   [max_rows, 2F] and scales h_s [max_rows, 2F/128]: s = amax / 448 (1 where
- *   that is 0), not below 2^-126, codes E4M3(h RN(1/s)).  act is formed from h
- *   itself.
+ *   [max_rows, 2F] and scales h_s [max_rows, 2F/128], by the rule above.  act
+ *   is formed from h itself.
  * moe_swiglu_backward_ckpt  from d_act [rows, F] bf16 and that checkpoint,
  *   with g = code * scale of the gate columns, u of the up columns, a = d_act,
  *   s(g) = 1 / (1 + exp(-g)):
@@ -763,7 +763,7 @@ moe_status moe_router_backward_dense(const uint16_t *x, const uint16_t *w_router
  *       for src 2 and 1 with ld = max_pad and scales_kb_major).  They need
  *       expert_offsets and pad (moe_dispatch's and moe_wgrad_pad_offsets');
  *       all outputs then cover the rows those name.
- *   Scales and codes by the same rule as h_q's.  Columns at and behind pad[E] are not written.
+ *   Scales and codes by the same rule.  Columns at and behind pad[E] are not written.
  *   Rows that expert_offsets names outside [0, rows) are not read or written.
  *   No output overlaps an input or another output.  Any of rows, slots and
  *   max_pad may be 0.

@@ -100,24 +100,109 @@ __device__ __forceinline__ void load_weight(const void *w, bool f32, int c, floa
     }
 }
 
-// Sums of a and b over the warps of a row's group: shuffles, then the warps'
-// parts added in warp order by every thread (the same bits in each).  `red`
-// is this round's own buffer of the group; `bar` its named barrier (0: the
-// whole CTA), `warps` of one: no exchange.
-__device__ __forceinline__ void row_sums(float &a, float &b, float2 *red, int warps, int warp, int lane, int bar)
+// Sums of a (and with `two` of b) over the warps of a row's group, the same
+// bits in every thread: within the warp the lower half-warp ends up with a's
+// sum and the upper one with b's (one exchange more than for a alone), the
+// warps' parts meet in shared memory and are added the same way.  `red` is
+// this round's own buffer, [2][32] floats, and `first` where the group's parts
+// start in each; `bar` its named barrier (0: the whole CTA).  One warp: no
+// exchange.
+__device__ __forceinline__ void row_sums(float &a, float &b, bool two, float *red, int first, int warps, int warp,
+                                         int lane, int bar)
 {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-        a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
-        b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
+    float v;
+    if (two) {
+        const bool up = lane & 16;
+        v = (up ? b : a) + __shfl_xor_sync(0xFFFFFFFFu, up ? a : b, 16);
+    } else {
+        v = a + __shfl_xor_sync(0xFFFFFFFFu, a, 16);
     }
-    if (warps == 1) return;
-    if (lane == 0) red[warp] = make_float2(a, b);
-    asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(warps * 32) : "memory");
-    a = b = 0.0f;
-    for (int w = 0; w < warps; w++) {
-        a += red[w].x;
-        b += red[w].y;
+#pragma unroll
+    for (int o = 8; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    if (warps > 1) {
+        const int l = lane & 15, k = (lane >> 4) * 32 + first;
+        if (l == 0) red[k + warp] = v;                 // without `two` both halves hold the same sum
+        asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(warps * 32) : "memory");
+        v = l < warps ? red[k + l] : 0.0f;
+        if (l + 16 < warps) v += red[k + l + 16];
+#pragma unroll
+        for (int o = 8; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    }
+    a = __shfl_sync(0xFFFFFFFFu, v, 0);
+    if (two) b = __shfl_sync(0xFFFFFFFFu, v, 16);
+}
+
+// ---- rows on their way through shared memory ----
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void *src)
+{
+    if (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
+}
+
+// the oldest of `stages` pending groups
+__device__ __forceinline__ void wait_oldest(int stages)
+{
+    if (stages == 1) cp_async_wait<0>();
+    else if (stages == 2) cp_async_wait<1>();
+    else if (stages == 3) cp_async_wait<2>();
+    else cp_async_wait<3>();
+}
+
+__device__ __forceinline__ void group_sync(int warps, int bar)
+{
+    if (warps == 1) __syncwarp();
+    else asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(warps * 32) : "memory");
+}
+
+// A row without whole vectors, copied as the 16-byte pieces it lies in, by
+// all threads of its group (thread t of nth): column c lands at
+// dst + (start & 15) + c * sizeof(T).  Bytes behind the row are not read; the
+// piece it starts in may hold bytes of the row before, but where it would
+// reach back beyond the tensor's first row the values are copied one by one.
+template <typename T>
+__device__ __forceinline__ void copy_odd(uint32_t dst, const T *base, int64_t at, int cols, int t, int nth)
+{
+    const uintptr_t start = reinterpret_cast<uintptr_t>(base + at), end = start + (size_t)cols * sizeof(T);
+    const uintptr_t from = start & ~(uintptr_t)15;
+    const int pieces = (int)((end - from + 15) >> 4);
+    for (int k = t; k < pieces; k += nth) {
+        const uintptr_t src = from + 16 * (uintptr_t)k;
+        if (src >= reinterpret_cast<uintptr_t>(base)) {
+            const uintptr_t left = end - src;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + 16 * k), "l"(src),
+                         "r"(left < 16 ? (int)left : 16)
+                         : "memory");
+        } else {
+            for (uintptr_t a = start; a < src + 16 && a < end; a += sizeof(T)) {
+                if (sizeof(T) == 4)
+                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst + (uint32_t)(a - from)), "r"(*reinterpret_cast<const uint32_t *>(a)) : "memory");
+                else
+                    asm volatile("st.shared.b16 [%0], %1;" ::"r"(dst + (uint32_t)(a - from)), "h"(*reinterpret_cast<const uint16_t *>(a)) : "memory");
+            }
+        }
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ int odd_shift(const T *base, int64_t at) { return (int)(reinterpret_cast<uintptr_t>(base + at) & 15); }
+
+// VEC values to pairs; of single values two that lie 32 apart, the second one 0 where it is absent
+template <typename T, int VEC>
+__device__ __forceinline__ void pairs(const T *p, bool second, uint64_t (&v)[(VEC + 1) / 2])
+{
+    if constexpr (VEC == 1) {
+        float a[1], b[1] = {0.0f};
+        load<T, 1>(p, a);
+        if (second) load<T, 1>(p + 32, b);
+        v[0] = pack2(a[0], b[0]);
+    } else {
+        float f[VEC];
+        load<T, VEC>(p, f);
+#pragma unroll
+        for (int j = 0; j < VEC / 2; j++) v[j] = pack2(f[2 * j], f[2 * j + 1]);
     }
 }
 
@@ -130,7 +215,8 @@ struct Fwd {
     uint8_t *y_q, *h_q;         // codes of y and of xhat, [rows, cols]
     float *y_s, *h_s;           // their scales, [rows, cols / 128]
     int64_t rows, ld_x, ld_y;
-    int cols, warps;            // warps of a row (a divisor of the CTA's, or all of them)
+    int cols, warps, groups;    // warps of a row, rows that a CTA has at work
+    int stages, stage_bytes;    // of a group's ring
     float eps;
     bool center, w_f32;
 };
@@ -194,127 +280,161 @@ __device__ __forceinline__ void encode(const uint64_t (&v)[VPT][VEC / 2], int c,
     }
 }
 
-// One row per group of warps, the row held in registers (EPT values a
-// thread, two in each 64-bit pair) from its one load to the stores.  A warp's
-// vectors lie side by side, so a thread's addresses are one base and
-// constants.  The mean is taken twice: the sum of x - mu' with the first mean
-// mu' gives what rounding left out of it, at no further exchange (it rides
-// with the sum of squares).
-template <typename T, int VEC, int EPT>
+// A row per group of warps, held in registers (EPT values a thread, two in
+// each 64-bit pair) from its one reading to the stores.  A warp's vectors lie
+// side by side, so a thread's addresses are one base and constants.  With
+// RING the groups take rows in turn over the whole grid, and the next rows are
+// on their way through a ring in shared memory (one row a CTA at a time left
+// 28 KB in flight an SM, half of what HBM needs: 8192 x 7168 bf16 67 us);
+// without, each group has one row, read straight to registers.  The mean is
+// taken twice: the sum of x - mu' with the first mean mu' gives what rounding
+// left out of it, at no further exchange (it rides with the sum of squares).
+template <typename T, int VEC, int EPT, bool RING>
 __global__ void __launch_bounds__(EPT == 8 ? 1024 : 512, EPT == 16 ? 2 : 1) norm_kernel(Fwd p)
 {
     constexpr int N = VEC > 1 ? EPT / VEC : EPT / 2, H = VEC > 1 ? VEC / 2 : 1;      // vectors, or pairs of single values
     constexpr int STEP = VEC > 1 ? 32 * VEC : 64;              // columns from one to the next
-    __shared__ float2 red[2][32];
+    extern __shared__ __align__(16) uint8_t ring[];
+    __shared__ float red[2][64];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int group = warp / p.warps, gw = warp - group * p.warps;
-    const int64_t row = (int64_t)blockIdx.x * ((blockDim.x >> 5) / p.warps) + group;
-    if (row >= p.rows) return;                         // only where a row is one warp: no barrier below
     const int c = gw * 32 * EPT + lane * VEC;          // the thread's first column
-    const T *x = static_cast<const T *>(p.x) + row * p.ld_x + c;
     const float inv_n = 1.0f / (float)p.cols;
     const auto in = [&](int i) { return c + i * STEP < p.cols; };
     const auto in2 = [&](int i) { return c + i * STEP + 32 < p.cols; };              // a pair's second single value
-    uint64_t v[N][H];
+    const int64_t first = (int64_t)blockIdx.x * p.groups + group, step = (int64_t)gridDim.x * p.groups;
+    uint8_t *mine = ring + group * p.stages * p.stage_bytes;
+    const auto issue = [&](int64_t row, int stage) {
+        if (row < p.rows) {
+            const uint32_t dst = smem_u32(mine) + stage * p.stage_bytes;
+            if constexpr (VEC > 1) {
+                const T *src = static_cast<const T *>(p.x) + row * p.ld_x + c;
 #pragma unroll
-    for (int i = 0; i < N; i++) {
-        if constexpr (VEC > 1) {
-            float f[VEC] = {};
-            if (in(i)) load<T, VEC>(x + i * STEP, f);
-#pragma unroll
-            for (int j = 0; j < H; j++) v[i][j] = pack2(f[2 * j], f[2 * j + 1]);
-        } else {
-            float a[1] = {0.0f}, b[1] = {0.0f};
-            if (in(i)) load<T, 1>(x + i * STEP, a);
-            if (in2(i)) load<T, 1>(x + i * STEP + 32, b);
-            v[i][0] = pack2(a[0], b[0]);
+                for (int i = 0; i < N; i++)
+                    if (in(i)) copy_async<16>(dst + c * (int)sizeof(T) + i * 512, src + i * STEP);
+            } else {
+                copy_odd<T>(dst, static_cast<const T *>(p.x), row * p.ld_x, p.cols, gw * 32 + lane, p.warps * 32);
+            }
         }
-    }
-    float sum = 0.0f, sq = 0.0f;
-    if (p.center) {
-        uint64_t s2 = 0;
+        cp_async_commit();
+    };
+    int stage = 0, par = 0;
+    if constexpr (RING)
+        for (int s = 0; s < p.stages; s++) issue(first + s * step, s);
+    for (int64_t row = first; row < p.rows; row += step, par ^= 1) {
+        uint64_t v[N][H];
+        {
+            const T *x = static_cast<const T *>(p.x) + row * p.ld_x + c;
+            if constexpr (RING) {
+                wait_oldest(p.stages);
+                const uint8_t *st = mine + stage * p.stage_bytes;
+                if (VEC == 1) {
+                    group_sync(p.warps, group + 1);        // the row's pieces were copied by others
+                    st += odd_shift(static_cast<const T *>(p.x), row * p.ld_x);
+                }
+                x = reinterpret_cast<const T *>(st) + c;
+            }
 #pragma unroll
-        for (int i = 0; i < N; i++) {
+            for (int i = 0; i < N; i++) {
 #pragma unroll
-            for (int j = 0; j < H; j++) s2 = add2(s2, v[i][j]);
+                for (int j = 0; j < H; j++) v[i][j] = 0;
+                if (in(i)) pairs<T, VEC>(x + i * STEP, in2(i), v[i]);
+            }
         }
-        unpack2(s2, sum, sq);
-        sum += sq;
-        sq = 0.0f;
-        row_sums(sum, sq, red[0], p.warps, gw, lane, 0);
-    }
-    const float mu = sum * inv_n;
-    uint64_t s2 = 0, q2 = 0;
-#pragma unroll
-    for (int i = 0; i < N; i++) {
+        float sum = 0.0f, sq = 0.0f;
         if (p.center) {
-            // absent columns stay 0
-            const float m0 = in(i) ? -mu : 0.0f, m1 = VEC > 1 ? m0 : in2(i) ? -mu : 0.0f;
-            const uint64_t m = pack2(m0, m1);
+            uint64_t s2 = 0;
 #pragma unroll
-            for (int j = 0; j < H; j++) {
-                v[i][j] = add2(v[i][j], m);
-                s2 = add2(s2, v[i][j]);
+            for (int i = 0; i < N; i++) {
+#pragma unroll
+                for (int j = 0; j < H; j++) s2 = add2(s2, v[i][j]);
             }
+            unpack2(s2, sum, sq);
+            sum += sq;
+            sq = 0.0f;
+            row_sums(sum, sq, false, red[0], group * p.warps, p.warps, gw, lane, group + 1);
         }
-#pragma unroll
-        for (int j = 0; j < H; j++) q2 = fma2(v[i][j], v[i][j], q2);
-    }
-    float a, b;
-    unpack2(s2, a, b);
-    sum = a + b;
-    unpack2(q2, a, b);
-    sq = a + b;
-    row_sums(sum, sq, red[1], p.warps, gw, lane, 0);
-    const float rest = sum * inv_n;                    // 0 without center
-    float var = fmaf(sq, inv_n, -rest * rest);
-    if (var < 0.0f) var = 0.0f;                        // a NaN stays
-    const float rstd = rsqrtf(var + p.eps);
-    if (gw == 0 && lane == 0) {
-        if (p.mean) p.mean[row] = mu + rest;
-        if (p.rstd) p.rstd[row] = rstd;
-    }
-    const uint64_t r2 = pack2(rstd, rstd), c2 = pack2(-rest * rstd, -rest * rstd);
-#pragma unroll
-    for (int i = 0; i < N; i++) {
-#pragma unroll
-        for (int j = 0; j < H; j++) v[i][j] = p.center ? fma2(v[i][j], r2, c2) : mul2(v[i][j], r2);
-    }
-    T *y = static_cast<T *>(p.y) + row * p.ld_y + c;
-    if constexpr (VEC > 1) {
-        const int64_t at = row * p.cols, at_s = row * (p.cols >> 7);
-        if (p.h_q) encode<VEC, N>(v, c, p.cols, lane, p.h_q + at, p.h_s + at_s);
+        const float mu = sum * inv_n;
+        uint64_t s2 = 0, q2 = 0;
 #pragma unroll
         for (int i = 0; i < N; i++) {
-            float w[VEC] = {}, f[VEC] = {};
-            if (in(i)) {
-                load_weight<VEC>(p.w, p.w_f32, c + i * STEP, 1.0f, w);
-                if (p.b) load_weight<VEC>(p.b, p.w_f32, c + i * STEP, 0.0f, f);
+            if (p.center) {
+                // absent columns stay 0
+                const float m0 = in(i) ? -mu : 0.0f, m1 = VEC > 1 ? m0 : in2(i) ? -mu : 0.0f;
+                const uint64_t m = pack2(m0, m1);
+#pragma unroll
+                for (int j = 0; j < H; j++) {
+                    v[i][j] = add2(v[i][j], m);
+                    s2 = add2(s2, v[i][j]);
+                }
             }
 #pragma unroll
-            for (int j = 0; j < H; j++) {
-                v[i][j] = fma2(v[i][j], pack2(w[2 * j], w[2 * j + 1]), pack2(f[2 * j], f[2 * j + 1]));
-                unpack2(v[i][j], f[2 * j], f[2 * j + 1]);
-            }
-            if (in(i)) store<T, VEC>(y + i * STEP, f);
+            for (int j = 0; j < H; j++) q2 = fma2(v[i][j], v[i][j], q2);
         }
-        if (p.y_q) encode<VEC, N>(v, c, p.cols, lane, p.y_q + at, p.y_s + at_s);
-    } else {
+        float a, b;
+        unpack2(s2, a, b);
+        sum = a + b;
+        unpack2(q2, a, b);
+        sq = a + b;
+        // with one round a row the buffers alternate: a warp a row ahead writes the other one
+        row_sums(sq, sum, p.center, red[p.center ? 1 : par], group * p.warps, p.warps, gw, lane, group + 1);
+        if constexpr (RING) {
+            if (VEC == 1 && p.warps == 1) __syncwarp();
+            issue(row + p.stages * step, stage);           // the row is in registers (of others too: past their barrier)
+        }
+        if (RING && ++stage == p.stages) stage = 0;
+        const float rest = p.center ? sum * inv_n : 0.0f;
+        float var = fmaf(sq, inv_n, -rest * rest);
+        if (var < 0.0f) var = 0.0f;                        // a NaN stays
+        const float rstd = rsqrtf(var + p.eps);
+        if (gw == 0 && lane == 0) {
+            if (p.mean) p.mean[row] = mu + rest;
+            if (p.rstd) p.rstd[row] = rstd;
+        }
+        const uint64_t r2 = pack2(rstd, rstd), c2 = pack2(-rest * rstd, -rest * rstd);
 #pragma unroll
         for (int i = 0; i < N; i++) {
-            float h[2];
-            unpack2(v[i][0], h[0], h[1]);
 #pragma unroll
-            for (int j = 0; j < 2; j++) {
-                if (!(j ? in2(i) : in(i))) continue;
-                float w[1], f[1];
-                load_weight<1>(p.w, p.w_f32, c + i * STEP + 32 * j, 1.0f, w);
-                load_weight<1>(p.b, p.w_f32, c + i * STEP + 32 * j, 0.0f, f);
-                f[0] = fmaf(h[j], w[0], f[0]);
-                store<T, 1>(y + i * STEP + 32 * j, f);
+            for (int j = 0; j < H; j++) v[i][j] = p.center ? fma2(v[i][j], r2, c2) : mul2(v[i][j], r2);
+        }
+        T *y = static_cast<T *>(p.y) + row * p.ld_y + c;
+        if constexpr (VEC > 1) {
+            const int64_t at = row * p.cols, at_s = row * (p.cols >> 7);
+            if (p.h_q) encode<VEC, N>(v, c, p.cols, lane, p.h_q + at, p.h_s + at_s);
+#pragma unroll
+            for (int i = 0; i < N; i++) {
+                float w[VEC] = {}, f[VEC] = {};
+                if (in(i)) {
+                    load_weight<VEC>(p.w, p.w_f32, c + i * STEP, 1.0f, w);
+                    if (p.b) load_weight<VEC>(p.b, p.w_f32, c + i * STEP, 0.0f, f);
+                }
+#pragma unroll
+                for (int j = 0; j < H; j++) {
+                    v[i][j] = fma2(v[i][j], pack2(w[2 * j], w[2 * j + 1]), pack2(f[2 * j], f[2 * j + 1]));
+                    unpack2(v[i][j], f[2 * j], f[2 * j + 1]);
+                }
+                if (in(i)) store<T, VEC>(y + i * STEP, f);
+            }
+            if (p.y_q) encode<VEC, N>(v, c, p.cols, lane, p.y_q + at, p.y_s + at_s);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; i++) {
+                float h[2];
+                unpack2(v[i][0], h[0], h[1]);
+#pragma unroll
+                for (int j = 0; j < 2; j++) {
+                    if (!(j ? in2(i) : in(i))) continue;
+                    float w[1], f[1];
+                    load_weight<1>(p.w, p.w_f32, c + i * STEP + 32 * j, 1.0f, w);
+                    load_weight<1>(p.b, p.w_f32, c + i * STEP + 32 * j, 0.0f, f);
+                    f[0] = fmaf(h[j], w[0], f[0]);
+                    store<T, 1>(y + i * STEP + 32 * j, f);
+                }
             }
         }
+        if constexpr (!RING) break;
     }
+    cp_async_wait<0>();
 }
 
 // ----------------------------------------------------------------- backward
@@ -333,41 +453,6 @@ struct Bwd {
     int stage_bytes, at_x, at_s, at_dya;
     bool center, w_f32, want_w, want_b;
 };
-
-template <int BYTES>
-__device__ __forceinline__ void copy_async(uint32_t dst, const void *src)
-{
-    if (BYTES == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
-}
-
-// the oldest of `stages` pending groups
-__device__ __forceinline__ void wait_oldest(int stages)
-{
-    if (stages == 1) cp_async_wait<0>();
-    else if (stages == 2) cp_async_wait<1>();
-    else if (stages == 3) cp_async_wait<2>();
-    else cp_async_wait<3>();
-}
-
-// VEC values to pairs; of single values two that lie 32 apart, the second one 0 where it is absent
-template <typename T, int VEC>
-__device__ __forceinline__ void pairs(const T *p, bool second, uint64_t (&v)[(VEC + 1) / 2])
-{
-    if constexpr (VEC == 1) {
-        float a[1], b[1] = {0.0f};
-        load<T, 1>(p, a);
-        if (second) load<T, 1>(p + 32, b);
-        v[0] = pack2(a[0], b[0]);
-    } else {
-        float f[VEC];
-        load<T, VEC>(p, f);
-#pragma unroll
-        for (int j = 0; j < VEC / 2; j++) v[j] = pack2(f[2 * j], f[2 * j + 1]);
-    }
-}
 
 // VEC codes of one block to fp32, times its scale
 template <int VEC>
@@ -391,9 +476,9 @@ __device__ __forceinline__ void decode(const uint8_t *q, float s, uint64_t (&v)[
 
 // Rows over groups of warps, grid-wide in turn; a thread owns the same EPT
 // columns of every row of its group, so the sums over rows stay in registers
-// until the CTA's last row.  Whole vectors come through a ring of rows in
-// shared memory, copied asynchronously by the thread that reads them; single
-// values are read where they are used.  With KEEP a thread holds g and xhat of
+// until the CTA's last row.  Rows come through a ring in shared memory, whole
+// vectors copied asynchronously by the thread that reads them, rows without
+// as the pieces they lie in (and a barrier).  With KEEP a thread holds g and xhat of
 // its columns from the row's means to dx; without (rows too long for that
 // beside the sums) it reads them again.  At the end the groups' sums are
 // joined in group order through shared memory and leave as this CTA's part;
@@ -406,9 +491,9 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) dnorm_kernel(Bwd p)
 {
     // vectors, or pairs of single values 32 columns apart
     constexpr int N = VEC > 1 ? EPT / VEC : EPT / 2, H = (VEC + 1) / 2, STEP = VEC > 1 ? 32 * VEC : 64;
-    constexpr bool RING = VEC > 1, KEEP = EPT == 16;
+    constexpr bool KEEP = EPT == 16;
     extern __shared__ __align__(16) uint8_t ring[];
-    __shared__ float2 red[2][32];
+    __shared__ float red[2][64];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int group = warp / p.warps, gw = warp - group * p.warps;
     const int c = gw * 32 * EPT + lane * VEC, left = p.cols - c;       // the thread's first column, and those from there on
@@ -421,7 +506,13 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) dnorm_kernel(Bwd p)
     const auto in2 = [&](int i) { return i * STEP + 32 < left; };      // a pair's second single value
 
     const auto issue = [&](int64_t row, int stage) {
-        if constexpr (RING) {
+        if constexpr (VEC == 1) {
+            if (row < p.rows) {
+                const uint32_t dst = mine_u + stage * p.stage_bytes;
+                copy_odd<T>(dst, static_cast<const T *>(p.dy), row * p.ld_dy, p.cols, gw * 32 + lane, p.warps * 32);
+                copy_odd<T>(dst + p.at_x, static_cast<const T *>(p.x), row * p.ld_x, p.cols, gw * 32 + lane, p.warps * 32);
+            }
+        } else {
             if (row < p.rows) {
                 const uint32_t dst = mine_u + stage * p.stage_bytes;
                 const T *dy = static_cast<const T *>(p.dy) + row * p.ld_dy + c;
@@ -455,20 +546,22 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) dnorm_kernel(Bwd p)
                     }
                 }
             }
-            cp_async_commit();
         }
+        cp_async_commit();
     };
     // vector i of the row: a = dy + dy_add and xhat = (x - mu) r, or from its codes
     const auto get = [&](int64_t row, const uint8_t *st, int i, uint64_t rs2, uint64_t nmu2, uint64_t (&a)[H], uint64_t (&h)[H]) {
-        if constexpr (RING) {
+        if constexpr (VEC > 1) {
             pairs<T, VEC>(reinterpret_cast<const T *>(st) + c + i * STEP, false, a);
             if constexpr (CKPT)
                 decode<VEC>(st + p.at_x + c + i * STEP,
                             *reinterpret_cast<const float *>(st + p.at_s + (c >> 7) * 4 + i * STEP / 32), h);
             else pairs<T, VEC>(reinterpret_cast<const T *>(st + p.at_x) + c + i * STEP, false, h);
         } else {
-            pairs<T, VEC>(static_cast<const T *>(p.dy) + row * p.ld_dy + c + i * STEP, in2(i), a);
-            pairs<T, VEC>(static_cast<const T *>(p.x) + row * p.ld_x + c + i * STEP, in2(i), h);
+            const T *dy = reinterpret_cast<const T *>(st + odd_shift(static_cast<const T *>(p.dy), row * p.ld_dy));
+            const T *x = reinterpret_cast<const T *>(st + p.at_x + odd_shift(static_cast<const T *>(p.x), row * p.ld_x));
+            pairs<T, VEC>(dy + c + i * STEP, in2(i), a);
+            pairs<T, VEC>(x + c + i * STEP, in2(i), h);
         }
         if (!CKPT) {
 #pragma unroll
@@ -505,8 +598,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) dnorm_kernel(Bwd p)
     };
 
     uint64_t dw[N][H] = {}, db[BIAS ? N : 1][H] = {};
-    if constexpr (RING)
-        for (int s = 0; s < p.stages; s++) issue((int64_t)first + (int64_t)s * step, s);
+    for (int s = 0; s < p.stages; s++) issue((int64_t)first + (int64_t)s * step, s);
     float rs_next = 0.0f, mu_next = 0.0f;              // the next row's, loaded a row ahead
     const bool mean = p.center && !CKPT;
     if (first < p.rows) {
@@ -531,10 +623,9 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) dnorm_kernel(Bwd p)
             }
         }
         const uint8_t *st = mine + stage * p.stage_bytes;
-        if constexpr (RING) {
-            wait_oldest(p.stages);
-            if (CKPT) __syncwarp();                    // a block's scale was copied by one of its lanes
-        }
+        wait_oldest(p.stages);
+        if (CKPT) __syncwarp();                        // a block's scale was copied by one of its lanes
+        if (VEC == 1) group_sync(p.warps, group + 1);  // the row's pieces were copied by others
         uint64_t g[KEEP ? N : 1][H], h[KEEP ? N : 1][H];
         uint64_t s1 = 0, s2 = 0;
 #pragma unroll
@@ -554,7 +645,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) dnorm_kernel(Bwd p)
                 }
             }
         }
-        if (RING && KEEP) {
+        if (KEEP && VEC > 1) {
             if (CKPT) __syncwarp();
             issue(row + (int64_t)p.stages * step, stage);
         }
@@ -565,7 +656,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) dnorm_kernel(Bwd p)
             unpack2(s2, x, y);
             m2 = x + y;
             // the buffer alternates by row: a warp a row ahead writes the other one
-            row_sums(m1, m2, red[par] + group * p.warps, p.warps, gw, lane, group + 1);
+            row_sums(m2, m1, p.center, red[par], group * p.warps, p.warps, gw, lane, group + 1);
             m1 = p.center ? m1 * inv_n : 0.0f, m2 *= inv_n;
             const uint64_t nm1 = pack2(-m1, -m1), nm2 = pack2(-m2, -m2);
             T *dx = static_cast<T *>(p.dx) + row * p.ld_dx + c;
@@ -604,13 +695,12 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) dnorm_kernel(Bwd p)
                 }
             }
         }
-        if constexpr (RING) {
-            if (!KEEP) {
-                if (CKPT) __syncwarp();
-                issue(row + (int64_t)p.stages * step, stage);
-            }
-            if (++stage == p.stages) stage = 0;
+        if (!KEEP || VEC == 1) {
+            if (CKPT) __syncwarp();
+            if (VEC == 1) group_sync(p.warps, group + 1);       // everyone has read the row
+            issue(row + (int64_t)p.stages * step, stage);
         }
+        if (++stage == p.stages) stage = 0;
     }
     if (!p.want_w && !p.want_b) return;
     cp_async_wait<0>();
@@ -693,13 +783,45 @@ static int bwd_ctas(int64_t rows, int groups)
     return (int)(n < sm_count() ? n : sm_count());
 }
 
-template <int EPT>
-static void fwd_launch(const Fwd &p, bool f32, bool vec, unsigned grid, int threads, cudaStream_t st)
+template <typename T, int VEC, int EPT, bool RING>
+static cudaError_t fwd_launch(const Fwd &p, unsigned grid, int smem, cudaStream_t st)
 {
-    if (f32)
-        vec ? norm_kernel<float, 4, EPT><<<grid, threads, 0, st>>>(p) : norm_kernel<float, 1, EPT><<<grid, threads, 0, st>>>(p);
-    else
-        vec ? norm_kernel<uint16_t, 8, EPT><<<grid, threads, 0, st>>>(p) : norm_kernel<uint16_t, 1, EPT><<<grid, threads, 0, st>>>(p);
+    if (RING) {
+        static std::atomic<uint64_t> done{0};
+        const cudaError_t e = allow_smem(reinterpret_cast<const void *>(norm_kernel<T, VEC, EPT, RING>), EPT == 16 ? SMEM_MAX / 2 : SMEM_MAX, done);
+        if (e != cudaSuccess) return e;
+    }
+    norm_kernel<T, VEC, EPT, RING><<<grid, p.warps * p.groups * 32, smem, st>>>(p);
+    return cudaGetLastError();
+}
+
+// The forward's plan.  Few rows (one a CTA and SM at most): 8 values a thread,
+// read straight to registers, for a row's latency.  Else a ring: 16 values a
+// thread, two CTAs an SM; 32 where a CTA would not hold the row else, and one
+// CTA.  Groups as many as 512 threads hold, up to four stages each.
+template <typename T, int VEC>
+static cudaError_t fwd_plan(Fwd &p, cudaStream_t st)
+{
+    const int sms = sm_count(), es = sizeof(T);
+    const int ept = p.cols > 8192 ? 32 : p.rows <= sms ? 8 : 16;
+    p.warps = (p.cols + 32 * ept - 1) / (32 * ept);
+    p.groups = 1;
+    p.stages = p.stage_bytes = 0;
+    if (ept == 8) return fwd_launch<T, VEC, 8, false>(p, (unsigned)p.rows, 0, st);
+    const int per_sm = ept == 16 ? 2 : 1, room = SMEM_MAX / per_sm;
+    const int64_t each = (p.rows + sms * per_sm - 1) / (sms * per_sm);
+    int groups = 16 / p.warps;
+    if (groups > 8 && p.warps > 1) groups = 8;         // named barriers
+    if (groups > each) groups = (int)each;
+    p.stage_bytes = (p.cols * es + (VEC == 1 ? 16 : 0) + 15) & ~15;
+    while (groups > 1 && 2 * groups * p.stage_bytes > room) groups--;
+    p.groups = groups;
+    p.stages = room / (groups * p.stage_bytes);
+    if (p.stages > 4) p.stages = 4;
+    const int64_t want = (p.rows + groups - 1) / groups;
+    const unsigned grid = (unsigned)(want < (int64_t)sms * per_sm ? want : (int64_t)sms * per_sm);
+    const int smem = groups * p.stages * p.stage_bytes;
+    return ept == 16 ? fwd_launch<T, VEC, 16, true>(p, grid, smem, st) : fwd_launch<T, VEC, 32, true>(p, grid, smem, st);
 }
 
 template <typename T, int VEC, int EPT, bool CKPT, bool BIAS>
@@ -741,25 +863,22 @@ static int bwd_plan(Bwd &p, bool vec, int es, int &ept, int &smem)
     const int per_sm = (p.rows + sm_count() - 1) / sm_count();
     if (groups > 8) groups = 8;                        // named barriers, and the parts joined one after another
     if (groups > per_sm) groups = per_sm;
-    p.stages = p.stage_bytes = 0;
-    p.at_x = p.at_s = p.at_dya = -1;
-    if (vec) {
-        const auto lay = [&](bool dya) {
-            int n = p.cols * es;
-            p.at_x = n;
-            n += p.h_q ? p.cols : p.cols * es;
-            p.at_s = n;
-            if (p.h_q) n = (n + p.cols / 128 * 4 + 15) & ~15;
-            p.at_dya = dya ? n : -1;
-            if (dya) n += p.cols * 4;
-            p.stage_bytes = n;
-        };
-        lay(p.dy_add != nullptr);
-        if (p.stage_bytes > SMEM_MAX) lay(false);
-        while (groups > 1 && 2 * groups * p.stage_bytes > SMEM_MAX) groups--;
-        p.stages = SMEM_MAX / (groups * p.stage_bytes);
-        if (p.stages > 4) p.stages = 4;
-    }
+    const auto lay = [&](bool dya) {
+        const int row = (p.cols * es + (vec ? 0 : 16) + 15) & ~15;
+        int n = row;
+        p.at_x = n;
+        n += p.h_q ? p.cols : row;
+        p.at_s = n;
+        if (p.h_q) n = (n + p.cols / 128 * 4 + 15) & ~15;
+        p.at_dya = dya ? n : -1;
+        if (dya) n += p.cols * 4;
+        p.stage_bytes = n;
+    };
+    lay(vec && p.dy_add);
+    if (p.stage_bytes > SMEM_MAX) lay(false);
+    while (groups > 1 && 2 * groups * p.stage_bytes > SMEM_MAX) groups--;
+    p.stages = SMEM_MAX / (groups * p.stage_bytes);
+    if (p.stages > 4) p.stages = 4;
     p.groups = groups;
     const int ring = groups * p.stages * p.stage_bytes, join = groups > 1 ? 2 * p.cols * (int)sizeof(float) : 0;
     smem = ring > join ? ring : join;
@@ -792,20 +911,12 @@ MOE_API moe_status moe_layer_norm(const void *x, int dtype, int64_t rows, int64_
                      aligned16(weight) && aligned16(bias);
     if ((y_q || xhat_q) && (!vec || !aligned16(y_q) || !aligned16(xhat_q))) return MOE_ERR_ALIGN;
     if (clash(y, ld_y, x, ld_x, rows, (int)cols, es)) return MOE_ERR_UNSUPPORTED;
-    Fwd p{x, weight, bias, y, mean, rstd, y_q, xhat_q, y_s, xhat_s, rows, ld_x, ld_y, (int)cols, 1, eps,
+    Fwd p{x, weight, bias, y, mean, rstd, y_q, xhat_q, y_s, xhat_s, rows, ld_x, ld_y, (int)cols, 1, 1, 0, 0, eps,
           center != 0, w_dtype == MOE_TYPE_F32};
-    // 8 values a thread where rows are few (a row's latency), 16 where they
-    // fill the GPU, 32 where a CTA would not hold the row else
-    const int ept = cols > 8192 ? 32 : rows < sm_count() ? 8 : 16;
-    p.warps = (int)((cols + 32 * ept - 1) / (32 * ept));
-    const int per_cta = p.warps == 1 ? 4 : 1;
-    const unsigned grid = (unsigned)((rows + per_cta - 1) / per_cta);
-    const int threads = p.warps * per_cta * 32;
     cudaStream_t st = as_stream(stream);
-    if (ept == 8) fwd_launch<8>(p, f32, vec, grid, threads, st);
-    else if (ept == 16) fwd_launch<16>(p, f32, vec, grid, threads, st);
-    else fwd_launch<32>(p, f32, vec, grid, threads, st);
-    return launch_status();
+    const cudaError_t e = f32 ? (vec ? fwd_plan<float, 4>(p, st) : fwd_plan<float, 1>(p, st))
+                              : (vec ? fwd_plan<uint16_t, 8>(p, st) : fwd_plan<uint16_t, 1>(p, st));
+    return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 MOE_API size_t moe_layer_norm_backward_workspace_size(int64_t rows, int64_t cols)

@@ -149,6 +149,32 @@ def test_backward(L, rows, cols, dt, mode):
     assert bool(((db.double() - rdb).abs() <= n * sb + 1e-30).all())
 
 
+@pytest.mark.parametrize("rows,cols,dt,ld", [(6000, 5000, torch.bfloat16, 5000), (5000, 4097, torch.float32, 4097),
+                                             (5000, 4097, torch.bfloat16, 4099), (30000, 130, torch.bfloat16, 130),
+                                             (3000, 16000, torch.float32, 16000), (30000, 128, torch.float32, 128)])
+def test_many_rows(L, rows, cols, dt, ld):
+    """Rows enough that every group goes through its stages many times, forward and backward."""
+    g = torch.Generator(device=DEV).manual_seed(cols)
+    x, dy = rows_of(rows, cols, dt, g, ld), rows_of(rows, cols, dt, g, ld)
+    w, b = torch.randn(cols, device=DEV, generator=g), torch.randn(cols, device=DEV, generator=g)
+    for center in (True, False):
+        y, mean, rstd, _, _ = L.moe_layer_norm(x, w, b, center=center, mean=True, rstd=True)
+        dx, dw, db = L.moe_layer_norm_backward(dy, rstd, x=x, mean=mean, weight=w, center=center, dbias=center)
+        tw = tb = sw = sb = 0
+        for r in range(0, rows, 1000):
+            s = slice(r, min(rows, r + 1000))
+            ry, _, rr, h = R.norm(x[s], w, b, 1e-5, center)
+            check(y[s], ry, (h.abs() + 1) * w.double().abs() + b.double().abs(), dt, "y")
+            h = (x[s].double() - (mean[s].double()[:, None] if center else 0)) * rstd[s].double()[:, None]
+            rdx, rdw, rdb, size, aw, ab = R.norm_backward(dy[s], h, rstd[s], w, center)
+            check(dx[s], rdx, size, dt, "dx")
+            tw, tb, sw, sb = tw + rdw, tb + rdb, sw + aw, sb + ab
+        n = (rows // 100 + 64) * R.U
+        assert bool(((dw.double() - tw).abs() <= n * sw).all())
+        if center:
+            assert bool(((db.double() - tb).abs() <= n * sb).all())
+
+
 def test_backward_place_strides_and_parts(L):
     """dx over dy and over dx_add; strided rows; each output alone gives the same bits."""
     g = torch.Generator(device=DEV).manual_seed(3)

@@ -206,6 +206,60 @@ __device__ __forceinline__ void pairs(const T *p, bool second, uint64_t (&v)[(VE
     }
 }
 
+// A weight in fp32 in shared memory (`none` where there is none), for a CTA
+// that meets many rows: no conversion and no question of its type a row.
+// Vectors of eight lie as two halves, so that a warp reads whole banks.
+template <int VEC, bool F32>
+__device__ __forceinline__ void stage_weight_of(float *dst, const void *w, int cols)
+{
+    if constexpr (VEC == 1) {
+#pragma unroll 8
+        for (int c = threadIdx.x; c < cols; c += blockDim.x)
+            dst[c] = F32 ? __ldg(static_cast<const float *>(w) + c) : bf16_bits_to_f32(__ldg(static_cast<const uint16_t *>(w) + c));
+    } else {
+#pragma unroll 4
+        for (int q = threadIdx.x; q < cols >> 2; q += blockDim.x) {
+            float4 f;
+            if constexpr (F32) {
+                f = __ldg(static_cast<const float4 *>(w) + q);
+            } else {
+                const uint2 v = __ldg(static_cast<const uint2 *>(w) + q);
+                f = make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u), __uint_as_float(v.y << 16),
+                                __uint_as_float(v.y & 0xFFFF0000u));
+            }
+            *reinterpret_cast<float4 *>(dst + (VEC == 8 ? (q >> 1) * 4 + (q & 1 ? cols >> 1 : 0) : 4 * q)) = f;
+        }
+    }
+}
+template <int VEC>
+__device__ __forceinline__ void stage_weight(float *dst, const void *w, bool f32, int cols, float none)
+{
+    if (!w) {
+        for (int c = threadIdx.x; c < cols; c += blockDim.x) dst[c] = none;
+    } else if (f32) {
+        stage_weight_of<VEC, true>(dst, w, cols);
+    } else {
+        stage_weight_of<VEC, false>(dst, w, cols);
+    }
+}
+// the pairs of a vector from column c on (of single values c and, if present, c + 32)
+template <int VEC>
+__device__ __forceinline__ void staged_weight(const float *s, int c, int cols, bool second, uint64_t (&w)[(VEC + 1) / 2])
+{
+    if constexpr (VEC == 1) {
+        w[0] = pack2(s[c], second ? s[c + 32] : 0.0f);
+    } else {
+        const float4 a = *reinterpret_cast<const float4 *>(s + (VEC == 8 ? c >> 1 : c));
+        w[0] = pack2(a.x, a.y);
+        w[1] = pack2(a.z, a.w);
+        if constexpr (VEC == 8) {
+            const float4 b = *reinterpret_cast<const float4 *>(s + (cols >> 1) + (c >> 1));
+            w[2] = pack2(b.x, b.y);
+            w[3] = pack2(b.z, b.w);
+        }
+    }
+}
+
 // ------------------------------------------------------------------ forward
 
 struct Fwd {
@@ -217,6 +271,7 @@ struct Fwd {
     int64_t rows, ld_x, ld_y;
     int cols, warps, groups;    // warps of a row, rows that a CTA has at work
     int stages, stage_bytes;    // of a group's ring
+    int weight_floats, weight_bytes;    // of one weight, and of both, in shared memory
     float eps;
     bool center, w_f32;
 };
@@ -303,7 +358,9 @@ __global__ void __launch_bounds__(EPT == 8 ? 1024 : 512, EPT == 16 ? 2 : 1) norm
     const auto in = [&](int i) { return c + i * STEP < p.cols; };
     const auto in2 = [&](int i) { return c + i * STEP + 32 < p.cols; };              // a pair's second single value
     const int64_t first = (int64_t)blockIdx.x * p.groups + group, step = (int64_t)gridDim.x * p.groups;
-    uint8_t *mine = ring + group * p.stages * p.stage_bytes;
+    // RING: the weights, then the groups' rings
+    float *sw = reinterpret_cast<float *>(ring), *sb = sw + p.weight_floats;
+    uint8_t *mine = ring + p.weight_bytes + group * p.stages * p.stage_bytes;
     const auto issue = [&](int64_t row, int stage) {
         if (row < p.rows) {
             const uint32_t dst = smem_u32(mine) + stage * p.stage_bytes;
@@ -319,8 +376,12 @@ __global__ void __launch_bounds__(EPT == 8 ? 1024 : 512, EPT == 16 ? 2 : 1) norm
         cp_async_commit();
     };
     int stage = 0, par = 0;
-    if constexpr (RING)
+    if constexpr (RING) {
         for (int s = 0; s < p.stages; s++) issue(first + s * step, s);
+        stage_weight<VEC>(sw, p.w, p.w_f32, p.cols, 1.0f);
+        if (p.b) stage_weight<VEC>(sb, p.b, p.w_f32, p.cols, 0.0f);
+        __syncthreads();
+    }
     for (int64_t row = first; row < p.rows; row += step, par ^= 1) {
         uint64_t v[N][H];
         {
@@ -403,14 +464,26 @@ __global__ void __launch_bounds__(EPT == 8 ? 1024 : 512, EPT == 16 ? 2 : 1) norm
             if (p.h_q) encode<VEC, N>(v, c, p.cols, lane, p.h_q + at, p.h_s + at_s);
 #pragma unroll
             for (int i = 0; i < N; i++) {
-                float w[VEC] = {}, f[VEC] = {};
+                uint64_t w[H], f2[H];
+                float f[VEC] = {};
+#pragma unroll
+                for (int j = 0; j < H; j++) w[j] = f2[j] = 0;
                 if (in(i)) {
-                    load_weight<VEC>(p.w, p.w_f32, c + i * STEP, 1.0f, w);
-                    if (p.b) load_weight<VEC>(p.b, p.w_f32, c + i * STEP, 0.0f, f);
+                    if constexpr (RING) {
+                        staged_weight<VEC>(sw, c + i * STEP, p.cols, false, w);
+                        if (p.b) staged_weight<VEC>(sb, c + i * STEP, p.cols, false, f2);
+                    } else {
+                        load_weight<VEC>(p.w, p.w_f32, c + i * STEP, 1.0f, f);
+#pragma unroll
+                        for (int j = 0; j < H; j++) w[j] = pack2(f[2 * j], f[2 * j + 1]);
+                        load_weight<VEC>(p.b, p.w_f32, c + i * STEP, 0.0f, f);
+#pragma unroll
+                        for (int j = 0; j < H; j++) f2[j] = pack2(f[2 * j], f[2 * j + 1]);
+                    }
                 }
 #pragma unroll
                 for (int j = 0; j < H; j++) {
-                    v[i][j] = fma2(v[i][j], pack2(w[2 * j], w[2 * j + 1]), pack2(f[2 * j], f[2 * j + 1]));
+                    v[i][j] = fma2(v[i][j], w[j], f2[j]);
                     unpack2(v[i][j], f[2 * j], f[2 * j + 1]);
                 }
                 if (in(i)) store<T, VEC>(y + i * STEP, f);
@@ -419,17 +492,24 @@ __global__ void __launch_bounds__(EPT == 8 ? 1024 : 512, EPT == 16 ? 2 : 1) norm
         } else {
 #pragma unroll
             for (int i = 0; i < N; i++) {
-                float h[2];
-                unpack2(v[i][0], h[0], h[1]);
-#pragma unroll
-                for (int j = 0; j < 2; j++) {
-                    if (!(j ? in2(i) : in(i))) continue;
-                    float w[1], f[1];
-                    load_weight<1>(p.w, p.w_f32, c + i * STEP + 32 * j, 1.0f, w);
-                    load_weight<1>(p.b, p.w_f32, c + i * STEP + 32 * j, 0.0f, f);
-                    f[0] = fmaf(h[j], w[0], f[0]);
-                    store<T, 1>(y + i * STEP + 32 * j, f);
+                if (!in(i)) continue;
+                uint64_t w[1], f2[1] = {0};
+                if constexpr (RING) {
+                    staged_weight<1>(sw, c + i * STEP, p.cols, in2(i), w);
+                    if (p.b) staged_weight<1>(sb, c + i * STEP, p.cols, in2(i), f2);
+                } else {
+                    float a1[1], b1[1] = {0.0f};
+                    load_weight<1>(p.w, p.w_f32, c + i * STEP, 1.0f, a1);
+                    if (in2(i)) load_weight<1>(p.w, p.w_f32, c + i * STEP + 32, 1.0f, b1);
+                    w[0] = pack2(a1[0], b1[0]);
+                    load_weight<1>(p.b, p.w_f32, c + i * STEP, 0.0f, a1);
+                    if (in2(i)) load_weight<1>(p.b, p.w_f32, c + i * STEP + 32, 0.0f, b1);
+                    f2[0] = pack2(a1[0], b1[0]);
                 }
+                float lo[1], hi[1];
+                unpack2(fma2(v[i][0], w[0], f2[0]), lo[0], hi[0]);
+                store<T, 1>(y + i * STEP, lo);
+                if (in2(i)) store<T, 1>(y + i * STEP + 32, hi);
             }
         }
         if constexpr (!RING) break;
@@ -450,7 +530,7 @@ struct Bwd {
     int64_t ld_dy, ld_x, ld_add, ld_dx;
     int rows, cols, warps, groups, stages;
     // a stage of a group in shared memory: dy, then x or the codes, the scales, dy_add (-1: not staged)
-    int stage_bytes, at_x, at_s, at_dya;
+    int stage_bytes, at_x, at_s, at_dya, weight_bytes;
     bool center, w_f32, want_w, want_b;
 };
 
@@ -499,7 +579,8 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) dnorm_kernel(Bwd p)
     const int c = gw * 32 * EPT + lane * VEC, left = p.cols - c;       // the thread's first column, and those from there on
     const float inv_n = 1.0f / (float)p.cols;
     const int first = (int)blockIdx.x * p.groups + group, step = (int)gridDim.x * p.groups;
-    uint8_t *mine = ring + group * p.stages * p.stage_bytes;
+    float *sw = reinterpret_cast<float *>(ring);       // the weight, then the groups' rings
+    uint8_t *mine = ring + p.weight_bytes + group * p.stages * p.stage_bytes;
     const uint32_t mine_u = smem_u32(mine);
     const int half = p.cols * 2;                       // bytes of the first halves of dy_add's vectors of eight
     const auto in = [&](int i) { return i * STEP < left; };
@@ -583,22 +664,12 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) dnorm_kernel(Bwd p)
             }
         }
     };
-    const auto weights = [&](int i, uint64_t (&w)[H]) {
-        float f[VEC > 1 ? VEC : 2];
-        if constexpr (VEC > 1) {
-            load_weight<VEC>(p.w, p.w_f32, c + i * STEP, 1.0f, f);
-        } else {
-            float b[1] = {0.0f}, a[1];
-            load_weight<1>(p.w, p.w_f32, c + i * STEP, 1.0f, a);
-            if (in2(i)) load_weight<1>(p.w, p.w_f32, c + i * STEP + 32, 1.0f, b);
-            f[0] = a[0], f[1] = b[0];
-        }
-#pragma unroll
-        for (int j = 0; j < H; j++) w[j] = pack2(f[2 * j], f[2 * j + 1]);
-    };
+    const auto weights = [&](int i, uint64_t (&w)[H]) { staged_weight<VEC>(sw, c + i * STEP, p.cols, in2(i), w); };
 
     uint64_t dw[N][H] = {}, db[BIAS ? N : 1][H] = {};
     for (int s = 0; s < p.stages; s++) issue((int64_t)first + (int64_t)s * step, s);
+    stage_weight<VEC>(sw, p.w, p.w_f32, p.cols, 1.0f);
+    __syncthreads();
     float rs_next = 0.0f, mu_next = 0.0f;              // the next row's, loaded a row ahead
     const bool mean = p.center && !CKPT;
     if (first < p.rows) {
@@ -704,7 +775,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) dnorm_kernel(Bwd p)
     }
     if (!p.want_w && !p.want_b) return;
     cp_async_wait<0>();
-    float *joined = reinterpret_cast<float *>(ring);   // [2][cols], groups > 1
+    float *joined = sw + (p.weight_bytes >> 2);        // [2][cols], groups > 1
     for (int gr = 0; gr < p.groups; gr++) {
         if (p.groups > 1) __syncthreads();             // the first one: the ring is done with
         if (group != gr) continue;
@@ -808,7 +879,9 @@ static cudaError_t fwd_plan(Fwd &p, cudaStream_t st)
     p.groups = 1;
     p.stages = p.stage_bytes = 0;
     if (ept == 8) return fwd_launch<T, VEC, 8, false>(p, (unsigned)p.rows, 0, st);
-    const int per_sm = ept == 16 ? 2 : 1, room = SMEM_MAX / per_sm;
+    p.weight_floats = (p.cols + 3) & ~3;
+    p.weight_bytes = p.weight_floats * 4 * (p.b ? 2 : 1);
+    const int per_sm = ept == 16 ? 2 : 1, room = SMEM_MAX / per_sm - p.weight_bytes;
     const int64_t each = (p.rows + sms * per_sm - 1) / (sms * per_sm);
     int groups = 16 / p.warps;
     if (groups > 8 && p.warps > 1) groups = 8;         // named barriers
@@ -820,7 +893,7 @@ static cudaError_t fwd_plan(Fwd &p, cudaStream_t st)
     if (p.stages > 4) p.stages = 4;
     const int64_t want = (p.rows + groups - 1) / groups;
     const unsigned grid = (unsigned)(want < (int64_t)sms * per_sm ? want : (int64_t)sms * per_sm);
-    const int smem = groups * p.stages * p.stage_bytes;
+    const int smem = p.weight_bytes + groups * p.stages * p.stage_bytes;
     return ept == 16 ? fwd_launch<T, VEC, 16, true>(p, grid, smem, st) : fwd_launch<T, VEC, 32, true>(p, grid, smem, st);
 }
 
@@ -874,14 +947,16 @@ static int bwd_plan(Bwd &p, bool vec, int es, int &ept, int &smem)
         if (dya) n += p.cols * 4;
         p.stage_bytes = n;
     };
+    p.weight_bytes = (p.cols * 4 + 15) & ~15;
+    const int room = SMEM_MAX - p.weight_bytes;
     lay(vec && p.dy_add);
-    if (p.stage_bytes > SMEM_MAX) lay(false);
-    while (groups > 1 && 2 * groups * p.stage_bytes > SMEM_MAX) groups--;
-    p.stages = SMEM_MAX / (groups * p.stage_bytes);
+    if (p.stage_bytes > room) lay(false);
+    while (groups > 1 && 2 * groups * p.stage_bytes > room) groups--;
+    p.stages = room / (groups * p.stage_bytes);
     if (p.stages > 4) p.stages = 4;
     p.groups = groups;
     const int ring = groups * p.stages * p.stage_bytes, join = groups > 1 ? 2 * p.cols * (int)sizeof(float) : 0;
-    smem = ring > join ? ring : join;
+    smem = p.weight_bytes + (ring > join ? ring : join);
     return bwd_ctas(p.rows, groups);
 }
 
@@ -911,7 +986,7 @@ MOE_API moe_status moe_layer_norm(const void *x, int dtype, int64_t rows, int64_
                      aligned16(weight) && aligned16(bias);
     if ((y_q || xhat_q) && (!vec || !aligned16(y_q) || !aligned16(xhat_q))) return MOE_ERR_ALIGN;
     if (clash(y, ld_y, x, ld_x, rows, (int)cols, es)) return MOE_ERR_UNSUPPORTED;
-    Fwd p{x, weight, bias, y, mean, rstd, y_q, xhat_q, y_s, xhat_s, rows, ld_x, ld_y, (int)cols, 1, 1, 0, 0, eps,
+    Fwd p{x, weight, bias, y, mean, rstd, y_q, xhat_q, y_s, xhat_s, rows, ld_x, ld_y, (int)cols, 1, 1, 0, 0, 0, 0, eps,
           center != 0, w_dtype == MOE_TYPE_F32};
     cudaStream_t st = as_stream(stream);
     const cudaError_t e = f32 ? (vec ? fwd_plan<float, 4>(p, st) : fwd_plan<float, 1>(p, st))
@@ -966,7 +1041,7 @@ MOE_API moe_status moe_layer_norm_backward(const void *dy, int dtype, int64_t ro
     if (sums && !aligned16(workspace)) return MOE_ERR_ALIGN;
     if (!sums && !dx) return MOE_OK;
     Bwd p{dy, x, dx_add, weight, dy_add, xhat_q, xhat_s, mean, rstd, dx, static_cast<float *>(workspace),
-          ld_dy, ld_x, ld_add, ld_dx, (int)rows, (int)cols, 1, 1, 0, 0, 0, 0, 0, center != 0, w_dtype == MOE_TYPE_F32,
+          ld_dy, ld_x, ld_add, ld_dx, (int)rows, (int)cols, 1, 1, 0, 0, 0, 0, 0, 0, center != 0, w_dtype == MOE_TYPE_F32,
           dweight != nullptr, dbias != nullptr};
     int ept, smem;
     const int grid = bwd_plan(p, vec, es, ept, smem);

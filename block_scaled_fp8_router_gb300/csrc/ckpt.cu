@@ -314,7 +314,7 @@ __global__ void __launch_bounds__(THREADS, 1) swiglu_ckpt_kernel(Args p)
 #pragma unroll
                 for (int w = 1; w < WARPS; w++) m = fmaxf(m, red[w * 3 * TILE + tid]);
                 const float s = computed_scale(m);
-                col_y[tid] = __frcp_rn(s);
+                col_y[tid] = rcp(s);
                 const int k = tid >> 7, ch = at.cb * TILE + (tid & 127);
                 if (k == 2) {
                     if (p.actT_s) p.actT_s[(int64_t)at.kb * p.F + ch] = s;
@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(THREADS, 1) swiglu_ckpt_kernel(Args p)
             leave();
         }
         if (ROW) {
-            const float s = computed_scale(rm), ry = __frcp_rn(s);
+            const float s = computed_scale(rm), ry = rcp(s);
             if ((lane >> 1) < at.n) p.dh_s[(int64_t)(at.row + (lane >> 1)) * 2 * nb + (lane & 1) * nb + at.cb] = s;
             uint8_t *q = p.dh_q + (int64_t)at.row * 2 * p.F + at.cb * TILE + c0, *q2 = q + p.F;
 #pragma unroll

@@ -170,11 +170,15 @@ __device__ __forceinline__ uint16_t e4m3x2_div(float v0, float v1, float s, floa
 }
 
 // ---- codes of computed values (a checkpoint, a gradient's operand) ----
-// The scale amax / 448 (1 where that is 0), not below 2^-126 so that its
-// reciprocal is finite; a code is E4M3(v RN(1 / s)): one product an element,
-// where the quotient of the given tensors' quantiser takes five, and no less
-// exact for a value that is itself off by some 2^-24.
-__device__ __forceinline__ float computed_scale(float amax) { return fmaxf(block_scale(amax), 0x1p-126f); }
+// The scale amax / 448 to within a unit in the last place (1 where amax is 0),
+// not below 2^-126 so that its reciprocal is finite; a code is E4M3(v y) with
+// y = 1 / s to within a unit: a product each, where the quotients of the given
+// tensors' quantiser take a division a block and five steps an element.  The
+// value itself is off by more.
+__device__ __forceinline__ float computed_scale(float amax)
+{
+    return amax == 0.0f ? 1.0f : fmaxf(amax * (1.0f / 448.0f), 0x1p-126f);
+}
 
 // the largest magnitude of three (a NaN is passed over)
 __device__ __forceinline__ float amax3(float a, float b, float c)

@@ -473,7 +473,9 @@ __global__ void __launch_bounds__(FT_THREADS, 1)
                     s.redh[cg][r_in] = make_float2(mg, mu);
                     if (pair_bar_or(q, aborted || *abort_flag)) aborted = true;
                     const float2 m0 = s.redh[0][r_in], m1 = s.redh[1][r_in];
-                    const float sg = computed_scale(fmaxf(m0.x, m1.x)), su = computed_scale(fmaxf(m0.y, m1.y));
+                    // not below 2^-126, so that the reciprocals are finite
+                    const float sg = fmaxf(block_scale(fmaxf(m0.x, m1.x)), 0x1p-126f);
+                    const float su = fmaxf(block_scale(fmaxf(m0.y, m1.y)), 0x1p-126f);
                     if (row_ok && !aborted) {
                         uint8_t *dst = p.h_q + row * 2 * p.F + tl.n_blk * 128 + 64 * cg;
 #pragma unroll

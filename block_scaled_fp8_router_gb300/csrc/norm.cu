@@ -162,18 +162,23 @@ __device__ __forceinline__ void group_sync(int warps, int bar)
 // dst + (start & 15) + c * sizeof(T).  Bytes behind the row are not read; the
 // piece it starts in may hold bytes of the row before, but where it would
 // reach back beyond the tensor's first row the values are copied one by one.
+// `pieces` is the same for every row (one more than the row may touch: zeros),
+// so that nothing of another row stays behind this one.
+// the most pieces that a row of that many bytes lies in
+__host__ __device__ constexpr int odd_pieces(int bytes) { return (bytes + 14 + 15) / 16; }
+
 template <typename T>
 __device__ __forceinline__ void copy_odd(uint32_t dst, const T *base, int64_t at, int cols, int t, int nth)
 {
     const uintptr_t start = reinterpret_cast<uintptr_t>(base + at), end = start + (size_t)cols * sizeof(T);
     const uintptr_t from = start & ~(uintptr_t)15;
-    const int pieces = (int)((end - from + 15) >> 4);
+    const int pieces = odd_pieces(cols * (int)sizeof(T));
     for (int k = t; k < pieces; k += nth) {
         const uintptr_t src = from + 16 * (uintptr_t)k;
         if (src >= reinterpret_cast<uintptr_t>(base)) {
-            const uintptr_t left = end - src;
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + 16 * k), "l"(src),
-                         "r"(left < 16 ? (int)left : 16)
+            const int left = src < end ? (int)(end - src) : 0;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + 16 * k), "l"(left ? src : from),
+                         "r"(left < 16 ? left : 16)
                          : "memory");
         } else {
             for (uintptr_t a = start; a < src + 16 && a < end; a += sizeof(T)) {
@@ -206,11 +211,21 @@ __device__ __forceinline__ void pairs(const T *p, bool second, uint64_t (&v)[(VE
     }
 }
 
+// Zeros, once, in shared memory behind the columns of a row: a thread whose
+// columns lie there reads them and needs no question (its stores do).
+__device__ __forceinline__ void clear(uint8_t *p, int bytes)
+{
+    for (int b = 16 * (int)threadIdx.x; b < bytes; b += 16 * (int)blockDim.x)
+        *reinterpret_cast<uint4 *>(p + b) = make_uint4(0u, 0u, 0u, 0u);
+    __syncthreads();
+}
+
 // A weight in fp32 in shared memory (`none` where there is none), for a CTA
 // that meets many rows: no conversion and no question of its type a row.
-// Vectors of eight lie as two halves, so that a warp reads whole banks.
+// Vectors of eight lie as two halves, so that a warp reads whole banks.  wide:
+// the columns that the row's threads have together; zeros behind the last one.
 template <int VEC, bool F32>
-__device__ __forceinline__ void stage_weight_of(float *dst, const void *w, int cols)
+__device__ __forceinline__ void stage_weight_of(float *dst, const void *w, int cols, int wide)
 {
     if constexpr (VEC == 1) {
 #pragma unroll 8
@@ -227,33 +242,31 @@ __device__ __forceinline__ void stage_weight_of(float *dst, const void *w, int c
                 f = make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u), __uint_as_float(v.y << 16),
                                 __uint_as_float(v.y & 0xFFFF0000u));
             }
-            *reinterpret_cast<float4 *>(dst + (VEC == 8 ? (q >> 1) * 4 + (q & 1 ? cols >> 1 : 0) : 4 * q)) = f;
+            *reinterpret_cast<float4 *>(dst + (VEC == 8 ? (q >> 1) * 4 + (q & 1 ? wide >> 1 : 0) : 4 * q)) = f;
         }
     }
 }
 template <int VEC>
-__device__ __forceinline__ void stage_weight(float *dst, const void *w, bool f32, int cols, float none)
+__device__ __forceinline__ void stage_weight(float *dst, const void *w, bool f32, int cols, int wide, float none)
 {
-    if (!w) {
-        for (int c = threadIdx.x; c < cols; c += blockDim.x) dst[c] = none;
-    } else if (f32) {
-        stage_weight_of<VEC, true>(dst, w, cols);
-    } else {
-        stage_weight_of<VEC, false>(dst, w, cols);
-    }
+    for (int c = (w ? cols : 0) + threadIdx.x; c < wide; c += blockDim.x)
+        dst[VEC == 8 ? (c >> 3) * 4 + (c & 3) + (c & 4 ? wide >> 1 : 0) : c] = c < cols ? none : 0.0f;
+    if (!w) return;
+    if (f32) stage_weight_of<VEC, true>(dst, w, cols, wide);
+    else stage_weight_of<VEC, false>(dst, w, cols, wide);
 }
-// the pairs of a vector from column c on (of single values c and, if present, c + 32)
+// the pairs of a vector from column c on (of single values c and c + 32)
 template <int VEC>
-__device__ __forceinline__ void staged_weight(const float *s, int c, int cols, bool second, uint64_t (&w)[(VEC + 1) / 2])
+__device__ __forceinline__ void staged_weight(const float *s, int c, int wide, uint64_t (&w)[(VEC + 1) / 2])
 {
     if constexpr (VEC == 1) {
-        w[0] = pack2(s[c], second ? s[c + 32] : 0.0f);
+        w[0] = pack2(s[c], s[c + 32]);
     } else {
         const float4 a = *reinterpret_cast<const float4 *>(s + (VEC == 8 ? c >> 1 : c));
         w[0] = pack2(a.x, a.y);
         w[1] = pack2(a.z, a.w);
         if constexpr (VEC == 8) {
-            const float4 b = *reinterpret_cast<const float4 *>(s + (cols >> 1) + (c >> 1));
+            const float4 b = *reinterpret_cast<const float4 *>(s + (wide >> 1) + (c >> 1));
             w[2] = pack2(b.x, b.y);
             w[3] = pack2(b.z, b.w);
         }
@@ -269,9 +282,10 @@ struct Fwd {
     uint8_t *y_q, *h_q;         // codes of y and of xhat, [rows, cols]
     float *y_s, *h_s;           // their scales, [rows, cols / 128]
     int64_t rows, ld_x, ld_y;
-    int cols, warps, groups;    // warps of a row, rows that a CTA has at work
+    int cols, wide;             // the row's columns, and those that its threads have together
+    int warps, groups;          // warps of a row, rows that a CTA has at work
     int stages, stage_bytes;    // of a group's ring
-    int weight_floats, weight_bytes;    // of one weight, and of both, in shared memory
+    int weight_bytes;           // of the weights in shared memory
     float eps;
     bool center, w_f32;
 };
@@ -314,7 +328,7 @@ __device__ __forceinline__ void encode(const uint64_t (&v)[VPT][VEC / 2], int c,
             m[i] = amax3(a, b, m[i]);
         }
     }
-    const float sc = computed_scale(scatter_max<VPT, G>(m, lane)), y = __frcp_rn(sc);
+    const float sc = computed_scale(scatter_max<VPT, G>(m, lane)), y = rcp(sc);
     const int mine = (lane & (G - 1)) / EACH;                  // the vector whose scale this lane has
     const int c_mine = c - (lane & (G - 1)) * VEC + mine * 32 * VEC;
     if ((lane & (EACH - 1)) == 0 && c_mine < cols) s[c_mine >> 7] = sc;
@@ -359,7 +373,7 @@ __global__ void __launch_bounds__(EPT == 8 ? 1024 : 512, EPT == 16 ? 2 : 1) norm
     const auto in2 = [&](int i) { return c + i * STEP + 32 < p.cols; };              // a pair's second single value
     const int64_t first = (int64_t)blockIdx.x * p.groups + group, step = (int64_t)gridDim.x * p.groups;
     // RING: the weights, then the groups' rings
-    float *sw = reinterpret_cast<float *>(ring), *sb = sw + p.weight_floats;
+    float *sw = reinterpret_cast<float *>(ring), *sb = sw + p.wide;
     uint8_t *mine = ring + p.weight_bytes + group * p.stages * p.stage_bytes;
     const auto issue = [&](int64_t row, int stage) {
         if (row < p.rows) {
@@ -377,9 +391,10 @@ __global__ void __launch_bounds__(EPT == 8 ? 1024 : 512, EPT == 16 ? 2 : 1) norm
     };
     int stage = 0, par = 0;
     if constexpr (RING) {
+        if (VEC == 1 || p.wide != p.cols) clear(ring + p.weight_bytes, p.groups * p.stages * p.stage_bytes);
         for (int s = 0; s < p.stages; s++) issue(first + s * step, s);
-        stage_weight<VEC>(sw, p.w, p.w_f32, p.cols, 1.0f);
-        if (p.b) stage_weight<VEC>(sb, p.b, p.w_f32, p.cols, 0.0f);
+        stage_weight<VEC>(sw, p.w, p.w_f32, p.cols, p.wide, 1.0f);
+        if (p.b) stage_weight<VEC>(sb, p.b, p.w_f32, p.cols, p.wide, 0.0f);
         __syncthreads();
     }
     for (int64_t row = first; row < p.rows; row += step, par ^= 1) {
@@ -399,7 +414,7 @@ __global__ void __launch_bounds__(EPT == 8 ? 1024 : 512, EPT == 16 ? 2 : 1) norm
             for (int i = 0; i < N; i++) {
 #pragma unroll
                 for (int j = 0; j < H; j++) v[i][j] = 0;
-                if (in(i)) pairs<T, VEC>(x + i * STEP, in2(i), v[i]);
+                if (RING || in(i)) pairs<T, VEC>(x + i * STEP, RING || in2(i), v[i]);
             }
         }
         float sum = 0.0f, sq = 0.0f;
@@ -468,10 +483,10 @@ __global__ void __launch_bounds__(EPT == 8 ? 1024 : 512, EPT == 16 ? 2 : 1) norm
                 float f[VEC] = {};
 #pragma unroll
                 for (int j = 0; j < H; j++) w[j] = f2[j] = 0;
-                if (in(i)) {
+                if (RING || in(i)) {
                     if constexpr (RING) {
-                        staged_weight<VEC>(sw, c + i * STEP, p.cols, false, w);
-                        if (p.b) staged_weight<VEC>(sb, c + i * STEP, p.cols, false, f2);
+                        staged_weight<VEC>(sw, c + i * STEP, p.wide, w);
+                        if (p.b) staged_weight<VEC>(sb, c + i * STEP, p.wide, f2);
                     } else {
                         load_weight<VEC>(p.w, p.w_f32, c + i * STEP, 1.0f, f);
 #pragma unroll
@@ -492,12 +507,11 @@ __global__ void __launch_bounds__(EPT == 8 ? 1024 : 512, EPT == 16 ? 2 : 1) norm
         } else {
 #pragma unroll
             for (int i = 0; i < N; i++) {
-                if (!in(i)) continue;
                 uint64_t w[1], f2[1] = {0};
                 if constexpr (RING) {
-                    staged_weight<1>(sw, c + i * STEP, p.cols, in2(i), w);
-                    if (p.b) staged_weight<1>(sb, c + i * STEP, p.cols, in2(i), f2);
-                } else {
+                    staged_weight<1>(sw, c + i * STEP, p.wide, w);
+                    if (p.b) staged_weight<1>(sb, c + i * STEP, p.wide, f2);
+                } else if (in(i)) {
                     float a1[1], b1[1] = {0.0f};
                     load_weight<1>(p.w, p.w_f32, c + i * STEP, 1.0f, a1);
                     if (in2(i)) load_weight<1>(p.w, p.w_f32, c + i * STEP + 32, 1.0f, b1);
@@ -508,7 +522,7 @@ __global__ void __launch_bounds__(EPT == 8 ? 1024 : 512, EPT == 16 ? 2 : 1) norm
                 }
                 float lo[1], hi[1];
                 unpack2(fma2(v[i][0], w[0], f2[0]), lo[0], hi[0]);
-                store<T, 1>(y + i * STEP, lo);
+                if (in(i)) store<T, 1>(y + i * STEP, lo);
                 if (in2(i)) store<T, 1>(y + i * STEP + 32, hi);
             }
         }
@@ -528,7 +542,7 @@ struct Bwd {
     void *dx;
     float *part;                // per CTA: cols sums of a xhat, cols sums of a
     int64_t ld_dy, ld_x, ld_add, ld_dx;
-    int rows, cols, warps, groups, stages;
+    int rows, cols, wide, warps, groups, stages;
     // a stage of a group in shared memory: dy, then x or the codes, the scales, dy_add (-1: not staged)
     int stage_bytes, at_x, at_s, at_dya, weight_bytes;
     bool center, w_f32, want_w, want_b;
@@ -582,7 +596,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) dnorm_kernel(Bwd p)
     float *sw = reinterpret_cast<float *>(ring);       // the weight, then the groups' rings
     uint8_t *mine = ring + p.weight_bytes + group * p.stages * p.stage_bytes;
     const uint32_t mine_u = smem_u32(mine);
-    const int half = p.cols * 2;                       // bytes of the first halves of dy_add's vectors of eight
+    const int half = p.wide * 2;                       // bytes of the first halves of dy_add's vectors of eight
     const auto in = [&](int i) { return i * STEP < left; };
     const auto in2 = [&](int i) { return i * STEP + 32 < left; };      // a pair's second single value
 
@@ -630,45 +644,43 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) dnorm_kernel(Bwd p)
         }
         cp_async_commit();
     };
-    // vector i of the row: a = dy + dy_add and xhat = (x - mu) r, or from its codes
-    const auto get = [&](int64_t row, const uint8_t *st, int i, uint64_t rs2, uint64_t nmu2, uint64_t (&a)[H], uint64_t (&h)[H]) {
-        if constexpr (VEC > 1) {
-            pairs<T, VEC>(reinterpret_cast<const T *>(st) + c + i * STEP, false, a);
-            if constexpr (CKPT)
-                decode<VEC>(st + p.at_x + c + i * STEP,
-                            *reinterpret_cast<const float *>(st + p.at_s + (c >> 7) * 4 + i * STEP / 32), h);
-            else pairs<T, VEC>(reinterpret_cast<const T *>(st + p.at_x) + c + i * STEP, false, h);
+    // vector i of the row: a = dy + dy_add and xhat = (x - mu) r, or from its codes.  dy, x: the row in shared memory
+    const auto get = [&](int64_t row, const uint8_t *st, const T *dy, const T *x, int i, uint64_t rs2, uint64_t nmu2,
+                         uint64_t (&a)[H], uint64_t (&h)[H]) {
+        pairs<T, VEC>(dy + i * STEP, true, a);
+        if constexpr (CKPT) {
+            decode<VEC>(st + p.at_x + c + i * STEP,
+                        *reinterpret_cast<const float *>(st + p.at_s + (c >> 7) * 4 + i * STEP / 32), h);
         } else {
-            const T *dy = reinterpret_cast<const T *>(st + odd_shift(static_cast<const T *>(p.dy), row * p.ld_dy));
-            const T *x = reinterpret_cast<const T *>(st + p.at_x + odd_shift(static_cast<const T *>(p.x), row * p.ld_x));
-            pairs<T, VEC>(dy + c + i * STEP, in2(i), a);
-            pairs<T, VEC>(x + c + i * STEP, in2(i), h);
-        }
-        if (!CKPT) {
+            pairs<T, VEC>(x + i * STEP, true, h);
 #pragma unroll
             for (int j = 0; j < H; j++) h[j] = mul2(add2(h[j], nmu2), rs2);
         }
-        if (p.dy_add) {
+        if (p.at_dya >= 0) {
             if constexpr (VEC > 1) {
 #pragma unroll
                 for (int k = 0; k < VEC / 4; k++) {
-                    const float4 d = p.at_dya >= 0
-                                         ? *reinterpret_cast<const float4 *>(st + p.at_dya + k * half + c / VEC * 16 + i * 512)
-                                         : __ldg(reinterpret_cast<const float4 *>(p.dy_add + row * p.cols + c + i * STEP + 4 * k));
+                    const float4 d = *reinterpret_cast<const float4 *>(st + p.at_dya + k * half + c / VEC * 16 + i * 512);
                     a[2 * k] = add2(a[2 * k], pack2(d.x, d.y));
                     a[2 * k + 1] = add2(a[2 * k + 1], pack2(d.z, d.w));
                 }
+            }
+        } else if (p.dy_add && in(i)) {
+            const float *d = p.dy_add + row * p.cols + c + i * STEP;
+            if constexpr (VEC > 1) {
+#pragma unroll
+                for (int j = 0; j < H; j++) a[j] = add2(a[j], pack2(__ldg(d + 2 * j), __ldg(d + 2 * j + 1)));
             } else {
-                const float *d = p.dy_add + row * p.cols + c + i * STEP;
                 a[0] = add2(a[0], pack2(__ldg(d), in2(i) ? __ldg(d + 32) : 0.0f));
             }
         }
     };
-    const auto weights = [&](int i, uint64_t (&w)[H]) { staged_weight<VEC>(sw, c + i * STEP, p.cols, in2(i), w); };
+    const auto weights = [&](int i, uint64_t (&w)[H]) { staged_weight<VEC>(sw, c + i * STEP, p.wide, w); };
 
     uint64_t dw[N][H] = {}, db[BIAS ? N : 1][H] = {};
+    if (VEC == 1 || p.wide != p.cols) clear(ring + p.weight_bytes, p.groups * p.stages * p.stage_bytes);
     for (int s = 0; s < p.stages; s++) issue((int64_t)first + (int64_t)s * step, s);
-    stage_weight<VEC>(sw, p.w, p.w_f32, p.cols, 1.0f);
+    stage_weight<VEC>(sw, p.w, p.w_f32, p.cols, p.wide, 1.0f);
     __syncthreads();
     float rs_next = 0.0f, mu_next = 0.0f;              // the next row's, loaded a row ahead
     const bool mean = p.center && !CKPT;
@@ -697,23 +709,26 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) dnorm_kernel(Bwd p)
         wait_oldest(p.stages);
         if (CKPT) __syncwarp();                        // a block's scale was copied by one of its lanes
         if (VEC == 1) group_sync(p.warps, group + 1);  // the row's pieces were copied by others
+        const T *dy = reinterpret_cast<const T *>(st) + c, *x = reinterpret_cast<const T *>(st + p.at_x) + c;
+        if (VEC == 1) {
+            dy = reinterpret_cast<const T *>(st + odd_shift(static_cast<const T *>(p.dy), row * p.ld_dy)) + c;
+            x = reinterpret_cast<const T *>(st + p.at_x + odd_shift(static_cast<const T *>(p.x), row * p.ld_x)) + c;
+        }
         uint64_t g[KEEP ? N : 1][H], h[KEEP ? N : 1][H];
         uint64_t s1 = 0, s2 = 0;
 #pragma unroll
         for (int i = 0; i < N; i++) {
             uint64_t (&hi)[H] = h[KEEP ? i : 0], (&gi)[H] = g[KEEP ? i : 0];
-            if (in(i)) {
-                uint64_t a[H], w[H];
-                get(row, st, i, rs2, nmu2, a, hi);
-                weights(i, w);
+            uint64_t a[H], w[H];
+            get(row, st, dy, x, i, rs2, nmu2, a, hi);
+            weights(i, w);
 #pragma unroll
-                for (int j = 0; j < H; j++) {
-                    gi[j] = mul2(a[j], w[j]);
-                    s1 = add2(s1, gi[j]);
-                    s2 = fma2(gi[j], hi[j], s2);
-                    dw[i][j] = fma2(a[j], hi[j], dw[i][j]);
-                    if (BIAS) db[i][j] = add2(db[i][j], a[j]);
-                }
+            for (int j = 0; j < H; j++) {
+                gi[j] = mul2(a[j], w[j]);
+                s1 = add2(s1, gi[j]);
+                s2 = fma2(gi[j], hi[j], s2);
+                dw[i][j] = fma2(a[j], hi[j], dw[i][j]);
+                if (BIAS) db[i][j] = add2(db[i][j], a[j]);
             }
         }
         if (KEEP && VEC > 1) {
@@ -721,11 +736,11 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) dnorm_kernel(Bwd p)
             issue(row + (int64_t)p.stages * step, stage);
         }
         if (p.dx) {
-            float m1, m2, x, y;
-            unpack2(s1, x, y);
-            m1 = x + y;
-            unpack2(s2, x, y);
-            m2 = x + y;
+            float m1, m2, lo, up;
+            unpack2(s1, lo, up);
+            m1 = lo + up;
+            unpack2(s2, lo, up);
+            m2 = lo + up;
             // the buffer alternates by row: a warp a row ahead writes the other one
             row_sums(m2, m1, p.center, red[par], group * p.warps, p.warps, gw, lane, group + 1);
             m1 = p.center ? m1 * inv_n : 0.0f, m2 *= inv_n;
@@ -733,18 +748,17 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) dnorm_kernel(Bwd p)
             T *dx = static_cast<T *>(p.dx) + row * p.ld_dx + c;
 #pragma unroll
             for (int i = 0; i < N; i++) {
-                if (!in(i)) continue;
                 uint64_t (&hi)[H] = h[KEEP ? i : 0], (&gi)[H] = g[KEEP ? i : 0];
                 if (!KEEP) {
                     uint64_t w[H];
-                    get(row, st, i, rs2, nmu2, gi, hi);
+                    get(row, st, dy, x, i, rs2, nmu2, gi, hi);
                     weights(i, w);
 #pragma unroll
                     for (int j = 0; j < H; j++) gi[j] = mul2(gi[j], w[j]);
                 }
                 constexpr int M = VEC > 1 ? VEC : 2;
                 float f[M], d[M] = {};
-                if (p.dx_add) {
+                if (p.dx_add && in(i)) {
                     float r[VEC];
                     Vec<T, VEC>::get(add[i], r);
 #pragma unroll
@@ -758,10 +772,10 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) dnorm_kernel(Bwd p)
                 for (int j = 0; j < H; j++)
                     unpack2(fma2(fma2(hi[j], nm2, add2(gi[j], nm1)), rs2, pack2(d[2 * j], d[2 * j + 1])), f[2 * j], f[2 * j + 1]);
                 if constexpr (VEC > 1) {
-                    store<T, VEC>(dx + i * STEP, f);
+                    if (in(i)) store<T, VEC>(dx + i * STEP, f);
                 } else {
                     const float lo[1] = {f[0]}, hi1[1] = {f[1]};
-                    store<T, 1>(dx + i * STEP, lo);
+                    if (in(i)) store<T, 1>(dx + i * STEP, lo);
                     if (in2(i)) store<T, 1>(dx + i * STEP + 32, hi1);
                 }
             }
@@ -876,17 +890,17 @@ static cudaError_t fwd_plan(Fwd &p, cudaStream_t st)
     const int sms = sm_count(), es = sizeof(T);
     const int ept = p.cols > 8192 ? 32 : p.rows <= sms ? 8 : 16;
     p.warps = (p.cols + 32 * ept - 1) / (32 * ept);
+    p.wide = p.warps * 32 * ept;
     p.groups = 1;
     p.stages = p.stage_bytes = 0;
     if (ept == 8) return fwd_launch<T, VEC, 8, false>(p, (unsigned)p.rows, 0, st);
-    p.weight_floats = (p.cols + 3) & ~3;
-    p.weight_bytes = p.weight_floats * 4 * (p.b ? 2 : 1);
+    p.weight_bytes = p.wide * 4 * (p.b ? 2 : 1);
     const int per_sm = ept == 16 ? 2 : 1, room = SMEM_MAX / per_sm - p.weight_bytes;
     const int64_t each = (p.rows + sms * per_sm - 1) / (sms * per_sm);
     int groups = 16 / p.warps;
     if (groups > 8 && p.warps > 1) groups = 8;         // named barriers
     if (groups > each) groups = (int)each;
-    p.stage_bytes = (p.cols * es + (VEC == 1 ? 16 : 0) + 15) & ~15;
+    p.stage_bytes = p.wide * es + (VEC == 1 ? 32 : 0);
     while (groups > 1 && 2 * groups * p.stage_bytes > room) groups--;
     p.groups = groups;
     p.stages = room / (groups * p.stage_bytes);
@@ -932,22 +946,23 @@ static int bwd_plan(Bwd &p, bool vec, int es, int &ept, int &smem)
 {
     ept = p.cols > 8192 ? 32 : 16;
     p.warps = (p.cols + 32 * ept - 1) / (32 * ept);
+    p.wide = p.warps * 32 * ept;
     int groups = BWD_THREADS / 32 / p.warps;
     const int per_sm = (p.rows + sm_count() - 1) / sm_count();
     if (groups > 8) groups = 8;                        // named barriers, and the parts joined one after another
     if (groups > per_sm) groups = per_sm;
     const auto lay = [&](bool dya) {
-        const int row = (p.cols * es + (vec ? 0 : 16) + 15) & ~15;
+        const int row = p.wide * es + (vec ? 0 : 32);
         int n = row;
         p.at_x = n;
-        n += p.h_q ? p.cols : row;
+        n += p.h_q ? p.wide : row;
         p.at_s = n;
-        if (p.h_q) n = (n + p.cols / 128 * 4 + 15) & ~15;
+        if (p.h_q) n = (n + p.wide / 128 * 4 + 15) & ~15;
         p.at_dya = dya ? n : -1;
-        if (dya) n += p.cols * 4;
+        if (dya) n += p.wide * 4;
         p.stage_bytes = n;
     };
-    p.weight_bytes = (p.cols * 4 + 15) & ~15;
+    p.weight_bytes = p.wide * 4;
     const int room = SMEM_MAX - p.weight_bytes;
     lay(vec && p.dy_add);
     if (p.stage_bytes > room) lay(false);
@@ -986,7 +1001,7 @@ MOE_API moe_status moe_layer_norm(const void *x, int dtype, int64_t rows, int64_
                      aligned16(weight) && aligned16(bias);
     if ((y_q || xhat_q) && (!vec || !aligned16(y_q) || !aligned16(xhat_q))) return MOE_ERR_ALIGN;
     if (clash(y, ld_y, x, ld_x, rows, (int)cols, es)) return MOE_ERR_UNSUPPORTED;
-    Fwd p{x, weight, bias, y, mean, rstd, y_q, xhat_q, y_s, xhat_s, rows, ld_x, ld_y, (int)cols, 1, 1, 0, 0, 0, 0, eps,
+    Fwd p{x, weight, bias, y, mean, rstd, y_q, xhat_q, y_s, xhat_s, rows, ld_x, ld_y, (int)cols, 0, 1, 1, 0, 0, 0, eps,
           center != 0, w_dtype == MOE_TYPE_F32};
     cudaStream_t st = as_stream(stream);
     const cudaError_t e = f32 ? (vec ? fwd_plan<float, 4>(p, st) : fwd_plan<float, 1>(p, st))
@@ -1041,7 +1056,7 @@ MOE_API moe_status moe_layer_norm_backward(const void *dy, int dtype, int64_t ro
     if (sums && !aligned16(workspace)) return MOE_ERR_ALIGN;
     if (!sums && !dx) return MOE_OK;
     Bwd p{dy, x, dx_add, weight, dy_add, xhat_q, xhat_s, mean, rstd, dx, static_cast<float *>(workspace),
-          ld_dy, ld_x, ld_add, ld_dx, (int)rows, (int)cols, 1, 1, 0, 0, 0, 0, 0, 0, center != 0, w_dtype == MOE_TYPE_F32,
+          ld_dy, ld_x, ld_add, ld_dx, (int)rows, (int)cols, 0, 1, 1, 0, 0, 0, 0, 0, 0, center != 0, w_dtype == MOE_TYPE_F32,
           dweight != nullptr, dbias != nullptr};
     int ept, smem;
     const int grid = bwd_plan(p, vec, es, ept, smem);

@@ -325,7 +325,9 @@ __global__ void __launch_bounds__(THREADS, 1) swiglu_ckpt_kernel(Args p)
             leave();
         }
         if (ROW) {
-            const float s = computed_scale(rm), ry = rcp(s);
+            // computed_scale by the quotient's code: its branch keeps the encoding behind it apart from what is before
+            // (65536 x 2048, this side alone: 139 us against 151 in one piece)
+            const float s = fmaxf(block_scale(rm), 0x1p-126f), ry = rcp(s);
             if ((lane >> 1) < at.n) p.dh_s[(int64_t)(at.row + (lane >> 1)) * 2 * nb + (lane & 1) * nb + at.cb] = s;
             uint8_t *q = p.dh_q + (int64_t)at.row * 2 * p.F + at.cb * TILE + c0, *q2 = q + p.F;
 #pragma unroll

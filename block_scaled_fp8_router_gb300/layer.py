@@ -78,6 +78,16 @@ def quantize_weights(w13: torch.Tensor, w2: torch.Tensor, out: MoEWeightsFP8 | N
     return out
 
 
+@dataclass
+class MoENorm:
+    """The norm before the layer: weight and bias [d] (bf16 or fp32, one type;
+    each may be None), layer norm (center) or its RMS form."""
+    weight: torch.Tensor | None = None
+    bias: torch.Tensor | None = None
+    eps: float = 1e-6
+    center: bool = False
+
+
 class MoELayerFP8:
     """Forward of one MoE layer on one GPU with preallocated buffers.
 
@@ -89,15 +99,27 @@ class MoELayerFP8:
     Weights with power-of-two (UE8M0) scales select the block-scaled-MMA
     variant: x is quantised with power-of-two scales and the FFN is
     moe_grouped_ffn_mx (sorted form).
+
+    norm: the layer runs on the norm of x (one pass gives the normalised rows
+    and the FFN's codes of them); norm_backward takes the layer's gradients on
+    to x.  ckpt8: what a train forward keeps for the backward is in 8 bits: the
+    pre-activations (a quarter of their fp32 size) and the norm's rows (the
+    caller need not keep x); out_sorted is scratch, the gates' gradient comes
+    from the checkpoint.  fp32-scale sorted form only.
     """
 
     def __init__(self, weights: MoEWeightsFP8, T_max: int, k: int, score_fn: int, renorm: int = 1,
-                 route_scale: float = 1.0, device=None, gathered: bool = False):
+                 route_scale: float = 1.0, device=None, gathered: bool = False, norm: MoENorm | None = None,
+                 ckpt8: bool = False):
         self.w = weights
+        self.norm = norm
+        self.ckpt8 = ckpt8
         self.gathered = gathered
         self.mx = weights.ue8m0
         if self.mx and gathered:
             raise ValueError("the power-of-two variant runs in the sorted form")
+        if ckpt8 and (self.mx or gathered):
+            raise ValueError("ckpt8 needs the fp32-scale sorted form")
         self.k, self.score_fn, self.renorm, self.route_scale = k, score_fn, renorm, route_scale
         dev = weights.w13_q.device if device is None else device
         E, d, F = weights.E, weights.d, weights.F
@@ -120,6 +142,21 @@ class MoELayerFP8:
         ws = L.moe_grouped_ffn_mx_workspace_size(A, d, F) if self.mx else L.moe_grouped_ffn_workspace_size(A, d, F)
         self.ffn_ws = e((ws,), torch.uint8)
         self.dev_status = torch.zeros((1,), dtype=torch.int32, device=dev)
+        if norm is not None:
+            self.xn = e((T_max, d), torch.bfloat16)
+            self.n_mean, self.n_rstd = e((T_max,), torch.float32), e((T_max,), torch.float32)
+            if ckpt8:
+                self.xhat_q, self.xhat_s = e((T_max, d), torch.uint8), e((T_max, d // 128), torch.float32)
+
+    def _normalise(self, x: torch.Tensor, train: bool) -> torch.Tensor:
+        """The norm of x, with the FFN's codes of it in xq, xs (fp32 scales) and what norm_backward needs."""
+        T, n = x.shape[0], self.norm
+        L.moe_layer_norm(x, n.weight, n.bias, eps=n.eps, center=n.center, y=self.xn[:T],
+                         mean=self.n_mean[:T] if train and n.center else None, rstd=self.n_rstd[:T] if train else None,
+                         codes=None if self.mx else (self.xq[:T], self.xs[:T]),
+                         ckpt=(self.xhat_q[:T], self.xhat_s[:T]) if train and self.ckpt8 else None)
+        self._x_norm = x if train and not self.ckpt8 else None
+        return self.xn[:T]
 
     def route(self, x: torch.Tensor, replay_kT: torch.Tensor | None = None, capture_kT: torch.Tensor | None = None):
         T = x.shape[0]
@@ -135,11 +172,16 @@ class MoELayerFP8:
     def forward(self, x: torch.Tensor, replay_kT: torch.Tensor | None = None,
                 capture_kT: torch.Tensor | None = None, y: torch.Tensor | None = None,
                 train: bool = False) -> torch.Tensor:
-        """train=True also keeps GEMM1's pre-activations for backward()."""
+        """train=True also keeps GEMM1's pre-activations for backward() (in 8
+        bits with ckpt8)."""
         T = x.shape[0]
         if T > self.T_max:
             raise ValueError(f"T={T} exceeds T_max={self.T_max}")
         A = T * self.k
+        if not train and (self.norm is not None or self.ckpt8):
+            self._T_train = None                        # nothing is kept: what was is of another forward
+        if self.norm is not None:
+            x = self._normalise(x, train)
         ids, gates = self.route(x, replay_kT, capture_kT)
         y = self.y[:T] if y is None else y
         if self.mx:
@@ -151,7 +193,9 @@ class MoELayerFP8:
                                  self.w.w13_s, self.w.w2_q, self.w.w2_s, out_sorted=self.out_sorted[:A],
                                  workspace=self.ffn_ws, dev_status=self.dev_status)
             return L.moe_combine(self.out_sorted[:A], self.sl2[:A], gates, y=y)
-        xq, xs = L.fp8_block_quant(x, 1, q=self.xq[:T], scales=self.xs[:T])
+        xq, xs = self.xq[:T], self.xs[:T]
+        if self.norm is None:
+            L.fp8_block_quant(x, 1, q=xq, scales=xs)
         if self.gathered:
             L.moe_dispatch(ids, self.w.E, expert_counts=self.counts, expert_offsets=self.offsets,
                            sorted_to_slot=self.s2s[:A], slot_to_sorted=self.sl2[:A], workspace=self.dsp_ws,
@@ -164,7 +208,18 @@ class MoELayerFP8:
                        expert_offsets=self.offsets, sorted_to_slot=self.s2s[:A], slot_to_sorted=self.sl2[:A],
                        rows_sorted=self.xq_sorted[:A], scales_sorted=self.xs_sorted[:A], workspace=self.dsp_ws,
                        dev_status=self.dev_status)
-        if train:
+        if train and self.ckpt8:
+            if getattr(self, "h_q", None) is None:
+                Am, twoF = self.T_max * self.k, 2 * self.w.F
+                self.h_q = torch.empty((Am, twoF), dtype=torch.uint8, device=x.device)
+                self.h_s = torch.empty((Am, twoF // 128), dtype=torch.float32, device=x.device)
+            L.moe_grouped_ffn_fp8_ckpt(self.xq_sorted[:A], self.xs_sorted[:A], self.offsets, self.w.w13_q,
+                                       self.w.w13_s, self.w.w2_q, self.w.w2_s, h_q=self.h_q[:A], h_s=self.h_s[:A],
+                                       out_sorted=self.out_sorted[:A], workspace=self.ffn_ws,
+                                       dev_status=self.dev_status)
+            self._T_train = T
+            self._x_train = x
+        elif train:
             if getattr(self, "h", None) is None or self.h.shape[0] < A:
                 self.h = torch.empty((self.T_max * self.k, 2 * self.w.F), dtype=torch.float32, device=x.device)
             L.moe_grouped_ffn_fp8_train(self.xq_sorted[:A], self.xs_sorted[:A], self.offsets, self.w.w13_q,
@@ -184,7 +239,8 @@ class MoELayerFP8:
         routing fixed (replayed): returns (dx [T, d] bf16 from the experts,
         d_gates [T, k] fp32), and with weight_grads also (dW13 [E, 2F, d],
         dW2 [E, d, F]) fp32.  The router's gradients from these d_gates are
-        router_backward's (not part of this call)."""
+        router_backward's (not part of this call).  With a norm, dx is the
+        gradient of its output (norm_backward takes it on)."""
         T = getattr(self, "_T_train", None)
         if T is None or self.mx or self.gathered:
             raise ValueError("backward needs a forward(train=True) of the fp32-scale sorted form")
@@ -200,6 +256,25 @@ class MoELayerFP8:
                             dx_sorted=e((Am, d), torch.bfloat16), dx=e((self.T_max, d), torch.bfloat16))
         b = self._bw
         w2t_q, w2t_s, w13t_q, w13t_s = self.w.transposed()
+        if self.ckpt8:
+            L.moe_combine_backward(dy, self.gates[:T], None, self.sl2[:A], d_out_q=b["d_out_q"][:A],
+                                   d_out_s=b["d_out_s"][:A], dev_status=self.dev_status)
+            L.moe_grouped_gemm_fp8(b["d_out_q"][:A], b["d_out_s"][:A], self.offsets, w2t_q, w2t_s,
+                                   out=b["d_act"][:A], dev_status=self.dev_status)
+            c = self._ckpt_buffers(weight_grads)
+            more = {}
+            if weight_grads:
+                L.moe_wgrad_pad_offsets(self.offsets, pad=c["pad"])
+                more = dict(expert_offsets=self.offsets, pad=c["pad"], ld=c["ld"], dhT=c["dhT"], actT=c["actT"])
+            L.moe_swiglu_backward_ckpt(b["d_act"][:A], self.h_q[:A], self.h_s[:A], gates=self.gates[:T],
+                                       slot_to_sorted=self.sl2[:A], dh=(b["dh_q"][:A], b["dh_s"][:A]),
+                                       d_gates=b["d_gates"][:T], workspace=c["ws"], **more)
+            L.moe_grouped_gemm_fp8(b["dh_q"][:A], b["dh_s"][:A], self.offsets, w13t_q, w13t_s,
+                                   out=b["dx_sorted"][:A], dev_status=self.dev_status)
+            dx = L.moe_dispatch_backward(b["dx_sorted"][:A], self.sl2[:A], T, self.k, dx=b["dx"][:T])
+            if not weight_grads:
+                return dx, b["d_gates"][:T]
+            return (dx, b["d_gates"][:T], *self._weight_grads_ckpt(dy, T))
         L.moe_combine_backward(dy, self.gates[:T], self.out_sorted[:A], self.sl2[:A], d_out_q=b["d_out_q"][:A],
                                d_out_s=b["d_out_s"][:A], d_gates=b["d_gates"][:T], dev_status=self.dev_status)
         L.moe_grouped_gemm_fp8(b["d_out_q"][:A], b["d_out_s"][:A], self.offsets, w2t_q, w2t_s, out=b["d_act"][:A],
@@ -211,6 +286,53 @@ class MoELayerFP8:
         if not weight_grads:
             return dx, b["d_gates"][:T]
         return (dx, b["d_gates"][:T], *self._weight_grads(dy, T))
+
+    def _ckpt_buffers(self, weight_grads: bool) -> dict:
+        """The 8-bit backward's buffers, made for every T up to T_max at the first call that needs them."""
+        A, E, d, F = self.T_max * self.k, self.w.E, self.w.d, self.w.F
+        e = lambda shape, dt: torch.empty(shape, dtype=dt, device=self.ids.device)
+        c = getattr(self, "_c8", None)
+        if c is None:
+            self._c8 = c = dict(ws=e((L.moe_swiglu_backward_ckpt_workspace_size(A, F),), torch.uint8))
+        if weight_grads and "pad" not in c:
+            ld = L.wgrad_ld(A, E)
+            op = lambda C: (e((C, ld), torch.uint8), e((ld // 128, C), torch.float32))
+            c.update(pad=e((E + 1,), torch.int32), ld=ld, dhT=op(2 * F), actT=op(F), rows=op(d),
+                     dW2=e((E, d, F), torch.float32), dW13=e((E, 2 * F, d), torch.float32))
+        return c
+
+    def _weight_grads_ckpt(self, dy: torch.Tensor, T: int):
+        """dW13, dW2 from the operands that moe_swiglu_backward_ckpt wrote."""
+        A, d, c = T * self.k, self.w.d, self._c8
+        kw = dict(sorted_to_slot=self.s2s[:A], k=self.k, q=c["rows"][0], scales=c["rows"][1])
+        L.moe_wgrad_quant(L.WGRAD_SRC_GDY, self.offsets, c["pad"], d, c["ld"], True, dy=dy, gates=self.gates[:T], **kw)
+        L.moe_wgrad_gemm(*c["rows"], *c["actT"], c["pad"], out=c["dW2"], dev_status=self.dev_status)
+        L.moe_wgrad_quant(L.WGRAD_SRC_X, self.offsets, c["pad"], d, c["ld"], True, x=self._x_train, **kw)
+        L.moe_wgrad_gemm(*c["dhT"], *c["rows"], c["pad"], out=c["dW13"], dev_status=self.dev_status)
+        return c["dW13"], c["dW2"]
+
+    def norm_backward(self, dn: torch.Tensor, dn_router: torch.Tensor | None = None, dres: torch.Tensor | None = None):
+        """Backward of the norm of the last forward(train=True): from dn [T, d]
+        bf16, the gradient of its output (as backward() returns it), with
+        dn_router [T, d] fp32 (as router_backward or router_losses return it)
+        added -> (dx [T, d] bf16 with dres [T, d] bf16, the residual's gradient,
+        added; dweight [d] fp32 or None; dbias [d] fp32 or None).  The results
+        stay the layer's buffers until the next call."""
+        T, n = getattr(self, "_T_train", None), self.norm
+        if T is None or n is None:
+            raise ValueError("norm_backward needs a layer with a norm and its forward(train=True)")
+        if getattr(self, "_nb", None) is None:
+            d = self.w.d
+            e = lambda shape, dt: torch.empty(shape, dtype=dt, device=self.ids.device)
+            self._nb = dict(dx=e((self.T_max, d), torch.bfloat16), dw=e((d,), torch.float32), db=e((d,), torch.float32),
+                            ws=e((L.moe_layer_norm_backward_workspace_size(self.T_max, d),), torch.uint8))
+        b = self._nb
+        return L.moe_layer_norm_backward(dn, self.n_rstd[:T], x=self._x_norm,
+                                         mean=self.n_mean[:T] if n.center and not self.ckpt8 else None,
+                                         ckpt=(self.xhat_q[:T], self.xhat_s[:T]) if self.ckpt8 else None, weight=n.weight,
+                                         center=n.center, dy_add=dn_router, dx_add=dres, dx=b["dx"][:T],
+                                         dweight=None if n.weight is None else b["dw"],
+                                         dbias=None if n.bias is None else b["db"], workspace=b["ws"])
 
     def router_backward(self, d_gates: torch.Tensor):
         """Gradients of the router of the last forward(train=True), its ids

@@ -11,9 +11,12 @@ payload, as the trainer of asynchronous RL does) -> head.  Each step runs
   layer.backward           the experts' gradients and those of the gates;
   layer.router_losses      dense router logits, balance and z losses with
                            per-expert counts, and the router's gradients;
+  layer.norm_backward      with --norm (an RMS norm before the layer): its
+                           gradient, the router's and the residual's joined in;
 
-and a plain SGD update of the head, the embedding and the router (the expert
-weights stay as quantised).  Run: python examples/rl_step.py
+and a plain SGD update of the head, the embedding, the router and the norm (the
+expert weights stay as quantised).  --ckpt8 keeps what the backward needs in 8
+bits.  Run: python examples/rl_step.py [--norm] [--ckpt8]
 """
 import argparse
 import os
@@ -24,20 +27,21 @@ import torch
 sys.path.insert(0, os.path.join(os.path.dirname(os.path.abspath(__file__)), ".."))
 
 from block_scaled_fp8_router_gb300 import moe_r3 as L  # noqa: E402
-from block_scaled_fp8_router_gb300.layer import MoELayerFP8, MoEWeightsFP8, quantize_weights  # noqa: E402
+from block_scaled_fp8_router_gb300.layer import MoELayerFP8, MoENorm, MoEWeightsFP8, quantize_weights  # noqa: E402
 
 
 class TinyPolicy:
     """embedding [V, d] -> MoE layer with a residual -> head [V, d], bf16."""
 
-    def __init__(self, V=4000, d=256, E=16, k=4, F=256, T_max=1024, seed=0, device="cuda"):
+    def __init__(self, V=4000, d=256, E=16, k=4, F=256, T_max=1024, seed=0, device="cuda", norm=False, ckpt8=False):
         g = torch.Generator(device=device).manual_seed(seed)
         r = lambda *s: torch.randn(*s, device=device, generator=g)
         self.emb = r(V, d).bfloat16()
         self.head = (0.05 * r(V, d)).bfloat16()
         w = MoEWeightsFP8((0.1 * r(E, d)).bfloat16(), *quantize_weights((0.06 * r(E, 2 * F, d)).bfloat16(),
                                                                         (0.06 * r(E, d, F)).bfloat16()))
-        self.layer = MoELayerFP8(w, T_max, k, L.MOE_SCORE_SIGMOID, renorm=1, route_scale=2.5)
+        n = MoENorm(torch.ones(d, device=device)) if norm else None
+        self.layer = MoELayerFP8(w, T_max, k, L.MOE_SCORE_SIGMOID, renorm=1, route_scale=2.5, norm=n, ckpt8=ckpt8)
 
     def hidden(self, tokens, replay_kT=None, capture_kT=None):
         self.x = self.emb[tokens]
@@ -80,7 +84,11 @@ def step(policy, b, lr=0.02, kl_coef=0.02, balance_coef=1e-2, z_coef=1e-4):
     dx_experts, d_gates = policy.layer.backward(dh)
     losses, counts, dx_router, dw = policy.layer.router_losses(balance_coef, z_coef, d_gates=d_gates,
                                                                token_mask=b["weights"] != 0, seq_offsets=b["offsets"])
-    dx = dh.float() + dx_experts.float() + dx_router
+    if policy.layer.norm is None:
+        dx = dh.float() + dx_experts.float() + dx_router
+    else:
+        dx, d_norm, _ = policy.layer.norm_backward(dx_experts, dx_router, dres=dh)
+        policy.layer.norm.weight.sub_(lr * d_norm)
     policy.head.sub_((lr * d_head).bfloat16())
     policy.emb.index_add_(0, b["tokens"], (-lr * dx).bfloat16())
     policy.layer.w.w_router.sub_((lr * dw).bfloat16())
@@ -90,8 +98,10 @@ def step(policy, b, lr=0.02, kl_coef=0.02, balance_coef=1e-2, z_coef=1e-4):
 def main():
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     ap.add_argument("--steps", type=int, default=8)
+    ap.add_argument("--norm", action="store_true", help="an RMS norm before the layer")
+    ap.add_argument("--ckpt8", action="store_true", help="what the backward needs, kept in 8 bits")
     a = ap.parse_args()
-    policy = TinyPolicy()
+    policy = TinyPolicy(norm=a.norm, ckpt8=a.ckpt8)
     b = rollout(policy, n_seqs=8, length=96, prompt=24)
     for i in range(a.steps):
         stats, losses, counts = step(policy, b)

@@ -170,24 +170,24 @@ __host__ __device__ constexpr int odd_pieces(int bytes) { return (bytes + 14 + 1
 template <typename T>
 __device__ __forceinline__ void copy_odd(uint32_t dst, const T *base, int64_t at, int cols, int t, int nth)
 {
-    const uintptr_t start = reinterpret_cast<uintptr_t>(base + at), end = start + (size_t)cols * sizeof(T);
-    const uintptr_t from = start & ~(uintptr_t)15;
+    const char *start = reinterpret_cast<const char *>(base + at);
+    const int shift = (int)(reinterpret_cast<uintptr_t>(start) & 15), bytes = shift + cols * (int)sizeof(T);
+    const char *from = start - shift;
     const int pieces = odd_pieces(cols * (int)sizeof(T));
-    for (int k = t; k < pieces; k += nth) {
-        const uintptr_t src = from + 16 * (uintptr_t)k;
-        if (src >= reinterpret_cast<uintptr_t>(base)) {
-            const int left = src < end ? (int)(end - src) : 0;
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + 16 * k), "l"(left ? src : from),
-                         "r"(left < 16 ? left : 16)
-                         : "memory");
-        } else {
-            for (uintptr_t a = start; a < src + 16 && a < end; a += sizeof(T)) {
-                if (sizeof(T) == 4)
-                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst + (uint32_t)(a - from)), "r"(*reinterpret_cast<const uint32_t *>(a)) : "memory");
-                else
-                    asm volatile("st.shared.b16 [%0], %1;" ::"r"(dst + (uint32_t)(a - from)), "h"(*reinterpret_cast<const uint16_t *>(a)) : "memory");
-            }
+    int k = t;
+    if (from < reinterpret_cast<const char *>(base)) {         // the first row, where the tensor starts off a boundary
+        for (int c = t; c < cols && c * (int)sizeof(T) < 16 - shift; c += nth) {
+            const uint32_t to = dst + shift + c * (int)sizeof(T);
+            if (sizeof(T) == 4) asm volatile("st.shared.b32 [%0], %1;" ::"r"(to), "r"(reinterpret_cast<const uint32_t *>(start)[c]) : "memory");
+            else asm volatile("st.shared.b16 [%0], %1;" ::"r"(to), "h"(reinterpret_cast<const uint16_t *>(start)[c]) : "memory");
         }
+        if (k == 0) k = nth;                                   // its first piece is done
+    }
+    for (; k < pieces; k += nth) {
+        const int left = bytes - 16 * k;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + 16 * k), "l"(left > 0 ? from + 16 * k : from + 16),
+                     "r"(left > 0 ? (left < 16 ? left : 16) : 0)
+                     : "memory");
     }
 }
 

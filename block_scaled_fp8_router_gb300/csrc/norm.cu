@@ -432,9 +432,9 @@ __global__ void __launch_bounds__(EPT == 8 ? 1024 : 512, EPT == 16 ? 2 : 1) norm
         }
         const float mu = sum * inv_n;
         uint64_t s2 = 0, q2 = 0;
+        if (p.center) {
 #pragma unroll
-        for (int i = 0; i < N; i++) {
-            if (p.center) {
+            for (int i = 0; i < N; i++) {
                 // absent columns stay 0
                 const float m0 = in(i) ? -mu : 0.0f, m1 = VEC > 1 ? m0 : in2(i) ? -mu : 0.0f;
                 const uint64_t m = pack2(m0, m1);
@@ -444,6 +444,9 @@ __global__ void __launch_bounds__(EPT == 8 ? 1024 : 512, EPT == 16 ? 2 : 1) norm
                     s2 = add2(s2, v[i][j]);
                 }
             }
+        }
+#pragma unroll
+        for (int i = 0; i < N; i++) {
 #pragma unroll
             for (int j = 0; j < H; j++) q2 = fma2(v[i][j], v[i][j], q2);
         }
@@ -468,10 +471,18 @@ __global__ void __launch_bounds__(EPT == 8 ? 1024 : 512, EPT == 16 ? 2 : 1) norm
             if (p.rstd) p.rstd[row] = rstd;
         }
         const uint64_t r2 = pack2(rstd, rstd), c2 = pack2(-rest * rstd, -rest * rstd);
+        if (p.center) {
 #pragma unroll
-        for (int i = 0; i < N; i++) {
+            for (int i = 0; i < N; i++) {
 #pragma unroll
-            for (int j = 0; j < H; j++) v[i][j] = p.center ? fma2(v[i][j], r2, c2) : mul2(v[i][j], r2);
+                for (int j = 0; j < H; j++) v[i][j] = fma2(v[i][j], r2, c2);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; i++) {
+#pragma unroll
+                for (int j = 0; j < H; j++) v[i][j] = mul2(v[i][j], r2);
+            }
         }
         T *y = static_cast<T *>(p.y) + row * p.ld_y + c;
         if constexpr (VEC > 1) {
@@ -574,13 +585,14 @@ __device__ __forceinline__ void decode(const uint8_t *q, float s, uint64_t (&v)[
 // vectors copied asynchronously by the thread that reads them, rows without
 // as the pieces they lie in (and a barrier).  With KEEP a thread holds g and xhat of
 // its columns from the row's means to dx; without (rows too long for that
-// beside the sums) it reads them again.  At the end the groups' sums are
+// beside the sums) it reads them again.  FULL: with the rows' means and the sums
+// of db; else the RMS form without.  At the end the groups' sums are
 // joined in group order through shared memory and leave as this CTA's part;
 // reduce_kernel adds the parts in CTA order (no atomics: the same bits every
 // time).
 constexpr int BWD_THREADS = 512;                       // at up to 128 registers
 
-template <typename T, int VEC, int EPT, bool CKPT, bool BIAS>
+template <typename T, int VEC, int EPT, bool CKPT, bool FULL>
 __global__ void __launch_bounds__(BWD_THREADS, 1) dnorm_kernel(Bwd p)
 {
     // vectors, or pairs of single values 32 columns apart
@@ -654,7 +666,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) dnorm_kernel(Bwd p)
         } else {
             pairs<T, VEC>(x + i * STEP, true, h);
 #pragma unroll
-            for (int j = 0; j < H; j++) h[j] = mul2(add2(h[j], nmu2), rs2);
+            for (int j = 0; j < H; j++) h[j] = mul2(FULL ? add2(h[j], nmu2) : h[j], rs2);
         }
         if (p.at_dya >= 0) {
             if constexpr (VEC > 1) {
@@ -677,13 +689,13 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) dnorm_kernel(Bwd p)
     };
     const auto weights = [&](int i, uint64_t (&w)[H]) { staged_weight<VEC>(sw, c + i * STEP, p.wide, w); };
 
-    uint64_t dw[N][H] = {}, db[BIAS ? N : 1][H] = {};
+    uint64_t dw[N][H] = {}, db[FULL ? N : 1][H] = {};
     if (VEC == 1 || p.wide != p.cols) clear(ring + p.weight_bytes, p.groups * p.stages * p.stage_bytes);
     for (int s = 0; s < p.stages; s++) issue((int64_t)first + (int64_t)s * step, s);
     stage_weight<VEC>(sw, p.w, p.w_f32, p.cols, p.wide, 1.0f);
     __syncthreads();
     float rs_next = 0.0f, mu_next = 0.0f;              // the next row's, loaded a row ahead
-    const bool mean = p.center && !CKPT;
+    const bool mean = FULL && !CKPT && p.center;
     if (first < p.rows) {
         rs_next = __ldg(p.rstd + first);
         if (mean) mu_next = __ldg(p.mean + first);
@@ -725,10 +737,10 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) dnorm_kernel(Bwd p)
 #pragma unroll
             for (int j = 0; j < H; j++) {
                 gi[j] = mul2(a[j], w[j]);
-                s1 = add2(s1, gi[j]);
+                if (FULL) s1 = add2(s1, gi[j]);
                 s2 = fma2(gi[j], hi[j], s2);
                 dw[i][j] = fma2(a[j], hi[j], dw[i][j]);
-                if (BIAS) db[i][j] = add2(db[i][j], a[j]);
+                if (FULL) db[i][j] = add2(db[i][j], a[j]);
             }
         }
         if (KEEP && VEC > 1) {
@@ -742,8 +754,8 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) dnorm_kernel(Bwd p)
             unpack2(s2, lo, up);
             m2 = lo + up;
             // the buffer alternates by row: a warp a row ahead writes the other one
-            row_sums(m2, m1, p.center, red[par], group * p.warps, p.warps, gw, lane, group + 1);
-            m1 = p.center ? m1 * inv_n : 0.0f, m2 *= inv_n;
+            row_sums(m2, m1, FULL, red[par], group * p.warps, p.warps, gw, lane, group + 1);
+            m1 = FULL && p.center ? m1 * inv_n : 0.0f, m2 *= inv_n;
             const uint64_t nm1 = pack2(-m1, -m1), nm2 = pack2(-m2, -m2);
             T *dx = static_cast<T *>(p.dx) + row * p.ld_dx + c;
 #pragma unroll
@@ -770,7 +782,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) dnorm_kernel(Bwd p)
                 }
 #pragma unroll
                 for (int j = 0; j < H; j++)
-                    unpack2(fma2(fma2(hi[j], nm2, add2(gi[j], nm1)), rs2, pack2(d[2 * j], d[2 * j + 1])), f[2 * j], f[2 * j + 1]);
+                    unpack2(fma2(fma2(hi[j], nm2, FULL ? add2(gi[j], nm1) : gi[j]), rs2, pack2(d[2 * j], d[2 * j + 1])), f[2 * j], f[2 * j + 1]);
                 if constexpr (VEC > 1) {
                     if (in(i)) store<T, VEC>(dx + i * STEP, f);
                 } else {
@@ -801,14 +813,14 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) dnorm_kernel(Bwd p)
 #pragma unroll
             for (int j = 0; j < H; j++) {
                 unpack2(dw[i][j], w[2 * j], w[2 * j + 1]);
-                if (BIAS) unpack2(db[i][j], b[2 * j], b[2 * j + 1]);
+                if (FULL) unpack2(db[i][j], b[2 * j], b[2 * j + 1]);
             }
 #pragma unroll
             for (int j = 0; j < (VEC > 1 ? VEC : 2); j++) {
                 if (VEC == 1 && j && !in2(i)) continue;
                 const int k = c + i * STEP + (VEC > 1 ? j : 32 * j);
                 to[k] = gr ? joined[k] + w[j] : w[j];
-                if (BIAS) to[p.cols + k] = gr ? joined[p.cols + k] + b[j] : b[j];
+                if (FULL) to[p.cols + k] = gr ? joined[p.cols + k] + b[j] : b[j];
             }
         }
     }
@@ -911,20 +923,20 @@ static cudaError_t fwd_plan(Fwd &p, cudaStream_t st)
     return ept == 16 ? fwd_launch<T, VEC, 16, true>(p, grid, smem, st) : fwd_launch<T, VEC, 32, true>(p, grid, smem, st);
 }
 
-template <typename T, int VEC, int EPT, bool CKPT, bool BIAS>
+template <typename T, int VEC, int EPT, bool CKPT, bool FULL>
 static cudaError_t bwd_launch(const Bwd &p, int grid, int smem, cudaStream_t st)
 {
     static std::atomic<uint64_t> done{0};
-    const cudaError_t e = allow_smem(reinterpret_cast<const void *>(dnorm_kernel<T, VEC, EPT, CKPT, BIAS>), SMEM_MAX, done);
+    const cudaError_t e = allow_smem(reinterpret_cast<const void *>(dnorm_kernel<T, VEC, EPT, CKPT, FULL>), SMEM_MAX, done);
     if (e != cudaSuccess) return e;
-    dnorm_kernel<T, VEC, EPT, CKPT, BIAS><<<grid, p.warps * p.groups * 32, smem, st>>>(p);
+    dnorm_kernel<T, VEC, EPT, CKPT, FULL><<<grid, p.warps * p.groups * 32, smem, st>>>(p);
     return cudaGetLastError();
 }
 
 template <typename T, int VEC, int EPT, bool CKPT>
 static cudaError_t bwd_launch_bias(const Bwd &p, int grid, int smem, cudaStream_t st)
 {
-    return p.want_b ? bwd_launch<T, VEC, EPT, CKPT, true>(p, grid, smem, st) : bwd_launch<T, VEC, EPT, CKPT, false>(p, grid, smem, st);
+    return p.want_b || p.center ? bwd_launch<T, VEC, EPT, CKPT, true>(p, grid, smem, st) : bwd_launch<T, VEC, EPT, CKPT, false>(p, grid, smem, st);
 }
 
 template <typename T, int VEC>

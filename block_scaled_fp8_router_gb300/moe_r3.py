@@ -119,6 +119,8 @@ def _stream(stream) -> int:
 
 
 def _want(t: torch.Tensor, dtype, shape, name: str) -> None:
+    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+        return
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.shape != shape and tuple(t.shape) != tuple(shape):
@@ -952,54 +954,57 @@ def moe_router_backward_dense(x, w_router, d_logits, dx=True, dw_router=True, wo
 MOE_TYPE_BF16, MOE_TYPE_F32 = 0, 1
 
 
+# The calls below check what they are given and trust what they allocate: at
+# their smallest sizes a call is the host's time.
+
 def _pair(v, q_shape, s_shape, name, like):
     """(codes, scales) of an optional output: True allocates, a pair of tensors
-    is written, False / None skips."""
+    is written, False / None skips -> the pair and its addresses."""
     if v is None or v is False:
-        return None
+        return None, None, None
     if v is True:
-        return _empty(q_shape, torch.uint8, like), _empty(s_shape, torch.float32, like)
-    q, s = v
-    _want(q, torch.uint8, q_shape, name + " codes")
-    _want(s, torch.float32, s_shape, name + " scales")
-    return q, s
+        v = (_empty(q_shape, torch.uint8, like), _empty(s_shape, torch.float32, like))
+    else:
+        q, s = v
+        _want(q, torch.uint8, q_shape, name + " codes")
+        _want(s, torch.float32, s_shape, name + " scales")
+        _one_device(like, q, s)
+    return v, v[0].data_ptr(), v[1].data_ptr()
 
 
 def _vector(v, n, name, like):
-    """An optional fp32 output [n]: True allocates, a tensor is written, False / None skips."""
+    """An optional fp32 output [n]: True allocates, a tensor is written, False / None skips -> it and its address."""
     if v is None or v is False:
-        return None
+        return None, None
     if v is True:
-        return _empty((n,), torch.float32, like)
-    _want(v, torch.float32, (n,), name)
-    return v
+        v = _empty((n,), torch.float32, like)
+    else:
+        _want(v, torch.float32, (n,), name)
+        _one_device(like, v)
+    return v, v.data_ptr()
 
 
-def _half(pair, i):
-    return None if pair is None else pair[i].data_ptr()
-
-
-def _weights(weight, bias, cols, like) -> int:
+def _weights(weight, bias, cols) -> int:
     """The type code of a norm's weight and bias (one type, [cols])."""
     dt = None
     for t, name in ((weight, "weight"), (bias, "bias")):
         if t is None:
             continue
-        if t.dtype not in (torch.bfloat16, torch.float32) or dt not in (None, t.dtype):
+        if dt is not None and t.dtype != dt or t.dtype not in (torch.bfloat16, torch.float32):
             raise TypeError(f"{name}: expected torch.bfloat16 or torch.float32, the same for weight and bias, got {t.dtype}")
         dt = t.dtype
         _want(t, dt, (cols,), name)
-    return MOE_TYPE_F32 if dt == torch.float32 else MOE_TYPE_BF16
+    return MOE_TYPE_F32 if dt is torch.float32 else MOE_TYPE_BF16
 
 
 def _one_device(like, *tensors) -> None:
     """Every tensor on like's device, and that the current one (the launches go there)."""
-    dev = like.get_device()
+    dev = torch._C._cuda_getDevice()
+    if like.get_device() != dev:
+        raise ValueError(f"the tensors are on {like.device}, which is not the current device")
     for t in tensors:
         if t is not None and t.get_device() != dev:
             raise ValueError(f"expected every tensor on {like.device}, got one on {t.device}")
-    if dev != torch._C._cuda_getDevice():
-        raise ValueError(f"the tensors are on {like.device}, which is not the current device")
 
 
 def moe_layer_norm(x, weight=None, bias=None, eps=1e-5, center=True, y=None, mean=None, rstd=None, codes=None,
@@ -1011,17 +1016,19 @@ def moe_layer_norm(x, weight=None, bias=None, eps=1e-5, center=True, y=None, mea
     written, False / None skips.  y may be x."""
     dt, ld = _logit_rows(x, "x")
     rows, cols = x.shape
-    w_dt = _weights(weight, bias, cols, x)
+    w_dt = MOE_TYPE_BF16 if weight is None and bias is None else _weights(weight, bias, cols)
     if y is None:
-        y = _empty((rows, cols), x.dtype, x)
-    _, ld_y = _logit_rows(y, "y", like=x)
-    mean, rstd = _vector(mean, rows, "mean", x), _vector(rstd, rows, "rstd", x)
-    codes = _pair(codes, (rows, cols), (rows, cols // 128), "codes", x)
-    ckpt = _pair(ckpt, (rows, cols), (rows, cols // 128), "ckpt", x)
-    _one_device(x, weight, bias, y, mean, rstd, *(codes or ()), *(ckpt or ()))
+        y, ld_y = _empty((rows, cols), x.dtype, x), cols
+    else:
+        _, ld_y = _logit_rows(y, "y", like=x)
+    _one_device(x, weight, bias, y)
+    mean, p_mean = _vector(mean, rows, "mean", x)
+    rstd, p_rstd = _vector(rstd, rows, "rstd", x)
+    codes, p_q, p_s = _pair(codes, (rows, cols), (rows, cols // 128), "codes", x)
+    ckpt, p_hq, p_hs = _pair(ckpt, (rows, cols), (rows, cols // 128), "ckpt", x)
     _check("moe_layer_norm", _lib.moe_layer_norm(
-        _ptr(x), dt, rows, cols, ld, _ptr(weight), _ptr(bias), w_dt, eps, int(center), _ptr(y), ld_y, _ptr(mean),
-        _ptr(rstd), _half(codes, 0), _half(codes, 1), _half(ckpt, 0), _half(ckpt, 1), _stream(stream)))
+        x.data_ptr(), dt, rows, cols, ld, _ptr(weight), _ptr(bias), w_dt, eps, 1 if center else 0, y.data_ptr(), ld_y,
+        p_mean, p_rstd, p_q, p_s, p_hq, p_hs, _stream(stream)))
     return y, mean, rstd, codes, ckpt
 
 
@@ -1042,36 +1049,41 @@ def moe_layer_norm_backward(dy, rstd, x=None, mean=None, ckpt=None, weight=None,
     if (x is None) == (ckpt is None):
         raise ValueError("one of x and ckpt")
     ld_x = ld_add = ld_dx = cols
+    p_mean = p_hq = p_hs = None
     if x is not None:
         _, ld_x = _logit_rows(x, "x", like=dy)
         if center:
             if mean is None:
                 raise ValueError("mean: needed with x and center")
             _want(mean, torch.float32, (rows,), "mean")
+            p_mean = mean.data_ptr()
     else:
-        ckpt = _pair(ckpt, (rows, cols), (rows, cols // 128), "ckpt", dy)
         mean = None
-    w_dt = _weights(weight, None, cols, dy)
+        _, p_hq, p_hs = _pair(ckpt, (rows, cols), (rows, cols // 128), "ckpt", dy)
+    w_dt = MOE_TYPE_BF16 if weight is None else _weights(weight, None, cols)
     if dy_add is not None:
         _want(dy_add, torch.float32, (rows, cols), "dy_add")
     if dx is True:
         dx = _empty((rows, cols), dy.dtype, dy)
     elif dx is False:
         dx = None
-    if dx is not None:
+    elif dx is not None:
         _, ld_dx = _logit_rows(dx, "dx", like=dy)
     if dx_add is not None:
         if dx is None:
             raise ValueError("dx_add needs dx")
         _, ld_add = _logit_rows(dx_add, "dx_add", like=dy)
-    dweight, dbias = _vector(dweight, cols, "dweight", dy), _vector(dbias, cols, "dbias", dy)
-    if workspace is None and (dweight is not None or dbias is not None):
-        workspace = _workspace(moe_layer_norm_backward_workspace_size(rows, cols), dy, stream)
-    _one_device(dy, rstd, x, mean, *(ckpt or ()), weight, dy_add, dx_add, dx, dweight, dbias, workspace)
+    _one_device(dy, rstd, x, mean, weight, dy_add, dx_add, dx, workspace)
+    dweight, p_dw = _vector(dweight, cols, "dweight", dy)
+    dbias, p_db = _vector(dbias, cols, "dbias", dy)
+    p_ws, n_ws = None, 0
+    if p_dw is not None or p_db is not None:
+        if workspace is None:
+            workspace = _workspace(moe_layer_norm_backward_workspace_size(rows, cols), dy, stream)
+        p_ws, n_ws = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     _check("moe_layer_norm_backward", _lib.moe_layer_norm_backward(
-        _ptr(dy), dt, rows, cols, ld, _ptr(dy_add), _ptr(x), ld_x, _half(ckpt, 0), _half(ckpt, 1), _ptr(weight), w_dt,
-        _ptr(mean if center else None), _ptr(rstd), int(center), _ptr(dx_add), ld_add, _ptr(dx), ld_dx, _ptr(dweight),
-        _ptr(dbias), _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(),
+        dy.data_ptr(), dt, rows, cols, ld, _ptr(dy_add), _ptr(x), ld_x, p_hq, p_hs, _ptr(weight), w_dt, p_mean,
+        rstd.data_ptr(), 1 if center else 0, _ptr(dx_add), ld_add, _ptr(dx), ld_dx, p_dw, p_db, p_ws, n_ws,
         _stream(stream)))
     return dx, dweight, dbias
 
@@ -1126,8 +1138,9 @@ def moe_swiglu_backward_ckpt(d_act, h_q, h_s, gates=None, slot_to_sorted=None, e
     _want(d_act, torch.bfloat16, (rows, F), "d_act")
     _want(h_q, torch.uint8, (rows, 2 * F), "h_q")
     _want(h_s, torch.float32, (rows, 2 * F // 128), "h_s")
-    dh = _pair(dh, (rows, 2 * F), (rows, 2 * F // 128), "dh", d_act)
-    slots = 0
+    slots = E = n_ws = 0
+    p_g = p_sl = p_dg = p_off = p_pad = p_ws = None
+    dh, p_q, p_s = _pair(dh, (rows, 2 * F), (rows, 2 * F // 128), "dh", d_act)
     if d_gates is False:
         d_gates = None
     if d_gates is not None:
@@ -1138,25 +1151,27 @@ def moe_swiglu_backward_ckpt(d_act, h_q, h_s, gates=None, slot_to_sorted=None, e
         _want(slot_to_sorted, torch.int32, (slots,), "slot_to_sorted")
         if d_gates is True:
             d_gates = _empty(gates.shape, torch.float32, d_act)
-        _want(d_gates, torch.float32, gates.shape, "d_gates")
-        if workspace is None and slots:
+        else:
+            _want(d_gates, torch.float32, gates.shape, "d_gates")
+        if workspace is None:
             workspace = _workspace(moe_swiglu_backward_ckpt_workspace_size(rows, F), d_act, stream)
-    E = 0
-    dhT = _pair(dhT, (2 * F, ld), (ld // 128, 2 * F), "dhT", d_act)
-    actT = _pair(actT, (F, ld), (ld // 128, F), "actT", d_act)
+        _one_device(d_act, gates, slot_to_sorted, d_gates, workspace)
+        p_g, p_sl, p_dg, p_ws = gates.data_ptr(), slot_to_sorted.data_ptr(), d_gates.data_ptr(), workspace.data_ptr()
+        n_ws = workspace.numel() * workspace.element_size()
+    dhT, p_tq, p_ts = _pair(dhT, (2 * F, ld), (ld // 128, 2 * F), "dhT", d_act)
+    actT, p_aq, p_as = _pair(actT, (F, ld), (ld // 128, F), "actT", d_act)
     if dhT is not None or actT is not None:
         if expert_offsets is None or pad is None:
             raise ValueError("dhT and actT need expert_offsets and pad")
         E = expert_offsets.numel() - 1
         _want(expert_offsets, torch.int32, (E + 1,), "expert_offsets")
         _want(pad, torch.int32, (E + 1,), "pad")
-    _one_device(d_act, h_q, h_s, *(dh or ()), gates, slot_to_sorted, d_gates, expert_offsets, pad, *(dhT or ()),
-                 *(actT or ()), workspace)
+        _one_device(d_act, expert_offsets, pad)
+        p_off, p_pad = expert_offsets.data_ptr(), pad.data_ptr()
+    _one_device(d_act, h_q, h_s)
     _check("moe_swiglu_backward_ckpt", _lib.moe_swiglu_backward_ckpt(
-        _ptr(d_act), _ptr(h_q), _ptr(h_s), rows, F, _ptr(gates), _ptr(slot_to_sorted), slots, _half(dh, 0),
-        _half(dh, 1), _ptr(d_gates), _ptr(expert_offsets), _ptr(pad), E, ld, _half(dhT, 0), _half(dhT, 1),
-        _half(actT, 0), _half(actT, 1), _ptr(workspace),
-        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream)))
+        d_act.data_ptr(), h_q.data_ptr(), h_s.data_ptr(), rows, F, p_g, p_sl, slots, p_q, p_s, p_dg, p_off, p_pad, E, ld,
+        p_tq, p_ts, p_aq, p_as, p_ws, n_ws, _stream(stream)))
     return dh, d_gates, dhT, actT
 
 

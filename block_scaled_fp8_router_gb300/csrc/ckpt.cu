@@ -36,18 +36,6 @@ constexpr int RW = TILE / WARPS;
 constexpr int THREADS = WARPS * 32;
 constexpr int MAX_E = 1024;
 
-// four codes (value 0 in the low byte) to fp32
-__device__ __forceinline__ void decode4(uint32_t q, float (&f)[4])
-{
-#pragma unroll
-    for (int i = 0; i < 2; i++) {
-        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(q >> (16 * i)), __NV_E4M3);
-        const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&h));
-        f[2 * i] = v.x;
-        f[2 * i + 1] = v.y;
-    }
-}
-
 // One row's four columns: a (bf16), gate and up codes -> d_gate, d_up, act,
 // two columns in each 64-bit pair, and a act summed into dot.  Products with
 // the row's scales and sums with constants are scalar (a packed operand
@@ -58,8 +46,8 @@ __device__ __forceinline__ void swiglu4(uint2 a, uint32_t gq, uint32_t uq, float
                                         uint64_t (&du)[2], uint64_t (&act)[2], uint64_t &dot)
 {
     float g_[4], u_[4];
-    decode4(gq, g_);
-    decode4(uq, u_);
+    e4m3x4_unpack(gq, g_);
+    e4m3x4_unpack(uq, u_);
     const uint32_t aw[2] = {a.x, a.y};
     dot = 0;
     const uint64_t gs2 = pack2(-gs, -gs), us2 = pack2(us, us);
@@ -97,7 +85,7 @@ __device__ __forceinline__ uint32_t encode4(const uint64_t (&v)[2], float y)
     float a, b, c, d;
     unpack2(v[0], a, b);
     unpack2(v[1], c, d);
-    return (uint32_t)pack_e4m3x2(a * y, b * y) | ((uint32_t)pack_e4m3x2(c * y, d * y) << 16);
+    return e4m3x4_pack(a * y, b * y, c * y, d * y);
 }
 
 // eight sums of a warp's lanes, sum i left in every lane with lane / 4 = i:
@@ -354,8 +342,8 @@ __global__ void __launch_bounds__(THREADS, 1) swiglu_ckpt_kernel(Args p)
                         float a[4], b[4];
 #pragma unroll
                         for (int r = 0; r < 4; r++) unpack2(mul2(v[k][i + r][j], y[j]), a[r], b[r]);
-                        lo[i / 4] = (uint32_t)pack_e4m3x2(a[0], a[1]) | ((uint32_t)pack_e4m3x2(a[2], a[3]) << 16);
-                        hi[i / 4] = (uint32_t)pack_e4m3x2(b[0], b[1]) | ((uint32_t)pack_e4m3x2(b[2], b[3]) << 16);
+                        lo[i / 4] = e4m3x4_pack(a[0], a[1], a[2], a[3]);
+                        hi[i / 4] = e4m3x4_pack(b[0], b[1], b[2], b[3]);
                     }
                     uint2 *dst = reinterpret_cast<uint2 *>(codes + (k * TILE + c0 + 2 * j) * TILE) + (warp ^ (lane & 15));
                     dst[0] = make_uint2(lo[0], lo[1]);

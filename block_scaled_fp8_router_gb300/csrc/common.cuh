@@ -73,6 +73,31 @@ __device__ __forceinline__ uint16_t pack_e4m3x2(float lo, float hi)
     return (uint16_t)__nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
 }
 
+// four floats -> four E4M3 codes (nearest even, saturating), `a` in the low byte
+__device__ __forceinline__ uint32_t e4m3x4_pack(float a, float b, float c, float d)
+{
+    uint32_t q;
+    asm("{\n\t.reg .b16 l, h;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n\t"
+        "mov.b32 %0, {l, h};\n\t}"
+        : "=r"(q)
+        : "f"(a), "f"(b), "f"(c), "f"(d));
+    return q;
+}
+
+// four E4M3 codes -> four floats, exact (the low byte first)
+__device__ __forceinline__ void e4m3x4_unpack(uint32_t q, float (&f)[4])
+{
+    asm("{\n\t.reg .b16 l, h, w, x, y, z;\n\t.reg .b32 u, v;\n\t"
+        "mov.b32 {l, h}, %4;\n\t"
+        "cvt.rn.f16x2.e4m3x2 u, l;\n\tcvt.rn.f16x2.e4m3x2 v, h;\n\t"
+        "mov.b32 {w, x}, u;\n\tmov.b32 {y, z}, v;\n\t"
+        "cvt.f32.f16 %0, w;\n\tcvt.f32.f16 %1, x;\n\tcvt.f32.f16 %2, y;\n\tcvt.f32.f16 %3, z;\n\t}"
+        : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3])
+        : "r"(q));
+}
+
 // block scale of the DeepSeek-V3 recipe: amax / 448 (IEEE division), 1 when
 // 0.  For 2^-100 <= amax <= 2^127 the quotient comes from the constant
 // RN(1/448) and one fused correction step q + RN(amax - 448 q) / 448 (the

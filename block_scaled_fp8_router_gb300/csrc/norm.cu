@@ -342,7 +342,7 @@ __device__ __forceinline__ void encode(const uint64_t (&v)[VPT][VEC / 2], int c,
             float a, b, e, f;
             unpack2(v[i][2 * k], a, b);
             unpack2(v[i][2 * k + 1], e, f);
-            w[k] = (uint32_t)pack_e4m3x2(a * yi, b * yi) | ((uint32_t)pack_e4m3x2(e * yi, f * yi) << 16);
+            w[k] = e4m3x4_pack(a * yi, b * yi, e * yi, f * yi);
         }
         if constexpr (VEC == 8) *reinterpret_cast<uint2 *>(q + c + i * 32 * VEC) = make_uint2(w[0], w[1]);
         else *reinterpret_cast<uint32_t *>(q + c + i * 32 * VEC) = w[0];
@@ -572,10 +572,11 @@ __device__ __forceinline__ void decode(const uint8_t *q, float s, uint64_t (&v)[
     }
     const uint64_t s2 = pack2(s, s);
 #pragma unroll
-    for (int i = 0; i < VEC / 2; i++) {
-        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[i / 2] >> (16 * (i & 1))), __NV_E4M3);
-        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
-        v[i] = mul2(pack2(f.x, f.y), s2);
+    for (int i = 0; i < VEC / 4; i++) {
+        float f[4];
+        e4m3x4_unpack(w[i], f);
+        v[2 * i] = mul2(pack2(f[0], f[1]), s2);
+        v[2 * i + 1] = mul2(pack2(f[2], f[3]), s2);
     }
 }
 

@@ -211,13 +211,12 @@ __device__ __forceinline__ void pairs(const T *p, bool second, uint64_t (&v)[(VE
     }
 }
 
-// Zeros, once, in shared memory behind the columns of a row: a thread whose
-// columns lie there reads them and needs no question (its stores do).
-__device__ __forceinline__ void clear(uint8_t *p, int bytes)
+// Zeros in shared memory behind the columns of a row (bytes from..to, both
+// multiples of 4), once: a thread whose columns lie there reads them and needs
+// no question (its stores do).  No row's copy writes there.
+__device__ __forceinline__ void clear(uint8_t *p, int from, int to)
 {
-    for (int b = 16 * (int)threadIdx.x; b < bytes; b += 16 * (int)blockDim.x)
-        *reinterpret_cast<uint4 *>(p + b) = make_uint4(0u, 0u, 0u, 0u);
-    __syncthreads();
+    for (int b = from + 4 * (int)threadIdx.x; b < to; b += 4 * (int)blockDim.x) *reinterpret_cast<uint32_t *>(p + b) = 0u;
 }
 
 // A weight in fp32 in shared memory (`none` where there is none), for a CTA
@@ -391,8 +390,10 @@ __global__ void __launch_bounds__(EPT == 8 ? 1024 : 512, EPT == 16 ? 2 : 1) norm
     };
     int stage = 0, par = 0;
     if constexpr (RING) {
-        if (VEC == 1 || p.wide != p.cols) clear(ring + p.weight_bytes, p.groups * p.stages * p.stage_bytes);
         for (int s = 0; s < p.stages; s++) issue(first + s * step, s);
+        for (int s = 0; s < p.groups * p.stages; s++)
+            clear(ring + p.weight_bytes + s * p.stage_bytes,
+                  VEC == 1 ? 16 * odd_pieces(p.cols * (int)sizeof(T)) : p.cols * (int)sizeof(T), p.stage_bytes);
         stage_weight<VEC>(sw, p.w, p.w_f32, p.cols, p.wide, 1.0f);
         if (p.b) stage_weight<VEC>(sb, p.b, p.w_f32, p.cols, p.wide, 0.0f);
         __syncthreads();
@@ -691,8 +692,20 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) dnorm_kernel(Bwd p)
     const auto weights = [&](int i, uint64_t (&w)[H]) { staged_weight<VEC>(sw, c + i * STEP, p.wide, w); };
 
     uint64_t dw[N][H] = {}, db[FULL ? N : 1][H] = {};
-    if (VEC == 1 || p.wide != p.cols) clear(ring + p.weight_bytes, p.groups * p.stages * p.stage_bytes);
     for (int s = 0; s < p.stages; s++) issue((int64_t)first + (int64_t)s * step, s);
+    if (VEC == 1 || p.wide != p.cols) {
+        const int row = VEC == 1 ? 16 * odd_pieces(p.cols * (int)sizeof(T)) : p.cols * (int)sizeof(T);
+        for (int s = 0; s < p.groups * p.stages; s++) {
+            uint8_t *st = ring + p.weight_bytes + s * p.stage_bytes;
+            clear(st, row, p.at_x);
+            clear(st, p.at_x + (CKPT ? p.cols : row), p.at_s);
+            if (CKPT) clear(st, p.at_s + p.cols / 32, p.at_s + p.wide / 32);
+            if (p.at_dya >= 0) {                       // of eights two halves
+                clear(st, p.at_dya + p.cols * (VEC == 8 ? 2 : 4), p.at_dya + p.wide * (VEC == 8 ? 2 : 4));
+                if (VEC == 8) clear(st, p.at_dya + half + p.cols * 2, p.at_dya + half + p.wide * 2);
+            }
+        }
+    }
     stage_weight<VEC>(sw, p.w, p.w_f32, p.cols, p.wide, 1.0f);
     __syncthreads();
     float rs_next = 0.0f, mu_next = 0.0f;              // the next row's, loaded a row ahead
@@ -1076,9 +1089,7 @@ MOE_API moe_status moe_layer_norm_backward(const void *dy, int dtype, int64_t ro
     const cudaError_t e = f32 ? (vec ? bwd_launch_for<float, 4>(p, ept, grid, smem, st) : bwd_launch_for<float, 1>(p, ept, grid, smem, st))
                               : (vec ? bwd_launch_for<uint16_t, 8>(p, ept, grid, smem, st) : bwd_launch_for<uint16_t, 1>(p, ept, grid, smem, st));
     if (e != cudaSuccess) return MOE_ERR_CUDA;
-    if (sums) {
-        reduce_kernel<<<dim3((unsigned)((cols + 31) / 32), 2), 256, 0, st>>>(p.part, grid, (int)cols, dweight, dbias);
-        return launch_status();
-    }
-    return MOE_OK;
+    if (!sums) return MOE_OK;
+    reduce_kernel<<<dim3((unsigned)((cols + 31) / 32), 2), 256, 0, st>>>(p.part, grid, (int)cols, dweight, dbias);
+    return launch_status();
 }

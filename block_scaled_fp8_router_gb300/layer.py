@@ -173,7 +173,9 @@ class MoELayerFP8:
                 capture_kT: torch.Tensor | None = None, y: torch.Tensor | None = None,
                 train: bool = False) -> torch.Tensor:
         """train=True also keeps GEMM1's pre-activations for backward() (in 8
-        bits with ckpt8)."""
+        bits with ckpt8).  x [T, d] bf16; with a norm its rows may have a
+        stride of whole 16-byte vectors, and without ckpt8 they stay as they are
+        until norm_backward."""
         T = x.shape[0]
         if T > self.T_max:
             raise ValueError(f"T={T} exceeds T_max={self.T_max}")

@@ -122,6 +122,30 @@ def test_norm_in_front(L, norm, ckpt8):
     del keep
 
 
+def test_norm_before_the_other_forms(L):
+    """The gathered form takes the same codes (the sorted form's bits); the power-of-two form quantises the normalised rows."""
+    from block_scaled_fp8_router_gb300.layer import MoELayerFP8, MoEWeightsFP8, quantize_weights
+    lay, g = make(norm="ln")
+    gat, _ = make(norm="ln", gathered=True)
+    x = (2 * torch.randn(150, 256, device=DEV, generator=g)).bfloat16()
+    assert torch.equal(lay.forward(x), gat.forward(x))
+    r = lambda *s: torch.randn(*s, device=DEV, generator=g)
+    w = MoEWeightsFP8((0.1 * r(8, 256)).bfloat16(), *quantize_weights((0.06 * r(8, 256, 256)).bfloat16(),
+                                                                      (0.06 * r(8, 256, 128)).bfloat16(), ue8m0=True))
+    mx = MoELayerFP8(w, 150, 2, 1, norm=lay.norm)
+    y = mx.forward(x).clone()
+    assert torch.equal(y, MoELayerFP8(w, 150, 2, 1).forward(mx.xn[:150].contiguous()))
+    # rows of a wider buffer, and the layer with fewer rows than it was made for
+    for ld in (300, 304):
+        wide = torch.zeros(37, ld, dtype=torch.bfloat16, device=DEV)
+        wide[:, :256] = x[:37]
+        if ld % 8:                                        # the codes need rows of whole 16-byte vectors: refused
+            with pytest.raises(L.MoEError):
+                lay.forward(wide[:, :256])
+        else:
+            assert torch.equal(lay.forward(wide[:, :256]).clone(), lay.forward(x[:37].contiguous()))
+
+
 def test_step_in_a_graph(L):
     """Forward, backward with weight gradients, router losses and the norm's
     backward captured once, replayed on other batches, and run eagerly in between."""

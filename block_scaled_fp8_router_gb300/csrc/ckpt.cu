@@ -37,28 +37,27 @@ constexpr int THREADS = WARPS * 32;
 constexpr int MAX_E = 1024;
 
 // One row's four columns: a (bf16), gate and up codes -> d_gate, d_up, act,
-// two columns in each 64-bit pair, and a act summed into dot.  Products with
-// the row's scales and sums with constants are scalar (a packed operand
-// would have to be doubled first), the rest packed.  It is -sg that the
-// reciprocal gives: silu p = (-g)(-sg), and p - p sg comes out of one fused
-// multiply-add, exact where sg is next to 1.
+// two columns in each 64-bit pair, and a act summed into dot.  g below is
+// minus the gate, and the reciprocal gives -sg, so that silu p = (-g)(-sg)
+// takes no sign, and p - p sg comes out of one fused multiply-add, exact where
+// sg is next to 1.
 __device__ __forceinline__ void swiglu4(uint2 a, uint32_t gq, uint32_t uq, float gs, float us, uint64_t (&dg)[2],
                                         uint64_t (&du)[2], uint64_t (&act)[2], uint64_t &dot)
 {
-    float g_[4], u_[4];
-    e4m3x4_unpack(gq, g_);
-    e4m3x4_unpack(uq, u_);
+    float gc[4], uc[4];
+    e4m3x4_unpack(gq, gc);
+    e4m3x4_unpack(uq, uc);
     const uint32_t aw[2] = {a.x, a.y};
-    dot = 0;
     const uint64_t gs2 = pack2(-gs, -gs), us2 = pack2(us, us);
+    dot = 0;
 #pragma unroll
     for (int i = 0; i < 2; i++) {
-        const uint64_t g = mul2(pack2(g_[2*i], g_[2*i+1]), gs2), u = mul2(pack2(u_[2*i], u_[2*i+1]), us2);
+        const uint64_t g = mul2(pack2(gc[2 * i], gc[2 * i + 1]), gs2), u = mul2(pack2(uc[2 * i], uc[2 * i + 1]), us2);
         const uint64_t a2 = pack2(__uint_as_float(aw[i] << 16), __uint_as_float(aw[i] & 0xFFFF0000u));
         float t0, t1;
         unpack2(g, t0, t1);
         const uint64_t nsg = pack2(rcp(-1.0f - ex2(t0 * LOG2E)), rcp(-1.0f - ex2(t1 * LOG2E)));
-        const uint64_t p = mul2(g, nsg);
+        const uint64_t p = mul2(g, nsg);                                      // silu
         du[i] = mul2(a2, p);
         dg[i] = mul2(mul2(a2, u), sub2(fma2(p, nsg, p), nsg));
         act[i] = mul2(p, u);

@@ -16,6 +16,8 @@
 // from the codes with both additions 122 us = 5.3 TB/s; the measured copy has
 // 6.8), by the exchanges of a row and its instructions where a value is one
 // instruction each (rows without whole vectors: 2.4-3.4 TB/s).
+#include <type_traits>
+
 #include "losses.cuh"
 
 namespace moe {
@@ -495,32 +497,35 @@ __global__ void __launch_bounds__(EPT == 8 ? 1024 : 512, EPT == 16 ? 2 : 1) norm
         if constexpr (VEC > 1) {
             const int64_t at = row * p.cols, at_s = row * (p.cols >> 7);
             if (p.h_q) encode<VEC, N>(v, c, p.cols, lane, p.h_q + at, p.h_s + at_s);
+const auto weigh = [&](auto biased) {
 #pragma unroll
-            for (int i = 0; i < N; i++) {
-                uint64_t w[H], f2[H];
-                float f[VEC] = {};
-#pragma unroll
-                for (int j = 0; j < H; j++) w[j] = f2[j] = 0;
-                if (RING || in(i)) {
+                for (int i = 0; i < N; i++) {
+                    constexpr bool B = decltype(biased)::value;
+                    uint64_t w[H] = {}, f2[H] = {};
+                    float f[VEC];
                     if constexpr (RING) {
                         staged_weight<VEC>(sw, c + i * STEP, p.wide, w);
-                        if (p.b) staged_weight<VEC>(sb, c + i * STEP, p.wide, f2);
-                    } else {
+                        if (B) staged_weight<VEC>(sb, c + i * STEP, p.wide, f2);
+                    } else if (in(i)) {
                         load_weight<VEC>(p.w, p.w_f32, c + i * STEP, 1.0f, f);
 #pragma unroll
                         for (int j = 0; j < H; j++) w[j] = pack2(f[2 * j], f[2 * j + 1]);
-                        load_weight<VEC>(p.b, p.w_f32, c + i * STEP, 0.0f, f);
+                        if (B) {
+                            load_weight<VEC>(p.b, p.w_f32, c + i * STEP, 0.0f, f);
 #pragma unroll
-                        for (int j = 0; j < H; j++) f2[j] = pack2(f[2 * j], f[2 * j + 1]);
+                            for (int j = 0; j < H; j++) f2[j] = pack2(f[2 * j], f[2 * j + 1]);
+                        }
                     }
-                }
 #pragma unroll
-                for (int j = 0; j < H; j++) {
-                    v[i][j] = fma2(v[i][j], w[j], f2[j]);
-                    unpack2(v[i][j], f[2 * j], f[2 * j + 1]);
+                    for (int j = 0; j < H; j++) {
+                        v[i][j] = B ? fma2(v[i][j], w[j], f2[j]) : mul2(v[i][j], w[j]);
+                        unpack2(v[i][j], f[2 * j], f[2 * j + 1]);
+                    }
+                    if (in(i)) store<T, VEC>(y + i * STEP, f);
                 }
-                if (in(i)) store<T, VEC>(y + i * STEP, f);
-            }
+            };
+            if (p.b) weigh(std::true_type());
+            else weigh(std::false_type());
             if (p.y_q) encode<VEC, N>(v, c, p.cols, lane, p.y_q + at, p.y_s + at_s);
         } else {
 #pragma unroll
@@ -792,20 +797,28 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) dnorm_kernel(Bwd p)
                     for (int j = 0; j < H; j++) gi[j] = mul2(gi[j], w[j]);
                 }
                 constexpr int M = VEC > 1 ? VEC : 2;
-                float f[M], d[M] = {};
-                if (p.dx_add && in(i)) {
-                    float r[VEC];
-                    Vec<T, VEC>::get(add[i], r);
+                float f[M];
+                if (p.dx_add) {
+                    float d[M] = {};
+                    if (in(i)) {
+                        float r[VEC];
+                        Vec<T, VEC>::get(add[i], r);
 #pragma unroll
-                    for (int j = 0; j < VEC; j++) d[j] = r[j];
-                    if (VEC == 1 && in2(i)) {
-                        Vec<T, VEC>::get(more[VEC > 1 ? 0 : i], r);
-                        d[1] = r[0];
+                        for (int j = 0; j < VEC; j++) d[j] = r[j];
+                        if (VEC == 1 && in2(i)) {
+                            Vec<T, VEC>::get(more[VEC > 1 ? 0 : i], r);
+                            d[1] = r[0];
+                        }
                     }
-                }
 #pragma unroll
-                for (int j = 0; j < H; j++)
-                    unpack2(fma2(fma2(hi[j], nm2, FULL ? add2(gi[j], nm1) : gi[j]), rs2, pack2(d[2 * j], d[2 * j + 1])), f[2 * j], f[2 * j + 1]);
+                    for (int j = 0; j < H; j++)
+                        unpack2(fma2(fma2(hi[j], nm2, FULL ? add2(gi[j], nm1) : gi[j]), rs2, pack2(d[2 * j], d[2 * j + 1])),
+                                f[2 * j], f[2 * j + 1]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < H; j++)
+                        unpack2(mul2(fma2(hi[j], nm2, FULL ? add2(gi[j], nm1) : gi[j]), rs2), f[2 * j], f[2 * j + 1]);
+                }
                 if constexpr (VEC > 1) {
                     if (in(i)) store<T, VEC>(dx + i * STEP, f);
                 } else {

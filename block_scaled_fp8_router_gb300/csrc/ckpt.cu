@@ -362,25 +362,26 @@ __global__ void __launch_bounds__(THREADS, 1) swiglu_ckpt_kernel(Args p)
     cp_async_wait<0>();
 }
 
-// d_gates[slot]: the blocks' dots of the slot's row in order, over its gate; 0
-// for a slot without a row and for a gate of 0 (its row of d_act holds
-// nothing, and every gate function's slope is 0 there)
+// d_gates[slot]: the blocks' dots of the slot's row, sixteen lanes a slot (a
+// fixed tree), over its gate; 0 for a slot without a row and for a gate of 0
+// (its row of d_act holds nothing, and every gate function's slope is 0 there)
 __global__ void __launch_bounds__(256) gate_kernel(const float *__restrict__ dots, const float *__restrict__ gates,
                                                    const int32_t *__restrict__ slot_to_sorted, int64_t slots,
                                                    int64_t rows, const int32_t *__restrict__ routed, int nb,
                                                    float *__restrict__ d_gates)
 {
     if (routed && __ldg(routed) < rows) rows = __ldg(routed);      // expert_offsets[E]
-    const int64_t p = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
-    if (p >= slots) return;
-    const int32_t r = __ldg(slot_to_sorted + p);
-    const float g = __ldg(gates + p);
+    const int64_t p = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) >> 4;
+    const int lane = threadIdx.x & 15;
+    const int32_t r = p < slots ? __ldg(slot_to_sorted + p) : -1;
+    const float g = p < slots ? __ldg(gates + p) : 0.0f;
+    const bool in = r >= 0 && r < rows && g != 0.0f;
     float s = 0.0f;
-    if (r >= 0 && r < rows && g != 0.0f) {
-        for (int b = 0; b < nb; b++) s += __ldg(dots + (int64_t)r * nb + b);
-        s = __fdiv_rn(s, g);
-    }
-    d_gates[p] = s;
+    if (in)
+        for (int b = lane; b < nb; b += 16) s += __ldg(dots + (int64_t)r * nb + b);
+#pragma unroll
+    for (int o = 8; o; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+    if (lane == 0 && p < slots) d_gates[p] = in ? __fdiv_rn(s, g) : 0.0f;
 }
 
 template <bool ROW, bool COL>
@@ -438,7 +439,7 @@ MOE_API moe_status moe_swiglu_backward_ckpt(const uint16_t *d_act, const uint8_t
         if (e != cudaSuccess) return MOE_ERR_CUDA;
     }
     if (d_gates && slots)
-        gate_kernel<<<(unsigned)((slots + 255) / 256), 256, 0, st>>>(ws, gates, slot_to_sorted, slots, rows,
+        gate_kernel<<<(unsigned)((slots + 15) / 16), 256, 0, st>>>(ws, gates, slot_to_sorted, slots, rows,
                                                                     col ? expert_offsets + E : nullptr, F / 128, d_gates);
     else if (!blocks)
         return MOE_OK;

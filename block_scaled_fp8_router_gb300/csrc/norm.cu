@@ -862,24 +862,28 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) dnorm_kernel(Bwd p)
     }
 }
 
-// dw and db: the CTAs' parts, 32 columns a CTA, eight runs of parts at a time
-// joined in run order
-__global__ void __launch_bounds__(256) reduce_kernel(const float *__restrict__ part, int parts, int cols, float *dw,
-                                                     float *db)
+// dw and db: the CTAs' parts, 32 columns a CTA: warp k adds parts k, k + 32, ...
+// of its lanes' columns, then the 32 warps' sums of column k (a fixed tree).
+// blockIdx.y: dw, then db.
+__global__ void __launch_bounds__(1024) reduce_kernel(const float *__restrict__ part, int parts, int cols, float *dw,
+                                                      float *db)
 {
-    __shared__ float run[8][32];
+    __shared__ float run[32][33];
     const int lane = threadIdx.x & 31, k = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane;
-    float *out = blockIdx.y ? db : dw;
-    if (!out) return;
+    float *out = blockIdx.y || !dw ? db : dw;
+    const float *from = part + (out == db ? cols : 0);
     float s = 0.0f;
-    if (c < cols)
-        for (int i = k; i < parts; i += 8) s += __ldg(part + ((int64_t)i * 2 + blockIdx.y) * cols + c);
+    if (c < cols) {
+#pragma unroll 5
+        for (int i = k; i < parts; i += 32) s += __ldg(from + (int64_t)i * 2 * cols + c);
+    }
     run[k][lane] = s;
     __syncthreads();
-    if (k || c >= cols) return;
-    for (int i = 1; i < 8; i++) s += run[i][lane];
-    out[c] = s;
+    s = run[lane][k];
+#pragma unroll
+    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+    if (lane == 0 && (int)blockIdx.x * 32 + k < cols) out[blockIdx.x * 32 + k] = s;
 }
 
 // ------------------------------------------------------------------- host
@@ -1112,6 +1116,7 @@ MOE_API moe_status moe_layer_norm_backward(const void *dy, int dtype, int64_t ro
                               : (vec ? bwd_launch_for<uint16_t, 8>(p, ept, grid, smem, st) : bwd_launch_for<uint16_t, 1>(p, ept, grid, smem, st));
     if (e != cudaSuccess) return MOE_ERR_CUDA;
     if (!sums) return MOE_OK;
-    reduce_kernel<<<dim3((unsigned)((cols + 31) / 32), 2), 256, 0, st>>>(p.part, grid, (int)cols, dweight, dbias);
+    reduce_kernel<<<dim3((unsigned)((cols + 31) / 32), dweight && dbias ? 2 : 1), 1024, 0, st>>>(p.part, grid, (int)cols,
+                                                                                               dweight, dbias);
     return launch_status();
 }

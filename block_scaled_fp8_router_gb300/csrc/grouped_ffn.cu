@@ -466,9 +466,9 @@ __global__ void __launch_bounds__(FT_THREADS, 1)
                     // tile's writes
                     float mg = 0.0f, mu = 0.0f;
 #pragma unroll
-                    for (int i = 0; i < 64; i++) {
-                        mg = fmaxf(mg, fabsf(acc[i]));
-                        mu = fmaxf(mu, fabsf(acc[64 + i]));
+                    for (int i = 0; i < 64; i += 2) {
+                        mg = amax3(acc[i], acc[i + 1], mg);
+                        mu = amax3(acc[64 + i], acc[65 + i], mu);
                     }
                     s.redh[cg][r_in] = make_float2(mg, mu);
                     if (pair_bar_or(q, aborted || *abort_flag)) aborted = true;
@@ -487,8 +487,7 @@ __global__ void __launch_bounds__(FT_THREADS, 1)
 #pragma unroll
                                 for (int i = 0; i < 4; i++) {
                                     const float *a = acc + 64 * half + 16 * u + 4 * i;
-                                    w[i] = (uint32_t)pack_e4m3x2(a[0] * y, a[1] * y) |
-                                           ((uint32_t)pack_e4m3x2(a[2] * y, a[3] * y) << 16);
+                                    w[i] = e4m3x4_pack(a[0] * y, a[1] * y, a[2] * y, a[3] * y);
                                 }
                                 reinterpret_cast<uint4 *>(dst + half * p.F)[u] = make_uint4(w[0], w[1], w[2], w[3]);
                             }

@@ -112,7 +112,7 @@ __device__ __forceinline__ void load_weight(const void *w, bool f32, int c, floa
 // bits in every thread: within the warp the lower half-warp ends up with a's
 // sum and the upper one with b's (one exchange more than for a alone), the
 // warps' parts meet in shared memory and are added the same way.  `red` is
-// this round's own buffer, [2][32] floats, and `first` where the group's parts
+// this exchange's own buffer, [2][32] floats, and `first` where the group's parts
 // start in each; `bar` its named barrier (0: the whole CTA).  One warp: no
 // exchange.
 __device__ __forceinline__ void row_sums(float &a, float &b, bool two, float *red, int first, int warps, int warp,
@@ -464,7 +464,7 @@ __global__ void __launch_bounds__(EPT == 8 ? 1024 : 512, EPT == 16 ? 2 : 1) norm
         sum = a + b;
         unpack2(q2, a, b);
         sq = a + b;
-        // with one round a row the buffers alternate: a warp a row ahead writes the other one
+        // with one exchange a row the buffers alternate: a warp a row ahead writes the other one
         row_sums(sq, sum, p.center, red[p.center ? 1 : par], group * p.warps, p.warps, gw, lane, group + 1);
         if constexpr (RING) {
             if (VEC == 1 && p.warps == 1) __syncwarp();

@@ -957,6 +957,30 @@ MOE_TYPE_BF16, MOE_TYPE_F32 = 0, 1
 # The calls below check what they are given and trust what they allocate: at
 # their smallest sizes a call is the host's time.
 
+_TYPES = {torch.bfloat16: MOE_TYPE_BF16, torch.float32: MOE_TYPE_F32}
+
+
+def _rows(t, name, like=None):
+    """(type code, row stride) of a [rows, cols] tensor: unit column stride, any
+    row stride >= cols (like: the type and shape to have)."""
+    if like is not None and (t.dtype is not like.dtype or t.shape != like.shape):
+        raise ValueError(f"{name}: expected {like.dtype} {tuple(like.shape)}, got {t.dtype} {tuple(t.shape)}")
+    dt = _TYPES.get(t.dtype)
+    if dt is None:
+        raise TypeError(f"{name}: expected torch.bfloat16 or torch.float32, got {t.dtype}")
+    stride = t.stride()
+    if len(stride) != 2:
+        raise ValueError(f"{name} must be 2-D")
+    rows, cols = t.shape
+    if stride[1] != 1 and cols > 1:
+        raise ValueError(f"{name}: must have unit column stride")
+    if rows <= 1:
+        return dt, cols
+    if stride[0] < cols:
+        raise ValueError(f"{name}: rows overlap")
+    return dt, stride[0]
+
+
 def _pair(v, q_shape, s_shape, name, like):
     """(codes, scales) of an optional output: True allocates, a pair of tensors
     is written, False / None skips -> the pair and its addresses."""
@@ -986,6 +1010,8 @@ def _vector(v, n, name, like):
 
 def _weights(weight, bias, cols) -> int:
     """The type code of a norm's weight and bias (one type, [cols])."""
+    if bias is None and weight.shape == (cols,) and weight.is_contiguous() and weight.dtype in _TYPES:
+        return _TYPES[weight.dtype]
     dt = None
     for t, name in ((weight, "weight"), (bias, "bias")):
         if t is None:
@@ -1014,13 +1040,13 @@ def moe_layer_norm(x, weight=None, bias=None, eps=1e-5, center=True, y=None, mea
     fp32; codes: y's 1x128 (codes, scales); ckpt: those of the normalised rows,
     for moe_layer_norm_backward.  Each of the four: True allocates, tensors are
     written, False / None skips.  y may be x."""
-    dt, ld = _logit_rows(x, "x")
+    dt, ld = _rows(x, "x")
     rows, cols = x.shape
     w_dt = MOE_TYPE_BF16 if weight is None and bias is None else _weights(weight, bias, cols)
     if y is None:
         y, ld_y = _empty((rows, cols), x.dtype, x), cols
     else:
-        _, ld_y = _logit_rows(y, "y", like=x)
+        _, ld_y = _rows(y, "y", like=x)
     _one_device(x, weight, bias, y)
     mean, p_mean = _vector(mean, rows, "mean", x)
     rstd, p_rstd = _vector(rstd, rows, "rstd", x)
@@ -1043,7 +1069,7 @@ def moe_layer_norm_backward(dy, rstd, x=None, mean=None, ckpt=None, weight=None,
     fp32; each or None).  dy_add [rows, cols] fp32 adds to dy, dx_add (dy's
     type) to dx.  dx, dweight, dbias: True allocates, a tensor is written
     (dx may be dy, x or dx_add), False / None skips."""
-    dt, ld = _logit_rows(dy, "dy")
+    dt, ld = _rows(dy, "dy")
     rows, cols = dy.shape
     _want(rstd, torch.float32, (rows,), "rstd")
     if (x is None) == (ckpt is None):
@@ -1051,7 +1077,7 @@ def moe_layer_norm_backward(dy, rstd, x=None, mean=None, ckpt=None, weight=None,
     ld_x = ld_add = ld_dx = cols
     p_mean = p_hq = p_hs = None
     if x is not None:
-        _, ld_x = _logit_rows(x, "x", like=dy)
+        _, ld_x = _rows(x, "x", like=dy)
         if center:
             if mean is None:
                 raise ValueError("mean: needed with x and center")
@@ -1068,11 +1094,11 @@ def moe_layer_norm_backward(dy, rstd, x=None, mean=None, ckpt=None, weight=None,
     elif dx is False:
         dx = None
     elif dx is not None:
-        _, ld_dx = _logit_rows(dx, "dx", like=dy)
+        _, ld_dx = _rows(dx, "dx", like=dy)
     if dx_add is not None:
         if dx is None:
             raise ValueError("dx_add needs dx")
-        _, ld_add = _logit_rows(dx_add, "dx_add", like=dy)
+        _, ld_add = _rows(dx_add, "dx_add", like=dy)
     _one_device(dy, rstd, x, mean, weight, dy_add, dx_add, dx, workspace)
     dweight, p_dw = _vector(dweight, cols, "dweight", dy)
     dbias, p_db = _vector(dbias, cols, "dbias", dy)

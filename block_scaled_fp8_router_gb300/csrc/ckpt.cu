@@ -169,8 +169,10 @@ __global__ void __launch_bounds__(THREADS, 1) swiglu_ckpt_kernel(Args p)
             s_off[e] = __ldg(p.offsets + e);
         }
         __syncthreads();
-        const int P = s_pad[p.E] < p.ld ? s_pad[p.E] : p.ld;
-        blocks = P > 0 ? P / TILE : 0;
+        // every block that the maps name (no more than E experts of these rows
+        // or ld can have); those behind ld give their rows' outputs only
+        const int P = s_pad[p.E], most = max(blocks + p.E, p.ld / TILE);
+        blocks = P <= 0 ? 0 : min(P / TILE, most);
     }
     // this CTA's tiles: the same number each, the first ones one more
     const int total = blocks * nb, each = total / (int)gridDim.x, more = total - each * (int)gridDim.x;
@@ -226,7 +228,7 @@ __global__ void __launch_bounds__(THREADS, 1) swiglu_ckpt_kernel(Args p)
     // lane's l & 15 was this warp's number.
     Where before{-1, 0, 0, 0};
     const auto leave = [&] {
-        if (before.kb < 0) return;
+        if (before.kb < 0 || (int64_t)before.kb * TILE >= p.ld) return;
         const int ch = tid >> 3, pc = tid & 7;
         const uint8_t *src = codes + ch * TILE + (((2 * pc) ^ warp) & ~1) * 8;
         const int64_t off = (int64_t)(before.cb * TILE + ch) * p.ld + before.kb * TILE + 16 * pc;
@@ -306,7 +308,8 @@ __global__ void __launch_bounds__(THREADS, 1) swiglu_ckpt_kernel(Args p)
                 const float s = computed_scale(m);
                 col_y[tid] = rcp(s);
                 const int k = tid >> 7, ch = at.cb * TILE + (tid & 127);
-                if (k == 2) {
+                if ((int64_t)at.kb * TILE >= p.ld) {
+                } else if (k == 2) {
                     if (p.actT_s) p.actT_s[(int64_t)at.kb * p.F + ch] = s;
                 } else if (p.dhT_s) {
                     p.dhT_s[(int64_t)at.kb * 2 * p.F + k * p.F + ch] = s;
@@ -418,7 +421,12 @@ MOE_API moe_status moe_swiglu_backward_ckpt(const uint16_t *d_act, const uint8_t
     const bool col = dhT_q || dhT_s || actT_q || actT_s;
     if (rows < 0 || rows >= (1LL << 31) || F <= 0 || F % 128 != 0 || slots < 0 || slots >= (1LL << 31)) return MOE_ERR_SHAPE;
     if (col && (E < 1 || E > 1024 || max_pad < 0 || max_pad % 128 != 0)) return MOE_ERR_SHAPE;
-    if ((col ? max_pad / 128 : (rows + 127) / 128) * (F / 128) >= (1LL << 31) || max_pad >= (1LL << 31)) return MOE_ERR_SHAPE;
+    int64_t blocks = (rows + 127) / 128;                          // at most
+    if (col) {
+        blocks += rows ? E : 0;
+        if (max_pad / 128 > blocks) blocks = max_pad / 128;
+    }
+    if (blocks * (F / 128) >= (1LL << 31) || max_pad >= (1LL << 31)) return MOE_ERR_SHAPE;
     if (!dh_q != !dh_s || !dhT_q != !dhT_s || !actT_q != !actT_s) return MOE_ERR_NULL;
     if (col && (!expert_offsets || !pad)) return MOE_ERR_NULL;
     if (d_gates && slots && (!gates || !slot_to_sorted)) return MOE_ERR_NULL;
@@ -432,7 +440,6 @@ MOE_API moe_status moe_swiglu_backward_ckpt(const uint16_t *d_act, const uint8_t
     cudaStream_t st = as_stream(stream);
     float *ws = dots ? static_cast<float *>(workspace) : nullptr;
     Args p{d_act, h_q, h_s, expert_offsets, pad, dh_q, dhT_q, actT_q, dh_s, dhT_s, actT_s, ws, rows, (int)max_pad, F, E};
-    const int64_t blocks = col ? max_pad / 128 : (rows + 127) / 128;
     if (blocks && (dh_q || col || dots)) {
         const cudaError_t e = dh_q ? (col ? launch<true, true>(p, blocks, st) : launch<true, false>(p, blocks, st))
                                    : (col ? launch<false, true>(p, blocks, st) : launch<false, false>(p, blocks, st));

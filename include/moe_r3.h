@@ -763,7 +763,8 @@ moe_status moe_router_backward_dense(const uint16_t *x, const uint16_t *w_router
  *       for src 2 and 1 with ld = max_pad and scales_kb_major).  They need
  *       expert_offsets and pad (moe_dispatch's and moe_wgrad_pad_offsets');
  *       all outputs then cover the rows those name.
- *   Scales and codes by the same rule.  Columns at and behind pad[E] are not written.
+ *   Scales and codes by the same rule.  Columns at and behind pad[E] are not written,
+ *   and none behind max_pad are (the rows of those have their other outputs).
  *   Rows that expert_offsets names outside [0, rows) are not read or written.
  *   No output overlaps an input or another output.  Any of rows, slots and
  *   max_pad may be 0.

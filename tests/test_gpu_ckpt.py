@@ -247,6 +247,26 @@ def test_bad_maps_stay_inside(L):
     assert torch.equal(dhT[0], want[2][0]) and torch.equal(dhT[1], want[2][1])
 
 
+@pytest.mark.parametrize("ld", [0, 128, 384])
+def test_fewer_columns_than_the_maps_name(L, ld):
+    """max_pad below pad[E]: every row and gate as without it, the columns of
+    the blocks in front of it as with room for all."""
+    g = torch.Generator(device=DEV).manual_seed(ld)
+    off, offs = offsets_of([40, 0, 130, 257])
+    A, F = off[-1], 256
+    d_act, h_q, h_s = inputs(A, F, g)
+    pad = torch.tensor([0, 128, 128, 384, 768], dtype=torch.int32, device=DEV)
+    sl2 = torch.randperm(A, device=DEV, generator=g).int()
+    kw = dict(gates=0.1 + torch.rand(A, device=DEV, generator=g), slot_to_sorted=sl2, expert_offsets=offs, pad=pad,
+              d_gates=True, dhT=True, actT=True)
+    want = L.moe_swiglu_backward_ckpt(d_act, h_q, h_s, ld=768, **kw)
+    work = torch.full((A * F // 128,), float("nan"), device=DEV)
+    got = L.moe_swiglu_backward_ckpt(d_act, h_q, h_s, ld=ld, workspace=work, **kw)
+    assert torch.equal(got[0][0], want[0][0]) and torch.equal(got[0][1], want[0][1]) and torch.equal(got[1], want[1])
+    for a, b in zip(got[2:], want[2:]):
+        assert torch.equal(a[0], b[0][:, :ld]) and torch.equal(a[1], b[1][:ld // 128])
+
+
 def test_empty(L):
     e = lambda *s, dt=torch.uint8: torch.empty(*s, dtype=dt, device=DEV)
     f, i = torch.float32, torch.int32

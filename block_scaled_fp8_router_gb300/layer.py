@@ -180,8 +180,8 @@ class MoELayerFP8:
         if T > self.T_max:
             raise ValueError(f"T={T} exceeds T_max={self.T_max}")
         A = T * self.k
-        if not train and (self.norm is not None or self.ckpt8):
-            self._T_train = None                        # nothing is kept: what was is of another forward
+        if self.norm is not None or self.ckpt8:
+            self._T_train = None                        # what was kept is overwritten from here on; a train forward sets it
         if self.norm is not None:
             x = self._normalise(x, train)
         ids, gates = self.route(x, replay_kT, capture_kT)

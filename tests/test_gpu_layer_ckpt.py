@@ -220,6 +220,21 @@ def test_refusals(L):
         lay.forward(torch.zeros(4, 256, device=DEV), train=True)          # not bf16
 
 
+@pytest.mark.parametrize("norm,ckpt8", [("rms", False), (None, True), ("rms", True)])
+def test_a_forward_that_fails_keeps_nothing(L, norm, ckpt8):
+    """Its norm has already written over what the forward before it kept."""
+    lay, g = make(norm=norm, ckpt8=ckpt8)
+    x = torch.randn(40, 256, device=DEV, generator=g).bfloat16()
+    lay.forward(x, train=True)
+    with pytest.raises(ValueError):
+        lay.forward(x[:20], replay_kT=torch.zeros(3, 7, dtype=torch.int32, device=DEV), train=True)
+    with pytest.raises(ValueError):
+        lay.backward(x)
+    lay.forward(x, train=True)
+    dx, _ = lay.backward(x)
+    assert dx.shape == x.shape
+
+
 @pytest.mark.parametrize("norm,ckpt8", [(True, False), (False, True), (True, True)])
 def test_example_step(L, norm, ckpt8):
     sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))

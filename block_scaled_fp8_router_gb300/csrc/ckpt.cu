@@ -433,6 +433,10 @@ MOE_API moe_status moe_swiglu_backward_ckpt(const uint16_t *d_act, const uint8_t
     if (rows && (dh_q || col || d_gates) && (!d_act || !h_q || !h_s)) return MOE_ERR_NULL;
     if (!aligned16(d_act) || !aligned16(h_q) || !aligned16(dh_q) || !aligned16(dhT_q) || !aligned16(actT_q))
         return MOE_ERR_ALIGN;
+    for (const void *v : {(const void *)h_s, (const void *)dh_s, (const void *)dhT_s, (const void *)actT_s,
+                          (const void *)gates, (const void *)slot_to_sorted, (const void *)d_gates,
+                          (const void *)expert_offsets, (const void *)pad})
+        if (reinterpret_cast<uintptr_t>(v) % 4) return MOE_ERR_ALIGN;
     if (!dh_q && !col && !(d_gates && slots)) return MOE_OK;
     const bool dots = d_gates && slots && rows;
     if (dots && (!workspace || workspace_bytes < moe_swiglu_backward_ckpt_workspace_size(rows, F))) return MOE_ERR_WORKSPACE;

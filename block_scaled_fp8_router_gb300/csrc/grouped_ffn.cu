@@ -1361,7 +1361,7 @@ MOE_API moe_status moe_grouped_ffn_fp8_ckpt(const uint8_t *xq_sorted, const floa
                                             void *workspace, size_t workspace_bytes, int32_t *dev_status, void *stream)
 {
     if (max_rows != 0 && (!h_q || !h_s)) return MOE_ERR_NULL;
-    if (!aligned16(h_q)) return MOE_ERR_ALIGN;
+    if (!aligned16(h_q) || reinterpret_cast<uintptr_t>(h_s) % 4) return MOE_ERR_ALIGN;
     return ffn_launch<false, true>(xq_sorted, max_rows, xs_sorted, nullptr, 1, expert_offsets, max_rows, E, d, F, w13_q,
                                    w13_s, w2_q, w2_s, out_sorted, workspace, workspace_bytes, dev_status, stream,
                                    nullptr, h_q, h_s);

@@ -16,6 +16,7 @@
 // from the codes with both additions 122 us = 5.3 TB/s; the measured copy has
 // 6.8), by the exchanges of a row and its instructions where a value is one
 // instruction each (rows without whole vectors: 2.4-3.4 TB/s).
+#include <initializer_list>
 #include <type_traits>
 
 #include "losses.cuh"
@@ -497,7 +498,7 @@ __global__ void __launch_bounds__(EPT == 8 ? 1024 : 512, EPT == 16 ? 2 : 1) norm
         if constexpr (VEC > 1) {
             const int64_t at = row * p.cols, at_s = row * (p.cols >> 7);
             if (p.h_q) encode<VEC, N>(v, c, p.cols, lane, p.h_q + at, p.h_s + at_s);
-const auto weigh = [&](auto biased) {
+            const auto weigh = [&](auto biased) {
 #pragma unroll
                 for (int i = 0; i < N; i++) {
                     constexpr bool B = decltype(biased)::value;
@@ -895,11 +896,35 @@ static bool overlap(const void *a, int64_t na, const void *b, int64_t nb)
     return x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
 }
 
+struct Span {
+    const void *p;
+    int64_t bytes;
+};
+
+// whether any of the outputs lies over any of the inputs
+template <int M, int N>
+static bool overlap_any(const Span (&outs)[M], const Span (&ins)[N])
+{
+    for (const Span &o : outs)
+        for (const Span &i : ins)
+            if (overlap(o.p, o.bytes, i.p, i.bytes)) return true;
+    return false;
+}
+
+static int64_t span(int64_t rows, int64_t ld, int64_t cols, int es) { return ((rows - 1) * ld + cols) * es; }
+
+static bool aligned4(std::initializer_list<const void *> ps)
+{
+    uintptr_t bits = 0;
+    for (const void *p : ps) bits |= reinterpret_cast<uintptr_t>(p);
+    return bits % 4 == 0;
+}
+
 // whether the rows of an output (elements es wide) lie over an input's other
 // than row on row: a row would be written before another is read
 static bool clash(const void *out, int64_t ld_out, const void *in, int64_t ld_in, int64_t rows, int cols, int es)
 {
-    if (!overlap(out, ((rows - 1) * ld_out + cols) * es, in, ((rows - 1) * ld_in + cols) * es)) return false;
+    if (!overlap(out, span(rows, ld_out, cols, es), in, span(rows, ld_in, cols, es))) return false;
     if (out == in) return rows > 1 && ld_out != ld_in;
     if (rows == 1 || ld_out != ld_in) return true;
     const int64_t off = ((int64_t)((intptr_t)out - (intptr_t)in) / es % ld_in + ld_in) % ld_in;
@@ -1052,7 +1077,15 @@ MOE_API moe_status moe_layer_norm(const void *x, int dtype, int64_t rows, int64_
     const bool vec = cols % per == 0 && rows_aligned(x, ld_x, rows, es, 16) && rows_aligned(y, ld_y, rows, es, 16) &&
                      aligned16(weight) && aligned16(bias);
     if ((y_q || xhat_q) && (!vec || !aligned16(y_q) || !aligned16(xhat_q))) return MOE_ERR_ALIGN;
-    if (clash(y, ld_y, x, ld_x, rows, (int)cols, es)) return MOE_ERR_UNSUPPORTED;
+    if (!aligned4({mean, rstd, y_s, xhat_s})) return MOE_ERR_ALIGN;
+    const Span in_x{x, span(rows, ld_x, cols, es)}, in_w{weight, cols * ws}, in_b{bias, cols * ws};
+    const int64_t codes = rows * cols, scales = rows * (cols / 128) * 4;
+    if (clash(y, ld_y, x, ld_x, rows, (int)cols, es) ||
+        overlap_any({{y, span(rows, ld_y, cols, es)}, {mean, rows * 4}, {rstd, rows * 4}, {y_q, codes}, {y_s, scales},
+                     {xhat_q, codes}, {xhat_s, scales}}, {in_w, in_b}) ||
+        overlap_any({{mean, rows * 4}, {rstd, rows * 4}, {y_q, codes}, {y_s, scales}, {xhat_q, codes}, {xhat_s, scales}},
+                    {in_x}))
+        return MOE_ERR_UNSUPPORTED;
     Fwd p{x, weight, bias, y, mean, rstd, y_q, xhat_q, y_s, xhat_s, rows, ld_x, ld_y, (int)cols, 0, 1, 1, 0, 0, 0, eps,
           center != 0, w_dtype == MOE_TYPE_F32};
     cudaStream_t st = as_stream(stream);
@@ -1097,16 +1130,24 @@ MOE_API moe_status moe_layer_norm_backward(const void *dy, int dtype, int64_t ro
                      (!dx_add || rows_aligned(dx_add, ld_add, rows, es, 16)) &&
                      (!dx || rows_aligned(dx, ld_dx, rows, es, 16)) && aligned16(dy_add) && aligned16(weight);
     if (xhat_q && (!vec || !aligned16(xhat_q))) return MOE_ERR_ALIGN;
+    if (!aligned4({mean, rstd, xhat_s, dweight, dbias})) return MOE_ERR_ALIGN;
     if (clash(dx, ld_dx, dy, ld_dy, rows, (int)cols, es) || clash(dx, ld_dx, x, ld_x, rows, (int)cols, es) ||
         clash(dx, ld_dx, dx_add, ld_add, rows, (int)cols, es) ||
-        (dx && (overlap(dx, ((rows - 1) * ld_dx + cols) * es, dy_add, rows * cols * 4) ||
-                overlap(dx, ((rows - 1) * ld_dx + cols) * es, xhat_q, rows * cols))))
+        overlap_any({{dx, span(rows, ld_dx, cols, es)}}, {{dy_add, rows * cols * 4}, {xhat_q, rows * cols}}))
         return MOE_ERR_UNSUPPORTED;
     const bool sums = dweight || dbias;
     if (sums && (!workspace || workspace_bytes < moe_layer_norm_backward_workspace_size(rows, cols)))
         return MOE_ERR_WORKSPACE;
     if (sums && !aligned16(workspace)) return MOE_ERR_ALIGN;
     if (!sums && !dx) return MOE_OK;
+    const Span sums_w{dweight, cols * 4}, sums_b{dbias, cols * 4}, 
+        parts{sums ? workspace : nullptr, (int64_t)moe_layer_norm_backward_workspace_size(rows, cols)},
+        in_w{weight, cols * ws}, in_m{center && x ? mean : nullptr, rows * 4}, in_r{rstd, rows * 4},
+        in_s{xhat_s, rows * (cols / 128) * 4};
+    if (overlap_any({{dx, span(rows, ld_dx, cols, es)}, sums_w, sums_b, parts}, {in_w, in_m, in_r, in_s}) ||
+        overlap_any({sums_w, sums_b, parts}, {{dy, span(rows, ld_dy, cols, es)}, {x, span(rows, ld_x, cols, es)},
+                    {dx_add, span(rows, ld_add, cols, es)}, {dy_add, rows * cols * 4}, {xhat_q, rows * cols}}))
+        return MOE_ERR_UNSUPPORTED;
     Bwd p{dy, x, dx_add, weight, dy_add, xhat_q, xhat_s, mean, rstd, dx, static_cast<float *>(workspace),
           ld_dy, ld_x, ld_add, ld_dx, (int)rows, (int)cols, 0, 1, 1, 0, 0, 0, 0, 0, 0, center != 0, w_dtype == MOE_TYPE_F32,
           dweight != nullptr, dbias != nullptr};

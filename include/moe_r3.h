@@ -741,7 +741,8 @@ moe_status moe_router_backward_dense(const uint16_t *x, const uint16_t *w_router
  * workspace (with dweight or dbias): moe_layer_norm_backward_workspace_size
  * bytes, 16-byte aligned, no initialisation.
  * Errors: SHAPE (also eps < 0 or not finite), NULL, ALIGN, WORKSPACE,
- * UNSUPPORTED (an output over an input other than row on row), CUDA.
+ * UNSUPPORTED (an output or the workspace over an input other than row on row),
+ * CUDA.
  *
  * moe_grouped_ffn_fp8_ckpt  moe_grouped_ffn_fp8 that also writes GEMM1's
  *   pre-activations h (gate columns, then up) as 1 x 128 codes h_q

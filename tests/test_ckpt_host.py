@@ -65,6 +65,40 @@ def test_norm_backward(lib):
     assert bwd(lib, dw=z, ws=m, n=need) == ALIGN
 
 
+def test_norm_outputs_over_inputs(lib):
+    P = lambda v: ctypes.c_void_p(v)
+    full = lambda **kw: lib.moe_layer_norm(*[dict(dict(
+        x=P(0x100000), dt=0, rows=4, cols=256, ld=256, w=P(0x200000), b=P(0x210000), wd=1, eps=1e-5, c=1, y=P(0x300000), ldy=256,
+        m=P(0x400000), r=P(0x410000), yq=P(0x500000), ys=P(0x510000), hq=P(0x600000), hs=P(0x610000), st=None), **kw)[n]
+        for n in "x dt rows cols ld w b wd eps c y ldy m r yq ys hq hs st".split()])
+    for kw in (dict(yq=P(0x100000)), dict(hq=P(0x100100)), dict(ys=P(0x1007F0)), dict(hs=P(0x100000)), dict(m=P(0x100400)),
+               dict(r=P(0x1007FC)), dict(y=P(0x200000)), dict(y=P(0x210000 - 2048 + 16)), dict(m=P(0x200010)), dict(hs=P(0x2103F0))):
+        assert full(**kw) == UNSUPPORTED, kw
+    for kw in (dict(m=P(0x400002)), dict(r=P(0x410001)), dict(ys=P(0x510002)), dict(hs=P(0x610003))):
+        assert full(**kw) == ALIGN, kw
+    need = lib.moe_layer_norm_backward_workspace_size(4, 256)
+    base = dict(w=P(0x200000), wd=1, mean=P(0x400000), rstd=P(0x410000), dx=P(0x300000), dw=P(0x500000), db=P(0x510000),
+                ws=P(0x10000000), n=need, dadd=P(0x620000), add=P(0x630000))
+    for kw in (dict(dx=P(0x200010)), dict(dx=P(0x400000)), dict(dx=P(0x410000 - 2048 + 16)), dict(dw=P(0x200000)), dict(db=P(0x410004)),
+               dict(dw=x), dict(db=y), dict(dw=P(0x6207FC)), dict(dw=P(0x630FFC)), dict(ws=x), dict(ws=P(0x400000))):
+        assert bwd(lib, **dict(base, **kw)) == UNSUPPORTED, kw
+    q = dict(x_=None, mean=None, hq=P(0x700000), hs=P(0x710000))
+    for kw in (dict(dx=P(0x710000)), dict(dw=P(0x700000)), dict(db=P(0x710000)), dict(ws=P(0x700000))):
+        assert bwd(lib, **dict(base, **q, **kw)) == UNSUPPORTED, kw
+    for kw in (dict(mean=P(0x400002)), dict(rstd=P(0x410002)), dict(dw=P(0x500001)), dict(db=P(0x510002))):
+        assert bwd(lib, **dict(base, **kw)) == ALIGN, kw
+    assert bwd(lib, **dict(base, **dict(q, hs=P(0x710002)))) == ALIGN
+
+
+def test_swiglu_and_ffn_align_fp32_and_maps(lib):
+    P = lambda v: ctypes.c_void_p(v)
+    base = dict(dh=P(0x2000000), dhs=P(0x2100000), gates=P(0x2200000), sl=P(0x2210000), slots=4, dg=P(0x2220000), ws=P(0x2230000), n=1 << 20,
+                off=P(0x2400000), pad=P(0x2410000), t=P(0x2500000), ts=P(0x2600000), c=P(0x2700000), cs=P(0x2800000))
+    for name in ("hs", "dhs", "gates", "sl", "dg", "off", "pad", "ts", "cs"):
+        assert swi(lib, **dict(base, **{name: P(0x3000002)})) == ALIGN, name
+    assert lib.moe_grouped_ffn_fp8_ckpt(x, x, x, 16, 8, 256, 512, x, x, x, x, x, x, P(0x3000002), x, 1 << 30, None, None) == ALIGN
+
+
 def swi(lib, a=x, hq=y, hs=z, rows=4, F=256, gates=None, sl=None, slots=0, dh=None, dhs=None, dg=None, off=None, pad=None,
         E=1, ld=128, t=None, ts=None, c=None, cs=None, ws=None, n=0):
     return lib.moe_swiglu_backward_ckpt(a, hq, hs, rows, F, gates, sl, slots, dh, dhs, dg, off, pad, E, ld, t, ts, c, cs, ws,

@@ -185,10 +185,10 @@ __device__ __forceinline__ void copy_odd(uint32_t dst, const T *base, int64_t at
     const int pieces = odd_pieces(cols * (int)sizeof(T));
     int k = t;
     if (from < reinterpret_cast<const char *>(base)) {         // the first row, where the tensor starts off a boundary
-        for (int c = t; c < cols && c * (int)sizeof(T) < 16 - shift; c += nth) {
+        for (int c = t; c * (int)sizeof(T) < 16 - shift; c += nth) {                 // zeros behind a row that ends here
             const uint32_t to = dst + shift + c * (int)sizeof(T);
-            if (sizeof(T) == 4) asm volatile("st.shared.b32 [%0], %1;" ::"r"(to), "r"(reinterpret_cast<const uint32_t *>(start)[c]) : "memory");
-            else asm volatile("st.shared.b16 [%0], %1;" ::"r"(to), "h"(reinterpret_cast<const uint16_t *>(start)[c]) : "memory");
+            if (sizeof(T) == 4) asm volatile("st.shared.b32 [%0], %1;" ::"r"(to), "r"(c < cols ? reinterpret_cast<const uint32_t *>(start)[c] : 0u) : "memory");
+            else asm volatile("st.shared.b16 [%0], %1;" ::"r"(to), "h"(c < cols ? reinterpret_cast<const uint16_t *>(start)[c] : (uint16_t)0) : "memory");
         }
         if (k == 0) k = nth;                                   // its first piece is done
     }

@@ -88,6 +88,32 @@ def test_forward_strides_and_place(L, dt, cols, ld, shift):
         assert torch.equal(both[:, cols:], y) and torch.equal(both[:, :cols], x)
 
 
+@pytest.mark.parametrize("dt,cols,shift", [(torch.bfloat16, 4, 3), (torch.bfloat16, 1, 1), (torch.bfloat16, 6, 1),
+                                           (torch.float32, 1, 1), (torch.float32, 2, 1), (torch.float32, 1, 2)])
+@pytest.mark.parametrize("center", [True, False])
+def test_first_row_ends_in_its_first_16_bytes(L, dt, cols, shift, center):
+    """Rows shorter than the rest of the 16 bytes that the tensor starts in, on
+    SMs whose shared memory holds NaN: nothing behind the row is added in."""
+    g = torch.Generator(device=DEV).manual_seed(cols + 10 * shift)
+    rows = 400
+    x, dy = rows_of(rows, cols, dt, g, shift=shift), rows_of(rows, cols, dt, g, shift=shift)
+    w = 1 + 0.3 * torch.randn(cols, device=DEV, generator=g)
+    bad = torch.full((1000, 8191), float("nan"), device=DEV)
+    dirty = lambda: L.moe_layer_norm(bad, bad[0], bad[0], rstd=True)[2]
+    r_bad = dirty()
+    y, mean, rstd, _, _ = L.moe_layer_norm(x, w, eps=1e-2, center=center, mean=True, rstd=True)
+    ry, mu, r, h = R.norm(x, w, None, 1e-2, center)
+    size = (h.abs() + r[:, None] * (mu.abs() if center else 0 * mu)[:, None] + 1) * w.double().abs()
+    L.moe_layer_norm_backward(bad, r_bad, x=bad, weight=bad[0], center=False)
+    dx, dw, db = L.moe_layer_norm_backward(dy, rstd, x=x, mean=mean, weight=w, center=center, dbias=True)
+    check(mean, mu, mu.abs() + 1 / r, torch.float32, "mean")
+    check(y, ry, size, dt, "y")
+    h = (x.double() - mean.double()[:, None]) * rstd.double()[:, None]
+    rdx, rdw, rdb, size, sw, sb = R.norm_backward(dy, h, rstd, w, center)
+    check(dx, rdx, size, dt, "dx")
+    assert bool(((dw.double() - rdw).abs() <= K * sw).all()) and bool(((db.double() - rdb).abs() <= K * sb).all())
+
+
 def test_forward_far_mean_and_constant_rows(L):
     """A mean a thousand times the spread; a constant row is 0 before the bias; scale of the RMS form."""
     g = torch.Generator(device=DEV).manual_seed(5)

@@ -344,13 +344,14 @@ __device__ __forceinline__ void encode(const uint64_t (&v)[VPT][VEC / 2], int c,
     for (int i = 0; i < VPT; i++) {
         const float yi = __shfl_sync(0xFFFFFFFFu, y, (lane & ~(G - 1)) + i * EACH);
         if (c + i * 32 * VEC >= cols) continue;
+        const uint64_t y2 = pack2(yi, yi);
         uint32_t w[VEC / 4];
 #pragma unroll
         for (int k = 0; k < VEC / 4; k++) {
             float a, b, e, f;
-            unpack2(v[i][2 * k], a, b);
-            unpack2(v[i][2 * k + 1], e, f);
-            w[k] = e4m3x4_pack(a * yi, b * yi, e * yi, f * yi);
+            unpack2(mul2(v[i][2 * k], y2), a, b);
+            unpack2(mul2(v[i][2 * k + 1], y2), e, f);
+            w[k] = e4m3x4_pack(a, b, e, f);
         }
         if constexpr (VEC == 8) *reinterpret_cast<uint2 *>(q + c + i * 32 * VEC) = make_uint2(w[0], w[1]);
         else *reinterpret_cast<uint32_t *>(q + c + i * 32 * VEC) = w[0];

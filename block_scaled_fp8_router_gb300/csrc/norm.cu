@@ -746,6 +746,14 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) dnorm_kernel(Bwd p)
                 if (in(i)) add[i] = *reinterpret_cast<const typename Vec<T, VEC>::Raw *>(src + i * STEP);
                 if (VEC == 1 && in2(i)) more[VEC > 1 ? 0 : i] = *reinterpret_cast<const typename Vec<T, VEC>::Raw *>(src + i * STEP + 32);
             }
+            // the next row's as far as L2, a lane for each 128 bytes (8192 x 7168 from codes with both additions: 119 us
+            // against 124; there is no room for it in the ring beside dy_add)
+            if (VEC > 1 && row + step < p.rows && (lane & 7) == 0) {
+                const T *next = src + step * p.ld_add;
+#pragma unroll
+                for (int i = 0; i < N; i++)
+                    if (in(i)) asm volatile("prefetch.global.L2 [%0];" ::"l"(next + i * STEP));
+            }
         }
         const uint8_t *st = mine + stage * p.stage_bytes;
         wait_oldest(p.stages);

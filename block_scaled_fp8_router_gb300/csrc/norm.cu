@@ -610,7 +610,13 @@ __device__ __forceinline__ void decode(const uint8_t *q, float s, uint64_t (&v)[
 // shared memory costs 1.5 times the whole.
 constexpr int BWD_THREADS = 512;                       // at up to 128 registers
 
-template <typename T, int VEC, int EPT, bool CKPT, bool FULL>
+// ADD: 0 without dy_add and dx_add; 1 with either or both, dy_add in the ring;
+// 2 with dy_add read in place (fp32 rows too long for the ring with it).  One
+// kernel that asked would hold the addresses beside the sums: 8192 x 7168 bf16
+// from codes without either 67 us against 74, 4096 x 16384 from x 93 against 138,
+// 8192 x 5001 88 against 102.  In the ring even where that leaves one stage: 4096 x
+// 16384 bf16 220 us against 268-288 in place, 8192 x 5001 137 against 353.
+template <typename T, int VEC, int EPT, bool CKPT, bool FULL, int ADD>
 __global__ void __launch_bounds__(BWD_THREADS, 1) dnorm_kernel(Bwd p)
 {
     // vectors, or pairs of single values 32 columns apart
@@ -636,6 +642,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) dnorm_kernel(Bwd p)
                 const uint32_t dst = mine_u + stage * p.stage_bytes;
                 copy_odd<T>(dst, static_cast<const T *>(p.dy), row * p.ld_dy, p.cols, gw * 32 + lane, p.warps * 32);
                 copy_odd<T>(dst + p.at_x, static_cast<const T *>(p.x), row * p.ld_x, p.cols, gw * 32 + lane, p.warps * 32);
+                if (ADD == 1 && p.at_dya >= 0) copy_odd<float>(dst + p.at_dya, p.dy_add, row * p.cols, p.cols, gw * 32 + lane, p.warps * 32);
             }
         } else {
             if (row < p.rows) {
@@ -661,7 +668,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) dnorm_kernel(Bwd p)
                     for (int i = 0; i < N; i++)
                         if (in(i)) copy_async<16>(dst + p.at_x + c * (int)sizeof(T) + i * 512, x + i * STEP);
                 }
-                if (p.at_dya >= 0) {
+                if (ADD == 1 && p.at_dya >= 0) {
                     const float *d = p.dy_add + at;
 #pragma unroll
                     for (int i = 0; i < N; i++) {
@@ -686,7 +693,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) dnorm_kernel(Bwd p)
 #pragma unroll
             for (int j = 0; j < H; j++) h[j] = mul2(FULL ? add2(h[j], nmu2) : h[j], rs2);
         }
-        if (p.at_dya >= 0) {
+        if (ADD == 1 && p.at_dya >= 0) {
             if constexpr (VEC > 1) {
 #pragma unroll
                 for (int k = 0; k < VEC / 4; k++) {
@@ -694,8 +701,11 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) dnorm_kernel(Bwd p)
                     a[2 * k] = add2(a[2 * k], pack2(d.x, d.y));
                     a[2 * k + 1] = add2(a[2 * k + 1], pack2(d.z, d.w));
                 }
+            } else {
+                const float *d = reinterpret_cast<const float *>(st + p.at_dya + odd_shift(p.dy_add, row * p.cols)) + c + i * STEP;
+                a[0] = add2(a[0], pack2(d[0], d[32]));
             }
-        } else if (p.dy_add && in(i)) {
+        } else if (ADD == 2 && p.dy_add && in(i)) {
             const float *d = p.dy_add + row * p.cols + c + i * STEP;
             if constexpr (VEC > 1) {
 #pragma unroll
@@ -716,7 +726,9 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) dnorm_kernel(Bwd p)
             clear(st, row, p.at_x);
             clear(st, p.at_x + (CKPT ? p.cols : row), p.at_s);
             if (CKPT) clear(st, p.at_s + p.cols / 32, p.at_s + p.wide / 32);
-            if (p.at_dya >= 0) {                       // of eights two halves
+            if (VEC == 1) {
+                if (ADD == 1 && p.at_dya >= 0) clear(st, p.at_dya + 16 * odd_pieces(p.cols * 4), p.stage_bytes);
+            } else if (ADD == 1 && p.at_dya >= 0) {    // of eights two halves
                 clear(st, p.at_dya + p.cols * (VEC == 8 ? 2 : 4), p.at_dya + p.wide * (VEC == 8 ? 2 : 4));
                 if (VEC == 8) clear(st, p.at_dya + half + p.cols * 2, p.at_dya + half + p.wide * 2);
             }
@@ -739,7 +751,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) dnorm_kernel(Bwd p)
             if (mean) mu_next = __ldg(p.mean + row + step);
         }
         typename Vec<T, VEC>::Raw add[N], more[VEC > 1 ? 1 : N];      // dx_add: on its way while the means are formed
-        if (p.dx_add) {
+        if (ADD && p.dx_add) {
             const T *src = static_cast<const T *>(p.dx_add) + row * p.ld_add + c;
 #pragma unroll
             for (int i = 0; i < N; i++) {
@@ -748,11 +760,13 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) dnorm_kernel(Bwd p)
             }
             // the next row's as far as L2, a lane for each 128 bytes (8192 x 7168 from codes with both additions: 119 us
             // against 124; there is no room for it in the ring beside dy_add)
-            if (VEC > 1 && row + step < p.rows && (lane & 7) == 0) {
+            if (row + step < p.rows && (lane & (VEC > 1 ? 7 : 31)) == 0) {
                 const T *next = src + step * p.ld_add;
 #pragma unroll
-                for (int i = 0; i < N; i++)
+                for (int i = 0; i < N; i++) {
                     if (in(i)) asm volatile("prefetch.global.L2 [%0];" ::"l"(next + i * STEP));
+                    if (VEC == 1 && sizeof(T) == 4 && in2(i)) asm volatile("prefetch.global.L2 [%0];" ::"l"(next + i * STEP + 32));
+                }
             }
         }
         const uint8_t *st = mine + stage * p.stage_bytes;
@@ -808,7 +822,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) dnorm_kernel(Bwd p)
                 }
                 constexpr int M = VEC > 1 ? VEC : 2;
                 float f[M];
-                if (p.dx_add) {
+                if (ADD && p.dx_add) {
                     float d[M] = {};
                     if (in(i)) {
                         float r[VEC];
@@ -997,14 +1011,22 @@ static cudaError_t fwd_plan(Fwd &p, cudaStream_t st)
     return ept == 16 ? fwd_launch<T, VEC, 16, true>(p, grid, smem, st) : fwd_launch<T, VEC, 32, true>(p, grid, smem, st);
 }
 
+template <typename T, int VEC, int EPT, bool CKPT, bool FULL, int ADD>
+static cudaError_t bwd_launch_add(const Bwd &p, int grid, int smem, cudaStream_t st)
+{
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = allow_smem(reinterpret_cast<const void *>(dnorm_kernel<T, VEC, EPT, CKPT, FULL, ADD>), SMEM_MAX, done);
+    if (e != cudaSuccess) return e;
+    dnorm_kernel<T, VEC, EPT, CKPT, FULL, ADD><<<grid, p.warps * p.groups * 32, smem, st>>>(p);
+    return cudaGetLastError();
+}
+
 template <typename T, int VEC, int EPT, bool CKPT, bool FULL>
 static cudaError_t bwd_launch(const Bwd &p, int grid, int smem, cudaStream_t st)
 {
-    static std::atomic<uint64_t> done{0};
-    const cudaError_t e = allow_smem(reinterpret_cast<const void *>(dnorm_kernel<T, VEC, EPT, CKPT, FULL>), SMEM_MAX, done);
-    if (e != cudaSuccess) return e;
-    dnorm_kernel<T, VEC, EPT, CKPT, FULL><<<grid, p.warps * p.groups * 32, smem, st>>>(p);
-    return cudaGetLastError();
+    if (!p.dy_add && !p.dx_add) return bwd_launch_add<T, VEC, EPT, CKPT, FULL, 0>(p, grid, smem, st);
+    if (EPT == 16 || !p.dy_add || p.at_dya >= 0) return bwd_launch_add<T, VEC, EPT, CKPT, FULL, 1>(p, grid, smem, st);
+    return bwd_launch_add<T, VEC, EPT, CKPT, FULL, EPT == 16 ? 1 : 2>(p, grid, smem, st);       // 16 a thread: always room
 }
 
 template <typename T, int VEC, int EPT, bool CKPT>
@@ -1045,12 +1067,12 @@ static int bwd_plan(Bwd &p, bool vec, int es, int &ept, int &smem)
         p.at_s = n;
         if (p.h_q) n = (n + p.wide / 128 * 4 + 15) & ~15;
         p.at_dya = dya ? n : -1;
-        if (dya) n += p.wide * 4;
+        if (dya) n += p.wide * 4 + (vec ? 0 : 32);
         p.stage_bytes = n;
     };
     p.weight_bytes = p.wide * 4;
     const int room = SMEM_MAX - p.weight_bytes;
-    lay(vec && p.dy_add);
+    lay(p.dy_add != nullptr);
     if (p.stage_bytes > room) lay(false);
     while (groups > 1 && 2 * groups * p.stage_bytes > room) groups--;
     p.stages = room / (groups * p.stage_bytes);

@@ -114,6 +114,27 @@ def test_first_row_ends_in_its_first_16_bytes(L, dt, cols, shift, center):
     assert bool(((dw.double() - rdw).abs() <= K * sw).all()) and bool(((db.double() - rdb).abs() <= K * sb).all())
 
 
+@pytest.mark.parametrize("rows,cols,dt,shift", [(400, 1, torch.bfloat16, 1), (300, 5, torch.float32, 3), (211, 1001, torch.bfloat16, 2),
+                                                (170, 3001, torch.float32, 1), (3, 16383, torch.float32, 1), (5, 9001, torch.bfloat16, 3)])
+@pytest.mark.parametrize("center", [True, False])
+def test_backward_odd_rows_with_both_additions(L, rows, cols, dt, shift, center):
+    """Staged where the rows fit beside each other, in place where not; starts off a 16-byte boundary, shared memory
+    that holds NaN."""
+    g = torch.Generator(device=DEV).manual_seed(rows + cols)
+    x, dy, res = (rows_of(rows, cols, dt, g, shift=s) for s in (shift, 0, shift))
+    add = rows_of(rows, cols, torch.float32, g, shift=shift)
+    w = 1 + 0.3 * torch.randn(cols, device=DEV, generator=g)
+    _, mean, rstd, _, _ = L.moe_layer_norm(x, w, eps=1e-2, center=center, mean=True, rstd=True)
+    bad = torch.full((1000, 8191), float("nan"), device=DEV)
+    r_bad = L.moe_layer_norm(bad, bad[0], bad[0], rstd=True)[2]
+    L.moe_layer_norm_backward(bad, r_bad, x=bad, weight=bad[0], center=False)
+    dx, dw, db = L.moe_layer_norm_backward(dy, rstd, x=x, mean=mean, weight=w, center=center, dy_add=add, dx_add=res, dbias=True)
+    h = (x.double() - mean.double()[:, None]) * rstd.double()[:, None]
+    rdx, rdw, rdb, size, sw, sb = R.norm_backward(dy, h, rstd, w, center, add, res)
+    check(dx, rdx, size, dt, "dx")
+    assert bool(((dw.double() - rdw).abs() <= K * sw).all()) and bool(((db.double() - rdb).abs() <= K * sb).all())
+
+
 def test_forward_far_mean_and_constant_rows(L):
     """A mean a thousand times the spread; a constant row is 0 before the bias; scale of the RMS form."""
     g = torch.Generator(device=DEV).manual_seed(5)

@@ -158,9 +158,9 @@ struct Where {
 // are an 8-byte piece of the channel's row of the code tile (piece w at
 // w ^ (l & 15): no bank conflicts either way); a channel leaves as one
 // 128-byte run.
-// Bound by instructions with COL (70% issue; the five codes a pair alone take
-// 15 clocks of a scheduler's conversions a warp): 313 us of 198 that the bytes
-// need.  ROW alone 141 us = 5.8 TB/s.
+// Bound by instructions with COL (59% issue, in step between two barriers a
+// tile; the five codes a pair alone take 15 clocks of a scheduler's conversions
+// a warp): 313 us of 198 that the bytes need.  ROW alone 140-145 us = 5.7-5.8 TB/s.
 template <bool ROW, bool COL>
 __global__ void __launch_bounds__(THREADS, 1) swiglu_ckpt_kernel(Args p)
 {

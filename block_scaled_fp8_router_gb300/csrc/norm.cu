@@ -12,10 +12,10 @@
 // Everything between the loads and the stores is fp32.
 //
 // Both are bound by memory where there are many rows (8192 x 7168 bf16, GPU
-// alone: forward 40 us = 5.8 TB/s, with both codes 67 us = 5.3 TB/s, backward
-// from the codes with both additions 122 us = 5.3 TB/s; the measured copy has
-// 6.8), by the exchanges of a row and its instructions where a value is one
-// instruction each (rows without whole vectors: 2.4-3.4 TB/s).
+// alone: forward 39 us = 6.0 TB/s, with both codes 62 us = 5.7 TB/s, backward
+// from the codes with both additions 119-121 us = 5.4 TB/s; the measured copy
+// has 6.8), by the exchanges of a row and its instructions where a value is one
+// instruction each (rows without whole vectors: 2.2-3.6 TB/s).
 #include <initializer_list>
 #include <type_traits>
 
@@ -604,7 +604,7 @@ __device__ __forceinline__ void decode(const uint8_t *q, float s, uint64_t (&v)[
 // of db; else the RMS form without.  At the end the groups' sums are
 // joined in group order through shared memory and leave as this CTA's part;
 // reduce_kernel adds the parts in CTA order (no atomics: the same bits every
-// time).  8192 x 7168 bf16 from x: RMS 69 us (5.1 TB/s), FULL 80 (4.4: the
+// time).  8192 x 7168 bf16 from x: RMS 66 us (5.3 TB/s), FULL 79 (4.5: the
 // instructions of one group of 14 warps an SM).  More threads at fewer
 // registers (896 at 72) or two rows at a time spill, which next to 220 KB of
 // shared memory costs 1.5 times the whole.

@@ -209,9 +209,10 @@ __global__ void __launch_bounds__(THREADS, 1) swiglu_ckpt_kernel(Args p)
                         if (s_pad[mid] <= f_kb * TILE) lo = mid;
                         else hi = mid;
                     }
-                    r0 = (int64_t)s_off[lo] + (f_kb * TILE - s_pad[lo]);
+                    const int64_t in = (int64_t)f_kb * TILE - s_pad[lo];       // the block's place among the expert's rows
+                    r0 = s_off[lo] + in;
                     rend = s_off[lo + 1] < p.rows ? s_off[lo + 1] : p.rows;
-                    if (r0 < 0) rend = 0;
+                    if (in < 0 || r0 < 0) rend = r0;                           // in front of the expert's rows, or of all rows: empty
                 }
                 k_n = rend <= r0 ? 0 : rend - r0 < TILE ? (int)(rend - r0) : TILE;
                 k_r0 = k_n ? (int)r0 : 0;

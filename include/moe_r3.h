@@ -767,6 +767,8 @@ moe_status moe_router_backward_dense(const uint16_t *x, const uint16_t *w_router
  *   Scales and codes by the same rule.  Columns at and behind pad[E] are not written,
  *   and none behind max_pad are (the rows of those have their other outputs).
  *   Rows that expert_offsets names outside [0, rows) are not read or written.
+ *   A block of 128 columns that the maps begin in front of its expert's rows
+ *   or of row 0 is empty: zero codes, and none of its rows.
  *   No output overlaps an input or another output.  Any of rows, slots and
  *   max_pad may be 0.
  *   workspace (with d_gates): moe_swiglu_backward_ckpt_workspace_size bytes,

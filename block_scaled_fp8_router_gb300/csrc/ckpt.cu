@@ -138,6 +138,34 @@ constexpr int SMEM_ROW = 2 * STAGE;
 constexpr int SMEM_COL = 2 * STAGE + CODES + RED + 3 * TILE * 4 + 2 * (MAX_E + 1) * 4;
 static_assert(SMEM_COL <= 227 * 1024, "shared memory of a tile");
 
+// The rows of padded block kb: the first one, and the end of those that are
+// there (not behind it where there are none): those of the expert with
+// pad[e] <= 128 kb < pad[e + 1]
+struct Rows {
+    int64_t first, end;
+};
+__device__ __forceinline__ Rows block_rows(const int32_t *pad, const int32_t *off, int E, int64_t kb, int64_t rows)
+{
+    int lo = 0, hi = E;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (pad[mid] <= kb * TILE) lo = mid;
+        else hi = mid;
+    }
+    const int64_t in = kb * TILE - pad[lo];                    // the block's place among the expert's rows
+    const int64_t first = off[lo] + in;
+    const int64_t end = off[lo + 1] < rows ? off[lo + 1] : rows;
+    return {first, in < 0 || first < 0 ? first : end};         // in front of the expert's rows, or of all rows: empty
+}
+
+// the blocks that the maps name (no more than E experts of these rows or ld can have); those behind ld give their
+// rows' outputs only
+__device__ __forceinline__ int blocks_named(int P, int E, int64_t rows, int ld)
+{
+    const int most = max((int)((rows + TILE - 1) / TILE) + E, ld / TILE);
+    return P <= 0 ? 0 : min(P / TILE, most);
+}
+
 struct Where {
     int kb, cb;                 // the tile
     int row;                    // the warp's first row
@@ -178,10 +206,7 @@ __global__ void __launch_bounds__(THREADS, 1) swiglu_ckpt_kernel(Args p)
             s_off[e] = __ldg(p.offsets + e);
         }
         __syncthreads();
-        // every block that the maps name (no more than E experts of these rows
-        // or ld can have); those behind ld give their rows' outputs only
-        const int P = s_pad[p.E], most = max(blocks + p.E, p.ld / TILE);
-        blocks = P <= 0 ? 0 : min(P / TILE, most);
+        blocks = blocks_named(s_pad[p.E], p.E, p.rows, p.ld);
     }
     // this CTA's tiles: the same number each, the first ones one more
     const int total = blocks * nb, each = total / (int)gridDim.x, more = total - each * (int)gridDim.x;
@@ -203,16 +228,8 @@ __global__ void __launch_bounds__(THREADS, 1) swiglu_ckpt_kernel(Args p)
                 k_at = f_kb;
                 int64_t r0 = (int64_t)f_kb * TILE, rend = p.rows;
                 if (COL) {
-                    int lo = 0, hi = p.E;                              // pad[lo] <= 128 kb, 128 kb < pad[hi]
-                    while (hi - lo > 1) {
-                        const int mid = (lo + hi) >> 1;
-                        if (s_pad[mid] <= f_kb * TILE) lo = mid;
-                        else hi = mid;
-                    }
-                    const int64_t in = (int64_t)f_kb * TILE - s_pad[lo];       // the block's place among the expert's rows
-                    r0 = s_off[lo] + in;
-                    rend = s_off[lo + 1] < p.rows ? s_off[lo + 1] : p.rows;
-                    if (in < 0 || r0 < 0) rend = r0;                           // in front of the expert's rows, or of all rows: empty
+                    const Rows b = block_rows(s_pad, s_off, p.E, f_kb, p.rows);
+                    r0 = b.first, rend = b.end;
                 }
                 k_n = rend <= r0 ? 0 : rend - r0 < TILE ? (int)(rend - r0) : TILE;
                 k_r0 = k_n ? (int)r0 : 0;
@@ -375,26 +392,65 @@ __global__ void __launch_bounds__(THREADS, 1) swiglu_ckpt_kernel(Args p)
     cp_async_wait<0>();
 }
 
-// d_gates[slot]: the blocks' dots of the slot's row, sixteen lanes a slot (a
-// fixed tree), over its gate; 0 for a slot without a row and for a gate of 0
-// (its row of d_act holds nothing, and every gate function's slope is 0 there)
-__global__ void __launch_bounds__(256) gate_kernel(const float *__restrict__ dots, const float *__restrict__ gates,
-                                                   const int32_t *__restrict__ slot_to_sorted, int64_t slots,
-                                                   int64_t rows, const int32_t *__restrict__ routed, int nb,
-                                                   float *__restrict__ d_gates)
+// Whether a row's dots were written: whether the block in which its expert has
+// the row is named and holds it.
+__device__ __forceinline__ bool row_formed(int64_t r, int64_t rows, const int32_t *__restrict__ off,
+                                           const int32_t *__restrict__ pad, int E, int ld)
 {
-    if (routed && __ldg(routed) < rows) rows = __ldg(routed);      // expert_offsets[E]
-    const int64_t p = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) >> 4;
+    int lo = 0, hi = E;                                            // off[lo] <= r < off[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (off[mid] <= r) lo = mid;
+        else hi = mid;
+    }
+    const int64_t at = pad[lo] + (r - off[lo]);
+    if (at < 0 || at / TILE >= blocks_named(pad[E], E, rows, ld)) return false;
+    const Rows b = block_rows(pad, off, E, at / TILE, rows);
+    return r >= b.first && r < b.first + TILE && r < b.end;
+}
+
+constexpr int GATE_THREADS = 256, GATE_SLOTS = GATE_THREADS / 16;
+
+// d_gates[slot]: the blocks' dots of the slot's row, sixteen lanes a slot (a
+// fixed tree), over its gate; 0 for a slot whose row has no dots and for a
+// gate of 0 (its row of d_act holds nothing, and every gate function's slope
+// is 0 there).  With maps (off, pad) a CTA first sees whether they leave out
+// no row in front of off[E], as those of a dispatch do; else each row is
+// looked up, so that whatever the maps are, nothing is read that this call
+// did not write (looking up every row: 82 us for 24576 x 1408 with every operand against
+// 79, 323 for 65536 x 2048 against 314).
+__global__ void __launch_bounds__(GATE_THREADS) gate_kernel(const float *__restrict__ dots,
+                                                            const float *__restrict__ gates,
+                                                            const int32_t *__restrict__ slot_to_sorted, int64_t slots,
+                                                            int64_t rows, const int32_t *__restrict__ off,
+                                                            const int32_t *__restrict__ pad, int E, int ld, int nb,
+                                                            float *__restrict__ d_gates)
+{
     const int lane = threadIdx.x & 15;
-    const int32_t r = p < slots ? __ldg(slot_to_sorted + p) : -1;
-    const float g = p < slots ? __ldg(gates + p) : 0.0f;
-    const bool in = r >= 0 && r < rows && g != 0.0f;
-    float s = 0.0f;
-    if (in)
-        for (int b = lane; b < nb; b += 16) s += __ldg(dots + (int64_t)r * nb + b);
+    int64_t end = rows;
+    bool whole = true;
+    if (off) {
+        const int32_t P = __ldg(pad + E), A = __ldg(off + E);
+        bool ok = P % TILE == 0 && P / TILE <= blocks_named(P, E, rows, ld);
+        for (int e = threadIdx.x; e < E; e += GATE_THREADS) {
+            const int64_t o0 = __ldg(off + e), o1 = __ldg(off + e + 1), p0 = __ldg(pad + e), p1 = __ldg(pad + e + 1);
+            ok = ok && o0 <= o1 && p1 - p0 >= o1 - o0 && p0 % TILE == 0 && (e || (o0 == 0 && p0 == 0));
+        }
+        whole = __syncthreads_and(ok);
+        if (A < end) end = A;
+    }
+    for (int64_t p0 = blockIdx.x * (int64_t)GATE_SLOTS; p0 < slots; p0 += gridDim.x * (int64_t)GATE_SLOTS) {
+        const int64_t p = p0 + (threadIdx.x >> 4);
+        const int32_t r = p < slots ? __ldg(slot_to_sorted + p) : -1;
+        const float g = p < slots ? __ldg(gates + p) : 0.0f;
+        const bool in = r >= 0 && g != 0.0f && (whole ? r < end : r < rows && row_formed(r, rows, off, pad, E, ld));
+        float s = 0.0f;
+        if (in)
+            for (int b = lane; b < nb; b += 16) s += __ldg(dots + (int64_t)r * nb + b);
 #pragma unroll
-    for (int o = 8; o; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-    if (lane == 0 && p < slots) d_gates[p] = in ? __fdiv_rn(s, g) : 0.0f;
+        for (int o = 8; o; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+        if (lane == 0 && p < slots) d_gates[p] = in ? __fdiv_rn(s, g) : 0.0f;
+    }
 }
 
 template <bool ROW, bool COL>
@@ -459,10 +515,12 @@ MOE_API moe_status moe_swiglu_backward_ckpt(const uint16_t *d_act, const uint8_t
                                    : (col ? launch<false, true>(p, blocks, st) : launch<false, false>(p, blocks, st));
         if (e != cudaSuccess) return MOE_ERR_CUDA;
     }
-    if (d_gates && slots)
-        gate_kernel<<<(unsigned)((slots + 15) / 16), 256, 0, st>>>(ws, gates, slot_to_sorted, slots, rows,
-                                                                    col ? expert_offsets + E : nullptr, F / 128, d_gates);
-    else if (!blocks)
+    if (d_gates && slots) {
+        const int64_t each = (slots + GATE_SLOTS - 1) / GATE_SLOTS, most = (int64_t)sm_count() * 8;
+        gate_kernel<<<(unsigned)(each < most ? each : most), GATE_THREADS, 0, st>>>(
+            ws, gates, slot_to_sorted, slots, rows, col ? expert_offsets : nullptr, pad, E, (int)max_pad, F / 128, d_gates);
+    } else if (!blocks) {
         return MOE_OK;
+    }
     return launch_status();
 }

@@ -756,7 +756,8 @@ moe_status moe_router_backward_dense(const uint16_t *x, const uint16_t *w_router
  *       [rows, 2F/128] (the dgrad operand, as moe_swiglu_backward's);
  *     d_gates[p] (nullable, [slots]): for slot p with row r =
  *       slot_to_sorted[p], <d_act[r], act[r]> / gates[p]; 0 where r is
- *       outside [0, rows) or the gate is 0.  With d_act = W2^T (gate dy) that
+ *       outside [0, rows) or not among the rows that the maps name, or the
+ *       gate is 0.  With d_act = W2^T (gate dy) that
  *       is <dy, W2 act>;
  *     dhT_q, dhT_s and actT_q, actT_s (nullable pairs): dh and act in 128 x 1
  *       codes, channel-major [2F, max_pad] and [F, max_pad], scales

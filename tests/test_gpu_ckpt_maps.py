@@ -88,3 +88,39 @@ def test_rows_outside_are_left_alone(L, off, pad):
     r = sl2.long()
     dot_rows = rows[r]
     assert bool(dg[dot_rows].isfinite().all())
+
+
+LEFT_OUT = [([10, 60], [0, 128]),               # rows in front of the first expert's
+            ([0, 60, 300], [0, 128, 128]),      # an expert without columns
+            ([0, 60, 300], [0, 128, 256]),      # one with fewer columns than rows
+            ([0, 60, 300], [128, 256, 512]),    # columns that begin behind 0
+            ([0, 60, 300], [256, 0, 384]),      # columns out of order
+            ([0, 300, 60], [0, 384, 512]),      # rows out of order
+            ([0, 60, 300], [0, 128, 0])]        # no columns at all
+
+
+@pytest.mark.parametrize("off,pad", MAPS + LEFT_OUT)
+def test_gates_of_rows_left_out(L, off, pad):
+    """A slot whose row no block of the maps holds has a gradient of 0, whatever
+    the workspace held; the others as without maps.  (Maps out of order may leave
+    out more rows: each slot has the one or the other.)"""
+    A, F, E = 300, 256, len(off) - 1
+    g = torch.Generator(device=DEV).manual_seed(pad[-1] + off[-1])
+    r = lambda *s: torch.randn(*s, device=DEV, generator=g)  # noqa: E731
+    d_act, h_s = (1e-3 * r(A, F)).bfloat16(), 0.01 + 0.01 * torch.rand(A, 2 * F // 128, device=DEV, generator=g)
+    h_q = torch.randint(0, 0x70, (A, 2 * F), device=DEV, generator=g, dtype=torch.uint8)
+    gates, sl2 = 0.1 + torch.rand(A, device=DEV, generator=g), torch.randperm(A, device=DEV, generator=g).int()
+    want = L.moe_swiglu_backward_ckpt(d_act, h_q, h_s, gates=gates, slot_to_sorted=sl2, dh=False, d_gates=True)[1]
+    assert bool((want != 0).all())
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device=DEV)  # noqa: E731
+    ld = 512
+    work = torch.full((A * F // 128,), float("nan"), device=DEV)
+    _, dg, _, _ = L.moe_swiglu_backward_ckpt(d_act, h_q, h_s, gates=gates, slot_to_sorted=sl2, expert_offsets=i32(off),
+                                             pad=i32(pad), ld=ld, d_gates=True, dhT=True, actT=True, workspace=work)
+    rows = torch.zeros(A, dtype=torch.bool)
+    rows[[row for _, row in named(off, pad, E, A, max(pad))]] = True
+    has = rows.to(DEV)[sl2.long()]
+    if off == sorted(off) and pad == sorted(pad):
+        assert torch.equal(dg, torch.where(has, want, torch.zeros_like(want)))
+    else:
+        assert bool(((dg == 0) | (dg == want)).all())

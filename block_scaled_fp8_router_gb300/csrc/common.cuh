@@ -18,6 +18,38 @@ static inline cudaStream_t as_stream(void *s) { return reinterpret_cast<cudaStre
 
 static inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// bytes of a buffer that a call is given (p NULL: none)
+struct Span {
+    const void *p;
+    int64_t bytes;
+};
+
+static inline bool overlap(const void *a, int64_t na, const void *b, int64_t nb)
+{
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return a && b && na > 0 && nb > 0 && x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
+}
+
+// whether any of the outputs lies over any of the inputs
+template <int M, int N>
+static bool overlap_any(const Span (&outs)[M], const Span (&ins)[N])
+{
+    for (const Span &o : outs)
+        for (const Span &i : ins)
+            if (overlap(o.p, o.bytes, i.p, i.bytes)) return true;
+    return false;
+}
+
+// whether any two of the outputs lie over each other
+template <int M>
+static bool overlap_each(const Span (&outs)[M])
+{
+    for (int i = 1; i < M; i++)
+        for (int j = 0; j < i; j++)
+            if (overlap(outs[i].p, outs[i].bytes, outs[j].p, outs[j].bytes)) return true;
+    return false;
+}
+
 static inline int sm_count()
 {
     int dev = 0, n = 0;

@@ -1283,6 +1283,14 @@ static moe_status ffn_launch(const uint8_t *xq, int64_t x_rows, const float *xs,
     if (!aligned16(xq) || !aligned16(w13_q) || !aligned16(w2_q) || !aligned16(out) ||
         (reinterpret_cast<uintptr_t>(workspace) & 255) != 0)
         return MOE_ERR_ALIGN;
+    if (H8) {
+        const Span outs[] = {{out, max_rows * d * 2}, {h_q, max_rows * 2 * F}, {h_s, max_rows * (F / 128) * 8},
+                             {workspace, (int64_t)need}};
+        const int64_t w = (int64_t)E * d * F, ws = w / 16384 * 4;
+        const Span ins[] = {{xq, x_rows * d}, {xs, x_rows * (d / 128) * 4}, {expert_offsets, (E + 1) * 4},
+                            {w13_q, 2 * w}, {w13_s, 2 * ws}, {w2_q, w}, {w2_s, ws}};
+        if (overlap_any(outs, ins) || overlap_each(outs)) return MOE_ERR_UNSUPPORTED;
+    }
     auto enc = encode_fn();
     if (!enc) return MOE_ERR_CUDA;
     uint8_t *act_q = reinterpret_cast<uint8_t *>(workspace);

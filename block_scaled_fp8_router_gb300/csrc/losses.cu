@@ -823,12 +823,6 @@ static moe_status check_rows(const void *logits, int dtype, int64_t N, int64_t V
     return MOE_OK;
 }
 
-static bool overlap(const void *a, int64_t na, const void *b, int64_t nb)
-{
-    const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
-    return a && b && x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
-}
-
 // whether the gradient's rows lie over the logits' in a way other than row on
 // row: a row's CTAs would write what another row has yet to read
 static bool rows_clash(const void *logits, int64_t ld, const void *d, int64_t ld_d, int64_t N, int64_t V, int64_t es)

@@ -912,28 +912,6 @@ __global__ void __launch_bounds__(1024) reduce_kernel(const float *__restrict__ 
 
 // ------------------------------------------------------------------- host
 
-static bool overlap(const void *a, int64_t na, const void *b, int64_t nb)
-{
-    if (!a || !b) return false;
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
-}
-
-struct Span {
-    const void *p;
-    int64_t bytes;
-};
-
-// whether any of the outputs lies over any of the inputs
-template <int M, int N>
-static bool overlap_any(const Span (&outs)[M], const Span (&ins)[N])
-{
-    for (const Span &o : outs)
-        for (const Span &i : ins)
-            if (overlap(o.p, o.bytes, i.p, i.bytes)) return true;
-    return false;
-}
-
 static int64_t span(int64_t rows, int64_t ld, int64_t cols, int es) { return ((rows - 1) * ld + cols) * es; }
 
 static bool aligned4(std::initializer_list<const void *> ps)

@@ -747,7 +747,8 @@ moe_status moe_router_backward_dense(const uint16_t *x, const uint16_t *w_router
  * moe_grouped_ffn_fp8_ckpt  moe_grouped_ffn_fp8 that also writes GEMM1's
  *   pre-activations h (gate columns, then up) as 1 x 128 codes h_q
  *   [max_rows, 2F] and scales h_s [max_rows, 2F/128], by the rule above (here
- *   s and 1/s are correctly rounded).  act is formed from h itself.
+ *   s and 1/s are correctly rounded).  act is formed from h itself.  Neither
+ *   an output nor the workspace lies over an input or over one another.
  * moe_swiglu_backward_ckpt  from d_act [rows, F] bf16 and that checkpoint,
  *   with g = code * scale of the gate columns, u of the up columns, a = d_act,
  *   s(g) = 1 / (1 + exp(-g)):
@@ -770,11 +771,12 @@ moe_status moe_router_backward_dense(const uint16_t *x, const uint16_t *w_router
  *   Rows that expert_offsets names outside [0, rows) are not read or written.
  *   A block of 128 columns that the maps begin in front of its expert's rows
  *   or of row 0 is empty: zero codes, and none of its rows.
- *   No output overlaps an input or another output.  Any of rows, slots and
- *   max_pad may be 0.
+ *   Neither an output nor the workspace overlaps an input or another output.
+ *   Any of rows, slots and max_pad may be 0.
  *   workspace (with d_gates): moe_swiglu_backward_ckpt_workspace_size bytes,
  *   16-byte aligned, no initialisation.
  * Errors: NULL, SHAPE, ALIGN (codes, d_act not 16-byte aligned), WORKSPACE,
+ * UNSUPPORTED (an output or the workspace over an input or over one another),
  * CUDA.
  * ---------------------------------------------------------------------- */
 #define MOE_TYPE_BF16 0

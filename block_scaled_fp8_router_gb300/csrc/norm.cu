@@ -1089,11 +1089,10 @@ MOE_API moe_status moe_layer_norm(const void *x, int dtype, int64_t rows, int64_
     if (!aligned4({mean, rstd, y_s, xhat_s})) return MOE_ERR_ALIGN;
     const Span in_x{x, span(rows, ld_x, cols, es)}, in_w{weight, cols * ws}, in_b{bias, cols * ws};
     const int64_t codes = rows * cols, scales = rows * (cols / 128) * 4;
-    if (clash(y, ld_y, x, ld_x, rows, (int)cols, es) ||
-        overlap_any({{y, span(rows, ld_y, cols, es)}, {mean, rows * 4}, {rstd, rows * 4}, {y_q, codes}, {y_s, scales},
-                     {xhat_q, codes}, {xhat_s, scales}}, {in_w, in_b}) ||
-        overlap_any({{mean, rows * 4}, {rstd, rows * 4}, {y_q, codes}, {y_s, scales}, {xhat_q, codes}, {xhat_s, scales}},
-                    {in_x}))
+    const Span out_y{y, span(rows, ld_y, cols, es)};
+    const Span outs[] = {{mean, rows * 4}, {rstd, rows * 4}, {y_q, codes}, {y_s, scales}, {xhat_q, codes}, {xhat_s, scales}};
+    if (clash(y, ld_y, x, ld_x, rows, (int)cols, es) || overlap_any({out_y}, {in_w, in_b}) ||
+        overlap_any(outs, {in_x, in_w, in_b, out_y}) || overlap_each(outs))
         return MOE_ERR_UNSUPPORTED;
     Fwd p{x, weight, bias, y, mean, rstd, y_q, xhat_q, y_s, xhat_s, rows, ld_x, ld_y, (int)cols, 0, 1, 1, 0, 0, 0, eps,
           center != 0, w_dtype == MOE_TYPE_F32};
@@ -1149,11 +1148,12 @@ MOE_API moe_status moe_layer_norm_backward(const void *dy, int dtype, int64_t ro
         return MOE_ERR_WORKSPACE;
     if (sums && !aligned16(workspace)) return MOE_ERR_ALIGN;
     if (!sums && !dx) return MOE_OK;
-    const Span sums_w{dweight, cols * 4}, sums_b{dbias, cols * 4}, 
+    const Span sums_w{dweight, cols * 4}, sums_b{dbias, cols * 4},
         parts{sums ? workspace : nullptr, (int64_t)moe_layer_norm_backward_workspace_size(rows, cols)},
         in_w{weight, cols * ws}, in_m{center && x ? mean : nullptr, rows * 4}, in_r{rstd, rows * 4},
         in_s{xhat_s, rows * (cols / 128) * 4};
-    if (overlap_any({{dx, span(rows, ld_dx, cols, es)}, sums_w, sums_b, parts}, {in_w, in_m, in_r, in_s}) ||
+    const Span outs[] = {{dx, span(rows, ld_dx, cols, es)}, sums_w, sums_b, parts};
+    if (overlap_each(outs) || overlap_any(outs, {in_w, in_m, in_r, in_s}) ||
         overlap_any({sums_w, sums_b, parts}, {{dy, span(rows, ld_dy, cols, es)}, {x, span(rows, ld_x, cols, es)},
                     {dx_add, span(rows, ld_add, cols, es)}, {dy_add, rows * cols * 4}, {xhat_q, rows * cols}}))
         return MOE_ERR_UNSUPPORTED;

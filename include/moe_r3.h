@@ -729,9 +729,9 @@ moe_status moe_router_backward_dense(const uint16_t *x, const uint16_t *w_router
  *   dweight[c] = sum_t a xhat,  dbias[c] = sum_t a   (nullable, fp32).
  *   dy_add [rows, cols] fp32 (nullable): a second gradient of y, as the
  *   router's; dx_add (nullable, x's type, needs dx): the residual's.  dx may
- *   be dy, x or dx_add itself, row on row; else it overlaps none of the
- *   inputs.  Sums over rows run in an order fixed by the sizes and the
- *   device.  rows may be 0: dweight and dbias are zeroed.
+ *   be dy, x or dx_add itself, row on row; else no output and no workspace
+ *   overlaps an input or another output.  Sums over rows run in an order fixed
+ *   by the sizes and the device.  rows may be 0: dweight and dbias are zeroed.
  * Rows x, y, dy, dx, dx_add are all bf16 (MOE_TYPE_BF16) or all fp32
  * (MOE_TYPE_F32) as dtype says, unit column stride, row stride ld >= cols
  * elements, no alignment beyond the element's (whole 16-byte vectors are
@@ -741,8 +741,8 @@ moe_status moe_router_backward_dense(const uint16_t *x, const uint16_t *w_router
  * workspace (with dweight or dbias): moe_layer_norm_backward_workspace_size
  * bytes, 16-byte aligned, no initialisation.
  * Errors: SHAPE (also eps < 0 or not finite), NULL, ALIGN, WORKSPACE,
- * UNSUPPORTED (an output or the workspace over an input other than row on row),
- * CUDA.
+ * UNSUPPORTED (an output or the workspace over an input other than row on row,
+ * or over one another), CUDA.
  *
  * moe_grouped_ffn_fp8_ckpt  moe_grouped_ffn_fp8 that also writes GEMM1's
  *   pre-activations h (gate columns, then up) as 1 x 128 codes h_q

@@ -51,3 +51,29 @@ def test_ffn(lib):
         return lib.moe_grouped_ffn_fp8_ckpt(x, xs, off, rows, E, d, F, w13, w13s, w2, w2s, out, hq, hs, ws, n, None, None)
 
     one_over_another(call, spans, ["out", "hq", "hs", "ws"])
+
+
+def test_norm(lib):
+    rows, cols = 300, 256
+    n = rows * cols
+    spans = dict(x=2 * n, w=4 * cols, b=4 * cols, y=2 * n, mean=4 * rows, rstd=4 * rows, yq=n, ys=n // 32, hq=n, hs=n // 32)
+
+    def call(x, w, b, y, mean, rstd, yq, ys, hq, hs):
+        return lib.moe_layer_norm(x, 0, rows, cols, cols, w, b, 1, 1e-5, 1, y, cols, mean, rstd, yq, ys, hq, hs, None)
+
+    # y over x is the caller's to ask for, row on row
+    one_over_another(call, spans, ["mean", "rstd", "yq", "ys", "hq", "hs"])
+
+
+@pytest.mark.parametrize("codes", [False, True])
+def test_norm_backward(lib, codes):
+    rows, cols = 300, 256
+    n, ws = rows * cols, lib.moe_layer_norm_backward_workspace_size(rows, cols)
+    spans = dict(dy=2 * n, dya=4 * n, w=4 * cols, rstd=4 * rows, dxa=2 * n, dx=2 * n, dw=4 * cols, db=4 * cols, ws=ws)
+    spans.update(dict(hq=n, hs=n // 32) if codes else dict(x=2 * n, mean=4 * rows))
+
+    def call(dy, dya, w, rstd, dxa, dx, dw, db, ws, x=None, mean=None, hq=None, hs=None):
+        return lib.moe_layer_norm_backward(dy, 0, rows, cols, cols, dya, x, cols, hq, hs, w, 1, mean, rstd, 1, dxa, cols, dx,
+                                           cols, dw, db, ws, spans["ws"], None)
+
+    one_over_another(call, spans, ["dw", "db", "ws"])

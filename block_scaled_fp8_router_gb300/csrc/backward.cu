@@ -135,6 +135,8 @@ constexpr int CBT_MAX_D = 8192;
 constexpr int CBT_MAXB = CBT_MAX_D / 128 / (2 * CBT_WARPS);     // blocks per half-warp
 constexpr int CBT_HDR = 512;
 
+static_assert(CBT_HDR + 2 * CBT_MAX_D * 2 <= 48 * 1024, "dy's two buffers need no larger limit");
+
 struct CbtHdr {
     uint64_t dy_full[2], dy_empty[2], out_full[CBT_STAGES], out_empty[CBT_STAGES];
     float partial[CBT_STAGES][CBT_WARPS];
@@ -848,7 +850,11 @@ MOE_API moe_status moe_combine_backward(const uint16_t *dy, const float *gates, 
     if (d <= CBT_MAX_D) {
         const auto kernel = out_sorted ? combine_backward_tma_kernel<true> : combine_backward_tma_kernel<false>;
         const size_t smem = CBT_HDR + (size_t)(2 + (out_sorted ? CBT_STAGES : 0)) * d * 2;
-        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+        // the limit is the kernel's, not the launch's: once, at the largest d's size (another thread may launch
+        // another d between a limit of one's own and the launch); without out_sorted every d is below 48 KB
+        static std::atomic<uint64_t> done{0};
+        if (out_sorted && allow_smem(reinterpret_cast<const void *>(kernel), CBT_HDR + (2 + CBT_STAGES) * CBT_MAX_D * 2,
+                                     done) != cudaSuccess)
             return MOE_ERR_CUDA;
         // two CTAs per SM (both fit in the SM's shared memory for every
         // d <= CBT_MAX_D), persistent over tokens

@@ -634,6 +634,13 @@ static moe_status check_route_args(int T, int d, int E, int k, int score_fn)
     return MOE_OK;
 }
 
+// shared memory of a CTA of route_topk_kernel, ncta CTAs (<= 8) a cluster
+static constexpr size_t rc_smem(int ncta, int k)
+{
+    return sizeof(float) * (size_t)RC_TILE_FLOATS + sizeof(float2) * ((size_t)RC_BT * ncta * k + (size_t)RC_BT * ncta);
+}
+static_assert(rc_smem(8, 32) <= 227 * 1024, "shared memory of the largest E and k");
+
 } // namespace moe
 
 using namespace moe;
@@ -648,10 +655,10 @@ MOE_API moe_status moe_route_topk(const uint16_t *x, const uint16_t *w_router, i
     if (!x || !w_router || !topk_ids || !topk_gates) return MOE_ERR_NULL;
     if (!aligned16(x) || !aligned16(w_router)) return MOE_ERR_ALIGN;
     const int ncta = (E + RC_EC - 1) / RC_EC;  // <= 8: a portable cluster size
-    const size_t smem = sizeof(float) * (size_t)RC_TILE_FLOATS +
-                        sizeof(float2) * ((size_t)RC_BT * ncta * k + (size_t)RC_BT * ncta);
-    if (cudaFuncSetAttribute(route_topk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
-        cudaSuccess)
+    const size_t smem = rc_smem(ncta, k);
+    // the kernel's limit once, at its largest: another thread may launch other sizes
+    static std::atomic<uint64_t> done{0};
+    if (allow_smem(reinterpret_cast<const void *>(route_topk_kernel), (int)rc_smem(8, 32), done) != cudaSuccess)
         return MOE_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];

@@ -23,6 +23,16 @@ int many(call f, int n, const void *dy, const void *gates, const void *out, cons
 }
 """
 
+ROUTE = """
+typedef int (*call)(const void *, const void *, int, int, int, int, int, int, float, void *, void *, void *, void *, void *);
+int many(call f, int n, const void *x, const void *w, int T, int d, int E, int k, void *ids, void *gates, void *stream)
+{
+    int wrong = 0;
+    for (int i = 0; i < n; i++) wrong += f(x, w, T, d, E, k, 0, 1, 1.0f, ids, gates, 0, 0, stream) != 0;
+    return wrong;
+}
+"""
+
 
 @pytest.fixture(scope="module")
 def L():
@@ -75,6 +85,27 @@ def test_combine_backward_of_different_widths(L, tmp_path):
         return call, bufs, (dy, gates, out, sl2)
 
     made = [of(d) for d in (128, 8192, 4096, 7168)]
+    assert together([m[0] for m in made]) == [0] * 4
+    for _, (want, got), _ in made:
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+def test_route_of_different_experts(L, tmp_path):
+    many = loop_of(ROUTE, tmp_path)
+    fn = ctypes.cast(L._lib.moe_route_topk, ctypes.c_void_p)
+    g = torch.Generator(device=DEV).manual_seed(1)
+    T, d = 64, 128
+
+    def of(E, k):
+        x, w = (torch.randn(n, d, device=DEV, generator=g).bfloat16() for n in (T, E))
+        bufs = [(torch.empty(T, k, dtype=torch.int32, device=DEV), torch.empty(T, k, device=DEV)) for _ in range(2)]
+        L.moe_route_topk(x, w, k, 0, topk_ids=bufs[0][0], topk_gates=bufs[0][1])
+        P = lambda t: ctypes.c_void_p(t.data_ptr())  # noqa: E731
+        call = lambda stream: many(fn, 3000, P(x), P(w), T, d, E, k, *map(P, bufs[1]),  # noqa: E731
+                                   ctypes.c_void_p(stream.cuda_stream))
+        return call, bufs, (x, w)
+
+    made = [of(8, 2), of(1024, 32), of(256, 8), of(1024, 8)]
     assert together([m[0] for m in made]) == [0] * 4
     for _, (want, got), _ in made:
         assert all(torch.equal(a, b) for a, b in zip(want, got))

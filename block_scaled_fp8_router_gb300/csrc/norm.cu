@@ -1034,9 +1034,9 @@ static int bwd_plan(Bwd &p, bool vec, int es, int &ept, int &smem)
     p.warps = (p.cols + 32 * ept - 1) / (32 * ept);
     p.wide = p.warps * 32 * ept;
     int groups = BWD_THREADS / 32 / p.warps;
-    const int per_sm = (p.rows + sm_count() - 1) / sm_count();
+    const int64_t per_sm = ((int64_t)p.rows + sm_count() - 1) / sm_count();
     if (groups > 8) groups = 8;                        // named barriers, and the parts joined one after another
-    if (groups > per_sm) groups = per_sm;
+    if (groups > per_sm) groups = (int)per_sm;
     const auto lay = [&](bool dya) {
         const int row = p.wide * es + (vec ? 0 : 32);
         int n = row;

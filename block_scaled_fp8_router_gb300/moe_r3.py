@@ -1069,11 +1069,13 @@ def moe_layer_norm_backward(dy, rstd, x=None, mean=None, ckpt=None, weight=None,
     fp32; each or None).  dy_add [rows, cols] fp32 adds to dy, dx_add (dy's
     type) to dx.  dx, dweight, dbias: True allocates, a tensor is written
     (dx may be dy, x or dx_add), False / None skips."""
+    if ckpt is not None and not isinstance(ckpt, (tuple, list)):
+        raise TypeError("ckpt: expected (codes, scales), as moe_layer_norm returns them")
+    if (x is None) == (ckpt is None):
+        raise ValueError("one of x and ckpt")
     dt, ld = _rows(dy, "dy")
     rows, cols = dy.shape
     _want(rstd, torch.float32, (rows,), "rstd")
-    if (x is None) == (ckpt is None):
-        raise ValueError("one of x and ckpt")
     ld_x = ld_add = ld_dx = cols
     p_mean = p_hq = p_hs = None
     if x is not None:

@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(THREADS, 1) swiglu_ckpt_kernel(Args p)
 #pragma unroll
                 for (int w = 1; w < WARPS; w++) m = fmaxf(m, red[w * 3 * TILE + tid]);
                 const float s = computed_scale(m);
-                col_y[tid] = rcp(s);
+                col_y[tid] = computed_recip(s);
                 const int k = tid >> 7, ch = at.cb * TILE + (tid & 127);
                 if ((int64_t)at.kb * TILE >= p.ld) {
                 } else if (k == 2) {
@@ -345,9 +345,9 @@ __global__ void __launch_bounds__(THREADS, 1) swiglu_ckpt_kernel(Args p)
             leave();
         }
         if (ROW) {
-            // computed_scale by the quotient's code: its branch keeps the encoding behind it apart from what is before
-            // (65536 x 2048, this side alone: 139 us against 151 in one piece)
-            const float s = fmaxf(block_scale(rm), 0x1p-126f), ry = rcp(s);
+            // computed_scale's value by block_scale's code: its branch keeps the encoding behind it apart from what is
+            // before (65536 x 2048, this side alone: 139 us against 153 in one piece)
+            const float s = fmaxf(block_scale(rm), 0x1p-126f), ry = computed_recip(s);
             if ((lane >> 1) < at.n) p.dh_s[(int64_t)(at.row + (lane >> 1)) * 2 * nb + (lane & 1) * nb + at.cb] = s;
             uint8_t *q = p.dh_q + (int64_t)at.row * 2 * p.F + at.cb * TILE + c0, *q2 = q + p.F;
 #pragma unroll

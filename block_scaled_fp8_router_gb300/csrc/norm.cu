@@ -336,7 +336,7 @@ __device__ __forceinline__ void encode(const uint64_t (&v)[VPT][VEC / 2], int c,
             m[i] = amax3(a, b, m[i]);
         }
     }
-    const float sc = computed_scale(scatter_max<VPT, G>(m, lane)), y = rcp(sc);
+    const float sc = computed_scale(scatter_max<VPT, G>(m, lane)), y = computed_recip(sc);
     const int mine = (lane & (G - 1)) / EACH;                  // the vector whose scale this lane has
     const int c_mine = c - (lane & (G - 1)) * VEC + mine * 32 * VEC;
     if ((lane & (EACH - 1)) == 0 && c_mine < cols) s[c_mine >> 7] = sc;

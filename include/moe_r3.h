@@ -716,8 +716,10 @@ moe_status moe_router_backward_dense(const uint16_t *x, const uint16_t *w_router
  *   y_q, y_s (nullable pair): y's 1 x 128 codes and scales (the experts'
  *   operand), from y in fp32 before its rounding to x's type; xhat_q, xhat_s
  *   (nullable pair): xhat's, the checkpoint that moe_layer_norm_backward reads
- *   in place of x.  Scales s = amax / 448 (1 where amax is 0), not below
- *   2^-126, codes E4M3(v / s), s and 1/s to within a unit in the last place.
+ *   in place of x.  Scales s = amax / 448 correctly rounded (1 where that is
+ *   0), else not below 2^-126; codes E4M3(v y), the product rounded to fp32,
+ *   y = 1/s correctly rounded (to within a unit in the last place where s's
+ *   mantissa is all ones).
  *   y may be x itself with ld_y = ld_x; else no output overlaps an input or
  *   another output.  Infinities and NaN act on their own row only, as the
  *   formulas have it in fp32; squares beyond fp32 give r = 0.
@@ -746,9 +748,9 @@ moe_status moe_router_backward_dense(const uint16_t *x, const uint16_t *w_router
  *
  * moe_grouped_ffn_fp8_ckpt  moe_grouped_ffn_fp8 that also writes GEMM1's
  *   pre-activations h (gate columns, then up) as 1 x 128 codes h_q
- *   [max_rows, 2F] and scales h_s [max_rows, 2F/128], by the rule above (here
- *   s and 1/s are correctly rounded).  act is formed from h itself.  Neither
- *   an output nor the workspace lies over an input or over one another.
+ *   [max_rows, 2F] and scales h_s [max_rows, 2F/128], by the rule above.  act
+ *   is formed from h itself.  Neither an output nor the workspace lies over an
+ *   input or over one another.
  * moe_swiglu_backward_ckpt  from d_act [rows, F] bf16 and that checkpoint,
  *   with g = code * scale of the gate columns, u of the up columns, a = d_act,
  *   s(g) = 1 / (1 + exp(-g)):

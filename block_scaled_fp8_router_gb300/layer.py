@@ -103,14 +103,23 @@ class MoELayerFP8:
     norm: the layer runs on the norm of x (one pass gives the normalised rows
     and the FFN's codes of them); norm_backward takes the layer's gradients on
     to x.  ckpt8: what a train forward keeps for the backward is in 8 bits: the
-    pre-activations (a quarter of their fp32 size) and the norm's rows (the
-    caller need not keep x); out_sorted is scratch, the gates' gradient comes
-    from the checkpoint.  fp32-scale sorted form only.
+    pre-activations (a quarter of their fp32 size) and, beside the normalised
+    rows in bf16 that the router's and the weights' gradients read, the norm's
+    checkpoint in place of x (the caller need not keep it); the experts' outputs
+    are not kept, the gates' gradient comes from the checkpoint.  fp32-scale
+    sorted form only.
+
+    scratch: a ckpt8 layer of the same sizes whose scratch this one uses too
+    (what neither a later call nor the caller reads: quantised and sorted rows,
+    the experts' outputs, workspaces, the backward's operands), for a stack
+    whose layers run one after another on one stream, in any order of forwards
+    and backwards.  What a layer keeps for its backward and the tensors that it
+    returns are its own.
     """
 
     def __init__(self, weights: MoEWeightsFP8, T_max: int, k: int, score_fn: int, renorm: int = 1,
                  route_scale: float = 1.0, device=None, gathered: bool = False, norm: MoENorm | None = None,
-                 ckpt8: bool = False):
+                 ckpt8: bool = False, scratch: MoELayerFP8 | None = None):
         self.w = weights
         self.norm = norm
         self.ckpt8 = ckpt8
@@ -120,6 +129,13 @@ class MoELayerFP8:
             raise ValueError("the power-of-two variant runs in the sorted form")
         if ckpt8 and (self.mx or gathered):
             raise ValueError("ckpt8 needs the fp32-scale sorted form")
+        if scratch is not None:
+            if not (ckpt8 and scratch.ckpt8):
+                raise ValueError("scratch is shared between ckpt8 layers (the others keep some of it for their backward)")
+            sizes = lambda w, T, k: (T, k, w.E, w.d, w.F, w.w13_q.device)
+            if sizes(weights, T_max, k) != sizes(scratch.w, scratch.T_max, scratch.k):
+                raise ValueError("scratch: a layer of other sizes")
+        self._scratch = scratch
         self.k, self.score_fn, self.renorm, self.route_scale = k, score_fn, renorm, route_scale
         dev = weights.w13_q.device if device is None else device
         E, d, F = weights.E, weights.d, weights.F
@@ -128,19 +144,23 @@ class MoELayerFP8:
         e = lambda shape, dt: torch.empty(shape, dtype=dt, device=dev)
         self.ids = e((T_max, k), torch.int32)
         self.gates = e((T_max, k), torch.float32)
-        self.xq = e((T_max, d), torch.uint8)
-        self.xs = e((T_max, d // 128), torch.uint8 if self.mx else torch.float32)
         self.counts = e((E,), torch.int32)
         self.offsets = e((E + 1,), torch.int32)
         self.s2s = e((A,), torch.int32)
         self.sl2 = e((A,), torch.int32)
-        self.xq_sorted = None if gathered else e((A, d), torch.uint8)
-        self.xs_sorted = None if (gathered or self.mx) else e((A, d // 128), torch.float32)
-        self.out_sorted = e((A, d), torch.bfloat16)     # slot order when gathered
         self.y = e((T_max, d), torch.bfloat16)
-        self.dsp_ws = e((L.moe_dispatch_workspace_size(T_max, k, E),), torch.uint8)
-        ws = L.moe_grouped_ffn_mx_workspace_size(A, d, F) if self.mx else L.moe_grouped_ffn_workspace_size(A, d, F)
-        self.ffn_ws = e((ws,), torch.uint8)
+        if scratch is not None:
+            self.xq, self.xs, self.xq_sorted, self.xs_sorted = scratch.xq, scratch.xs, scratch.xq_sorted, scratch.xs_sorted
+            self.out_sorted, self.dsp_ws, self.ffn_ws = scratch.out_sorted, scratch.dsp_ws, scratch.ffn_ws
+        else:
+            self.xq = e((T_max, d), torch.uint8)
+            self.xs = e((T_max, d // 128), torch.uint8 if self.mx else torch.float32)
+            self.xq_sorted = None if gathered else e((A, d), torch.uint8)
+            self.xs_sorted = None if (gathered or self.mx) else e((A, d // 128), torch.float32)
+            self.out_sorted = e((A, d), torch.bfloat16)     # slot order when gathered
+            self.dsp_ws = e((L.moe_dispatch_workspace_size(T_max, k, E),), torch.uint8)
+            ws = L.moe_grouped_ffn_mx_workspace_size(A, d, F) if self.mx else L.moe_grouped_ffn_workspace_size(A, d, F)
+            self.ffn_ws = e((ws,), torch.uint8)
         self.dev_status = torch.zeros((1,), dtype=torch.int32, device=dev)
         if norm is not None:
             self.xn = e((T_max, d), torch.bfloat16)
@@ -247,15 +267,10 @@ class MoELayerFP8:
         if T is None or self.mx or self.gathered:
             raise ValueError("backward needs a forward(train=True) of the fp32-scale sorted form")
         A = T * self.k
-        E, d, F = self.w.E, self.w.d, self.w.F
-        dev = dy.device
         if getattr(self, "_bw", None) is None:
-            e = lambda shape, dt: torch.empty(shape, dtype=dt, device=dev)
-            Am = self.T_max * self.k
-            self._bw = dict(d_out_q=e((Am, d), torch.uint8), d_out_s=e((Am, d // 128), torch.float32),
-                            d_gates=e((self.T_max, self.k), torch.float32), d_act=e((Am, F), torch.bfloat16),
-                            dh_q=e((Am, 2 * F), torch.uint8), dh_s=e((Am, 2 * F // 128), torch.float32),
-                            dx_sorted=e((Am, d), torch.bfloat16), dx=e((self.T_max, d), torch.bfloat16))
+            e = lambda shape, dt: torch.empty(shape, dtype=dt, device=dy.device)
+            self._bw = dict(self._backward_scratch(dy.device), d_gates=e((self.T_max, self.k), torch.float32),
+                            dx=e((self.T_max, self.w.d), torch.bfloat16))
         b = self._bw
         w2t_q, w2t_s, w13t_q, w13t_s = self.w.transposed()
         if self.ckpt8:
@@ -289,18 +304,42 @@ class MoELayerFP8:
             return dx, b["d_gates"][:T]
         return (dx, b["d_gates"][:T], *self._weight_grads(dy, T))
 
-    def _ckpt_buffers(self, weight_grads: bool) -> dict:
-        """The 8-bit backward's buffers, made for every T up to T_max at the first call that needs them."""
+    def _backward_scratch(self, dev) -> dict:
+        """What every backward writes before it reads it."""
+        if self._scratch is not None:
+            return self._scratch._backward_scratch(dev)
+        if getattr(self, "_bs", None) is None:
+            d, F, Am = self.w.d, self.w.F, self.T_max * self.k
+            e = lambda shape, dt: torch.empty(shape, dtype=dt, device=dev)
+            self._bs = dict(d_out_q=e((Am, d), torch.uint8), d_out_s=e((Am, d // 128), torch.float32),
+                            d_act=e((Am, F), torch.bfloat16), dh_q=e((Am, 2 * F), torch.uint8),
+                            dh_s=e((Am, 2 * F // 128), torch.float32), dx_sorted=e((Am, d), torch.bfloat16))
+        return self._bs
+
+    def _ckpt_scratch(self, weight_grads: bool) -> dict:
+        """The same of the 8-bit backward alone, made for every T up to T_max at the first call that needs it."""
+        if self._scratch is not None:
+            return self._scratch._ckpt_scratch(weight_grads)
         A, E, d, F = self.T_max * self.k, self.w.E, self.w.d, self.w.F
         e = lambda shape, dt: torch.empty(shape, dtype=dt, device=self.ids.device)
-        c = getattr(self, "_c8", None)
+        c = getattr(self, "_cs", None)
         if c is None:
-            self._c8 = c = dict(ws=e((L.moe_swiglu_backward_ckpt_workspace_size(A, F),), torch.uint8))
+            self._cs = c = dict(ws=e((L.moe_swiglu_backward_ckpt_workspace_size(A, F),), torch.uint8))
         if weight_grads and "pad" not in c:
             ld = L.wgrad_ld(A, E)
             op = lambda C: (e((C, ld), torch.uint8), e((ld // 128, C), torch.float32))
-            c.update(pad=e((E + 1,), torch.int32), ld=ld, dhT=op(2 * F), actT=op(F), rows=op(d),
-                     dW2=e((E, d, F), torch.float32), dW13=e((E, 2 * F, d), torch.float32))
+            c.update(pad=e((E + 1,), torch.int32), ld=ld, dhT=op(2 * F), actT=op(F), rows=op(d))
+        return c
+
+    def _ckpt_buffers(self, weight_grads: bool) -> dict:
+        """The 8-bit backward's buffers: its scratch, and the weights' gradients."""
+        c = getattr(self, "_c8", None)
+        if c is None:
+            self._c8 = c = dict(self._ckpt_scratch(False))
+        if weight_grads and "dW2" not in c:
+            E, d, F = self.w.E, self.w.d, self.w.F
+            e = lambda *shape: torch.empty(shape, dtype=torch.float32, device=self.ids.device)
+            c.update(self._ckpt_scratch(True), dW2=e(E, d, F), dW13=e(E, 2 * F, d))
         return c
 
     def _weight_grads_ckpt(self, dy: torch.Tensor, T: int):

@@ -507,8 +507,8 @@ MOE_API moe_status moe_swiglu_backward_ckpt(const uint16_t *d_act, const uint8_t
     const bool dots = d_gates && slots && rows;
     if (dots && (!workspace || workspace_bytes < moe_swiglu_backward_ckpt_workspace_size(rows, F))) return MOE_ERR_WORKSPACE;
     if (dots && !aligned16(workspace)) return MOE_ERR_ALIGN;
-    const Span outs[] = {{dh_q, rows * 2 * F}, {dh_s, rows * (F / 128) * 8}, {dhT_q, 2 * F * max_pad},
-                         {dhT_s, max_pad / 128 * 2 * F * 4}, {actT_q, F * max_pad}, {actT_s, max_pad / 128 * F * 4},
+    const Span outs[] = {{dh_q, rows * 2 * F}, {dh_s, rows * (F / 128) * 8}, {dhT_q, max_pad * 2 * F},
+                         {dhT_s, max_pad / 128 * 2 * F * 4}, {actT_q, max_pad * F}, {actT_s, max_pad / 128 * F * 4},
                          {d_gates, slots * 4},
                          {dots ? workspace : nullptr, (int64_t)moe_swiglu_backward_ckpt_workspace_size(rows, F)}};
     const Span ins[] = {{d_act, rows * F * 2}, {h_q, rows * 2 * F}, {h_s, rows * (F / 128) * 8},

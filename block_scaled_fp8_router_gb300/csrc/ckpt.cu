@@ -179,16 +179,17 @@ struct Where {
 // instruction: lanes 0-15 its d_act, 16-23 its gate and 24-31 its up codes,
 // whose rows are all 2 F bytes apart).  Lane l takes columns 4 l .. 4 l + 3
 // and holds their d_gate, d_up and act in registers from there on (96 of
-// them; 65536 x 2048 of 256 experts: 313 us, where two passes that each
+// them; 65536 x 2048 of 256 experts: 316 us, where two passes that each
 // recomputed them from the codes took 598).  A row's largest
 // value is one warp reduction, its scale is formed by one lane.  The columns'
 // largest values meet in shared memory.  A lane's eight codes of a channel
 // are an 8-byte piece of the channel's row of the code tile (piece w at
 // w ^ (l & 15): no bank conflicts either way); a channel leaves as one
 // 128-byte run.
-// Bound by instructions with COL (59% issue, in step between two barriers a
-// tile; the five codes a pair alone take 15 clocks of a scheduler's conversions
-// a warp): 313 us of 198 that the bytes need.  ROW alone 140-145 us = 5.7-5.8 TB/s.
+// With COL neither memory nor issue is full (47% and 59%): the sixteen warps
+// go in step between two barriers a tile and wait together; 316 us of 196 that
+// the bytes need (the five codes a pair alone take 15 clocks of a scheduler's
+// conversions a warp).  ROW alone 138-143 us = 5.8-6.0 TB/s.
 template <bool ROW, bool COL>
 __global__ void __launch_bounds__(THREADS, 1) swiglu_ckpt_kernel(Args p)
 {

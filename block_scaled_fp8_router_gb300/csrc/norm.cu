@@ -12,7 +12,7 @@
 // Everything between the loads and the stores is fp32.
 //
 // Both are bound by memory where there are many rows (8192 x 7168 bf16, GPU
-// alone: forward 39 us = 6.0 TB/s, with both codes 62 us = 5.7 TB/s, backward
+// alone: forward 39 us = 6.0 TB/s, with both codes 63.5 us = 5.6 TB/s, backward
 // from the codes with both additions 119-121 us = 5.4 TB/s; the measured copy
 // has 6.8), by the exchanges of a row and its instructions where a value is one
 // instruction each (rows without whole vectors: 2.2-3.6 TB/s).
@@ -301,7 +301,8 @@ struct Fwd {
 // N values of each lane reduced (largest) over groups of G lanes, N <= G
 // powers of two: value i is left in the lanes of the group whose number
 // within it starts, in its log2(N) highest bits, with i.  Each step keeps
-// half of the values: 2 N shuffles fewer than a reduction of each.
+// half of the values: N - 1 + log2(G / N) shuffles, where a reduction of each
+// takes N log2(G) (N = 4, G = 16: 5 against 16).
 template <int N, int G>
 __device__ __forceinline__ float scatter_max(float (&v)[N], int lane)
 {
